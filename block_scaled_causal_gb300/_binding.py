@@ -49,6 +49,13 @@ def _load():
     lib.bf16_attn_bwd_static_capacity.argtypes = []
     lib.bf16_attn_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.bf16_attn_bwd_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    for name, params in (("mx_cache_write", CacheWriteParams), ("mx_cache_read", CacheReadParams),
+                         ("mx_cache_attn", CacheAttnParams)):
+        f = getattr(lib, name)
+        f.restype = i32
+        f.argtypes = [ctypes.POINTER(params), vp]
+    lib.mx_cache_attn_workspace_bytes.restype = ctypes.c_size_t
+    lib.mx_cache_attn_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     lib.bsc_read_device_status.restype = i32
     lib.bsc_read_device_status.argtypes = [vp, vp]
     return lib
@@ -112,6 +119,45 @@ class AttnBwdParams(ctypes.Structure):
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
+
+class CachePools(ctypes.Structure):
+    """Mirror of bsc_mx_cache."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "k_sc", "v", "v_sc")] + \
+        [(n, ctypes.c_longlong) for n in ("k_page_stride", "k_sc_page_stride", "v_page_stride", "v_sc_page_stride")] + \
+        [(n, ctypes.c_int) for n in ("format", "num_pages", "page_size", "Hkv", "D")]
+
+
+def _strides(*names):
+    return [("%s_stride_%s" % (n, d), ctypes.c_longlong) for n in names for d in "bth"]
+
+
+class CacheWriteParams(ctypes.Structure):
+    """Mirror of bsc_mx_cache_write_params."""
+    _fields_ = [("cache", CachePools), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + _strides("k", "v") + \
+        [(n, ctypes.c_int) for n in ("B", "T", "dtype", "rule")] + \
+        [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong), ("max_pages", ctypes.c_int),
+         ("seq_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
+
+
+class CacheReadParams(ctypes.Structure):
+    """Mirror of bsc_mx_cache_read_params."""
+    _fields_ = [("cache", CachePools), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + _strides("k", "v") + \
+        [(n, ctypes.c_int) for n in ("B", "T", "dtype")] + \
+        [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong), ("max_pages", ctypes.c_int),
+         ("seq_lens", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
+
+
+class CacheAttnParams(ctypes.Structure):
+    """Mirror of bsc_mx_cache_attn_params."""
+    _fields_ = [("cache", CachePools), ("q", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p)] + \
+        _strides("q", "o") + [(n, ctypes.c_int) for n in ("B", "T", "Hq", "dtype")] + \
+        [("softmax_scale", ctypes.c_float), ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
+         ("max_pages", ctypes.c_int), ("seq_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p),
+         ("dev_status", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+CACHE_MXFP8, CACHE_MXFP4 = 0, 1
+_ACT = {torch.bfloat16: 0, torch.float16: 1}
 
 lib = _load()
 
@@ -370,3 +416,164 @@ def mxfp8_quantize_qkv(q, k, v, layout=BSHD, rule=SCALE_FLOOR, token_norm=True, 
                        v_sc=_ptr(vsc), vtn_e4m3=_ptr(vtn), vtn_sc=_ptr(vtn_sc))
     _check(lib.mxfp8_quantize_qkv(ctypes.byref(p), _stream(stream)))
     return qq, qs, kq, ks, vt, vsc, vtn, vtn_sc
+
+
+class MxCache:
+    """The key/value cache: a handle on the caller's four uint8 CUDA pools (bsc_mx_cache in bsc.h).
+
+    k, v [num_pages, Hkv, page_size, D] (CACHE_MXFP8) or [..., D/2] (CACHE_MXFP4); k_sc, v_sc
+    [num_pages, Hkv, page_size, D/32].  Dimensions after the first are contiguous; the page stride is
+    free, so pools may be slices of one allocation.  The handle keeps the tensors alive and holds no
+    other state.  `mx_cache_alloc` makes one with new pools."""
+
+    __slots__ = ("k", "k_sc", "v", "v_sc", "fmt", "num_pages", "page_size", "Hkv", "D", "device", "params")
+
+    def __init__(self, k, k_sc, v, v_sc, fmt=CACHE_MXFP4):
+        if fmt not in (CACHE_MXFP8, CACHE_MXFP4):
+            raise ValueError("fmt must be CACHE_MXFP8 or CACHE_MXFP4")
+        pools = (k, k_sc, v, v_sc)
+        for t, n in zip(pools, ("k", "k_sc", "v", "v_sc")):
+            if not t.is_cuda or t.dtype != torch.uint8 or t.dim() != 4 or t.device != k.device:
+                raise ValueError("%s must be a 4-D CUDA uint8 tensor on one device with the others" % n)
+            if t.shape[0] and not t[0].is_contiguous():
+                raise ValueError("%s must be contiguous within a page" % n)
+        pages, Hkv, page_size, row = k.shape
+        D = row * 2 if fmt == CACHE_MXFP4 else row
+        if k.shape != v.shape or k_sc.shape != v_sc.shape or tuple(k_sc.shape) != (pages, Hkv, page_size, D // 32):
+            raise ValueError("k, v must be [pages, Hkv, page_size, row] and k_sc, v_sc [pages, Hkv, page_size, D/32]")
+        self.k, self.k_sc, self.v, self.v_sc = pools
+        self.fmt, self.num_pages, self.page_size, self.Hkv, self.D = fmt, pages, page_size, Hkv, D
+        self.device = k.device
+        self.params = CachePools(*(t.data_ptr() for t in pools), *(t.stride(0) for t in pools), fmt, pages, page_size,
+                                 Hkv, D)
+
+
+def mx_cache_alloc(num_pages, page_size, Hkv, D=128, fmt=CACHE_MXFP4, device="cuda"):
+    """An MxCache with new, zeroed pools (zero bytes stand for zeros)."""
+    shape = (num_pages, Hkv, page_size)
+    row = D // 2 if fmt == CACHE_MXFP4 else D
+    k, k_sc, v, v_sc = (torch.zeros(shape + (n,), dtype=torch.uint8, device=device) for n in (row, D // 32) * 2)
+    return MxCache(k, k_sc, v, v_sc, fmt)
+
+
+def _act_dims(x, layout, H, D, cache, name):
+    """(B, T, H), element strides (b, t, h) and the dtype code of an activation of `cache`'s head size."""
+    code = _ACT.get(x.dtype)
+    if code is None or x.device != cache.device or x.dim() != 4:
+        raise ValueError("%s must be a 4-D bfloat16 or float16 tensor on the cache's device" % name)
+    shape, st = x.shape, x.stride()
+    if layout == BSHD:
+        B, T, sb, s_t = shape[0], shape[1], st[0], st[1]
+    elif layout == SBHD:
+        T, B, s_t, sb = shape[0], shape[1], st[0], st[1]
+    else:
+        raise ValueError("layout must be BSHD or SBHD")
+    if shape[3] != D or (H is not None and shape[2] != H):
+        raise ValueError("%s does not have the cache's heads or head size" % name)
+    if st[3] != 1 and D > 1 and x.numel():
+        raise ValueError("%s must be contiguous along D" % name)
+    return (B, T, shape[2]), (sb, s_t, st[2]), code
+
+
+def _index(t, shape, cache, name):
+    """Pointer of an int32 index array of the given shape (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != cache.device or tuple(t.shape) != shape:
+        raise ValueError("%s must be an int32 tensor of shape %s on the cache's device" % (name, shape))
+    if len(shape) == 1 and shape[0] > 1 and t.stride(0) != 1:
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _table(page_table, B, cache):
+    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be [B, max_pages] with contiguous rows")
+    return (_index(page_table, (B, page_table.shape[1]), cache, "page_table"), page_table.stride(0), page_table.shape[1])
+
+
+def _status(t, cache):
+    if t is not None and (t.dtype != torch.int32 or t.device != cache.device or t.numel() < 1):
+        raise ValueError("dev_status must be an int32 tensor on the cache's device")
+    return None if t is None else t.data_ptr()
+
+
+def _on(stream, device):
+    """Context in which to allocate and launch: the device and stream of a call (so that memory
+    allocated inside belongs to the stream that uses it)."""
+    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
+
+
+def mx_cache_write(cache, k, v, page_table, seq_lens, new_lens=None, layout=BSHD, rule=SCALE_FLOOR, dev_status=None,
+                   stream=None):
+    """Quantises new tokens into the cache.  k, v: bf16 or fp16 [B, T, Hkv, D] (BSHD) or [T, B, Hkv, D]
+    (SBHD), any strides with D contiguous.  Token t < new_lens[b] (None: all T) of sequence b goes to position
+    seq_lens[b] - new_lens[b] + t; page_table [B, max_pages], seq_lens, new_lens [B]: int32 on the device."""
+    (B, T, H), ks, dt = _act_dims(k, layout, cache.Hkv, cache.D, cache, "k")
+    dims, vs, dv = _act_dims(v, layout, cache.Hkv, cache.D, cache, "v")
+    if dims != (B, T, H) or dv != dt:
+        raise ValueError("k and v must have the same shape and dtype")
+    p = CacheWriteParams(cache.params, k.data_ptr(), v.data_ptr(), *ks, *vs, B, T, dt, rule,
+                         *_table(page_table, B, cache), _index(seq_lens, (B,), cache, "seq_lens"),
+                         _index(new_lens, (B,), cache, "new_lens"), _status(dev_status, cache))
+    with _on(stream, cache.device):
+        _check(lib.mx_cache_write(ctypes.byref(p), _stream(stream)))
+
+
+def mx_cache_read(cache, page_table, seq_lens, T, starts=None, layout=BSHD, dtype=torch.bfloat16, k_out=None,
+                  v_out=None, dev_status=None, stream=None):
+    """Reads positions starts[b] .. starts[b] + T - 1 (None: from 0) of every sequence back as values:
+    (k, v), shaped [B, T, Hkv, D] or [T, B, Hkv, D]; zeros outside [0, seq_lens[b])."""
+    B = page_table.shape[0]
+    with _on(stream, cache.device):
+        shape = (B, T, cache.Hkv, cache.D) if layout == BSHD else (T, B, cache.Hkv, cache.D)
+        k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dtype, device=cache.device) if v_out is None else v_out
+        dk, ks, dt = _act_dims(k_out, layout, cache.Hkv, cache.D, cache, "k_out")
+        dv, vs, dt_v = _act_dims(v_out, layout, cache.Hkv, cache.D, cache, "v_out")
+        if dk != (B, T, cache.Hkv) or dv != dk or dt != dt_v:
+            raise ValueError("k_out and v_out must both be [B, T, Hkv, D] in the layout, of one dtype")
+        p = CacheReadParams(cache.params, k_out.data_ptr(), v_out.data_ptr(), *ks, *vs, B, T, dt,
+                            *_table(page_table, B, cache), _index(seq_lens, (B,), cache, "seq_lens"),
+                            _index(starts, (B,), cache, "starts"), _status(dev_status, cache))
+        _check(lib.mx_cache_read(ctypes.byref(p), _stream(stream)))
+    return k_out, v_out
+
+
+def mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D=128):
+    """Bytes of scratch mx_cache_attn needs (the C call of the same name)."""
+    return int(lib.mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D))
+
+
+def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, softmax_scale=None, o=None, lse=None,
+                  workspace=None, dev_status=None, stream=None):
+    """Attention of T queries per sequence over the cache; returns (O shaped and typed like q, LSE fp32
+    [B, Hq, T]).  Query t < new_lens[b] (None: all T) is the token at position seq_lens[b] - new_lens[b] + t and
+    attends the positions up to its own.  `workspace`: a device tensor of at least
+    mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D) bytes that no other running call uses, else one is
+    allocated here."""
+    (B, T, Hq), qs, dt = _act_dims(q, layout, None, cache.D, cache, "q")
+    with _on(stream, cache.device):
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dims, os_, dt_o = _act_dims(o, layout, Hq, cache.D, cache, "o")
+        if dims != (B, T, Hq) or dt_o != dt:
+            raise ValueError("o must have q's shape and dtype")
+        if lse is None:
+            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+        elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T) or lse.device != q.device or \
+                not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous float32 tensor [B, Hq, T] on the cache's device")
+        if workspace is None:
+            need = mx_cache_attn_workspace_bytes(B, T, Hq, cache.Hkv, cache.D)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        elif workspace.device != q.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        p = CacheAttnParams(cache.params, q.data_ptr(), o.data_ptr(), lse.data_ptr(), *qs, *os_, B, T, Hq, dt,
+                            cache.D ** -0.5 if softmax_scale is None else softmax_scale,
+                            *_table(page_table, B, cache), _index(seq_lens, (B,), cache, "seq_lens"),
+                            _index(new_lens, (B,), cache, "new_lens"), _status(dev_status, cache),
+                            None if workspace is None else workspace.data_ptr(),
+                            0 if workspace is None else workspace.numel() * workspace.element_size())
+        _check(lib.mx_cache_attn(ctypes.byref(p), _stream(stream)))
+    return o, lse

@@ -142,6 +142,65 @@ bsc_status quant_v_common(const void* v, int B, int S, int H, int D, bsc_layout 
                                        reinterpret_cast<cudaStream_t>(stream), rule));
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The checks that the three cache calls share.  *empty: a problem without sequences, tokens or heads.
+bsc_status check_cache(const bsc_mx_cache& c, int B, int T, int H, int dtype, long long table_stride, int max_pages,
+                       bool* empty) {
+  *empty = false;
+  if (B < 0 || T < 0 || H < 0 || c.Hkv < 0 || c.D < 0 || c.num_pages < 0 || c.page_size < 0 || max_pages < 0)
+    return BSC_ERR_SHAPE;
+  if (c.format != BSC_CACHE_MXFP8 && c.format != BSC_CACHE_MXFP4) return BSC_ERR_UNSUPPORTED;
+  if (dtype != BSC_BF16 && dtype != BSC_FP16) return BSC_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0 || H == 0) {
+    *empty = true;
+    return BSC_OK;
+  }
+  if (c.Hkv == 0 || c.num_pages == 0 || c.page_size == 0) return BSC_ERR_SHAPE;
+  if ((c.D != 64 && c.D != 128) || c.page_size % 16 != 0) return BSC_ERR_UNSUPPORTED;
+  if (B > 1 && table_stride < max_pages) return BSC_ERR_SHAPE;
+  // positions are 32-bit, and the grids (at most one warp per 16 tokens and KV head, or one block per
+  // query row) must fit theirs
+  if ((long long)max_pages * c.page_size >= (1LL << 31)) return BSC_ERR_UNSUPPORTED;
+  if ((long long)B * T >= (1LL << 31) / H || (long long)B * ((T + 15LL) / 16) * 2 >= (1LL << 31) / c.Hkv)
+    return BSC_ERR_UNSUPPORTED;
+  if (!c.k || !c.k_sc || !c.v || !c.v_sc) return BSC_ERR_NULL;
+  if (!aligned16(c.k) || !aligned16(c.k_sc) || !aligned16(c.v) || !aligned16(c.v_sc)) return BSC_ERR_ALIGN;
+  if (c.num_pages > 1) {
+    const long long slots = (long long)c.Hkv * c.page_size;
+    const long long data = slots * (c.format == BSC_CACHE_MXFP4 ? c.D / 2 : c.D), scales = slots * (c.D / 32);
+    for (const long long s : {c.k_page_stride, c.k_sc_page_stride, c.v_page_stride, c.v_sc_page_stride})
+      if (s % 16 != 0) return BSC_ERR_ALIGN;
+    if (c.k_page_stride < data || c.v_page_stride < data || c.k_sc_page_stride < scales ||
+        c.v_sc_page_stride < scales)
+      return BSC_ERR_SHAPE;
+  }
+  return BSC_OK;
+}
+
+// Strides of an activation: 16-byte rows, and no two output rows in one place.
+bsc_status check_strides(long long sb, long long st, long long sh, int B, int T, int H, bool output) {
+  if ((B > 1 && sb % 8 != 0) || (T > 1 && st % 8 != 0) || (H > 1 && sh % 8 != 0)) return BSC_ERR_ALIGN;
+  if (output && ((B > 1 && sb == 0) || (T > 1 && st == 0) || (H > 1 && sh == 0))) return BSC_ERR_SHAPE;
+  return BSC_OK;
+}
+
+bsc::CachePools cache_pools(const bsc_mx_cache& c) {
+  bsc::CachePools p{};
+  p.k = c.k;
+  p.k_sc = c.k_sc;
+  p.v = c.v;
+  p.v_sc = c.v_sc;
+  p.k_ps = c.k_page_stride;
+  p.k_sc_ps = c.k_sc_page_stride;
+  p.v_ps = c.v_page_stride;
+  p.v_sc_ps = c.v_sc_page_stride;
+  p.num_pages = c.num_pages;
+  p.page_size = c.page_size;
+  p.Hkv = c.Hkv;
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -157,6 +216,7 @@ const char* bsc_status_string(bsc_status s) {
     case BSC_ERR_UNSUPPORTED: return "BSC_ERR_UNSUPPORTED: unsupported size, option or device";
     case BSC_ERR_CUDA: return "BSC_ERR_CUDA: a CUDA call failed";
     case BSC_ERR_DEVICE_TIMEOUT: return "BSC_ERR_DEVICE_TIMEOUT: a device-side wait gave up";
+    case BSC_ERR_DEVICE_PAGE: return "BSC_ERR_DEVICE_PAGE: a page id or a length that the page table does not have";
   }
   return "unknown bsc_status";
 }
@@ -377,6 +437,104 @@ bsc_status bf16_attn_bwd(const bsc_attn_bwd_params* p, bsc_stream_t stream) {
   return from_cuda(bsc::launch_attn_bwd(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+bsc_status mx_cache_write(const bsc_mx_cache_write_params* p, bsc_stream_t stream) {
+  if (!p) return BSC_ERR_NULL;
+  if (p->rule != BSC_SCALE_FLOOR && p->rule != BSC_SCALE_CEIL) return BSC_ERR_UNSUPPORTED;
+  bool empty;
+  bsc_status s = check_cache(p->cache, p->B, p->T, p->cache.Hkv, p->dtype, p->table_stride, p->max_pages, &empty);
+  if (s != BSC_OK || empty) return s;
+  if (!p->k || !p->v || !p->seq_lens || !p->page_table) return BSC_ERR_NULL;
+  if (!aligned16(p->k) || !aligned16(p->v) || !aligned4(p->page_table) || !aligned4(p->seq_lens) ||
+      !aligned4(p->new_lens) || !aligned4(p->dev_status))
+    return BSC_ERR_ALIGN;
+  const int H = p->cache.Hkv;
+  if ((s = check_strides(p->k_stride_b, p->k_stride_t, p->k_stride_h, p->B, p->T, H, false)) != BSC_OK) return s;
+  if ((s = check_strides(p->v_stride_b, p->v_stride_t, p->v_stride_h, p->B, p->T, H, false)) != BSC_OK) return s;
+  if ((s = check_device()) != BSC_OK) return s;
+  bsc::CacheRwArgs a{};
+  a.c = cache_pools(p->cache);
+  a.pt = {p->page_table, p->table_stride, p->max_pages, p->seq_lens};
+  a.x[0] = const_cast<void*>(p->k);
+  a.x[1] = const_cast<void*>(p->v);
+  a.xs[0] = {p->k_stride_b, p->k_stride_t, p->k_stride_h};
+  a.xs[1] = {p->v_stride_b, p->v_stride_t, p->v_stride_h};
+  a.B = p->B;
+  a.T = p->T;
+  a.rule = p->rule;
+  a.first = p->new_lens;
+  a.dev_status = p->dev_status;
+  return from_cuda(bsc::launch_cache_write(a, p->cache.format, p->cache.D, p->dtype,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bsc_status mx_cache_read(const bsc_mx_cache_read_params* p, bsc_stream_t stream) {
+  if (!p) return BSC_ERR_NULL;
+  bool empty;
+  bsc_status s = check_cache(p->cache, p->B, p->T, p->cache.Hkv, p->dtype, p->table_stride, p->max_pages, &empty);
+  if (s != BSC_OK || empty) return s;
+  if (!p->k || !p->v || !p->seq_lens || !p->page_table) return BSC_ERR_NULL;
+  if (!aligned16(p->k) || !aligned16(p->v) || !aligned4(p->page_table) || !aligned4(p->seq_lens) ||
+      !aligned4(p->starts) || !aligned4(p->dev_status))
+    return BSC_ERR_ALIGN;
+  const int H = p->cache.Hkv;
+  if ((s = check_strides(p->k_stride_b, p->k_stride_t, p->k_stride_h, p->B, p->T, H, true)) != BSC_OK) return s;
+  if ((s = check_strides(p->v_stride_b, p->v_stride_t, p->v_stride_h, p->B, p->T, H, true)) != BSC_OK) return s;
+  if ((s = check_device()) != BSC_OK) return s;
+  bsc::CacheRwArgs a{};
+  a.c = cache_pools(p->cache);
+  a.pt = {p->page_table, p->table_stride, p->max_pages, p->seq_lens};
+  a.x[0] = p->k;
+  a.x[1] = p->v;
+  a.xs[0] = {p->k_stride_b, p->k_stride_t, p->k_stride_h};
+  a.xs[1] = {p->v_stride_b, p->v_stride_t, p->v_stride_h};
+  a.B = p->B;
+  a.T = p->T;
+  a.first = p->starts;
+  a.dev_status = p->dev_status;
+  return from_cuda(bsc::launch_cache_read(a, p->cache.format, p->cache.D, p->dtype,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
+  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
+  return bsc::cache_attn_workspace_bytes(B, T, Hq, Hkv, D);
+}
+
+bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream) {
+  if (!p) return BSC_ERR_NULL;
+  bool empty;
+  bsc_status s = check_cache(p->cache, p->B, p->T, p->Hq, p->dtype, p->table_stride, p->max_pages, &empty);
+  if (s != BSC_OK || empty) return s;
+  if (p->Hq % p->cache.Hkv != 0) return BSC_ERR_SHAPE;
+  if (!(std::isfinite(p->softmax_scale) && p->softmax_scale > 0.f)) return BSC_ERR_UNSUPPORTED;
+  const size_t need = mx_cache_attn_workspace_bytes(p->B, p->T, p->Hq, p->cache.Hkv, p->cache.D);
+  if (!p->q || !p->o || !p->seq_lens || !p->page_table || (need > 0 && !p->workspace)) return BSC_ERR_NULL;
+  if (!aligned16(p->q) || !aligned16(p->o) || !aligned16(p->workspace) || !aligned4(p->page_table) ||
+      !aligned4(p->seq_lens) || !aligned4(p->new_lens) || !aligned4(p->lse) || !aligned4(p->dev_status))
+    return BSC_ERR_ALIGN;
+  if ((s = check_strides(p->q_stride_b, p->q_stride_t, p->q_stride_h, p->B, p->T, p->Hq, false)) != BSC_OK) return s;
+  if ((s = check_strides(p->o_stride_b, p->o_stride_t, p->o_stride_h, p->B, p->T, p->Hq, true)) != BSC_OK) return s;
+  if (p->workspace_bytes < need) return BSC_ERR_SHAPE;
+  if ((s = check_device()) != BSC_OK) return s;
+  bsc::CacheAttnArgs a{};
+  a.c = cache_pools(p->cache);
+  a.pt = {p->page_table, p->table_stride, p->max_pages, p->seq_lens};
+  a.q = p->q;
+  a.o = p->o;
+  a.lse = p->lse;
+  a.qs = {p->q_stride_b, p->q_stride_t, p->q_stride_h};
+  a.os = {p->o_stride_b, p->o_stride_t, p->o_stride_h};
+  a.B = p->B;
+  a.T = p->T;
+  a.Hq = p->Hq;
+  a.new_lens = p->new_lens;
+  a.dev_status = p->dev_status;
+  a.scale_log2e = (float)((double)p->softmax_scale * 1.4426950408889634);
+  a.ws = p->workspace;
+  return from_cuda(bsc::launch_cache_attn(a, p->cache.format, p->cache.D, p->dtype,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
 bsc_status bsc_read_device_status(const int32_t* dev_status, bsc_stream_t stream) {
   if (!dev_status) return BSC_ERR_NULL;
   int32_t v = 0;
@@ -384,7 +542,7 @@ bsc_status bsc_read_device_status(const int32_t* dev_status, bsc_stream_t stream
           cudaSuccess ||
       cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return BSC_ERR_CUDA;
-  return v == 0 ? BSC_OK : BSC_ERR_DEVICE_TIMEOUT;
+  return v == 0 ? BSC_OK : (v & ~0xFF) == 0x200 ? BSC_ERR_DEVICE_PAGE : BSC_ERR_DEVICE_TIMEOUT;
 }
 
 }  // extern "C"

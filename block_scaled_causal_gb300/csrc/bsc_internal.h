@@ -89,4 +89,51 @@ size_t bwd_workspace_bytes(int B, int S, int Hq, int Hkv);
 
 cudaError_t launch_attn_bwd(const BwdArgs& args, cudaStream_t st);
 
+// The key/value cache.  Strides of the pools in bytes, of activations in elements.
+struct CachePools {
+  uint8_t* k;
+  uint8_t* k_sc;
+  uint8_t* v;
+  uint8_t* v_sc;
+  long long k_ps, k_sc_ps, v_ps, v_sc_ps;
+  int num_pages, page_size, Hkv;
+};
+struct CacheTable {
+  const int32_t* table;
+  long long stride;
+  int max_pages;
+  const int32_t* seq_lens;
+};
+struct RowStrides {
+  long long b, t, h;
+};
+struct CacheRwArgs {
+  CachePools c;
+  CacheTable pt;
+  void* x[2];              // K and V activations (read by the write call, written by the read call)
+  RowStrides xs[2];
+  int B, T;
+  int rule;
+  const int32_t* first;    // write: new_lens (nullptr: T); read: starts (nullptr: 0)
+  int32_t* dev_status;
+};
+cudaError_t launch_cache_write(const CacheRwArgs& a, int format, int D, int dtype, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheRwArgs& a, int format, int D, int dtype, cudaStream_t st);
+
+struct CacheAttnArgs {
+  CachePools c;
+  CacheTable pt;
+  const void* q;
+  void* o;
+  float* lse;              // may be nullptr
+  RowStrides qs, os;
+  int B, T, Hq;
+  const int32_t* new_lens; // may be nullptr
+  int32_t* dev_status;     // may be nullptr
+  float scale_log2e;
+  void* ws;
+};
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, int format, int D, int dtype, cudaStream_t st);
+size_t cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+
 }  // namespace bsc

@@ -1,0 +1,103 @@
+// What the kernels of the key/value cache share: element formats, scale rule, addresses.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "bsc_internal.h"
+#include "ptx.cuh"
+
+namespace bsc {
+
+constexpr int CACHE_FP8 = 0, CACHE_FP4 = 1;   // bsc_cache_format
+constexpr int32_t CACHE_BAD_PAGE = 0x201, CACHE_BAD_LEN = 0x202;
+
+// Bytes of one token's D elements of one head.
+template <int FMT, int D>
+constexpr int row_bytes() { return FMT == CACHE_FP4 ? D / 2 : D; }
+
+// Largest binade of an element, and the significand (fp32 fraction bits) of its largest value:
+// E4M3 448 = 1.75 * 2^8, E2M1 6 = 1.5 * 2^2.
+template <int FMT>
+struct Elem {
+  static constexpr uint32_t emax = FMT == CACHE_FP4 ? 2u : 8u;
+  static constexpr uint32_t top_frac = FMT == CACHE_FP4 ? 0x400000u : 0x600000u;
+};
+
+// The scale byte of a block from its absolute maximum (0xFF for NaN/Inf), and 2^-(byte - 127): the
+// rule of e8m0_from_amax for either format.  fp32-subnormal maxima clamp to byte 0.
+template <int FMT>
+__device__ __forceinline__ uint32_t block_scale(float amax, int ceil_rule, float& inv) {
+  const uint32_t bits = __float_as_uint(amax), eb = bits >> 23;
+  if (eb == 0xFFu) {
+    inv = 0.f;
+    return 0xFFu;
+  }
+  const uint32_t up = (ceil_rule && eb > 0u && (bits & 0x7FFFFFu) > Elem<FMT>::top_frac) ? 1u : 0u;
+  const uint32_t sb = eb + up > Elem<FMT>::emax ? eb + up - Elem<FMT>::emax : 0u;
+  inv = __uint_as_float((254u - sb) << 23);   // sb <= 253: a normal fp32
+  return sb;
+}
+
+// 2^(byte - 127) in fp32; byte 0 is the fp32-subnormal 2^-127, byte 255 NaN.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return byte == 0u ? __uint_as_float(0x00400000u) : byte == 255u ? __uint_as_float(0x7FC00000u)
+                                                                  : __uint_as_float(byte << 23);
+}
+
+// Two fp32 -> E2M1x2 (nearest even, saturated to +-6), low nibble `lo`.
+__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{ .reg .b8 t; cvt.rn.satfinite.e2m1x2.f32 t, %1, %2; cvt.u32.u8 %0, t; }" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The four bytes (eight E2M1) of a word -> f16x2 each (exact), low nibble in the low half.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a; cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d; }"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+// The four E4M3 of a word -> two f16x2 (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& h0, uint32_t& h1) {
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }" : "=r"(h0), "=r"(h1) : "r"(w));
+}
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Activations: bf16 (DT = 0) or fp16 (DT = 1), two to a word.
+template <int DT>
+__device__ __forceinline__ float2 act_to_f32(uint32_t w) {
+  if (DT == 0) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return f16x2_to_f32(w);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t f32_to_act(float lo, float hi) {
+  if (DT == 0) return pack_bf16x2(lo, hi);
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Slot (page * page_size + offset) of position `pos` of sequence `b`, or -1 where there is none;
+// `bad` collects a status code.
+__device__ __forceinline__ long long cache_slot(const CachePools& c, const CacheTable& pt, int b, long long pos,
+                                                int32_t& bad) {
+  if (pos < 0) return -1;
+  if (pos >= (long long)pt.max_pages * c.page_size) {
+    bad = CACHE_BAD_LEN;
+    return -1;
+  }
+  const int lp = (int)pos / c.page_size, off = (int)pos - lp * c.page_size;
+  const int page = __ldg(pt.table + b * pt.stride + lp);
+  if (page < 0 || page >= c.num_pages) {
+    bad = CACHE_BAD_PAGE;
+    return -1;
+  }
+  return (long long)page * c.page_size + off;
+}
+
+}  // namespace bsc

@@ -62,7 +62,8 @@ typedef enum {
   BSC_ERR_ALIGN = 3,          /* a pointer is not 16-byte aligned */
   BSC_ERR_UNSUPPORTED = 4,    /* D != 128, S % 32 != 0, wrong device, unsupported option */
   BSC_ERR_CUDA = 5,           /* a CUDA runtime/driver call failed (launch, tensor map) */
-  BSC_ERR_DEVICE_TIMEOUT = 6  /* a device-side wait gave up (see bsc_read_device_status) */
+  BSC_ERR_DEVICE_TIMEOUT = 6, /* a device-side wait gave up (see bsc_read_device_status) */
+  BSC_ERR_DEVICE_PAGE = 7     /* a cache call met a page id or a length its page table does not have */
 } bsc_status;
 
 typedef enum { BSC_BSHD = 0, BSC_SBHD = 1 } bsc_layout;
@@ -281,8 +282,134 @@ bsc_status bf16_attn_bwd_static(const bsc_attn_bwd_params* p, bsc_stream_t strea
 size_t bf16_attn_bwd_static_capacity(void);
 
 /*
- * Synchronises `stream`, reads the int32 at `dev_status` and returns BSC_OK (0) or
- * BSC_ERR_DEVICE_TIMEOUT (non-zero).  The only call that synchronises.
+ * The key/value cache for answering token by token: K and V of the tokens seen so far, block-scaled
+ * in 8 or 4 bits, in pages; written as tokens arrive, read back, and attended.
+ *
+ * Both K and V are quantised rowwise, one E8M0 scale per 32 elements along D, by the rule at the
+ * top of this file: a token's bytes depend on that token alone, so the cache grows without touching
+ * what it holds and no scale covers a later token (a columnwise V scale covers 32 tokens and could
+ * be written only when its block is complete).
+ *   BSC_CACHE_MXFP8   E4M3 elements, one byte each, as everywhere in this library
+ *   BSC_CACHE_MXFP4   OCP MX E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two
+ *                     per byte, the even element in the low nibble; the scale rule's 8 is 2 and its
+ *                     448 is 6 here; a block holding NaN/Inf has scale 0xFF and nibbles 0x7
+ * Pools: k, v [num_pages][Hkv][page_size][D bytes, or D/2] and k_sc, v_sc
+ * [num_pages][Hkv][page_size][D/32], with a byte stride from page to page (a multiple of 16, at
+ * least the page's own size), so K and V may be slices of one allocation.  page_size is a multiple
+ * of 16; D is 64 or 128.  Pages of a sequence need not be neighbours or in order.
+ *
+ * Position p of sequence b is slot p % page_size of page page_table[b * table_stride + p / page_size];
+ * entries past ceil(seq_lens[b] / page_size) are not read.  Two sequences may share pages (a common
+ * prefix) as long as no call writes to a shared one: if one call writes a slot twice, what it holds
+ * afterwards is unspecified.
+ *
+ * Activations (k, v, q, o) are bf16 or fp16 with element (b, t, h, d) at b*stride_b + t*stride_t +
+ * h*stride_h + d: strides in elements, multiples of 8 (the stride of a dimension of size 1 is
+ * ignored), so both of this library's layouts and slices of a fused projection are taken as they are.
+ * Those pointers and the pools are 16-byte aligned; page_table, seq_lens, new_lens, starts, lse and
+ * dev_status are 4-byte aligned.
+ *
+ * Lengths and page ids live on the device and cannot be checked before the launch.  A page id
+ * outside [0, num_pages) is never followed: its tokens are not written, read as zeros, and are not
+ * attended; a position past max_pages * page_size is treated the same way, a negative length as 0.
+ * If dev_status is given, it then receives 0x201 (page id) or 0x202 (length); it is left untouched
+ * otherwise, and bsc_read_device_status returns BSC_ERR_DEVICE_PAGE for both.
+ */
+typedef enum { BSC_CACHE_MXFP8 = 0, BSC_CACHE_MXFP4 = 1 } bsc_cache_format;
+typedef enum { BSC_BF16 = 0, BSC_FP16 = 1 } bsc_dtype;
+typedef struct {
+  uint8_t* k;             /* [num_pages][Hkv][page_size][D or D/2] */
+  uint8_t* k_sc;          /* [num_pages][Hkv][page_size][D/32] */
+  uint8_t* v;
+  uint8_t* v_sc;
+  long long k_page_stride, k_sc_page_stride, v_page_stride, v_sc_page_stride;   /* bytes */
+  int format;             /* bsc_cache_format */
+  int num_pages, page_size, Hkv, D;
+} bsc_mx_cache;
+
+typedef struct {
+  bsc_mx_cache cache;     /* [out] */
+  const void* k;          /* [in] T tokens of each sequence, `dtype`, Hkv heads */
+  const void* v;
+  long long k_stride_b, k_stride_t, k_stride_h, v_stride_b, v_stride_t, v_stride_h;
+  int B, T;
+  int dtype;              /* bsc_dtype */
+  int rule;               /* bsc_scale_rule */
+  const int32_t* page_table;  /* [in] [B][max_pages], rows table_stride apart */
+  long long table_stride;
+  int max_pages;
+  const int32_t* seq_lens;    /* [in] [B]: tokens of each sequence, the new ones included */
+  const int32_t* new_lens;    /* [in] [B]: how many of the T tokens are real (clamped to [0, T]); NULL: all */
+  int32_t* dev_status;        /* optional */
+} bsc_mx_cache_write_params;
+
+/* Quantises token t < n_b = new_lens[b] of sequence b into position seq_lens[b] - n_b + t.  Tokens
+ * t >= n_b and negative positions are skipped; nothing else in the pools changes. */
+bsc_status mx_cache_write(const bsc_mx_cache_write_params* p, bsc_stream_t stream);
+
+typedef struct {
+  bsc_mx_cache cache;     /* [in] */
+  void* k;                /* [out] `dtype`, Hkv heads; a stride of 0 is refused (BSC_ERR_SHAPE) */
+  void* v;
+  long long k_stride_b, k_stride_t, k_stride_h, v_stride_b, v_stride_t, v_stride_h;
+  int B, T;
+  int dtype;              /* bsc_dtype */
+  const int32_t* page_table;
+  long long table_stride;
+  int max_pages;
+  const int32_t* seq_lens;    /* [in] [B] */
+  const int32_t* starts;      /* [in] [B]: position of the first token read; NULL: 0 */
+  int32_t* dev_status;        /* optional */
+} bsc_mx_cache_read_params;
+
+/* Token t of sequence b of the outputs is position starts[b] + t: element * 2^(scale - 127), rounded
+ * once to nearest even in `dtype` (fp16 beyond 65504 is infinite); NaN where the scale is 0xFF.
+ * Positions outside [0, seq_lens[b]) read as zeros. */
+bsc_status mx_cache_read(const bsc_mx_cache_read_params* p, bsc_stream_t stream);
+
+typedef struct {
+  bsc_mx_cache cache;     /* [in] */
+  const void* q;          /* [in] T queries of each sequence, `dtype`, Hq heads */
+  void* o;                /* [out] `dtype`, Hq heads; a stride of 0 is refused (BSC_ERR_SHAPE) */
+  float* lse;             /* [out] [B][Hq][T], natural log; may be NULL */
+  long long q_stride_b, q_stride_t, q_stride_h, o_stride_b, o_stride_t, o_stride_h;
+  int B, T, Hq;
+  int dtype;              /* bsc_dtype */
+  float softmax_scale;    /* finite and > 0, else BSC_ERR_UNSUPPORTED */
+  const int32_t* page_table;
+  long long table_stride;
+  int max_pages;
+  const int32_t* seq_lens;    /* [in] [B]: tokens held, the T new ones included */
+  const int32_t* new_lens;    /* [in] [B]: how many of the T queries are real (clamped to [0, T]); NULL: all */
+  int32_t* dev_status;        /* optional */
+  /* [scratch] at least mx_cache_attn_workspace_bytes(...) bytes, 16-byte aligned, used by this call
+   * alone until it has run; contents on entry ignored. */
+  void* workspace;
+  size_t workspace_bytes;
+} bsc_mx_cache_attn_params;
+
+/*
+ * Attention of T new queries per sequence over the cache, causal: query t < n_b of sequence b is the
+ * token at position p = seq_lens[b] - n_b + t and attends the positions j <= p (its own K and V are
+ * written before the call).  GQA: query head h reads KV head h / (Hq/Hkv).  T = 1 is a decode step;
+ * T > 1 checks a draft or takes a chunk of a prompt.  With Kc, Vc the values the cache stands for,
+ *   s_j = softmax_scale * q . Kc_j,  O = sum_j exp(s_j - LSE) Vc_j,  LSE = ln sum_j exp(s_j).
+ * Rows that attend nothing (t >= n_b, p < 0, an empty sequence) get O = 0 and LSE = -inf.
+ * Row p is bit-for-bit independent of what positions after p hold, NaN and infinities included.
+ * Finite V is taken up to 2^100 in magnitude.  The result does not depend on the stream, on other calls
+ * or on timing (no atomics); it may differ in the last bits with the batch's lengths, which decide
+ * how the keys are split.
+ */
+bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream);
+
+/* Bytes of workspace mx_cache_attn needs at these sizes (whatever the lengths are); 0 if a size is
+ * not positive.  Host only, no CUDA call. */
+size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+
+/*
+ * Synchronises `stream`, reads the int32 at `dev_status` and returns BSC_OK (0),
+ * BSC_ERR_DEVICE_PAGE (0x2xx, the cache calls) or BSC_ERR_DEVICE_TIMEOUT (any other value).  The
+ * only call that synchronises.
  */
 bsc_status bsc_read_device_status(const int32_t* dev_status, bsc_stream_t stream);
 
