@@ -10,5 +10,6 @@ __all__ = ["ops", "inputs", "build"]
 def __getattr__(name):
     if name == "ops":
         from . import _binding as ops
+        globals()["ops"] = ops       # later uses find it without this function
         return ops
     raise AttributeError(name)

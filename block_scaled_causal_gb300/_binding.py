@@ -7,6 +7,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -479,7 +480,7 @@ def _index(t, shape, cache, name):
     """Pointer of an int32 index array of the given shape (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != cache.device or tuple(t.shape) != shape:
+    if t.dtype != torch.int32 or t.device != cache.device or t.shape != shape:
         raise ValueError("%s must be an int32 tensor of shape %s on the cache's device" % (name, shape))
     if len(shape) == 1 and shape[0] > 1 and t.stride(0) != 1:
         raise ValueError("%s must be contiguous" % name)
@@ -498,10 +499,20 @@ def _status(t, cache):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream, device):
-    """Context in which to allocate and launch: the device and stream of a call (so that memory
-    allocated inside belongs to the stream that uses it)."""
-    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
+def _elsewhere(cache, stream):
+    """The context a call has to enter before it allocates and launches: None where the current device is the
+    cache's and no stream is given; else the stream's (memory allocated inside belongs to the stream that
+    uses it) or the device's."""
+    if stream is not None:
+        if stream.device != cache.device:
+            raise ValueError("stream must be on the cache's device")
+        return torch.cuda.stream(stream)
+    return None if torch.cuda.current_device() == cache.device.index else torch.cuda.device(cache.device)
+
+
+# The current stream's handle without a Stream object around it (a call's largest host cost after the launches).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def mx_cache_write(cache, k, v, page_table, seq_lens, new_lens=None, layout=BSHD, rule=SCALE_FLOOR, dev_status=None,
@@ -509,6 +520,10 @@ def mx_cache_write(cache, k, v, page_table, seq_lens, new_lens=None, layout=BSHD
     """Quantises new tokens into the cache.  k, v: bf16 or fp16 [B, T, Hkv, D] (BSHD) or [T, B, Hkv, D]
     (SBHD), any strides with D contiguous.  Token t < new_lens[b] (None: all T) of sequence b goes to position
     seq_lens[b] - new_lens[b] + t; page_table [B, max_pages], seq_lens, new_lens [B]: int32 on the device."""
+    there = _elsewhere(cache, stream)
+    if there is not None:
+        with there:
+            return mx_cache_write(cache, k, v, page_table, seq_lens, new_lens, layout, rule, dev_status)
     (B, T, H), ks, dt = _act_dims(k, layout, cache.Hkv, cache.D, cache, "k")
     dims, vs, dv = _act_dims(v, layout, cache.Hkv, cache.D, cache, "v")
     if dims != (B, T, H) or dv != dt:
@@ -516,30 +531,33 @@ def mx_cache_write(cache, k, v, page_table, seq_lens, new_lens=None, layout=BSHD
     p = CacheWriteParams(cache.params, k.data_ptr(), v.data_ptr(), *ks, *vs, B, T, dt, rule,
                          *_table(page_table, B, cache), _index(seq_lens, (B,), cache, "seq_lens"),
                          _index(new_lens, (B,), cache, "new_lens"), _status(dev_status, cache))
-    with _on(stream, cache.device):
-        _check(lib.mx_cache_write(ctypes.byref(p), _stream(stream)))
+    _check(lib.mx_cache_write(ctypes.byref(p), _raw_stream(cache.device.index)))
 
 
 def mx_cache_read(cache, page_table, seq_lens, T, starts=None, layout=BSHD, dtype=torch.bfloat16, k_out=None,
                   v_out=None, dev_status=None, stream=None):
     """Reads positions starts[b] .. starts[b] + T - 1 (None: from 0) of every sequence back as values:
     (k, v), shaped [B, T, Hkv, D] or [T, B, Hkv, D]; zeros outside [0, seq_lens[b])."""
+    there = _elsewhere(cache, stream)
+    if there is not None:
+        with there:
+            return mx_cache_read(cache, page_table, seq_lens, T, starts, layout, dtype, k_out, v_out, dev_status)
     B = page_table.shape[0]
-    with _on(stream, cache.device):
-        shape = (B, T, cache.Hkv, cache.D) if layout == BSHD else (T, B, cache.Hkv, cache.D)
-        k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=dtype, device=cache.device) if v_out is None else v_out
-        dk, ks, dt = _act_dims(k_out, layout, cache.Hkv, cache.D, cache, "k_out")
-        dv, vs, dt_v = _act_dims(v_out, layout, cache.Hkv, cache.D, cache, "v_out")
-        if dk != (B, T, cache.Hkv) or dv != dk or dt != dt_v:
-            raise ValueError("k_out and v_out must both be [B, T, Hkv, D] in the layout, of one dtype")
-        p = CacheReadParams(cache.params, k_out.data_ptr(), v_out.data_ptr(), *ks, *vs, B, T, dt,
-                            *_table(page_table, B, cache), _index(seq_lens, (B,), cache, "seq_lens"),
-                            _index(starts, (B,), cache, "starts"), _status(dev_status, cache))
-        _check(lib.mx_cache_read(ctypes.byref(p), _stream(stream)))
+    shape = (B, T, cache.Hkv, cache.D) if layout == BSHD else (T, B, cache.Hkv, cache.D)
+    k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=dtype, device=cache.device) if v_out is None else v_out
+    dk, ks, dt = _act_dims(k_out, layout, cache.Hkv, cache.D, cache, "k_out")
+    dv, vs, dt_v = _act_dims(v_out, layout, cache.Hkv, cache.D, cache, "v_out")
+    if dk != (B, T, cache.Hkv) or dv != dk or dt != dt_v:
+        raise ValueError("k_out and v_out must both be [B, T, Hkv, D] in the layout, of one dtype")
+    p = CacheReadParams(cache.params, k_out.data_ptr(), v_out.data_ptr(), *ks, *vs, B, T, dt,
+                        *_table(page_table, B, cache), _index(seq_lens, (B,), cache, "seq_lens"),
+                        _index(starts, (B,), cache, "starts"), _status(dev_status, cache))
+    _check(lib.mx_cache_read(ctypes.byref(p), _raw_stream(cache.device.index)))
     return k_out, v_out
 
 
+@functools.lru_cache(maxsize=256)
 def mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D=128):
     """Bytes of scratch mx_cache_attn needs (the C call of the same name)."""
     return int(lib.mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D))
@@ -552,28 +570,37 @@ def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, so
     attends the positions up to its own.  `workspace`: a device tensor of at least
     mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D) bytes that no other running call uses, else one is
     allocated here."""
+    there = _elsewhere(cache, stream)
+    if there is not None:
+        with there:
+            return mx_cache_attn(q, cache, page_table, seq_lens, new_lens, layout, softmax_scale, o, lse, workspace,
+                                 dev_status)
     (B, T, Hq), qs, dt = _act_dims(q, layout, None, cache.D, cache, "q")
-    with _on(stream, cache.device):
-        if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        dims, os_, dt_o = _act_dims(o, layout, Hq, cache.D, cache, "o")
+    device = cache.device
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=device)
+        st = o.stride()
+        o_s = (st[0], st[1], st[2]) if layout == BSHD else (st[1], st[0], st[2])
+    else:
+        dims, o_s, dt_o = _act_dims(o, layout, Hq, cache.D, cache, "o")
         if dims != (B, T, Hq) or dt_o != dt:
             raise ValueError("o must have q's shape and dtype")
-        if lse is None:
-            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
-        elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T) or lse.device != q.device or \
-                not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous float32 tensor [B, Hq, T] on the cache's device")
-        if workspace is None:
-            need = mx_cache_attn_workspace_bytes(B, T, Hq, cache.Hkv, cache.D)
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        elif workspace.device != q.device or not workspace.is_contiguous():
+    if lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=device)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T) or lse.device != device or \
+            not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 tensor [B, Hq, T] on the cache's device")
+    if workspace is None:
+        need = mx_cache_attn_workspace_bytes(B, T, Hq, cache.Hkv, cache.D)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        if workspace.device != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        p = CacheAttnParams(cache.params, q.data_ptr(), o.data_ptr(), lse.data_ptr(), *qs, *os_, B, T, Hq, dt,
-                            cache.D ** -0.5 if softmax_scale is None else softmax_scale,
-                            *_table(page_table, B, cache), _index(seq_lens, (B,), cache, "seq_lens"),
-                            _index(new_lens, (B,), cache, "new_lens"), _status(dev_status, cache),
-                            None if workspace is None else workspace.data_ptr(),
-                            0 if workspace is None else workspace.numel() * workspace.element_size())
-        _check(lib.mx_cache_attn(ctypes.byref(p), _stream(stream)))
+        need = workspace.numel() * workspace.element_size()
+    p = CacheAttnParams(cache.params, q.data_ptr(), o.data_ptr(), lse.data_ptr(), *qs, *o_s, B, T, Hq, dt,
+                        cache.D ** -0.5 if softmax_scale is None else softmax_scale,
+                        *_table(page_table, B, cache), _index(seq_lens, (B,), cache, "seq_lens"),
+                        _index(new_lens, (B,), cache, "new_lens"), _status(dev_status, cache),
+                        workspace.data_ptr(), need)
+    _check(lib.mx_cache_attn(ctypes.byref(p), _raw_stream(device.index)))
     return o, lse

@@ -164,13 +164,17 @@ bsc_status check_cache(const bsc_mx_cache& c, int B, int T, int H, int dtype, lo
   if ((long long)max_pages * c.page_size >= (1LL << 31)) return BSC_ERR_UNSUPPORTED;
   if ((long long)B * T >= (1LL << 31) / H || (long long)B * ((T + 15LL) / 16) * 2 >= (1LL << 31) / c.Hkv)
     return BSC_ERR_UNSUPPORTED;
+  // the attention addresses a page in 32-bit units of 16 bytes
+  if ((long long)c.Hkv * c.page_size >= (1LL << 31) / c.D) return BSC_ERR_UNSUPPORTED;
   if (!c.k || !c.k_sc || !c.v || !c.v_sc) return BSC_ERR_NULL;
   if (!aligned16(c.k) || !aligned16(c.k_sc) || !aligned16(c.v) || !aligned16(c.v_sc)) return BSC_ERR_ALIGN;
   if (c.num_pages > 1) {
     const long long slots = (long long)c.Hkv * c.page_size;
     const long long data = slots * (c.format == BSC_CACHE_MXFP4 ? c.D / 2 : c.D), scales = slots * (c.D / 32);
-    for (const long long s : {c.k_page_stride, c.k_sc_page_stride, c.v_page_stride, c.v_sc_page_stride})
+    for (const long long s : {c.k_page_stride, c.k_sc_page_stride, c.v_page_stride, c.v_sc_page_stride}) {
       if (s % 16 != 0) return BSC_ERR_ALIGN;
+      if (s >= (1LL << 36)) return BSC_ERR_UNSUPPORTED;
+    }
     if (c.k_page_stride < data || c.v_page_stride < data || c.k_sc_page_stride < scales ||
         c.v_sc_page_stride < scales)
       return BSC_ERR_SHAPE;

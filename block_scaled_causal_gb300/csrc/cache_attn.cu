@@ -35,6 +35,8 @@
 // balanced, whatever the lengths, which only the device knows.  A run that covers a unit writes O; one
 // that covers part of it writes (O, log-sum-exp) to the workspace, two slots per block at most, and a second
 // kernel joins them in order.
+#include <atomic>
+
 #include "cache.cuh"
 
 namespace bsc {
@@ -42,6 +44,7 @@ namespace {
 
 constexpr int KT = 32, WARPS = 4, CHUNK = KT * WARPS, THREADS = WARPS * 32;
 constexpr int SMS = 152;
+constexpr int MOST_PARTS = SMS * 4;   // parts a unit can have: the blocks of the largest grid
 constexpr float SLACK = 4.f;    // a reference moves when a score passes it by this much (log2)
 constexpr float LIFT = 8.f;     // weights are 2^(x - m + LIFT)
 
@@ -126,22 +129,39 @@ __device__ __forceinline__ uint32_t scales_f16x2(uint32_t lo, uint32_t hi) {
   return ((uint32_t)max((int)lo - (int)C::SUB, 0) << 10) | ((uint32_t)max((int)hi - (int)C::SUB, 0) << 26);
 }
 
-// One element of a row in shared memory, as the fp32 value it stands for times 2^OFF.
+// The elements of the 32-bit word at byte `at` of key k's row in shared memory, each as the fp32 value it stands
+// for times 2^OFF.
 template <int FMT, class C>
-__device__ __forceinline__ float element(const uint8_t* rows, int k, int d, float scale) {
-  const int byte = FMT == CACHE_FP4 ? d >> 1 : d;
-  const uint32_t w = rows[piece_at<C::RB>(k, byte >> 4) + (byte & 15)];
-  float2 f;
-  if (FMT == CACHE_FP4) {
-    uint32_t h[4];
-    e2m1x8_to_f16(w, h);
-    f = f16x2_to_f32(h[0]);
-    return (d & 1 ? f.y : f.x) * scale * (float)(1 << C::OFF);
+__device__ __forceinline__ void word_values(const uint8_t* rows, int k, int at, float scale, float (&v)[FMT == CACHE_FP4 ? 8 : 4]) {
+  constexpr int N = FMT == CACHE_FP4 ? 4 : 2;
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(rows + piece_at<C::RB>(k, at >> 4) + (at & 15));
+  uint32_t h[4];
+  if (FMT == CACHE_FP4) e2m1x8_to_f16(w, h);
+  else e4m3x4_to_f16(w, h[0], h[1]);
+  const float f = (float)(1 << C::OFF);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 y = f16x2_to_f32(h[i]);
+    v[2 * i] = y.x * scale * f;
+    v[2 * i + 1] = y.y * scale * f;
   }
-  uint32_t h0, h1;
-  e4m3x4_to_f16(w, h0, h1);
-  f = f16x2_to_f32(h0);
-  return f.x * scale * (float)(1 << C::OFF);
+}
+// Keeps the loads of a rarely taken loop from being gathered in registers ahead of it.
+__device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t interleave_low(uint32_t x, uint32_t y) {    // low nibbles of x and y, byte by byte
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xCA;" : "=r"(r) : "r"(0x0F0F0F0Fu), "r"(x), "r"(y << 4));
+  return r;
+}
+__device__ __forceinline__ uint32_t interleave_high(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xCA;" : "=r"(r) : "r"(0x0F0F0F0Fu), "r"(x >> 4), "r"(y));
+  return r;
+}
+// Address `n` 16-byte units past row `row` of page `page`.
+__device__ __forceinline__ const uint8_t* unit_at(const uint8_t* pool, uint32_t page_units, uint32_t page, uint32_t n) {
+  return pool + ((unsigned long long)page * page_units + n) * 16;
 }
 
 // The list of chunks.  Sequence b has n_b = ceil(len_b / CHUNK) chunks per unit and U = Hkv * (row tiles) units.
@@ -203,6 +223,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
   const int G = a.Hq / a.c.Hkv, U = a.c.Hkv * row_tiles, page_size = a.c.page_size;
   const int R = a.T * G;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long total = chunks_before(a, a.B, U);
   const long long nblk = blocks_of(total, gridDim.x);
   if (blockIdx.x >= nblk) return;
@@ -211,8 +232,26 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
   long long base;
   int b = seq_of_chunk(a, x, U, base);
 
+  // ---- what a lane's place fixes ----
   uint8_t* const ring = smem + warp * C::STAGES * C::STAGE;
   const uint32_t ring_s = smem_u32(ring);
+  constexpr int PR = RB / 16, RPC = 32 / PR;      // pieces per row, rows per copy instruction
+  const int to0 = piece_at<RB>(lane / PR, lane % PR), to1 = piece_at<RB>(lane / PR + RPC, lane % PR) - RPC * RB;
+  constexpr int LB = C::KE * RB / D;              // bytes of a lane's K run: 8, 16 or 32
+  constexpr int VB = C::VE * RB / D;              // of its V run: 4, 8 or 16
+  const int ko = piece_at<RB>(key_of_row(g), t * LB / 16) + t * LB % 16;
+  const int vo0 = piece_at<RB>(t, g * VB / 16) + g * VB % 16, vo4 = piece_at<RB>(t + 4, g * VB / 16) + g * VB % 16;
+  const int kso = 2 * KT * RB + key_of_row(g) * NB + t * C::KE / 32;
+  const int vso = 2 * KT * RB + KT * NB + t * NB + g * C::VE / 32;
+  // pages of a multiple of 32 tokens: a tile lies in one page and is copied as a whole; else 16 keys at a time
+  const bool one_page = page_size % KT == 0;
+  const int sc_lanes = one_page ? 2 * NB : NB;    // pieces of scales per pool and copy
+  const bool sc_v = lane >= sc_lanes;
+  const int sc_p = sc_v ? lane - sc_lanes : lane;
+  const uint8_t* const sc_pool = sc_v ? a.c.v_sc : a.c.k_sc;
+  const uint32_t sc_units = (uint32_t)((sc_v ? a.c.v_sc_ps : a.c.k_sc_ps) >> 4);
+  const uint32_t k_units = (uint32_t)(a.c.k_ps >> 4), v_units = (uint32_t)(a.c.v_ps >> 4);
+  const uint32_t sc_to = 2 * KT * RB + (sc_v ? KT * NB : 0) + sc_p * 16;
 
   while (x < x_end) {
     // ---- the next piece: chunks [c0, c1) of unit (b, h, rt) ----
@@ -228,6 +267,78 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
     const int raw_len = max(__ldg(a.pt.seq_lens + b), 0);
     const int n_new = a.new_lens ? min(max(__ldg(a.new_lens + b), 0), a.T) : a.T;
     if (raw_len > len && tid == 0 && a.dev_status) *a.dev_status = CACHE_BAD_LEN;
+
+    // ---- the warp's tiles: keys (c0 + i) CHUNK + warp KT + [0, KT) ----
+    const int k_first = c0 * CHUNK + warp * KT;
+    const int last = min(c1 * CHUNK, len);
+    const int n_tiles = k_first < last ? (last - k_first + CHUNK - 1) / CHUNK : 0;
+
+    // page ids: lane 2 i + j has the 16-key group j of tile (window start) + i, for 16 tiles at a time
+    int w_page = -1;
+    uint32_t w_row = 0, present = 0;      // row in the page's [Hkv][page_size]; bit l: lane l's group is there
+    int st_in = 0, st_out = 0;
+    uint32_t there[C::STAGES] = {};       // the two `present` bits of the tiles in flight, oldest first
+    auto advance = [&](int tile) {        // copies of tile `tile` start; whole warps call it
+      uint32_t bits = 0;
+      if (tile < n_tiles) {
+        if ((tile & 15) == 0) {
+          const int i = tile + (lane >> 1), key = k_first + i * CHUNK + (lane & 1) * 16;
+          w_page = -1;
+          if (i < n_tiles && key < len) {
+            const int lp = key / page_size;
+            w_row = (uint32_t)(h * page_size + key - lp * page_size);
+            w_page = __ldg(a.pt.table + b * a.pt.stride + lp);
+            if (w_page < 0 || w_page >= a.c.num_pages) {
+              w_page = -1;
+              if (a.dev_status) *a.dev_status = CACHE_BAD_PAGE;
+            }
+          }
+          present = __ballot_sync(0xFFFFFFFFu, w_page >= 0);
+        }
+        const int slot = (tile & 15) * 2;
+        bits = (present >> slot) & 3u;
+        const uint32_t dst = ring_s + st_in * C::STAGE;
+        if (one_page) {
+          const uint32_t page = __shfl_sync(0xFFFFFFFFu, (uint32_t)w_page, slot), row = __shfl_sync(0xFFFFFFFFu, w_row, slot);
+          if (bits) {
+            const uint8_t* const ks = unit_at(a.c.k, k_units, page, row * PR + lane);
+            const uint8_t* const vs = unit_at(a.c.v, v_units, page, row * PR + lane);
+#pragma unroll
+            for (int i = 0; i < PR; ++i) {
+              const int to = (i & 1 ? to1 : to0) + i * RPC * RB;
+              cp16(dst + to, ks + i * 512);
+              cp16(dst + KT * RB + to, vs + i * 512);
+            }
+            if (lane < 4 * NB) cp16(dst + sc_to, unit_at(sc_pool, sc_units, page, (row >> 4) * NB + sc_p));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t page = __shfl_sync(0xFFFFFFFFu, (uint32_t)w_page, slot + j);
+            const uint32_t row = __shfl_sync(0xFFFFFFFFu, w_row, slot + j);
+            if ((bits >> j) & 1u) {
+              const uint8_t* const ks = unit_at(a.c.k, k_units, page, row * PR + lane);
+              const uint8_t* const vs = unit_at(a.c.v, v_units, page, row * PR + lane);
+#pragma unroll
+              for (int i = 0; i < PR / 2; ++i) {
+                const int to = (i & 1 ? to1 : to0) + i * RPC * RB + j * 16 * RB;
+                cp16(dst + to, ks + i * 512);
+                cp16(dst + KT * RB + to, vs + i * 512);
+              }
+              if (lane < 2 * NB)
+                cp16(dst + sc_to + j * 16 * NB, unit_at(sc_pool, sc_units, page, (row >> 4) * NB + sc_p));
+            }
+          }
+        }
+      }
+      cp_commit();
+      st_in = st_in + 1 == C::STAGES ? 0 : st_in + 1;
+#pragma unroll
+      for (int i = 0; i + 1 < C::STAGES; ++i) there[i] = there[i + 1];
+      there[C::STAGES - 1] = bits;
+    };
+#pragma unroll
+    for (int i = 0; i < C::STAGES - 1; ++i) advance(i);
 
     // ---- Q: lane (g, t) holds elements KE t .. KE t + KE - 1 of query row g of each 8-row tile ----
     uint32_t q[NT][C::KS][2];
@@ -285,58 +396,6 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
     }
     min_lim = __reduce_min_sync(0xFFFFFFFFu, min_lim);
 
-    // ---- the warp's tiles: keys (c0 + i) CHUNK + warp KT + [0, KT) ----
-    const int k_first = c0 * CHUNK + warp * KT;
-    const int last = min(c1 * CHUNK, len);
-    const int n_tiles = k_first < last ? (last - k_first + CHUNK - 1) / CHUNK : 0;
-
-    // page ids: lane 2 i + j has the 16-key group j of tile (window start) + i, for 16 tiles at a time
-    int w_page = -1, w_off = 0;
-    auto load_window = [&](int tile0) {
-      const int i = tile0 + (lane >> 1), key = k_first + i * CHUNK + (lane & 1) * 16;
-      w_page = -1;
-      if (i < n_tiles && key < len) {
-        const int lp = key / page_size;
-        w_off = key - lp * page_size;
-        w_page = __ldg(a.pt.table + b * a.pt.stride + lp);
-        if (w_page < 0 || w_page >= a.c.num_pages) {
-          w_page = -1;
-          if (a.dev_status) *a.dev_status = CACHE_BAD_PAGE;
-        }
-      }
-    };
-    // bit i: the 16 keys of group i & 1 of window tile i >> 1 are there
-    uint32_t present = 0;
-    auto issue = [&](int tile) {
-      if (tile < n_tiles) {
-        const uint32_t dst = ring_s + (tile % C::STAGES) * C::STAGE;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int slot = (tile & 15) * 2 + j;
-          const long long page = __shfl_sync(0xFFFFFFFFu, w_page, slot);
-          const int off = __shfl_sync(0xFFFFFFFFu, w_off, slot);
-          if (page >= 0) {
-            const long long in_page = (long long)h * page_size + off;
-            const uint8_t* ks = a.c.k + page * a.c.k_ps + in_page * RB;
-            const uint8_t* vs = a.c.v + page * a.c.v_ps + in_page * RB;
-#pragma unroll
-            for (int i = 0; i < RB / 32; ++i) {   // 16 rows are RB pieces of 16 bytes
-              const int p = i * 32 + lane, k = j * 16 + p / (RB / 16), at = piece_at<RB>(k, p % (RB / 16));
-              cp16(dst + at, ks + p * 16);
-              cp16(dst + KT * RB + at, vs + p * 16);
-            }
-            if (lane < 2 * NB) {                  // 16 keys' scales are NB pieces, K's then V's
-              const bool v = lane >= NB;
-              const int p = v ? lane - NB : lane;
-              const uint8_t* src = (v ? a.c.v_sc + page * a.c.v_sc_ps : a.c.k_sc + page * a.c.k_sc_ps) + in_page * NB;
-              cp16(dst + 2 * KT * RB + (v ? KT * NB : 0) + j * 16 * NB + p * 16, src + p * 16);
-            }
-          }
-        }
-      }
-      cp_commit();
-    };
-
     float acc[NT][C::MT][4], l[NT][2], m[NT][2], nm[NT][2];   // nm = LIFT - m (0 where m is -inf)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -346,29 +405,13 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
       m[nt][0] = m[nt][1] = -INFINITY;
     }
 
-    // a window is loaded when its first tile is issued; `present` follows two windows at most, so it is taken
-    // tile by tile: ring_present keeps the two bits of each stage
-    uint32_t ring_present = 0;
-    auto advance = [&](int tile) {
-      if ((tile & 15) == 0 && tile < n_tiles) {
-        load_window(tile);
-        present = __ballot_sync(0xFFFFFFFFu, w_page >= 0);
-      }
-      const int st = tile % C::STAGES;
-      ring_present = (ring_present & ~(3u << (2 * st))) | (((present >> (2 * (tile & 15))) & 3u) << (2 * st));
-      issue(tile);
-    };
-#pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) advance(i);
-
     for (int tile = 0; tile < n_tiles; ++tile) {
       cp_wait<C::STAGES - 2>();
       __syncwarp();
-      const int st = tile % C::STAGES;
-      const uint32_t there = (ring_present >> (2 * st)) & 3u;
       advance(tile + C::STAGES - 1);
 
-      uint8_t* const stage = ring + st * C::STAGE;
+      uint8_t* const stage = ring + st_out * C::STAGE;
+      st_out = st_out + 1 == C::STAGES ? 0 : st_out + 1;
       uint8_t* const vrows = stage + KT * RB;
       uint8_t* const ksc = stage + 2 * KT * RB;
       uint8_t* const vsc = ksc + KT * NB;
@@ -376,8 +419,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 
       // ---- which keys the matrix path leaves out: `gone` (past the sequence, no page), `odd` (scales) ----
       const int valid = len - k0;
-      uint32_t gone = (valid < KT ? 0xFFFFFFFFu << valid : 0u) | (there & 1 ? 0u : 0xFFFFu) |
-                      (there & 2 ? 0u : 0xFFFF0000u);
+      const uint32_t gone = (valid < KT ? 0xFFFFFFFFu << valid : 0u) | (there[0] & 1 ? 0u : 0xFFFFu) |
+                            (there[0] & 2 ? 0u : 0xFFFF0000u);
       bool ok;
       if (NB == 4) {
         ok = scales_in_range<C>(reinterpret_cast<const uint32_t*>(ksc)[lane]) &
@@ -393,19 +436,18 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
       float s[NT][2][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        const int ka = mt * 16 + key_of_row(g), kb = ka + 8;
-        const uint32_t sa = scale_f16<C>(ksc[ka * NB + t * C::KE / 32]), sb = scale_f16<C>(ksc[kb * NB + t * C::KE / 32]);
-        constexpr int LB = C::KE * RB / D;        // bytes of a lane's run: 8, 16 or 32
+        const uint32_t sa = scale_f16<C>(stage[kso + mt * 16 * NB]), sb = scale_f16<C>(stage[kso + (mt * 16 + 8) * NB]);
+        const uint8_t* const ra = stage + ko + mt * 16 * RB;
+        const uint8_t* const rb = ra + 8 * RB;
         uint32_t wa[LB / 4], wb[LB / 4];
         if (LB == 8) {
-          const uint2 ua = *reinterpret_cast<const uint2*>(stage + piece_at<RB>(ka, t >> 1) + (t & 1) * 8);
-          const uint2 ub = *reinterpret_cast<const uint2*>(stage + piece_at<RB>(kb, t >> 1) + (t & 1) * 8);
+          const uint2 ua = *reinterpret_cast<const uint2*>(ra), ub = *reinterpret_cast<const uint2*>(rb);
           wa[0] = ua.x; wa[1] = ua.y; wb[0] = ub.x; wb[1] = ub.y;
         } else {
 #pragma unroll
-          for (int i = 0; i < LB / 16; ++i) {
-            const uint4 ua = *reinterpret_cast<const uint4*>(stage + piece_at<RB>(ka, t * (LB / 16) + i));
-            const uint4 ub = *reinterpret_cast<const uint4*>(stage + piece_at<RB>(kb, t * (LB / 16) + i));
+          for (int i = 0; i < LB / 16; ++i) {   // the run's second piece is the first's neighbour: bit 4 of the offset
+            const int flip = i ? ((ko & 16) ? -16 : 16) : 0;
+            const uint4 ua = *reinterpret_cast<const uint4*>(ra + flip), ub = *reinterpret_cast<const uint4*>(rb + flip);
             wa[4 * i] = ua.x; wa[4 * i + 1] = ua.y; wa[4 * i + 2] = ua.z; wa[4 * i + 3] = ua.w;
             wb[4 * i] = ub.x; wb[4 * i + 1] = ub.y; wb[4 * i + 2] = ub.z; wb[4 * i + 3] = ub.w;
           }
@@ -448,15 +490,18 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
         for (int nt = 0; nt < NT; ++nt) dot[nt] = 0.f;
         const float sc = scale_value(ksc[k * NB + t * C::KE / 32]);
 #pragma unroll
-        for (int i = 0; i < C::KS; ++i) {
-          const int d = t * C::KE + 4 * i;
-          const float e0 = element<FMT, C>(stage, k, d, sc), e1 = element<FMT, C>(stage, k, d + 1, sc);
-          const float e2 = element<FMT, C>(stage, k, d + 2, sc), e3 = element<FMT, C>(stage, k, d + 3, sc);
+        for (int w = 0; w < LB / 4; ++w) {
+          constexpr int PW = FMT == CACHE_FP4 ? 2 : 1;      // k-steps per word
+          float e[4 * PW];
+          word_values<FMT, C>(stage, k, t * LB + 4 * w, sc, e);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float2 qa = f16x2_to_f32(q[nt][i][0]), qb = f16x2_to_f32(q[nt][i][1]);
-            dot[nt] += qa.x * e0 + qa.y * e1 + qb.x * e2 + qb.y * e3;
-          }
+          for (int j = 0; j < PW; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float2 qa = f16x2_to_f32(q[nt][w * PW + j][0]), qb = f16x2_to_f32(q[nt][w * PW + j][1]);
+              dot[nt] += qa.x * e[4 * j] + qa.y * e[4 * j + 1] + qb.x * e[4 * j + 2] + qb.y * e[4 * j + 3];
+            }
+          in_order();
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -550,17 +595,22 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
             }
             const bool sees0 = k0 + k < lim[nt][0], sees1 = k0 + k < lim[nt][1];
 #pragma unroll
-            for (int i = 0; i < C::MT; ++i) {
-              const float e0 = element<FMT, C>(vrows, k, g * C::VE + 2 * i, sc);
-              const float e1 = element<FMT, C>(vrows, k, g * C::VE + 2 * i + 1, sc);
-              if (sees0) {
-                acc[nt][i][0] += p[0] * e0;
-                acc[nt][i][2] += p[0] * e1;
+            for (int w = 0; w < VB / 4; ++w) {
+              constexpr int PW = FMT == CACHE_FP4 ? 4 : 2;  // 16-row tiles per word
+              float e[2 * PW];
+              word_values<FMT, C>(vrows, k, g * VB + 4 * w, sc, e);
+#pragma unroll
+              for (int i = 0; i < PW; ++i) {
+                if (sees0) {
+                  acc[nt][w * PW + i][0] += p[0] * e[2 * i];
+                  acc[nt][w * PW + i][2] += p[0] * e[2 * i + 1];
+                }
+                if (sees1) {
+                  acc[nt][w * PW + i][1] += p[1] * e[2 * i];
+                  acc[nt][w * PW + i][3] += p[1] * e[2 * i + 1];
+                }
               }
-              if (sees1) {
-                acc[nt][i][1] += p[1] * e0;
-                acc[nt][i][3] += p[1] * e1;
-              }
+              in_order();
             }
           }
         }
@@ -594,14 +644,12 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
           pb[nt][0] = transpose8(pack_f16x2(s[nt][mt][0], s[nt][mt][1]));
           pb[nt][1] = transpose8(pack_f16x2(s[nt][mt][2], s[nt][mt][3]));
         }
-        constexpr int VB = C::VE * RB / D;     // bytes of a lane's run: 4, 8 or 16
-        const int kk = mt * 16 + t, blk = g * C::VE / 32;
-        const uint32_t s01 = scales_f16x2<C>(vsc[kk * NB + blk], vsc[(kk + 4) * NB + blk]);
-        const uint32_t s23 = scales_f16x2<C>(vsc[(kk + 8) * NB + blk], vsc[(kk + 12) * NB + blk]);
+        const uint8_t* const sv = stage + vso + mt * 16 * NB;
+        const uint32_t s01 = scales_f16x2<C>(sv[0], sv[4 * NB]), s23 = scales_f16x2<C>(sv[8 * NB], sv[12 * NB]);
         uint32_t v[4][VB / 4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint8_t* src = vrows + piece_at<RB>(kk + 4 * i, g * VB / 16) + (g * VB) % 16;
+          const uint8_t* src = vrows + (i & 1 ? vo4 : vo0) + (i >> 1) * 8 * RB + mt * 16 * RB;
           if (VB == 4) {
             v[i][0] = *reinterpret_cast<const uint32_t*>(src);
           } else if (VB == 8) {
@@ -617,10 +665,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
           if (FMT == CACHE_FP4) {
             // even elements of two keys per byte, then odd ones
             uint32_t e01[4], o01[4], e23[4], o23[4];
-            e2m1x8_to_f16((v[0][w] & 0x0F0F0F0Fu) | ((v[1][w] << 4) & 0xF0F0F0F0u), e01);
-            e2m1x8_to_f16(((v[0][w] >> 4) & 0x0F0F0F0Fu) | (v[1][w] & 0xF0F0F0F0u), o01);
-            e2m1x8_to_f16((v[2][w] & 0x0F0F0F0Fu) | ((v[3][w] << 4) & 0xF0F0F0F0u), e23);
-            e2m1x8_to_f16(((v[2][w] >> 4) & 0x0F0F0F0Fu) | (v[3][w] & 0xF0F0F0F0u), o23);
+            e2m1x8_to_f16(interleave_low(v[0][w], v[1][w]), e01);
+            e2m1x8_to_f16(interleave_high(v[0][w], v[1][w]), o01);
+            e2m1x8_to_f16(interleave_low(v[2][w], v[3][w]), e23);
+            e2m1x8_to_f16(interleave_high(v[2][w], v[3][w]), o23);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint32_t a0 = mul_f16x2(e01[j], s01), a1 = mul_f16x2(o01[j], s01);
@@ -717,72 +765,87 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 }
 
 // Joins the parts of units that several blocks share, in their order along the keys, and writes the rows of
-// sequences that hold nothing.  One block per unit; SPREAD: one block per row, its warps on every 8th part.
+// sequences that hold nothing.  A block has `rows_pb` (a divisor of ROWS) rows of one unit; its warps are
+// spread over the rows, and over the parts of a row where there are more warps than rows.  The log-sum-exps
+// come in first, all at once, then every part's O is loaded independently: two latencies, whatever the
+// number of parts.  It is launched while the first kernel still runs (programmatic dependence) and waits for
+// it before it touches the workspace or O.
 constexpr int JOIN_WARPS = 8;
-template <int D, int DT, int NT, bool SPREAD>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const CacheAttnArgs a, int row_tiles, int grid) {
+template <int D, int DT, int NT>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const CacheAttnArgs a, int row_tiles, int grid,
+                                                                          int rows_pb) {
   constexpr int ROWS = 8 * NT, SLOT = ROWS * (D + 1), PL = D / 32;    // columns per lane
-  __shared__ float part_o[SPREAD ? JOIN_WARPS : 1][SPREAD ? D : 1];
-  __shared__ float2 part_ml[JOIN_WARPS];
+  __shared__ float zs[MOST_PARTS * 8];                                // [row of the block][part]
+  __shared__ __align__(16) float part_o[JOIN_WARPS][D];
+  __shared__ float part_sum[JOIN_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.Hq / a.c.Hkv, U = a.c.Hkv * row_tiles, R = a.T * G;
-  const int unit = SPREAD ? blockIdx.x / ROWS : blockIdx.x;
+  const int groups = ROWS / rows_pb, unit = blockIdx.x / groups, first_row = (blockIdx.x - unit * groups) * rows_pb;
   const int b = unit / U, u = unit - b * U, h = u / row_tiles, rt = u - h * row_tiles;
   const int len = seq_len(a, b), n_chunks = (len + CHUNK - 1) / CHUNK;
-  long long i0 = 0, i1 = -1;
+  long long i0 = 0;
+  int parts = 0;
+  bool mine = rt * ROWS + first_row < R;
   if (n_chunks > 0) {
     const long long total = chunks_before(a, a.B, U), n = blocks_of(total, grid);
     const long long x0 = chunks_before(a, b, U) + (long long)u * n_chunks;
     i0 = block_of_chunk(total, n, x0);
-    i1 = block_of_chunk(total, n, x0 + n_chunks - 1);
-    if (i0 == i1) return;               // one block had the whole unit and wrote it
+    parts = (int)(block_of_chunk(total, n, x0 + n_chunks - 1) - i0) + 1;
+    if (parts == 1) mine = false;       // one block had the whole unit and wrote it
   } else if (__ldg(a.pt.seq_lens + b) > 0 && threadIdx.x == 0 && a.dev_status) {
     *a.dev_status = CACHE_BAD_LEN;      // tokens, but a table without pages
   }
-  const float* const ws = reinterpret_cast<const float*>(a.ws);
-  const int row0 = SPREAD ? blockIdx.x % ROWS : warp, row_step = SPREAD ? ROWS : JOIN_WARPS;
-  for (int row = row0; row < ROWS; row += row_step) {
-    const int r = rt * ROWS + row;
-    if (r >= R) return;                 // whole warps, and whole blocks where they meet below
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!mine) return;
+  // part i of a row: block i0 + i; the first one holds its share in its odd slot, the others in their even one
+  const float* const ws = reinterpret_cast<const float*>(a.ws) + 2 * i0 * SLOT;
+  for (int i = threadIdx.x; i < parts * rows_pb; i += JOIN_WARPS * 32) {
+    const int row = i / parts, p = i - row * parts;
+    zs[i] = rt * ROWS + first_row + row < R ? __ldcg(ws + (2LL * p + (p == 0)) * SLOT + ROWS * D + first_row + row) : -INFINITY;
+  }
+  __syncthreads();
+  const int ways = rows_pb < JOIN_WARPS ? JOIN_WARPS / rows_pb : 1;
+  for (int row0 = 0; row0 < rows_pb; row0 += JOIN_WARPS) {
+    const int row = row0 + (rows_pb < JOIN_WARPS ? warp % rows_pb : warp), way = rows_pb < JOIN_WARPS ? warp / rows_pb : 0;
+    const int r = rt * ROWS + first_row + row;
     float m = -INFINITY, sum = 0.f, o[PL];
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, zs[row * parts + i]);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
 #pragma unroll
     for (int j = 0; j < PL; ++j) o[j] = 0.f;
-    // block i0 holds the unit's first chunks in its odd slot, the others in their even one
-    for (long long i = i0 + (SPREAD ? warp : 0); i <= i1; i += SPREAD ? JOIN_WARPS : 1) {
-      const float* slot = ws + (2 * i + (i == i0 ? 1 : 0)) * SLOT;
-      const float z = slot[ROWS * D + row];
-      float v[PL];
+    if (r < R) {
+#pragma unroll 4
+      for (int i = way; i < parts; i += ways) {
+        const float z = zs[row * parts + i];
+        const float f = z == -INFINITY ? 0.f : m == -INFINITY ? 1.f : ex2_approx(z - m);   // NaN stays
+        const float* src = ws + (2LL * i + (i == 0)) * SLOT + (first_row + row) * D + lane * PL;
+        float v[PL];
+        if (PL == 4) {
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+          v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
+        } else {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+          v[0] = y.x; v[1] = y.y;
+        }
+        sum += z != z ? z : f;
 #pragma unroll
-      for (int j = 0; j < PL; ++j) v[j] = slot[row * D + lane * PL + j];
-      if (z == -INFINITY) continue;
-      const float m2 = z > m ? z : m, keep = m == -INFINITY ? 0.f : ex2_approx(m - m2), f = ex2_approx(z - m2);
-      m = m2;
-      sum = sum * keep + f;
-#pragma unroll
-      for (int j = 0; j < PL; ++j) o[j] = o[j] * keep + f * v[j];
-    }
-    if (SPREAD) {
-      if (lane == 0) part_ml[warp] = make_float2(m, sum);
-#pragma unroll
-      for (int j = 0; j < PL; ++j) part_o[warp][lane * PL + j] = o[j];
-      __syncthreads();
-      if (warp != 0) return;
-      m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < JOIN_WARPS; ++w) m = fmaxf(m, part_ml[w].x);
-      sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < PL; ++j) o[j] = 0.f;
-#pragma unroll
-      for (int w = 0; w < JOIN_WARPS; ++w) {
-        const float2 y = part_ml[w];
-        if (y.x == -INFINITY && y.y == 0.f) continue;
-        const float f = ex2_approx(y.x - m);
-        sum += f * y.y;
-#pragma unroll
-        for (int j = 0; j < PL; ++j) o[j] += f * part_o[w][lane * PL + j];
+        for (int j = 0; j < PL; ++j) o[j] += f * v[j];
       }
     }
+    if (ways > 1) {                     // rows_pb < JOIN_WARPS: a single pass of the outer loop
+#pragma unroll
+      for (int j = 0; j < PL; ++j) part_o[warp][lane * PL + j] = o[j];
+      if (lane == 0) part_sum[warp] = sum;
+      __syncthreads();
+      if (way != 0) return;
+      for (int w = 1; w < ways; ++w) {
+        sum += part_sum[w * rows_pb + warp];
+#pragma unroll
+        for (int j = 0; j < PL; ++j) o[j] += part_o[w * rows_pb + warp][lane * PL + j];
+      }
+    }
+    if (r >= R) continue;
     const int tq = r / G, hq = h * G + r - tq * G;
     const bool none = sum == 0.f;
     uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + b * a.os.b + tq * a.os.t + hq * a.os.h + lane * PL;
@@ -797,24 +860,40 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
 template <int FMT, int D, int DT, int NT>
 cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   using C = Cfg<FMT, D, NT>;
+  static_assert(C::ROWS * SMS * C::OCC <= MOST_PARTS * 8, "the join's table of parts");
   const int rows = a.T * (a.Hq / a.c.Hkv), row_tiles = (rows + C::ROWS - 1) / C::ROWS;
   const long long units = (long long)a.B * a.c.Hkv * row_tiles;
   const long long chunks = ((long long)a.pt.max_pages * a.c.page_size + CHUNK - 1) / CHUNK;
   const long long grid = units * chunks < SMS * C::OCC ? units * chunks : SMS * C::OCC;
   if (grid > 0) {
     auto kernel = cache_attn_kernel<FMT, D, DT, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    // the opt-in to more than 48 KB of shared memory, once per device
+    static std::atomic<uint64_t> opted{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (!((opted.load(std::memory_order_relaxed) >> dev) & 1)) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+      if (e != cudaSuccess) return e;
+      opted.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     kernel<<<(unsigned)grid, THREADS, C::SMEM, st>>>(a, row_tiles);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // few units: many parts each, a block per row
-  if (units * C::ROWS <= SMS * 8)
-    cache_attn_join_kernel<D, DT, NT, true><<<(unsigned)(units * C::ROWS), JOIN_WARPS * 32, 0, st>>>(a, row_tiles, (int)grid);
-  else
-    cache_attn_join_kernel<D, DT, NT, false><<<(unsigned)units, JOIN_WARPS * 32, 0, st>>>(a, row_tiles, (int)grid);
-  return cudaGetLastError();
+  // few units have many parts each: a block per row then; many units, a block per unit
+  int rows_pb = C::ROWS;
+  while (rows_pb > 1 && units * (C::ROWS / rows_pb) * 2 <= SMS * 8) rows_pb /= 2;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(units * (C::ROWS / rows_pb)));
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, DT, NT>, a, row_tiles, (int)grid, rows_pb);
 }
 
 template <int FMT, int D, int DT>
