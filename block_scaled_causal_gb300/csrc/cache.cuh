@@ -46,10 +46,15 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
                                                                   : __uint_as_float(byte << 23);
 }
 
-// Two fp32 -> E2M1x2 (nearest even, saturated to +-6), low nibble `lo`.
-__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
+// E2M1: nearest even, saturated to +-6.
+// Eight fp32 -> eight E2M1, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&f)[8]) {
   uint32_t r;
-  asm("{ .reg .b8 t; cvt.rn.satfinite.e2m1x2.f32 t, %1, %2; cvt.u32.u8 %0, t; }" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("{ .reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d}; }"
+      : "=r"(r) : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
   return r;
 }
 // The four bytes (eight E2M1) of a word -> f16x2 each (exact), low nibble in the low half.
@@ -82,22 +87,23 @@ __device__ __forceinline__ uint32_t f32_to_act(float lo, float hi) {
   return r;
 }
 
-// Slot (page * page_size + offset) of position `pos` of sequence `b`, or -1 where there is none;
-// `bad` collects a status code.
-__device__ __forceinline__ long long cache_slot(const CachePools& c, const CacheTable& pt, int b, long long pos,
-                                                int32_t& bad) {
+// The page that holds position `pos` of sequence `b`, or -1 where there is none, and the row of that position and
+// head in the page's [Hkv][page_size]; `bad` collects a status code.
+__device__ __forceinline__ int cache_page(const CachePools& c, const CacheTable& pt, int b, long long pos, int h,
+                                          uint32_t& row, int32_t& bad) {
   if (pos < 0) return -1;
-  if (pos >= (long long)pt.max_pages * c.page_size) {
+  if (pos >= (long long)pt.max_pages * c.page_size) {   // < 2^31
     bad = CACHE_BAD_LEN;
     return -1;
   }
-  const int lp = (int)pos / c.page_size, off = (int)pos - lp * c.page_size;
+  const uint32_t lp = (uint32_t)pos / (uint32_t)c.page_size;
+  row = (uint32_t)h * c.page_size + (uint32_t)pos - lp * c.page_size;
   const int page = __ldg(pt.table + b * pt.stride + lp);
   if (page < 0 || page >= c.num_pages) {
     bad = CACHE_BAD_PAGE;
     return -1;
   }
-  return (long long)page * c.page_size + off;
+  return page;
 }
 
 }  // namespace bsc

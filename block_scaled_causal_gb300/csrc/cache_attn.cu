@@ -45,6 +45,7 @@ namespace {
 constexpr int KT = 32, WARPS = 4, CHUNK = KT * WARPS, THREADS = WARPS * 32;
 constexpr int SMS = 152;
 constexpr int MOST_PARTS = SMS * 4;   // parts a unit can have: the blocks of the largest grid
+constexpr int MIN_CHUNKS = 2;
 constexpr float SLACK = 4.f;    // a reference moves when a score passes it by this much (log2)
 constexpr float LIFT = 8.f;     // weights are 2^(x - m + LIFT)
 
@@ -90,6 +91,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with nothing to add to.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -122,11 +130,11 @@ __device__ __forceinline__ bool scales_in_range(uint32_t w) {
 // 2^(byte - 127 + OFF) in fp16 for bytes in range, 0 for byte 0: in both halves / for two bytes.
 template <class C>
 __device__ __forceinline__ uint32_t scale_f16(uint32_t byte) {
-  return (uint32_t)max((int)byte - (int)C::SUB, 0) * 0x04000400u;
+  return (uint32_t)__viaddmax_s32_relu((int)byte, -(int)C::SUB, 0) * 0x04000400u;
 }
 template <class C>
 __device__ __forceinline__ uint32_t scales_f16x2(uint32_t lo, uint32_t hi) {
-  return ((uint32_t)max((int)lo - (int)C::SUB, 0) << 10) | ((uint32_t)max((int)hi - (int)C::SUB, 0) << 26);
+  return __viaddmax_s16x2_relu(lo | hi << 16, (0x10000u - C::SUB) * 0x10001u, 0u) << 10;
 }
 
 // The elements of the 32-bit word at byte `at` of key k's row in shared memory, each as the fp32 value it stands
@@ -164,33 +172,36 @@ __device__ __forceinline__ const uint8_t* unit_at(const uint8_t* pool, uint32_t 
   return pool + ((unsigned long long)page * page_units + n) * 16;
 }
 
-// The list of chunks.  Sequence b has n_b = ceil(len_b / CHUNK) chunks per unit and U = Hkv * (row tiles) units.
+// The list of chunks.  Sequence b has ceil(len_b / CHUNK) chunks per unit and U = Hkv * (row tiles) units; the host
+// has checked that the longest list the page table allows has fewer than 2^31 chunks.
 __device__ __forceinline__ int seq_len(const CacheAttnArgs& a, int b) {
-  const long long cap = (long long)a.pt.max_pages * a.c.page_size;   // < 2^31
-  const int len = max(__ldg(a.pt.seq_lens + b), 0);
-  return len > cap ? (int)cap : len;
+  const int cap = a.pt.max_pages * a.c.page_size;   // < 2^31
+  return min(max(__ldg(a.pt.seq_lens + b), 0), cap);
 }
-__device__ __forceinline__ long long chunks_of(const CacheAttnArgs& a, int b, int U) {
-  return b < a.B ? (long long)((seq_len(a, b) + CHUNK - 1) / CHUNK) * U : 0;
+__device__ __forceinline__ uint32_t chunks_of(const CacheAttnArgs& a, int b, int U) {
+  return b < a.B ? (uint32_t)((seq_len(a, b) + (CHUNK - 1)) / CHUNK) * U : 0u;
 }
-// Sum over the sequences before b (b = B: all of them).  Whole warps call it.
-__device__ __forceinline__ long long chunks_before(const CacheAttnArgs& a, int b, int U) {
-  long long s = 0;
-  for (int i = threadIdx.x & 31; i < b; i += 32) s += chunks_of(a, i, U);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  return s;
+// Chunks of all sequences, and of those before b.  Whole warps call it.
+__device__ __forceinline__ uint32_t chunks_of_all(const CacheAttnArgs& a, int U, int b, uint32_t& before) {
+  uint32_t all = 0, first = 0;
+  for (int i = threadIdx.x & 31; i < a.B; i += 32) {
+    const uint32_t n = chunks_of(a, i, U);
+    all += n;
+    if (i < b) first += n;
+  }
+  before = __reduce_add_sync(0xFFFFFFFFu, first);
+  return __reduce_add_sync(0xFFFFFFFFu, all);
 }
-// The sequence that chunk x < total belongs to, and its first chunk.
-__device__ __forceinline__ int seq_of_chunk(const CacheAttnArgs& a, long long x, int U, long long& base) {
+// The sequence that chunk x of the list belongs to, and its first chunk.
+__device__ __forceinline__ int seq_of_chunk(const CacheAttnArgs& a, uint32_t x, int U, uint32_t& base) {
   const int lane = threadIdx.x & 31;
   base = 0;
-  for (int b0 = 0;; b0 += 32) {
-    const long long n = chunks_of(a, b0 + lane, U);
-    long long s = n;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const uint32_t n = chunks_of(a, b0 + lane, U);
+    uint32_t s = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
       if (lane >= o) s += y;
     }
     const uint32_t hit = __ballot_sync(0xFFFFFFFFu, base + s > x);
@@ -200,15 +211,26 @@ __device__ __forceinline__ int seq_of_chunk(const CacheAttnArgs& a, long long x,
       return b0 + l;
     }
     base += __shfl_sync(0xFFFFFFFFu, s, 31);
-    if (b0 + 32 >= a.B) return a.B;   // x is past the list
   }
+  return a.B;   // past the list
 }
-// Blocks that share the list, the first chunk of block i, and the block that has chunk x.
-__device__ __forceinline__ long long blocks_of(long long total, int grid) { return total < grid ? total : grid; }
-__device__ __forceinline__ long long first_chunk(long long total, long long n, long long i) { return total * i / n; }
-__device__ __forceinline__ long long block_of_chunk(long long total, long long n, long long x) {
-  return ((x + 1) * n - 1) / total;
-}
+// How the list is shared: n blocks, the first `more` of them with each + 1 chunks, the others with `each`.
+// A block costs a prologue and a part to join, so a block per chunk is taken only while there are fewer chunks than
+// SMs, and then MIN_CHUNKS chunks each until the grid is full.
+struct Share {
+  uint32_t n, each, more;
+  __device__ __forceinline__ Share(uint32_t total, uint32_t grid) {
+    n = total < SMS ? total : min(max(total / MIN_CHUNKS, (uint32_t)SMS), grid);
+    n = min(n, grid);
+    each = n ? total / n : 0;
+    more = total - n * each;
+  }
+  __device__ __forceinline__ uint32_t first(uint32_t i) const { return i * each + min(i, more); }   // of block i
+  __device__ __forceinline__ uint32_t block(uint32_t x) const {                                       // that has chunk x
+    const uint32_t big = more * (each + 1);
+    return x < big ? x / (each + 1) : more + (x - big) / each;
+  }
+};
 
 // A workspace slot: ROWS x D of O, then ROWS log-sum-exps (log2).
 template <class C, int D>
@@ -224,12 +246,11 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
   const int R = a.T * G;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long total = chunks_before(a, a.B, U);
-  const long long nblk = blocks_of(total, gridDim.x);
-  if (blockIdx.x >= nblk) return;
-  long long x = first_chunk(total, nblk, blockIdx.x);
-  const long long x_end = first_chunk(total, nblk, blockIdx.x + 1);
-  long long base;
+  uint32_t base;
+  const Share share(chunks_of_all(a, U, 0, base), gridDim.x);
+  if (blockIdx.x >= share.n) return;
+  uint32_t x = share.first(blockIdx.x);
+  const uint32_t x_end = share.first(blockIdx.x + 1);
   int b = seq_of_chunk(a, x, U, base);
 
   // ---- what a lane's place fixes ----
@@ -260,13 +281,23 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
       ++b;
       continue;
     }
-    const long long rel = x - base;
-    const int u = (int)(rel / n_chunks), c0 = (int)(rel - (long long)u * n_chunks);
-    const int c1 = (int)min((long long)n_chunks, c0 + (x_end - x));
+    const int u = (int)((x - base) / (uint32_t)n_chunks), c0 = (int)(x - base) - u * n_chunks;
+    const int c1 = min(n_chunks, c0 + (int)(x_end - x));
     const int h = u / row_tiles, rt = u - h * row_tiles;
     const int raw_len = max(__ldg(a.pt.seq_lens + b), 0);
     const int n_new = a.new_lens ? min(max(__ldg(a.new_lens + b), 0), a.T) : a.T;
     if (raw_len > len && tid == 0 && a.dev_status) *a.dev_status = CACHE_BAD_LEN;
+
+    // ---- Q's loads start: lane (g, t) has elements KE t .. KE t + KE - 1 of query row g of each 8-row tile ----
+    uint4 q_in[NT][C::KE / 8];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = rt * C::ROWS + nt * 8 + g, tq = r / G, hq = h * G + r - tq * G;
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + b * a.qs.b + tq * a.qs.t + hq * a.qs.h + t * C::KE;
+#pragma unroll
+      for (int i = 0; i < C::KE / 8; ++i)
+        q_in[nt][i] = r < R ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+    }
 
     // ---- the warp's tiles: keys (c0 + i) CHUNK + warp KT + [0, KT) ----
     const int k_first = c0 * CHUNK + warp * KT;
@@ -340,32 +371,25 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 #pragma unroll
     for (int i = 0; i < C::STAGES - 1; ++i) advance(i);
 
-    // ---- Q: lane (g, t) holds elements KE t .. KE t + KE - 1 of query row g of each 8-row tile ----
+    // ---- Q scaled and in fp16 ----
     uint32_t q[NT][C::KS][2];
     float c[NT][2];            // score -> log2 units, rows 2t and 2t + 1
     int lim[NT][2];            // keys j < lim are visible; rows that see nothing or do not exist: all
     int min_lim = len;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = rt * C::ROWS + nt * 8 + g, tq = r / G, hq = h * G + r - tq * G;
-      float f[C::KE];
+      const int r = rt * C::ROWS + nt * 8 + g, tq = r / G;
       float mx = 0.f;
-      if (r < R) {
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + b * a.qs.b + tq * a.qs.t + hq * a.qs.h + t * C::KE;
+      float f[C::KE];
 #pragma unroll
-        for (int i = 0; i < C::KE / 8; ++i) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int i = 0; i < C::KE / 8; ++i) {
+        const uint32_t w[4] = {q_in[nt][i].x, q_in[nt][i].y, q_in[nt][i].z, q_in[nt][i].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 p = act_to_f32<DT>(w[j]);
-            f[8 * i + 2 * j] = p.x;
-            f[8 * i + 2 * j + 1] = p.y;
-          }
+        for (int j = 0; j < 4; ++j) {
+          const float2 p = act_to_f32<DT>(w[j]);
+          f[8 * i + 2 * j] = p.x;
+          f[8 * i + 2 * j + 1] = p.y;
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < C::KE; ++i) f[i] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < C::KE; ++i) mx = fmaxf(mx, fabsf(f[i]));
@@ -452,8 +476,6 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
             wb[4 * i] = ub.x; wb[4 * i + 1] = ub.y; wb[4 * i + 2] = ub.z; wb[4 * i + 3] = ub.w;
           }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][mt][0] = s[nt][mt][1] = s[nt][mt][2] = s[nt][mt][3] = 0.f;
         if (FMT == CACHE_FP4) {
 #pragma unroll
           for (int i = 0; i < LB / 4; ++i) {
@@ -465,7 +487,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
               const uint32_t a0 = mul_f16x2(ha[2 * j], sa), a1 = mul_f16x2(hb[2 * j], sb);
               const uint32_t a2 = mul_f16x2(ha[2 * j + 1], sa), a3 = mul_f16x2(hb[2 * j + 1], sb);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt][mt], a0, a1, a2, a3, q[nt][2 * i + j][0], q[nt][2 * i + j][1]);
+              for (int nt = 0; nt < NT; ++nt)
+                if (2 * i + j == 0) mma_f16_first(s[nt][mt], a0, a1, a2, a3, q[nt][0][0], q[nt][0][1]);
+                else mma_f16(s[nt][mt], a0, a1, a2, a3, q[nt][2 * i + j][0], q[nt][2 * i + j][1]);
             }
           }
         } else {
@@ -477,7 +501,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
             const uint32_t a0 = mul_f16x2(ha[0], sa), a1 = mul_f16x2(hb[0], sb);
             const uint32_t a2 = mul_f16x2(ha[1], sa), a3 = mul_f16x2(hb[1], sb);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt][mt], a0, a1, a2, a3, q[nt][i][0], q[nt][i][1]);
+            for (int nt = 0; nt < NT; ++nt)
+              if (i == 0) mma_f16_first(s[nt][mt], a0, a1, a2, a3, q[nt][0][0], q[nt][0][1]);
+              else mma_f16(s[nt][mt], a0, a1, a2, a3, q[nt][i][0], q[nt][i][1]);
           }
         }
       }
@@ -714,7 +740,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
     __syncthreads();
     const bool whole = c0 == 0 && c1 == n_chunks;
     float* const slot = reinterpret_cast<float*>(a.ws) +
-                        (2LL * blockIdx.x + (c0 == 0 ? 1 : 0)) * slot_floats<C, D>();
+                        (2LL * blockIdx.x + (c0 == 0)) * slot_floats<C, D>();
     constexpr int LPR = D / 8;                 // threads per row, 8 columns each
     for (int i = tid; i < C::ROWS * LPR; i += THREADS) {
       const int row = i / LPR, d = (i % LPR) * 8, r = rt * C::ROWS + row;
@@ -757,7 +783,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
     __syncthreads();
 
     x += c1 - c0;
-    if (x == base + (long long)n_chunks * U) {
+    if (x == base + (uint32_t)n_chunks * U) {
       base = x;
       ++b;
     }
@@ -765,12 +791,12 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 }
 
 // Joins the parts of units that several blocks share, in their order along the keys, and writes the rows of
-// sequences that hold nothing.  A block has `rows_pb` (a divisor of ROWS) rows of one unit; its warps are
-// spread over the rows, and over the parts of a row where there are more warps than rows.  The log-sum-exps
+// sequences that hold nothing.  A block has `rows_pb` (a power of two, at most ROWS) rows of one unit; its warps
+// are spread over the rows, and over the parts of a row where there are more warps than rows.  The log-sum-exps
 // come in first, all at once, then every part's O is loaded independently: two latencies, whatever the
 // number of parts.  It is launched while the first kernel still runs (programmatic dependence) and waits for
 // it before it touches the workspace or O.
-constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_WARPS = 16;
 template <int D, int DT, int NT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const CacheAttnArgs a, int row_tiles, int grid,
                                                                           int rows_pb) {
@@ -783,14 +809,16 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
   const int groups = ROWS / rows_pb, unit = blockIdx.x / groups, first_row = (blockIdx.x - unit * groups) * rows_pb;
   const int b = unit / U, u = unit - b * U, h = u / row_tiles, rt = u - h * row_tiles;
   const int len = seq_len(a, b), n_chunks = (len + CHUNK - 1) / CHUNK;
-  long long i0 = 0;
+  const int left = R - rt * ROWS - first_row;         // rows of the block that exist
+  bool mine = left > 0;
+  uint32_t i0 = 0;
   int parts = 0;
-  bool mine = rt * ROWS + first_row < R;
   if (n_chunks > 0) {
-    const long long total = chunks_before(a, a.B, U), n = blocks_of(total, grid);
-    const long long x0 = chunks_before(a, b, U) + (long long)u * n_chunks;
-    i0 = block_of_chunk(total, n, x0);
-    parts = (int)(block_of_chunk(total, n, x0 + n_chunks - 1) - i0) + 1;
+    uint32_t x0;
+    const Share share(chunks_of_all(a, U, b, x0), grid);
+    x0 += (uint32_t)u * n_chunks;
+    i0 = share.block(x0);
+    parts = (int)(share.block(x0 + n_chunks - 1) - i0) + 1;
     if (parts == 1) mine = false;       // one block had the whole unit and wrote it
   } else if (__ldg(a.pt.seq_lens + b) > 0 && threadIdx.x == 0 && a.dev_status) {
     *a.dev_status = CACHE_BAD_LEN;      // tokens, but a table without pages
@@ -798,63 +826,63 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!mine) return;
   // part i of a row: block i0 + i; the first one holds its share in its odd slot, the others in their even one
-  const float* const ws = reinterpret_cast<const float*>(a.ws) + 2 * i0 * SLOT;
-  for (int i = threadIdx.x; i < parts * rows_pb; i += JOIN_WARPS * 32) {
-    const int row = i / parts, p = i - row * parts;
-    zs[i] = rt * ROWS + first_row + row < R ? __ldcg(ws + (2LL * p + (p == 0)) * SLOT + ROWS * D + first_row + row) : -INFINITY;
+  const float* const ws = reinterpret_cast<const float*>(a.ws) + 2LL * i0 * SLOT;
+  const int live = min(left, rows_pb);
+  for (int i = threadIdx.x; i < parts * live; i += JOIN_WARPS * 32) {
+    const int p = i / live, row = i - p * live;
+    zs[row * parts + p] = __ldcg(ws + (2LL * p + (p == 0)) * SLOT + ROWS * D + first_row + row);
   }
   __syncthreads();
-  const int ways = rows_pb < JOIN_WARPS ? JOIN_WARPS / rows_pb : 1;
-  for (int row0 = 0; row0 < rows_pb; row0 += JOIN_WARPS) {
-    const int row = row0 + (rows_pb < JOIN_WARPS ? warp % rows_pb : warp), way = rows_pb < JOIN_WARPS ? warp / rows_pb : 0;
-    const int r = rt * ROWS + first_row + row;
-    float m = -INFINITY, sum = 0.f, o[PL];
+  const int ways = JOIN_WARPS / rows_pb, row = warp & (rows_pb - 1), way = warp / rows_pb;
+  float m = -INFINITY, sum = 0.f, o[PL];
+#pragma unroll
+  for (int j = 0; j < PL; ++j) o[j] = 0.f;
+  if (row < live) {
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, zs[row * parts + i]);
 #pragma unroll
     for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-#pragma unroll
-    for (int j = 0; j < PL; ++j) o[j] = 0.f;
-    if (r < R) {
-#pragma unroll 4
-      for (int i = way; i < parts; i += ways) {
-        const float z = zs[row * parts + i];
-        const float f = z == -INFINITY ? 0.f : m == -INFINITY ? 1.f : ex2_approx(z - m);   // NaN stays
-        const float* src = ws + (2LL * i + (i == 0)) * SLOT + (first_row + row) * D + lane * PL;
-        float v[PL];
-        if (PL == 4) {
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
-          v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
-        } else {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
-          v[0] = y.x; v[1] = y.y;
-        }
-        sum += z != z ? z : f;
-#pragma unroll
-        for (int j = 0; j < PL; ++j) o[j] += f * v[j];
+    const float* const src = ws + (first_row + row) * D + lane * PL;
+#pragma unroll 8
+    for (int i = way; i < parts; i += ways) {
+      const float z = zs[row * parts + i];
+      const float f = z == -INFINITY ? 0.f : m == -INFINITY ? z : ex2_approx(z - m);   // NaN stays NaN
+      float v[PL];
+      if (PL == 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (2LL * i + (i == 0)) * SLOT));
+        v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
+      } else {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(src + (2LL * i + (i == 0)) * SLOT));
+        v[0] = y.x; v[1] = y.y;
       }
+      sum += f;
+#pragma unroll
+      for (int j = 0; j < PL; ++j) o[j] += f * v[j];
     }
-    if (ways > 1) {                     // rows_pb < JOIN_WARPS: a single pass of the outer loop
-#pragma unroll
-      for (int j = 0; j < PL; ++j) part_o[warp][lane * PL + j] = o[j];
-      if (lane == 0) part_sum[warp] = sum;
-      __syncthreads();
-      if (way != 0) return;
-      for (int w = 1; w < ways; ++w) {
-        sum += part_sum[w * rows_pb + warp];
-#pragma unroll
-        for (int j = 0; j < PL; ++j) o[j] += part_o[w * rows_pb + warp][lane * PL + j];
-      }
-    }
-    if (r >= R) continue;
-    const int tq = r / G, hq = h * G + r - tq * G;
-    const bool none = sum == 0.f;
-    uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + b * a.os.b + tq * a.os.t + hq * a.os.h + lane * PL;
-#pragma unroll
-    for (int j = 0; j < PL; j += 2)
-      *reinterpret_cast<uint32_t*>(dst + j) = none ? 0u : f32_to_act<DT>(o[j] / sum, o[j + 1] / sum);
-    if (lane == 0 && a.lse)
-      a.lse[((long long)b * a.Hq + hq) * a.T + tq] = none ? -INFINITY : (m + __log2f(sum)) * 0.6931471805599453f;
   }
+  if (ways > 1) {
+#pragma unroll
+    for (int j = 0; j < PL; ++j) part_o[warp][lane * PL + j] = o[j];
+    if (lane == 0) part_sum[warp] = sum;
+    __syncthreads();
+    if (way != 0) return;
+    for (int w = 1; w < ways; ++w) {
+      sum += part_sum[w * rows_pb + row];
+#pragma unroll
+      for (int j = 0; j < PL; ++j) o[j] += part_o[w * rows_pb + row][lane * PL + j];
+    }
+  }
+  if (row >= live) return;
+  const int r = rt * ROWS + first_row + row, tq = r / G, hq = h * G + r - tq * G;
+  const bool none = sum == 0.f;
+  uint16_t* const dst = reinterpret_cast<uint16_t*>(a.o) + b * a.os.b + tq * a.os.t + hq * a.os.h + lane * PL;
+  const float inv = 1.f / sum;
+  uint32_t w[PL / 2];
+#pragma unroll
+  for (int j = 0; j < PL / 2; ++j) w[j] = none ? 0u : f32_to_act<DT>(o[2 * j] * inv, o[2 * j + 1] * inv);
+  if (PL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[PL / 2 - 1]);
+  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if (lane == 0 && a.lse)
+    a.lse[((long long)b * a.Hq + hq) * a.T + tq] = none ? -INFINITY : (m + __log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int FMT, int D, int DT, int NT>
@@ -864,6 +892,7 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   const int rows = a.T * (a.Hq / a.c.Hkv), row_tiles = (rows + C::ROWS - 1) / C::ROWS;
   const long long units = (long long)a.B * a.c.Hkv * row_tiles;
   const long long chunks = ((long long)a.pt.max_pages * a.c.page_size + CHUNK - 1) / CHUNK;
+  if (units * chunks >= (1LL << 31) || units * C::ROWS >= (1LL << 31)) return cudaErrorNotSupported;
   const long long grid = units * chunks < SMS * C::OCC ? units * chunks : SMS * C::OCC;
   if (grid > 0) {
     auto kernel = cache_attn_kernel<FMT, D, DT, NT>;
@@ -881,9 +910,9 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // few units have many parts each: a block per row then; many units, a block per unit
+  // few units have many parts each: as many blocks per unit as the card takes at once
   int rows_pb = C::ROWS;
-  while (rows_pb > 1 && units * (C::ROWS / rows_pb) * 2 <= SMS * 8) rows_pb /= 2;
+  while (rows_pb > 1 && units * (C::ROWS / rows_pb) * 2 <= SMS * 2) rows_pb /= 2;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

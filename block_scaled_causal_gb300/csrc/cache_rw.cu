@@ -52,62 +52,54 @@ __global__ void __launch_bounds__(RW_WARPS * 32) cache_write_kernel(const CacheR
     const int r = i * RPI + sub;
     v[i] = r < rows ? __ldcs(reinterpret_cast<const uint4*>(x + (long long)(w.t0 + r) * xs.t)) : make_uint4(0, 0, 0, 0);
   }
-  // lane r < 16 finds row r's slot
+  // lane r < 16 finds where row r goes: its page and its row in the page's [Hkv][page_size]
   int32_t bad = 0;
-  long long slot = -1;
-  if (lane < rows) slot = cache_slot(a.c, a.pt, w.b, (len < 0 ? 0 : len) - n + w.t0 + lane, bad);
+  int page = -1;
+  uint32_t in_page = 0;
+  if (lane < rows) page = cache_page(a.c, a.pt, w.b, (len < 0 ? 0 : len) - n + w.t0 + lane, w.h, in_page, bad);
   if (bad && a.dev_status) *a.dev_status = bad;
 
-  uint8_t* const pool = w.which ? a.c.v : a.c.k;
+  uint8_t* const pool = (w.which ? a.c.v : a.c.k) + col * (RB / LPR);
   uint8_t* const pool_sc = w.which ? a.c.v_sc : a.c.k_sc;
   const long long ps = w.which ? a.c.v_ps : a.c.k_ps, ps_sc = w.which ? a.c.v_sc_ps : a.c.k_sc_ps;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     if (i * RPI >= rows) break;
     const int r = i * RPI + sub;
-    const long long sl = __shfl_sync(0xFFFFFFFFu, slot, r);
+    const int pg = __shfl_sync(0xFFFFFFFFu, page, r);
+    const uint32_t row = __shfl_sync(0xFFFFFFFFu, in_page, r);
+    // the block's maximum from bit patterns: without the sign they are in the values' order, NaN above Inf on top
     const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    float f[8];
-    float am = 0.f;
-    bool odd = false;      // a NaN, which no maximum would keep
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 p = act_to_f32<DT>(u[j]);
-      f[2 * j] = p.x;
-      f[2 * j + 1] = p.y;
-      am = fmaxf(am, fmaxf(fabsf(p.x), fabsf(p.y)));
-      odd |= (p.x != p.x) | (p.y != p.y);
-    }
-    if (odd) am = __uint_as_float(0x7F800000u);
-    am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-    am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+    uint32_t mx = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu), __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+    const float am = act_to_f32<DT>(max(mx & 0xFFFFu, mx >> 16)).x;
     float inv;
     const uint32_t sb = block_scale<FMT>(am, a.rule, inv);
     // the row's scale word: each block's byte in its place, joined over the row's lanes
     uint32_t word = sb << (8 * (col >> 2));
 #pragma unroll
     for (int o = 4; o < LPR; o <<= 1) word |= __shfl_xor_sync(0xFFFFFFFFu, word, o);
-    if (sl >= 0) {
-      const long long page = sl / a.c.page_size;
-      const int off = (int)(sl - page * a.c.page_size);
-      const long long in_page = (long long)w.h * a.c.page_size + off;
-      uint8_t* const dst = pool + page * ps + in_page * RB;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 p = __fmul2_rn(act_to_f32<DT>(u[j]), make_float2(inv, inv));
+      f[2 * j] = p.x;
+      f[2 * j + 1] = p.y;
+    }
+    if (pg >= 0) {
+      uint8_t* const dst = pool + pg * ps + (unsigned long long)row * RB;
       if (FMT == CACHE_FP4) {
-        const uint32_t q = sb == 0xFFu ? 0x77777777u
-                                       : cvt_e2m1x2(f[0] * inv, f[1] * inv) | cvt_e2m1x2(f[2] * inv, f[3] * inv) << 8 |
-                                             cvt_e2m1x2(f[4] * inv, f[5] * inv) << 16 |
-                                             cvt_e2m1x2(f[6] * inv, f[7] * inv) << 24;
-        *reinterpret_cast<uint32_t*>(dst + col * 4) = q;
+        const uint32_t q = cvt_e2m1x8(f);
+        *reinterpret_cast<uint32_t*>(dst) = sb == 0xFFu ? 0x77777777u : q;
       } else {
-        uint2 q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        if (sb != 0xFFu) {
-          q.x = cvt_e4m3x2(f[0] * inv, f[1] * inv) | (uint32_t)cvt_e4m3x2(f[2] * inv, f[3] * inv) << 16;
-          q.y = cvt_e4m3x2(f[4] * inv, f[5] * inv) | (uint32_t)cvt_e4m3x2(f[6] * inv, f[7] * inv) << 16;
-        }
-        *reinterpret_cast<uint2*>(dst + col * 8) = q;
+        uint2 q;
+        q.x = cvt_e4m3x2(f[0], f[1]) | (uint32_t)cvt_e4m3x2(f[2], f[3]) << 16;
+        q.y = cvt_e4m3x2(f[4], f[5]) | (uint32_t)cvt_e4m3x2(f[6], f[7]) << 16;
+        *reinterpret_cast<uint2*>(dst) = sb == 0xFFu ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu) : q;
       }
       if (col == 0) {
-        uint8_t* const sc = pool_sc + page * ps_sc + in_page * NB;
+        uint8_t* const sc = pool_sc + pg * ps_sc + (unsigned long long)row * NB;
         if (NB == 4)
           *reinterpret_cast<uint32_t*>(sc) = word;
         else
@@ -137,12 +129,11 @@ __global__ void __launch_bounds__(RW_WARPS * 32) cache_read_kernel(const CacheRw
   uint32_t word = 0;
   if (lane < rows) {
     const long long pos = start + w.t0 + lane;
-    const long long slot = pos < len ? cache_slot(a.c, a.pt, w.b, pos, bad) : -1;
-    if (slot >= 0) {
-      const long long page = slot / a.c.page_size;
-      const long long in_page = (long long)w.h * a.c.page_size + (slot - page * a.c.page_size);
-      at = page * ps + in_page * RB;
-      const uint8_t* const sc = pool_sc + page * ps_sc + in_page * NB;
+    uint32_t row = 0;
+    const int page = pos < len ? cache_page(a.c, a.pt, w.b, pos, w.h, row, bad) : -1;
+    if (page >= 0) {
+      at = page * ps + (unsigned long long)row * RB;
+      const uint8_t* const sc = pool_sc + page * ps_sc + (unsigned long long)row * NB;
       word = NB == 4 ? *reinterpret_cast<const uint32_t*>(sc) : *reinterpret_cast<const uint16_t*>(sc);
     }
   }
