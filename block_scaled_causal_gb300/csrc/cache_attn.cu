@@ -44,10 +44,10 @@ namespace {
 
 constexpr int KT = 32, WARPS = 4, CHUNK = KT * WARPS, THREADS = WARPS * 32;
 constexpr int SMS = 152;
-constexpr int MOST_PARTS = SMS * 4;   // parts a unit can have: the blocks of the largest grid
 constexpr int MIN_CHUNKS = 2;
 constexpr float SLACK = 4.f;    // a reference moves when a score passes it by this much (log2)
-constexpr float LIFT = 8.f;     // weights are 2^(x - m + LIFT)
+constexpr float LIFT = 8.f;     // a reference m gives weights 2^(x + r), r = LIFT - m
+constexpr float UNSET = 3e38f;  // r of a row without a score yet: 2^(-inf + r) = 0, and any score moves it
 
 template <int FMT, int D, int NT>
 struct Cfg {
@@ -61,8 +61,13 @@ struct Cfg {
   static constexpr int STAGE = 2 * KT * (RB + NB);       // K, V, K scales, V scales of 32 keys
   static constexpr int STAGES = FMT == CACHE_FP4 || D == 64 ? 3 : 2;
   static constexpr int RING = WARPS * STAGES * STAGE;
+  // From four row tiles on, Q's fragments do not fit beside O in registers: shared memory, [tile][k-step][lane],
+  // then c and lim of every row.
+  static constexpr bool QS = NT >= 4;
+  static constexpr int QF = QS ? NT * KS * 32 * 8 : 0;
+  static constexpr int QBYTES = QS ? QF + ROWS * 8 : 0;
   static constexpr int MERGE = WARPS * ROWS * (D + 4) * 4 + WARPS * ROWS * 8;
-  static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+  static constexpr int SMEM = RING + QBYTES > MERGE ? RING + QBYTES : MERGE;
   static constexpr int OCC = NT == 1 ? (STAGE * STAGES * WARPS > 56 * 1024 ? 3 : 4) : 2;   // blocks per SM
 };
 
@@ -289,10 +294,13 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
     if (raw_len > len && tid == 0 && a.dev_status) *a.dev_status = CACHE_BAD_LEN;
 
     // ---- Q's loads start: lane (g, t) has elements KE t .. KE t + KE - 1 of query row g of each 8-row tile ----
-    uint4 q_in[NT][C::KE / 8];
+    // (of all tiles, or each warp of its own where Q goes to shared memory)
+    constexpr int NQ = C::QS ? NT / WARPS : NT;
+    const int nt0 = C::QS ? warp * NQ : 0;
+    uint4 q_in[NQ][C::KE / 8];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = rt * C::ROWS + nt * 8 + g, tq = r / G, hq = h * G + r - tq * G;
+    for (int nt = 0; nt < NQ; ++nt) {
+      const int r = rt * C::ROWS + (nt0 + nt) * 8 + g, tq = r / G, hq = h * G + r - tq * G;
       const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + b * a.qs.b + tq * a.qs.t + hq * a.qs.h + t * C::KE;
 #pragma unroll
       for (int i = 0; i < C::KE / 8; ++i)
@@ -372,13 +380,16 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
     for (int i = 0; i < C::STAGES - 1; ++i) advance(i);
 
     // ---- Q scaled and in fp16 ----
-    uint32_t q[NT][C::KS][2];
-    float c[NT][2];            // score -> log2 units, rows 2t and 2t + 1
-    int lim[NT][2];            // keys j < lim are visible; rows that see nothing or do not exist: all
+    uint32_t q[NQ][C::KS][2];
+    float c_own[NQ][2];        // score -> log2 units, rows 2t and 2t + 1
+    int lim_own[NQ][2];        // keys j < lim are visible; rows that see nothing or do not exist: all
     int min_lim = len;
+    uint2* const qs = reinterpret_cast<uint2*>(smem + C::RING);
+    float* const cs = reinterpret_cast<float*>(smem + C::RING + C::QF);
+    int* const lims = reinterpret_cast<int*>(cs + C::ROWS);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = rt * C::ROWS + nt * 8 + g, tq = r / G;
+    for (int nt = 0; nt < NQ; ++nt) {
+      const int r = rt * C::ROWS + (nt0 + nt) * 8 + g, tq = r / G;
       float mx = 0.f;
       float f[C::KE];
 #pragma unroll
@@ -411,22 +422,41 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
         const long long past = (long long)raw_len - n_new + tq + 1;
         if (past > 0 && past < len) lg = (int)past;
       }
+      min_lim = min(min_lim, lg);
+      if (C::QS) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        c[nt][j] = __shfl_sync(0xFFFFFFFFu, cg, (2 * t + j) * 4);
-        lim[nt][j] = __shfl_sync(0xFFFFFFFFu, lg, (2 * t + j) * 4);
-        min_lim = min(min_lim, lim[nt][j]);
+        for (int i = 0; i < C::KS; ++i) qs[((nt0 + nt) * C::KS + i) * 32 + lane] = make_uint2(q[nt][i][0], q[nt][i][1]);
+        if (t == 0) {
+          cs[(nt0 + nt) * 8 + g] = cg;
+          lims[(nt0 + nt) * 8 + g] = lg;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          c_own[nt][j] = __shfl_sync(0xFFFFFFFFu, cg, (2 * t + j) * 4);
+          lim_own[nt][j] = __shfl_sync(0xFFFFFFFFu, lg, (2 * t + j) * 4);
+        }
       }
     }
+    if (C::QS) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < C::ROWS; i += 32) min_lim = min(min_lim, lims[i + lane]);
+    }
     min_lim = __reduce_min_sync(0xFFFFFFFFu, min_lim);
+    auto q_frag = [&](int nt, int i) {
+      return C::QS ? qs[(nt * C::KS + i) * 32 + lane] : make_uint2(q[C::QS ? 0 : nt][i][0], q[C::QS ? 0 : nt][i][1]);
+    };
+    auto c_of = [&](int nt, int j) { return C::QS ? cs[nt * 8 + 2 * t + j] : c_own[C::QS ? 0 : nt][j]; };
+    auto lim_of = [&](int nt, int j) { return C::QS ? lims[nt * 8 + 2 * t + j] : lim_own[C::QS ? 0 : nt][j]; };
 
-    float acc[NT][C::MT][4], l[NT][2], m[NT][2], nm[NT][2];   // nm = LIFT - m (0 where m is -inf)
+    float acc[NT][C::MT][4], l[NT][2], ref[NT][2];   // weights are 2^(c s + ref)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < C::MT; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
-      l[nt][0] = l[nt][1] = nm[nt][0] = nm[nt][1] = 0.f;
-      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+      ref[nt][0] = ref[nt][1] = UNSET;
     }
 
     for (int tile = 0; tile < n_tiles; ++tile) {
@@ -487,9 +517,11 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
               const uint32_t a0 = mul_f16x2(ha[2 * j], sa), a1 = mul_f16x2(hb[2 * j], sb);
               const uint32_t a2 = mul_f16x2(ha[2 * j + 1], sa), a3 = mul_f16x2(hb[2 * j + 1], sb);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                if (2 * i + j == 0) mma_f16_first(s[nt][mt], a0, a1, a2, a3, q[nt][0][0], q[nt][0][1]);
-                else mma_f16(s[nt][mt], a0, a1, a2, a3, q[nt][2 * i + j][0], q[nt][2 * i + j][1]);
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint2 qb = q_frag(nt, 2 * i + j);
+                if (2 * i + j == 0) mma_f16_first(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
+                else mma_f16(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
+              }
             }
           }
         } else {
@@ -501,9 +533,11 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
             const uint32_t a0 = mul_f16x2(ha[0], sa), a1 = mul_f16x2(hb[0], sb);
             const uint32_t a2 = mul_f16x2(ha[1], sa), a3 = mul_f16x2(hb[1], sb);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              if (i == 0) mma_f16_first(s[nt][mt], a0, a1, a2, a3, q[nt][0][0], q[nt][0][1]);
-              else mma_f16(s[nt][mt], a0, a1, a2, a3, q[nt][i][0], q[nt][i][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 qb = q_frag(nt, i);
+              if (i == 0) mma_f16_first(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
+              else mma_f16(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
+            }
           }
         }
       }
@@ -524,7 +558,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
           for (int j = 0; j < PW; ++j)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const float2 qa = f16x2_to_f32(q[nt][w * PW + j][0]), qb = f16x2_to_f32(q[nt][w * PW + j][1]);
+              const uint2 qf = q_frag(nt, w * PW + j);
+              const float2 qa = f16x2_to_f32(qf.x), qb = f16x2_to_f32(qf.y);
               dot[nt] += qa.x * e[4 * j] + qa.y * e[4 * j + 1] + qb.x * e[4 * j + 2] + qb.y * e[4 * j + 3];
             }
           in_order();
@@ -555,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                if (away || k0 + k >= lim[nt][j]) s[nt][mt][2 * half + j] = -INFINITY;
+                if (away || k0 + k >= lim_of(nt, j)) s[nt][mt][2 * half + j] = -INFINITY;
           }
       }
 
@@ -566,8 +601,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          top[nt][j] = c[nt][j] * fmaxf(fmaxf(s[nt][0][j], s[nt][0][2 + j]), fmaxf(s[nt][1][j], s[nt][1][2 + j]));
-          climb |= top[nt][j] > m[nt][j] + SLACK;
+          top[nt][j] = c_of(nt, j) * fmaxf(fmaxf(s[nt][0][j], s[nt][0][2 + j]), fmaxf(s[nt][1][j], s[nt][1][2 + j]));
+          climb |= top[nt][j] + ref[nt][j] > LIFT + SLACK;
         }
       if (__any_sync(0xFFFFFFFFu, climb)) {
 #pragma unroll
@@ -578,10 +613,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-            if (mx > m[nt][j] + SLACK) {
-              const float keep = ex2_approx(m[nt][j] - mx);   // 0 from -inf
-              m[nt][j] = mx;
-              nm[nt][j] = LIFT - mx;
+            if (mx + ref[nt][j] > LIFT + SLACK) {
+              const float keep = ex2_approx((LIFT - mx) - ref[nt][j]);   // 0 from UNSET
+              ref[nt][j] = LIFT - mx;
               l[nt][j] *= keep;
 #pragma unroll
               for (int i = 0; i < C::MT; ++i) {
@@ -599,7 +633,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            s[nt][mt][i] = ex2_approx(fmaf(s[nt][mt][i], c[nt][i & 1], nm[nt][i & 1]));
+            s[nt][mt][i] = ex2_approx(fmaf(s[nt][mt][i], c_of(nt, i & 1), ref[nt][i & 1]));
             l[nt][i & 1] += s[nt][mt][i];
           }
 
@@ -619,7 +653,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
               const float p2 = __shfl_sync(0xFFFFFFFFu, s[nt][1][j], src), p3 = __shfl_sync(0xFFFFFFFFu, s[nt][1][2 + j], src);
               p[j] = k < 16 ? (k < 8 ? p0 : p1) : (k < 24 ? p2 : p3);
             }
-            const bool sees0 = k0 + k < lim[nt][0], sees1 = k0 + k < lim[nt][1];
+            const bool sees0 = k0 + k < lim_of(nt, 0), sees1 = k0 + k < lim_of(nt, 1);
 #pragma unroll
             for (int w = 0; w < VB / 4; ++w) {
               constexpr int PW = FMT == CACHE_FP4 ? 4 : 2;  // 16-row tiles per word
@@ -732,7 +766,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
         const int row = nt * 8 + 2 * t + j;
-        if (g == 0) ml[warp * C::ROWS + row] = make_float2(m[nt][j], sum);
+        if (g == 0) ml[warp * C::ROWS + row] = make_float2(-ref[nt][j], sum);
         float* const dst = mo + (warp * C::ROWS + row) * (D + 4) + g * C::VE;
 #pragma unroll
         for (int i = 0; i < C::MT; ++i) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[nt][i][j], acc[nt][i][2 + j]);
@@ -745,15 +779,14 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
     for (int i = tid; i < C::ROWS * LPR; i += THREADS) {
       const int row = i / LPR, d = (i % LPR) * 8, r = rt * C::ROWS + row;
       if (r >= R) continue;
-      float mx = -INFINITY;
+      float mx = -UNSET;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, ml[w * C::ROWS + row].x);
       float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
-        const float2 part = ml[w * C::ROWS + row];
-        if (part.x == -INFINITY && part.y == 0.f) continue;    // no key of this warp's
-        const float f = part.x == -INFINITY ? 1.f : ex2_approx(part.x - mx);
+        const float2 part = ml[w * C::ROWS + row];     // (-UNSET, 0) where the warp had no key: weighs 0
+        const float f = ex2_approx(part.x - mx);
         sum += f * part.y;
         const float4* src = reinterpret_cast<const float4*>(mo + (w * C::ROWS + row) * (D + 4) + d);
         const float4 y0 = src[0], y1 = src[1];
@@ -764,7 +797,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
       const bool sees = tq < n_new && (long long)raw_len - n_new + tq >= 0;
       const bool none = !sees || sum == 0.f;
       const float inv = none ? 0.f : __fdividef(1.f, sum) * (1.f / (1 << C::OFF));
-      const float z = none ? -INFINITY : mx - LIFT + __log2f(sum);
+      const float z = none ? -INFINITY : mx + __log2f(sum);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = none ? 0.f : o[j] * inv;
       if (whole) {
@@ -791,7 +824,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 }
 
 // Joins the parts of units that several blocks share, in their order along the keys, and writes the rows of
-// sequences that hold nothing.  A block has `rows_pb` (a power of two, at most ROWS) rows of one unit; its warps
+// sequences that hold nothing.  A block has `rows_pb` (a power of two, at most ROWS and its warps) rows of one unit; its warps
 // are spread over the rows, and over the parts of a row where there are more warps than rows.  The log-sum-exps
 // come in first, all at once, then every part's O is loaded independently: two latencies, whatever the
 // number of parts.  It is launched while the first kernel still runs (programmatic dependence) and waits for
@@ -801,7 +834,8 @@ template <int D, int DT, int NT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const CacheAttnArgs a, int row_tiles, int grid,
                                                                           int rows_pb) {
   constexpr int ROWS = 8 * NT, SLOT = ROWS * (D + 1), PL = D / 32;    // columns per lane
-  __shared__ float zs[MOST_PARTS * 8];                                // [row of the block][part]
+  constexpr int MOST_PARTS = SMS * (NT == 1 ? 4 : 2);                 // blocks of the largest grid
+  __shared__ float zs[MOST_PARTS * (ROWS < JOIN_WARPS ? ROWS : JOIN_WARPS)];   // [row of the block][part]
   __shared__ __align__(16) float part_o[JOIN_WARPS][D];
   __shared__ float part_sum[JOIN_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -888,7 +922,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
 template <int FMT, int D, int DT, int NT>
 cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   using C = Cfg<FMT, D, NT>;
-  static_assert(C::ROWS * SMS * C::OCC <= MOST_PARTS * 8, "the join's table of parts");
+  static_assert(C::OCC <= (NT == 1 ? 4 : 2), "the join's table of parts, and the workspace");
   const int rows = a.T * (a.Hq / a.c.Hkv), row_tiles = (rows + C::ROWS - 1) / C::ROWS;
   const long long units = (long long)a.B * a.c.Hkv * row_tiles;
   const long long chunks = ((long long)a.pt.max_pages * a.c.page_size + CHUNK - 1) / CHUNK;
@@ -911,7 +945,7 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   // few units have many parts each: as many blocks per unit as the card takes at once
-  int rows_pb = C::ROWS;
+  int rows_pb = C::ROWS < JOIN_WARPS ? C::ROWS : JOIN_WARPS;
   while (rows_pb > 1 && units * (C::ROWS / rows_pb) * 2 <= SMS * 2) rows_pb /= 2;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
@@ -927,14 +961,15 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
 
 template <int FMT, int D, int DT>
 cudaError_t pick(const CacheAttnArgs& a, cudaStream_t st) {
-  return a.T * (a.Hq / a.c.Hkv) <= 8 ? launch<FMT, D, DT, 1>(a, st) : launch<FMT, D, DT, 2>(a, st);
+  const int rows = a.T * (a.Hq / a.c.Hkv);
+  return rows <= 8 ? launch<FMT, D, DT, 1>(a, st) : rows <= 16 ? launch<FMT, D, DT, 2>(a, st) : launch<FMT, D, DT, 4>(a, st);
 }
 
 }  // namespace
 
 size_t cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
   // two slots per block of the largest grid of either format
-  const long long rows = (long long)T * ((Hq + Hkv - 1) / Hkv) <= 8 ? 8 : 16;
+  const long long all = (long long)T * ((Hq + Hkv - 1) / Hkv), rows = all <= 8 ? 8 : all <= 16 ? 16 : 32;
   const int occ = rows == 8 ? 4 : 2;
   return (size_t)2 * SMS * occ * rows * (D + 1) * 4;
 }
