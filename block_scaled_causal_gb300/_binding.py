@@ -56,7 +56,7 @@ def _load():
         f.restype = i32
         f.argtypes = [ctypes.POINTER(params), vp]
     lib.mx_cache_attn_workspace_bytes.restype = ctypes.c_size_t
-    lib.mx_cache_attn_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    lib.mx_cache_attn_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, ctypes.c_longlong]
     lib.bsc_read_device_status.restype = i32
     lib.bsc_read_device_status.argtypes = [vp, vp]
     return lib
@@ -558,9 +558,10 @@ def mx_cache_read(cache, page_table, seq_lens, T, starts=None, layout=BSHD, dtyp
 
 
 @functools.lru_cache(maxsize=256)
-def mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D=128):
-    """Bytes of scratch mx_cache_attn needs (the C call of the same name)."""
-    return int(lib.mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D))
+def mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D=128, max_tokens=1 << 30):
+    """Bytes of scratch mx_cache_attn needs (the C call of the same name); max_tokens: page_table columns times
+    page size (left out: enough for any table)."""
+    return int(lib.mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D, max_tokens))
 
 
 def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, softmax_scale=None, o=None, lse=None,
@@ -568,14 +569,15 @@ def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, so
     """Attention of T queries per sequence over the cache; returns (O shaped and typed like q, LSE fp32
     [B, Hq, T]).  Query t < new_lens[b] (None: all T) is the token at position seq_lens[b] - new_lens[b] + t and
     attends the positions up to its own.  `workspace`: a device tensor of at least
-    mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D) bytes that no other running call uses, else one is
-    allocated here."""
+    mx_cache_attn_workspace_bytes(...) bytes that no other running call uses, else one is allocated here
+    where the call needs any."""
     there = _elsewhere(cache, stream)
     if there is not None:
         with there:
             return mx_cache_attn(q, cache, page_table, seq_lens, new_lens, layout, softmax_scale, o, lse, workspace,
                                  dev_status)
     (B, T, Hq), qs, dt = _act_dims(q, layout, None, cache.D, cache, "q")
+    table = _table(page_table, B, cache)
     device = cache.device
     if o is None:
         o = torch.empty(q.shape, dtype=q.dtype, device=device)
@@ -591,16 +593,16 @@ def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, so
             not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 tensor [B, Hq, T] on the cache's device")
     if workspace is None:
-        need = mx_cache_attn_workspace_bytes(B, T, Hq, cache.Hkv, cache.D)
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        need = mx_cache_attn_workspace_bytes(B, T, Hq, cache.Hkv, cache.D, table[2] * cache.page_size)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
         need = workspace.numel() * workspace.element_size()
     p = CacheAttnParams(cache.params, q.data_ptr(), o.data_ptr(), lse.data_ptr(), *qs, *o_s, B, T, Hq, dt,
-                        cache.D ** -0.5 if softmax_scale is None else softmax_scale,
-                        *_table(page_table, B, cache), _index(seq_lens, (B,), cache, "seq_lens"),
+                        cache.D ** -0.5 if softmax_scale is None else softmax_scale, *table, _index(seq_lens, (B,), cache, "seq_lens"),
                         _index(new_lens, (B,), cache, "new_lens"), _status(dev_status, cache),
-                        workspace.data_ptr(), need)
+                        workspace.data_ptr() if need else None, need)
     _check(lib.mx_cache_attn(ctypes.byref(p), _raw_stream(device.index)))
     return o, lse

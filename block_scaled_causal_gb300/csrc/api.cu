@@ -501,9 +501,9 @@ bsc_status mx_cache_read(const bsc_mx_cache_read_params* p, bsc_stream_t stream)
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
-  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
-  return bsc::cache_attn_workspace_bytes(B, T, Hq, Hkv, D);
+size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long long max_tokens) {
+  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_tokens < 0) return 0;
+  return bsc::cache_attn_workspace_bytes(B, T, Hq, Hkv, D, max_tokens);
 }
 
 bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream) {
@@ -513,7 +513,8 @@ bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream)
   if (s != BSC_OK || empty) return s;
   if (p->Hq % p->cache.Hkv != 0) return BSC_ERR_SHAPE;
   if (!(std::isfinite(p->softmax_scale) && p->softmax_scale > 0.f)) return BSC_ERR_UNSUPPORTED;
-  const size_t need = mx_cache_attn_workspace_bytes(p->B, p->T, p->Hq, p->cache.Hkv, p->cache.D);
+  const size_t need = mx_cache_attn_workspace_bytes(p->B, p->T, p->Hq, p->cache.Hkv, p->cache.D,
+                                                    (long long)p->max_pages * p->cache.page_size);
   if (!p->q || !p->o || !p->seq_lens || !p->page_table || (need > 0 && !p->workspace)) return BSC_ERR_NULL;
   if (!aligned16(p->q) || !aligned16(p->o) || !aligned16(p->workspace) || !aligned4(p->page_table) ||
       !aligned4(p->seq_lens) || !aligned4(p->new_lens) || !aligned4(p->lse) || !aligned4(p->dev_status))
@@ -537,8 +538,8 @@ bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream)
   a.dev_status = p->dev_status;
   a.scale_log2e = (float)((double)p->softmax_scale * 1.4426950408889634);
   a.ws = p->workspace;
-  return from_cuda(bsc::launch_cache_attn(a, p->cache.format, p->cache.D, p->dtype,
-                                          reinterpret_cast<cudaStream_t>(stream)));
+  a.fp16 = p->dtype == BSC_FP16;
+  return from_cuda(bsc::launch_cache_attn(a, p->cache.format, p->cache.D, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 bsc_status bsc_read_device_status(const int32_t* dev_status, bsc_stream_t stream) {

@@ -128,12 +128,13 @@ struct CacheAttnArgs {
   float* lse;              // may be nullptr
   RowStrides qs, os;
   int B, T, Hq;
+  int fp16;                // activations: 0 bf16, 1 fp16
   const int32_t* new_lens; // may be nullptr
   int32_t* dev_status;     // may be nullptr
   float scale_log2e;
   void* ws;
 };
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, int format, int D, int dtype, cudaStream_t st);
-size_t cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, int format, int D, cudaStream_t st);
+size_t cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long long max_tokens);
 
 }  // namespace bsc

@@ -87,6 +87,12 @@ __device__ __forceinline__ uint32_t f32_to_act(float lo, float hi) {
   return r;
 }
 
+// The same with the type known at run time.
+__device__ __forceinline__ float2 act_to_f32(uint32_t w, int fp16) { return fp16 ? act_to_f32<1>(w) : act_to_f32<0>(w); }
+__device__ __forceinline__ uint32_t f32_to_act(float lo, float hi, int fp16) {
+  return fp16 ? f32_to_act<1>(lo, hi) : f32_to_act<0>(lo, hi);
+}
+
 // The page that holds position `pos` of sequence `b`, or -1 where there is none, and the row of that position and
 // head in the page's [Hkv][page_size]; `bad` collects a status code.
 __device__ __forceinline__ int cache_page(const CachePools& c, const CacheTable& pt, int b, long long pos, int h,

@@ -36,11 +36,14 @@
 // that covers part of it writes (O, log-sum-exp) to the workspace, two slots per block at most, and a second
 // kernel joins them in order.
 #include <atomic>
+#include <cooperative_groups.h>
 
 #include "cache.cuh"
 
 namespace bsc {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int KT = 32, WARPS = 4, CHUNK = KT * WARPS, THREADS = WARPS * 32;
 constexpr int SMS = 152;
@@ -67,7 +70,8 @@ struct Cfg {
   static constexpr int QF = QS ? NT * KS * 32 * 8 : 0;
   static constexpr int QBYTES = QS ? QF + ROWS * 8 : 0;
   static constexpr int MERGE = WARPS * ROWS * (D + 4) * 4 + WARPS * ROWS * 8;
-  static constexpr int SMEM = RING + QBYTES > MERGE ? RING + QBYTES : MERGE;
+  static constexpr int JOINED = MERGE + ROWS * D * 4 + ROWS * 8;   // and the block's own part, in the cluster form
+  static constexpr int SMEM = RING + QBYTES > JOINED ? RING + QBYTES : JOINED;
   static constexpr int OCC = NT == 1 ? (STAGE * STAGES * WARPS > 56 * 1024 ? 3 : 4) : 2;   // blocks per SM
 };
 
@@ -241,8 +245,10 @@ struct Share {
 template <class C, int D>
 constexpr int slot_floats() { return C::ROWS * (D + 1); }
 
-template <int FMT, int D, int DT, int NT>
-__global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kernel(const CacheAttnArgs a, int row_tiles) {
+template <int FMT, int D, int NT, bool CLUSTER>
+__global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kernel(const CacheAttnArgs a, int row_tiles,
+                                                                                    int cluster_blocks) {
+  const int cs = CLUSTER ? cluster_blocks : 0;
   using C = Cfg<FMT, D, NT>;
   constexpr int RB = C::RB, NB = C::NB;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -250,13 +256,18 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
   const int G = a.Hq / a.c.Hkv, U = a.c.Hkv * row_tiles, page_size = a.c.page_size;
   const int R = a.T * G;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  uint32_t base;
-  const Share share(chunks_of_all(a, U, 0, base), gridDim.x);
-  if (blockIdx.x >= share.n) return;
-  uint32_t x = share.first(blockIdx.x);
-  const uint32_t x_end = share.first(blockIdx.x + 1);
-  int b = seq_of_chunk(a, x, U, base);
+  // List form (cs = 0): this block's run of the list.  Cluster form: unit blockIdx.x / cs, every cs-th chunk.
+  uint32_t base = 0, x = 0, x_end = 1;
+  const int unit = cs ? blockIdx.x / cs : 0, rank = cs ? blockIdx.x - unit * cs : 0;
+  int b = cs ? unit / U : 0;
+  if (cs == 0) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Share share(chunks_of_all(a, U, 0, base), gridDim.x);
+    if (blockIdx.x >= share.n) return;
+    x = share.first(blockIdx.x);
+    x_end = share.first(blockIdx.x + 1);
+    b = seq_of_chunk(a, x, U, base);
+  }
 
   // ---- what a lane's place fixes ----
   uint8_t* const ring = smem + warp * C::STAGES * C::STAGE;
@@ -280,14 +291,19 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
   const uint32_t sc_to = 2 * KT * RB + (sc_v ? KT * NB : 0) + sc_p * 16;
 
   while (x < x_end) {
-    // ---- the next piece: chunks [c0, c1) of unit (b, h, rt) ----
+    // ---- the next piece: chunks c0, c0 + step, ... (count of them) of unit (b, h, rt) ----
     const int len = seq_len(a, b), n_chunks = (len + CHUNK - 1) / CHUNK;
-    if (n_chunks == 0) {
-      ++b;
-      continue;
+    int u = unit - b * U, c0 = rank, count = n_chunks > rank ? (n_chunks - rank + cs - 1) / max(cs, 1) : 0;
+    const int step = cs ? cs : 1;
+    if (cs == 0) {
+      if (n_chunks == 0) {
+        ++b;
+        continue;
+      }
+      u = (int)((x - base) / (uint32_t)n_chunks);
+      c0 = (int)(x - base) - u * n_chunks;
+      count = min(n_chunks - c0, (int)(x_end - x));
     }
-    const int u = (int)((x - base) / (uint32_t)n_chunks), c0 = (int)(x - base) - u * n_chunks;
-    const int c1 = min(n_chunks, c0 + (int)(x_end - x));
     const int h = u / row_tiles, rt = u - h * row_tiles;
     const int raw_len = max(__ldg(a.pt.seq_lens + b), 0);
     const int n_new = a.new_lens ? min(max(__ldg(a.new_lens + b), 0), a.T) : a.T;
@@ -307,10 +323,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
         q_in[nt][i] = r < R ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
     }
 
-    // ---- the warp's tiles: keys (c0 + i) CHUNK + warp KT + [0, KT) ----
-    const int k_first = c0 * CHUNK + warp * KT;
-    const int last = min(c1 * CHUNK, len);
-    const int n_tiles = k_first < last ? (last - k_first + CHUNK - 1) / CHUNK : 0;
+    // ---- the warp's tiles: keys (c0 + i step) CHUNK + warp KT + [0, KT); only the last can be past the end ----
+    const int k_first = c0 * CHUNK + warp * KT, k_step = step * CHUNK;
+    const int n_tiles = count - (count > 0 && k_first + (count - 1) * k_step >= len);
 
     // page ids: lane 2 i + j has the 16-key group j of tile (window start) + i, for 16 tiles at a time
     int w_page = -1;
@@ -321,7 +336,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
       uint32_t bits = 0;
       if (tile < n_tiles) {
         if ((tile & 15) == 0) {
-          const int i = tile + (lane >> 1), key = k_first + i * CHUNK + (lane & 1) * 16;
+          const int i = tile + (lane >> 1), key = k_first + i * k_step + (lane & 1) * 16;
           w_page = -1;
           if (i < n_tiles && key < len) {
             const int lp = key / page_size;
@@ -385,8 +400,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
     int lim_own[NQ][2];        // keys j < lim are visible; rows that see nothing or do not exist: all
     int min_lim = len;
     uint2* const qs = reinterpret_cast<uint2*>(smem + C::RING);
-    float* const cs = reinterpret_cast<float*>(smem + C::RING + C::QF);
-    int* const lims = reinterpret_cast<int*>(cs + C::ROWS);
+    float* const c_all = reinterpret_cast<float*>(smem + C::RING + C::QF);
+    int* const lims = reinterpret_cast<int*>(c_all + C::ROWS);
 #pragma unroll
     for (int nt = 0; nt < NQ; ++nt) {
       const int r = rt * C::ROWS + (nt0 + nt) * 8 + g, tq = r / G;
@@ -397,7 +412,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
         const uint32_t w[4] = {q_in[nt][i].x, q_in[nt][i].y, q_in[nt][i].z, q_in[nt][i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 p = act_to_f32<DT>(w[j]);
+          const float2 p = act_to_f32(w[j], a.fp16);
           f[8 * i + 2 * j] = p.x;
           f[8 * i + 2 * j + 1] = p.y;
         }
@@ -427,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 #pragma unroll
         for (int i = 0; i < C::KS; ++i) qs[((nt0 + nt) * C::KS + i) * 32 + lane] = make_uint2(q[nt][i][0], q[nt][i][1]);
         if (t == 0) {
-          cs[(nt0 + nt) * 8 + g] = cg;
+          c_all[(nt0 + nt) * 8 + g] = cg;
           lims[(nt0 + nt) * 8 + g] = lg;
         }
       } else {
@@ -447,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
     auto q_frag = [&](int nt, int i) {
       return C::QS ? qs[(nt * C::KS + i) * 32 + lane] : make_uint2(q[C::QS ? 0 : nt][i][0], q[C::QS ? 0 : nt][i][1]);
     };
-    auto c_of = [&](int nt, int j) { return C::QS ? cs[nt * 8 + 2 * t + j] : c_own[C::QS ? 0 : nt][j]; };
+    auto c_of = [&](int nt, int j) { return C::QS ? c_all[nt * 8 + 2 * t + j] : c_own[C::QS ? 0 : nt][j]; };
     auto lim_of = [&](int nt, int j) { return C::QS ? lims[nt * 8 + 2 * t + j] : lim_own[C::QS ? 0 : nt][j]; };
 
     float acc[NT][C::MT][4], l[NT][2], ref[NT][2];   // weights are 2^(c s + ref)
@@ -469,7 +484,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
       uint8_t* const vrows = stage + KT * RB;
       uint8_t* const ksc = stage + 2 * KT * RB;
       uint8_t* const vsc = ksc + KT * NB;
-      const int k0 = k_first + tile * CHUNK;
+      const int k0 = k_first + tile * k_step;
 
       // ---- which keys the matrix path leaves out: `gone` (past the sequence, no page), `odd` (scales) ----
       const int valid = len - k0;
@@ -772,10 +787,35 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
         for (int i = 0; i < C::MT; ++i) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[nt][i][j], acc[nt][i][2 + j]);
       }
     __syncthreads();
-    const bool whole = c0 == 0 && c1 == n_chunks;
+    const bool whole = cs == 1 || (cs == 0 && count == n_chunks);
     float* const slot = reinterpret_cast<float*>(a.ws) +
                         (2LL * blockIdx.x + (c0 == 0)) * slot_floats<C, D>();
     constexpr int LPR = D / 8;                 // threads per row, 8 columns each
+    float* const co = reinterpret_cast<float*>(smem + C::MERGE);        // cluster form: [row][D], then (ref, sum) by row
+    float2* const cl = reinterpret_cast<float2*>(co + C::ROWS * D);
+    // Eight columns of a row from the weighted sum o, the sum of weights and their reference: O and its log-sum-exp
+    // where the unit is complete, a part of it to the workspace otherwise.
+    auto emit = [&](int row, int d, float (&o)[8], float mx, float sum) {
+      const int r = rt * C::ROWS + row, tq = r / G;
+      const bool sees = tq < n_new && (long long)raw_len - n_new + tq >= 0;
+      const bool none = !sees || sum == 0.f;
+      const float inv = none ? 0.f : __fdividef(1.f, sum) * (1.f / (1 << C::OFF));
+      const float z = none ? -INFINITY : mx + __log2f(sum);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = none ? 0.f : o[j] * inv;
+      if (whole || cs) {
+        const int hq = h * G + r - tq * G;
+        uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + b * a.os.b + tq * a.os.t + hq * a.os.h + d;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(f32_to_act(o[0], o[1], a.fp16), f32_to_act(o[2], o[3], a.fp16),
+                                                    f32_to_act(o[4], o[5], a.fp16), f32_to_act(o[6], o[7], a.fp16));
+        if (d == 0 && a.lse) a.lse[((long long)b * a.Hq + hq) * a.T + tq] = z * 0.6931471805599453f;
+      } else {
+        float4* dst = reinterpret_cast<float4*>(slot + row * D + d);
+        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+        if (d == 0) slot[C::ROWS * D + row] = z;
+      }
+    };
     for (int i = tid; i < C::ROWS * LPR; i += THREADS) {
       const int row = i / LPR, d = (i % LPR) * 8, r = rt * C::ROWS + row;
       if (r >= R) continue;
@@ -793,29 +833,43 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
         o[0] += f * y0.x; o[1] += f * y0.y; o[2] += f * y0.z; o[3] += f * y0.w;
         o[4] += f * y1.x; o[5] += f * y1.y; o[6] += f * y1.z; o[7] += f * y1.w;
       }
-      const int tq = r / G;
-      const bool sees = tq < n_new && (long long)raw_len - n_new + tq >= 0;
-      const bool none = !sees || sum == 0.f;
-      const float inv = none ? 0.f : __fdividef(1.f, sum) * (1.f / (1 << C::OFF));
-      const float z = none ? -INFINITY : mx + __log2f(sum);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = none ? 0.f : o[j] * inv;
-      if (whole) {
-        const int hq = h * G + r - tq * G;
-        uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + b * a.os.b + tq * a.os.t + hq * a.os.h + d;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(f32_to_act<DT>(o[0], o[1]), f32_to_act<DT>(o[2], o[3]),
-                                                    f32_to_act<DT>(o[4], o[5]), f32_to_act<DT>(o[6], o[7]));
-        if (d == 0 && a.lse) a.lse[((long long)b * a.Hq + hq) * a.T + tq] = z * 0.6931471805599453f;
-      } else {
-        float4* dst = reinterpret_cast<float4*>(slot + row * D + d);
+      if (cs > 1) {                            // this block's part, for the cluster
+        float4* const dst = reinterpret_cast<float4*>(co + row * D + d);
         dst[0] = make_float4(o[0], o[1], o[2], o[3]);
         dst[1] = make_float4(o[4], o[5], o[6], o[7]);
-        if (d == 0) slot[C::ROWS * D + row] = z;
+        if (d == 0) cl[row] = make_float2(mx, sum);
+      } else {
+        emit(row, d, o, mx, sum);
       }
     }
+    if constexpr (CLUSTER) if (cs > 1) {
+      // ---- the cluster's parts, each block taking every cs-th row from all blocks' shared memory ----
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.sync();
+      for (int i = tid; i < C::ROWS * LPR; i += THREADS) {
+        const int row = i / LPR, d = (i % LPR) * 8;
+        if (row % cs != rank || rt * C::ROWS + row >= R) continue;
+        float mx = -UNSET;
+        for (int w = 0; w < cs; ++w) mx = fmaxf(mx, cluster.map_shared_rank(cl, w)[row].x);
+        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll 4
+        for (int w = 0; w < cs; ++w) {
+          const float2 part = cluster.map_shared_rank(cl, w)[row];
+          const float f = ex2_approx(part.x - mx);
+          sum += f * part.y;
+          const float4* src = reinterpret_cast<const float4*>(cluster.map_shared_rank(co, w) + row * D + d);
+          const float4 y0 = src[0], y1 = src[1];
+          o[0] += f * y0.x; o[1] += f * y0.y; o[2] += f * y0.z; o[3] += f * y0.w;
+          o[4] += f * y1.x; o[5] += f * y1.y; o[6] += f * y1.z; o[7] += f * y1.w;
+        }
+        emit(row, d, o, mx, sum);
+      }
+      cluster.sync();                          // no block leaves while another reads its memory
+    }
+    if (CLUSTER) return;
     __syncthreads();
 
-    x += c1 - c0;
+    x += count;
     if (x == base + (uint32_t)n_chunks * U) {
       base = x;
       ++b;
@@ -830,7 +884,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 // number of parts.  It is launched while the first kernel still runs (programmatic dependence) and waits for
 // it before it touches the workspace or O.
 constexpr int JOIN_WARPS = 16;
-template <int D, int DT, int NT>
+template <int D, int NT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const CacheAttnArgs a, int row_tiles, int grid,
                                                                           int rows_pb) {
   constexpr int ROWS = 8 * NT, SLOT = ROWS * (D + 1), PL = D / 32;    // columns per lane
@@ -912,14 +966,28 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
   const float inv = 1.f / sum;
   uint32_t w[PL / 2];
 #pragma unroll
-  for (int j = 0; j < PL / 2; ++j) w[j] = none ? 0u : f32_to_act<DT>(o[2 * j] * inv, o[2 * j + 1] * inv);
+  for (int j = 0; j < PL / 2; ++j) w[j] = none ? 0u : f32_to_act(o[2 * j] * inv, o[2 * j + 1] * inv, a.fp16);
   if (PL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[PL / 2 - 1]);
   else *reinterpret_cast<uint32_t*>(dst) = w[0];
   if (lane == 0 && a.lse)
     a.lse[((long long)b * a.Hq + hq) * a.T + tq] = none ? -INFINITY : (m + __log2f(sum)) * 0.6931471805599453f;
 }
 
-template <int FMT, int D, int DT, int NT>
+// Short tables: a cluster of this many blocks per unit (1: a block), or 0 for the list.  A cluster joins its parts
+// through shared memory: one launch, no workspace.  But a unit then has 8 blocks at most, whatever the others'
+// lengths, so it is taken only where the longest sequence that the table allows is MOST_CLUSTER_CHUNKS chunks per
+// block.
+constexpr int MOST_CLUSTER_CHUNKS = 6;
+int tile_rows(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+int cluster_size(long long B, long long rows, int Hkv, long long max_tokens) {
+  const int tile = tile_rows(rows), occ = tile == 8 ? 4 : 2;
+  const long long units = B * Hkv * ((rows + tile - 1) / tile), chunks = (max_tokens + CHUNK - 1) / CHUNK;
+  int cs = 1;
+  while (cs < 8 && cs < chunks && units * cs * 2 <= SMS * occ) cs *= 2;
+  return chunks <= (long long)cs * MOST_CLUSTER_CHUNKS ? cs : 0;
+}
+
+template <int FMT, int D, int NT>
 cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   using C = Cfg<FMT, D, NT>;
   static_assert(C::OCC <= (NT == 1 ? 4 : 2), "the join's table of parts, and the workspace");
@@ -927,58 +995,69 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   const long long units = (long long)a.B * a.c.Hkv * row_tiles;
   const long long chunks = ((long long)a.pt.max_pages * a.c.page_size + CHUNK - 1) / CHUNK;
   if (units * chunks >= (1LL << 31) || units * C::ROWS >= (1LL << 31)) return cudaErrorNotSupported;
-  const long long grid = units * chunks < SMS * C::OCC ? units * chunks : SMS * C::OCC;
-  if (grid > 0) {
-    auto kernel = cache_attn_kernel<FMT, D, DT, NT>;
-    // the opt-in to more than 48 KB of shared memory, once per device
+  {  // the opt-in to more than 48 KB of shared memory, once per device
     static std::atomic<uint64_t> opted{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (!((opted.load(std::memory_order_relaxed) >> dev) & 1)) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+      e = cudaFuncSetAttribute(cache_attn_kernel<FMT, D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(cache_attn_kernel<FMT, D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
       if (e != cudaSuccess) return e;
       opted.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    kernel<<<(unsigned)grid, THREADS, C::SMEM, st>>>(a, row_tiles);
-    e = cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  cfg.stream = st;
+  cfg.attrs = attr;
+  if (const int cs = cluster_size(a.B, rows, a.c.Hkv, (long long)a.pt.max_pages * a.c.page_size)) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cs;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(units * cs));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.numAttrs = cs > 1;
+    return cudaLaunchKernelEx(&cfg, cache_attn_kernel<FMT, D, NT, true>, a, row_tiles, cs);
+  }
+  const long long grid = units * chunks < SMS * C::OCC ? units * chunks : SMS * C::OCC;
+  if (grid > 0) {
+    cache_attn_kernel<FMT, D, NT, false><<<(unsigned)grid, THREADS, C::SMEM, st>>>(a, row_tiles, 0);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   // few units have many parts each: as many blocks per unit as the card takes at once
   int rows_pb = C::ROWS < JOIN_WARPS ? C::ROWS : JOIN_WARPS;
   while (rows_pb > 1 && units * (C::ROWS / rows_pb) * 2 <= SMS * 2) rows_pb /= 2;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)(units * (C::ROWS / rows_pb)));
   cfg.blockDim = dim3(JOIN_WARPS * 32);
-  cfg.stream = st;
-  cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, DT, NT>, a, row_tiles, (int)grid, rows_pb);
+  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, NT>, a, row_tiles, (int)grid, rows_pb);
 }
 
-template <int FMT, int D, int DT>
+template <int FMT, int D>
 cudaError_t pick(const CacheAttnArgs& a, cudaStream_t st) {
-  const int rows = a.T * (a.Hq / a.c.Hkv);
-  return rows <= 8 ? launch<FMT, D, DT, 1>(a, st) : rows <= 16 ? launch<FMT, D, DT, 2>(a, st) : launch<FMT, D, DT, 4>(a, st);
+  const int tile = tile_rows(a.T * (a.Hq / a.c.Hkv));
+  return tile == 8 ? launch<FMT, D, 1>(a, st) : tile == 16 ? launch<FMT, D, 2>(a, st) : launch<FMT, D, 4>(a, st);
 }
 
 }  // namespace
 
-size_t cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
+size_t cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long long max_tokens) {
+  const long long all = (long long)T * (Hq / Hkv);
+  if (all <= 0 || cluster_size(B, all, Hkv, max_tokens)) return 0;
   // two slots per block of the largest grid of either format
-  const long long all = (long long)T * ((Hq + Hkv - 1) / Hkv), rows = all <= 8 ? 8 : all <= 16 ? 16 : 32;
-  const int occ = rows == 8 ? 4 : 2;
+  const int rows = tile_rows(all), occ = rows == 8 ? 4 : 2;
   return (size_t)2 * SMS * occ * rows * (D + 1) * 4;
 }
 
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, int format, int D, int dtype, cudaStream_t st) {
-  using F = cudaError_t (*)(const CacheAttnArgs&, cudaStream_t);
-  static const F f[8] = {pick<0, 64, 0>, pick<0, 64, 1>, pick<0, 128, 0>, pick<0, 128, 1>,
-                         pick<1, 64, 0>, pick<1, 64, 1>, pick<1, 128, 0>, pick<1, 128, 1>};
-  return f[format * 4 + (D == 128) * 2 + dtype](a, st);
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, int format, int D, cudaStream_t st) {
+  if (format == CACHE_FP4) return D == 128 ? pick<CACHE_FP4, 128>(a, st) : pick<CACHE_FP4, 64>(a, st);
+  return D == 128 ? pick<CACHE_FP8, 128>(a, st) : pick<CACHE_FP8, 64>(a, st);
 }
 
 }  // namespace bsc

@@ -402,9 +402,10 @@ typedef struct {
  */
 bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream);
 
-/* Bytes of workspace mx_cache_attn needs at these sizes (whatever the lengths are); 0 if a size is
- * not positive.  Host only, no CUDA call. */
-size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+/* Bytes of workspace mx_cache_attn needs at these sizes, whatever the lengths are; max_tokens =
+ * max_pages * page_size.  0 where it needs none (short tables; then workspace may be NULL) and if a
+ * size is not positive.  Host only, no CUDA call. */
+size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long long max_tokens);
 
 /*
  * Synchronises `stream`, reads the int32 at `dev_status` and returns BSC_OK (0),

@@ -176,7 +176,9 @@ def test_read_refusals(ops, pool, kw, want):
     ({}, dict(q=0), 1), ({}, dict(o=0), 1), ({}, dict(o=FAKE + 8), 3), ({}, dict(lse=FAKE + 2), 3),
     ({}, dict(Hq=6), 2), ({}, dict(Hq=-8), 2), ({}, dict(Hq=0), 0), ({}, dict(softmax_scale=0.0), 4),
     ({}, dict(softmax_scale=float("nan")), 4), ({}, dict(softmax_scale=-1.0), 4), ({}, dict(q_stride_t=516), 3),
-    ({}, dict(o_stride_h=0), 2), ({}, dict(workspace=FAKE + 8), 3), ({}, dict(new_lens=FAKE + 2), 3)])
+    ({}, dict(o_stride_h=0), 2), ({}, dict(workspace=FAKE + 8), 3), ({}, dict(new_lens=FAKE + 2), 3),
+    ({}, dict(max_pages=1 << 16, table_stride=1 << 16, workspace=0), 1),
+    ({}, dict(max_pages=1 << 16, table_stride=1 << 16, workspace_bytes=1 << 16), 2)])
 def test_attn_refusals(ops, pool, kw, want):
     base = dict(q=FAKE, o=FAKE, lse=FAKE, B=2, T=4, Hq=8, dtype=0, softmax_scale=0.088, page_table=FAKE,
                 table_stride=32, max_pages=32, seq_lens=FAKE, new_lens=FAKE, dev_status=FAKE, workspace=FAKE,
@@ -194,6 +196,11 @@ def test_null_params_and_status(ops):
 def test_workspace_bytes(ops):
     for bad in ((0, 1, 8, 4, 128), (1, 0, 8, 4, 128), (1, 1, 0, 4, 128), (1, 1, 8, 0, 128), (1, 1, 8, 4, 0)):
         assert ops.mx_cache_attn_workspace_bytes(*bad) == 0
+    # short tables need none; long ones the same whatever their length, two slots of fp32 rows per block
+    assert ops.mx_cache_attn_workspace_bytes(1, 1, 8, 4, 128, 1024) == 0
+    assert ops.mx_cache_attn_workspace_bytes(1, 1, 8, 4, 128, 1 << 20) == 2 * 608 * 8 * 129 * 4
+    assert ops.mx_cache_attn_workspace_bytes(8, 4, 8, 2, 64, 1 << 17) == 2 * 304 * 16 * 65 * 4
+    assert ops.mx_cache_attn_workspace_bytes(8, 40, 8, 2, 64) == 2 * 304 * 32 * 65 * 4
 
 
 def test_binding_refuses_cpu_pools(ops):

@@ -21,6 +21,15 @@ def ops():
     return _binding
 
 
+@pytest.fixture(autouse=True, params=[0, 8192], ids=["short", "wide"])
+def table_width(request):
+    """Every test twice: page tables just wide enough (the attention's cluster form) and 8192 tokens wider
+    (its list form, with parts joined through the workspace)."""
+    Filled.more = request.param
+    yield
+    Filled.more = 0
+
+
 def f64(x):
     return x.detach().cpu().double().numpy()
 
@@ -50,6 +59,7 @@ def garbage_cache(ops, rng, pages, page, Hkv, D, fmt, gap=0):
 
 class Filled:
     """Sequences of the given lengths in a cache of garbage, bytes by the oracle's quantiser."""
+    more = 0
 
     def __init__(self, ops, seed, lens, Hkv, D, fmt, page, v_mult=None, k_mult=1.0, gap=0):
         rng = np.random.default_rng(seed)
@@ -58,7 +68,7 @@ class Filled:
         pages = len(lens) * width + 2
         self.cache, self.whole = garbage_cache(ops, rng, pages, page, Hkv, D, fmt, gap)
         perm = rng.permutation(pages)
-        table = np.full((len(lens), width), -7, np.int32)          # entries that must not be read
+        table = np.full((len(lens), width + Filled.more // page), -7, np.int32)    # entries that must not be read
         host = [p.cpu().numpy().copy() for p in (self.cache.k, self.cache.k_sc, self.cache.v, self.cache.v_sc)]
         self.K, self.V = [], []
         for b, n in enumerate(lens):
@@ -114,6 +124,10 @@ def check_attn(f, q, o, lse, new, scale, layout, absent=None, cols=None):
         assert np.array_equal(none, np.isneginf(L[b])) and np.all(ob[b][none.T] == 0)
         err = np.abs(np.where(none, 0, L[b]) - np.where(none, 0, ref))
         assert np.all(err <= tol_l), (b, err.max())
+
+
+def widened(table, page):
+    return torch.nn.functional.pad(table, (0, Filled.more // page), value=-7)
 
 
 def make_q(seed, B, T, Hq, D, dtype, layout, mult=1.0):
@@ -515,7 +529,7 @@ def test_prompt_then_decode(ops, fmt):
     q = rand_act(rng, (B, total, Hq, D), "bf16").cuda()
     k, v = (rand_act(rng, (B, total, Hkv, D), "bf16").cuda() for _ in range(2))
     cache = ops.mx_cache_alloc(B * 5, page, Hkv, D, fmt)
-    table = torch.tensor(rng.permutation(B * 5).reshape(B, 5), dtype=torch.int32).cuda()
+    table = widened(torch.tensor(rng.permutation(B * 5).reshape(B, 5), dtype=torch.int32).cuda(), page)
     ops.forward(q[:, :S].contiguous(), k[:, :S].contiguous(), v[:, :S].contiguous())
     ops.mx_cache_write(cache, k[:, :S], v[:, :S], table, i32([S] * B))
     f = type("F", (), {})()
@@ -539,7 +553,7 @@ def test_one_decode_step_in_a_graph(ops):
     rng = np.random.default_rng(78)
     B, Hq, Hkv, D = 2, 8, 2, 128
     cache = ops.mx_cache_alloc(2 * 3, 16, Hkv, D, 1)
-    table = torch.tensor(rng.permutation(6).reshape(2, 3), dtype=torch.int32).cuda()
+    table = widened(torch.tensor(rng.permutation(6).reshape(2, 3), dtype=torch.int32).cuda(), 16)
     q, k, v = (rand_act(rng, (40, B, h, D), "bf16").cuda() for h in (Hq, Hkv, Hkv))
     lens = i32([0, 0])
     sq, sk, sv = (x[:1].transpose(0, 1).clone() for x in (q, k, v))
