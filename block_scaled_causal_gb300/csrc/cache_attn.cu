@@ -245,6 +245,292 @@ struct Share {
 template <class C, int D>
 constexpr int slot_floats() { return C::ROWS * (D + 1); }
 
+// A lane's place in a tile's rows: offsets in a stage of its K run, its V runs (keys t and t + 4), its scales.
+struct Place {
+  int lane, g, t, ko, vo0, vo4, kso, vso;
+};
+// One tile of 32 keys: scores, weights, and both products into acc, l and the references.  SPECIAL: some keys
+// are left out (`gone`), need the scalar path (`odd`) or are hidden from some row; a plain tile's code has none of
+// that.  Both add the same things in the same order for the keys that a row sees.
+template <int FMT, int D, int NT, bool SPECIAL, class QFrag, class COf, class LimOf>
+__device__ __forceinline__ void tile_work(uint8_t* const stage, const int k0, const uint32_t gone, const uint32_t odd,
+                                          const Place& at, float (&acc)[NT][D / 16][4], float (&l)[NT][2],
+                                          float (&ref)[NT][2], QFrag q_frag, COf c_of, LimOf lim_of) {
+  using C = Cfg<FMT, D, NT>;
+  constexpr int RB = C::RB, NB = C::NB;
+  constexpr int LB = C::KE * RB / D, VB = C::VE * RB / D;   // bytes of a lane's K run and of its V run
+  const int lane = at.lane, g = at.g, t = at.t, ko = at.ko, vo0 = at.vo0, vo4 = at.vo4, kso = at.kso, vso = at.vso;
+  uint8_t* const vrows = stage + KT * RB;
+  uint8_t* const ksc = stage + 2 * KT * RB;
+  uint8_t* const vsc = ksc + KT * NB;
+  const uint32_t left_out = gone | odd;
+
+  // ---- scores ----
+  float s[NT][2][4];
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    const uint32_t sa = scale_f16<C>(stage[kso + mt * 16 * NB]), sb = scale_f16<C>(stage[kso + (mt * 16 + 8) * NB]);
+    const uint8_t* const ra = stage + ko + mt * 16 * RB;
+    const uint8_t* const rb = ra + 8 * RB;
+    uint32_t wa[LB / 4], wb[LB / 4];
+    if (LB == 8) {
+      const uint2 ua = *reinterpret_cast<const uint2*>(ra), ub = *reinterpret_cast<const uint2*>(rb);
+      wa[0] = ua.x; wa[1] = ua.y; wb[0] = ub.x; wb[1] = ub.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < LB / 16; ++i) {   // the run's second piece is the first's neighbour: bit 4 of the offset
+        const int flip = i ? ((ko & 16) ? -16 : 16) : 0;
+        const uint4 ua = *reinterpret_cast<const uint4*>(ra + flip), ub = *reinterpret_cast<const uint4*>(rb + flip);
+        wa[4 * i] = ua.x; wa[4 * i + 1] = ua.y; wa[4 * i + 2] = ua.z; wa[4 * i + 3] = ua.w;
+        wb[4 * i] = ub.x; wb[4 * i + 1] = ub.y; wb[4 * i + 2] = ub.z; wb[4 * i + 3] = ub.w;
+      }
+    }
+    if (FMT == CACHE_FP4) {
+#pragma unroll
+      for (int i = 0; i < LB / 4; ++i) {
+        uint32_t ha[4], hb[4];
+        e2m1x8_to_f16(wa[i], ha);
+        e2m1x8_to_f16(wb[i], hb);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t a0 = mul_f16x2(ha[2 * j], sa), a1 = mul_f16x2(hb[2 * j], sb);
+          const uint32_t a2 = mul_f16x2(ha[2 * j + 1], sa), a3 = mul_f16x2(hb[2 * j + 1], sb);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 qb = q_frag(nt, 2 * i + j);
+            if (2 * i + j == 0) mma_f16_first(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
+            else mma_f16(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < LB / 4; ++i) {
+        uint32_t ha[2], hb[2];
+        e4m3x4_to_f16(wa[i], ha[0], ha[1]);
+        e4m3x4_to_f16(wb[i], hb[0], hb[1]);
+        const uint32_t a0 = mul_f16x2(ha[0], sa), a1 = mul_f16x2(hb[0], sb);
+        const uint32_t a2 = mul_f16x2(ha[1], sa), a3 = mul_f16x2(hb[1], sb);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 qb = q_frag(nt, i);
+          if (i == 0) mma_f16_first(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
+          else mma_f16(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
+        }
+      }
+    }
+  }
+
+  // ---- scores of the odd keys, one at a time in fp32; then the masks ----
+  if constexpr (SPECIAL) for (uint32_t rest = odd; rest; rest &= rest - 1) {
+    const int k = __ffs(rest) - 1;
+    float dot[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) dot[nt] = 0.f;
+    const float sc = scale_value(ksc[k * NB + t * C::KE / 32]);
+#pragma unroll
+    for (int w = 0; w < LB / 4; ++w) {
+      constexpr int PW = FMT == CACHE_FP4 ? 2 : 1;      // k-steps per word
+      float e[4 * PW];
+      word_values<FMT, C>(stage, k, t * LB + 4 * w, sc, e);
+#pragma unroll
+      for (int j = 0; j < PW; ++j)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 qf = q_frag(nt, w * PW + j);
+          const float2 qa = f16x2_to_f32(qf.x), qb = f16x2_to_f32(qf.y);
+          dot[nt] += qa.x * e[4 * j] + qa.y * e[4 * j + 1] + qb.x * e[4 * j + 2] + qb.y * e[4 * j + 3];
+        }
+      in_order();
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      dot[nt] += __shfl_xor_sync(0xFFFFFFFFu, dot[nt], 1);
+      dot[nt] += __shfl_xor_sync(0xFFFFFFFFu, dot[nt], 2);
+      const float s0 = __shfl_sync(0xFFFFFFFFu, dot[nt], 8 * t), s1 = __shfl_sync(0xFFFFFFFFu, dot[nt], 8 * t + 4);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          if (k == mt * 16 + half * 8 + key_of_row(g)) {
+            s[nt][mt][2 * half] = s0;
+            s[nt][mt][2 * half + 1] = s1;
+          }
+    }
+  }
+  if constexpr (SPECIAL) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int k = mt * 16 + half * 8 + key_of_row(g);
+        const bool away = (gone >> k) & 1u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (away || k0 + k >= lim_of(nt, j)) s[nt][mt][2 * half + j] = -INFINITY;
+      }
+  }
+
+  // ---- the reference: moved for a row when one of its own scores is SLACK above it ----
+  float top[NT][2];
+  bool climb = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      top[nt][j] = c_of(nt, j) * fmaxf(fmaxf(s[nt][0][j], s[nt][0][2 + j]), fmaxf(s[nt][1][j], s[nt][1][2 + j]));
+      climb |= top[nt][j] + ref[nt][j] > LIFT + SLACK;
+    }
+  if (__any_sync(0xFFFFFFFFu, climb)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float mx = top[nt][j];
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+        if (mx + ref[nt][j] > LIFT + SLACK) {
+          const float keep = ex2_approx((LIFT - mx) - ref[nt][j]);   // 0 from UNSET
+          ref[nt][j] = LIFT - mx;
+          l[nt][j] *= keep;
+#pragma unroll
+          for (int i = 0; i < C::MT; ++i) {
+            acc[nt][i][j] *= keep;
+            acc[nt][i][2 + j] *= keep;
+          }
+        }
+      }
+  }
+
+  // ---- weights ----
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[nt][mt][i] = ex2_approx(fmaf(s[nt][mt][i], c_of(nt, i & 1), ref[nt][i & 1]));
+        l[nt][i & 1] += s[nt][mt][i];
+      }
+
+  // ---- odd keys' part of O in fp32, only for rows that see them; then they and absent keys become zeros ----
+  if constexpr (SPECIAL) if (left_out != 0u) {
+    for (uint32_t rest = odd; rest; rest &= rest - 1) {
+      const int k = __ffs(rest) - 1;
+      // the lane that holds key k's weights for rows 2t, 2t + 1: row r of a 16-key tile with key_of_row(r) = k % 8
+      const int src = ((k & 3) * 2 + ((k >> 2) & 1)) * 4 + t;
+      const float sc = scale_value(vsc[k * NB + g * C::VE / 32]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float p0 = __shfl_sync(0xFFFFFFFFu, s[nt][0][j], src), p1 = __shfl_sync(0xFFFFFFFFu, s[nt][0][2 + j], src);
+          const float p2 = __shfl_sync(0xFFFFFFFFu, s[nt][1][j], src), p3 = __shfl_sync(0xFFFFFFFFu, s[nt][1][2 + j], src);
+          p[j] = k < 16 ? (k < 8 ? p0 : p1) : (k < 24 ? p2 : p3);
+        }
+        const bool sees0 = k0 + k < lim_of(nt, 0), sees1 = k0 + k < lim_of(nt, 1);
+#pragma unroll
+        for (int w = 0; w < VB / 4; ++w) {
+          constexpr int PW = FMT == CACHE_FP4 ? 4 : 2;  // 16-row tiles per word
+          float e[2 * PW];
+          word_values<FMT, C>(vrows, k, g * VB + 4 * w, sc, e);
+#pragma unroll
+          for (int i = 0; i < PW; ++i) {
+            if (sees0) {
+              acc[nt][w * PW + i][0] += p[0] * e[2 * i];
+              acc[nt][w * PW + i][2] += p[0] * e[2 * i + 1];
+            }
+            if (sees1) {
+              acc[nt][w * PW + i][1] += p[1] * e[2 * i];
+              acc[nt][w * PW + i][3] += p[1] * e[2 * i + 1];
+            }
+          }
+          in_order();
+        }
+      }
+    }
+    __syncwarp();
+    if ((left_out >> lane) & 1u) {
+#pragma unroll
+      for (int i = 0; i < RB / 16; ++i)
+        *reinterpret_cast<uint4*>(vrows + piece_at<RB>(lane, i)) = make_uint4(0, 0, 0, 0);
+      if (NB == 4)
+        reinterpret_cast<uint32_t*>(vsc)[lane] = 0u;
+      else
+        reinterpret_cast<uint16_t*>(vsc)[lane] = 0;
+    }
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        if ((left_out >> (mt * 16 + half * 8 + key_of_row(g))) & 1u) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[nt][mt][2 * half] = s[nt][mt][2 * half + 1] = 0.f;
+        }
+    __syncwarp();
+  }
+
+  // ---- O^T += V^T P^T ----
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      pb[nt][0] = transpose8(pack_f16x2(s[nt][mt][0], s[nt][mt][1]));
+      pb[nt][1] = transpose8(pack_f16x2(s[nt][mt][2], s[nt][mt][3]));
+    }
+    const uint8_t* const sv = stage + vso + mt * 16 * NB;
+    const uint32_t s01 = scales_f16x2<C>(sv[0], sv[4 * NB]), s23 = scales_f16x2<C>(sv[8 * NB], sv[12 * NB]);
+    uint32_t v[4][VB / 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* src = vrows + (i & 1 ? vo4 : vo0) + (i >> 1) * 8 * RB + mt * 16 * RB;
+      if (VB == 4) {
+        v[i][0] = *reinterpret_cast<const uint32_t*>(src);
+      } else if (VB == 8) {
+        const uint2 y = *reinterpret_cast<const uint2*>(src);
+        v[i][0] = y.x; v[i][1] = y.y;
+      } else {
+        const uint4 y = *reinterpret_cast<const uint4*>(src);
+        v[i][0] = y.x; v[i][1] = y.y; v[i][2] = y.z; v[i][3] = y.w;
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < VB / 4; ++w) {
+      if (FMT == CACHE_FP4) {
+        // even elements of two keys per byte, then odd ones
+        uint32_t e01[4], o01[4], e23[4], o23[4];
+        e2m1x8_to_f16(interleave_low(v[0][w], v[1][w]), e01);
+        e2m1x8_to_f16(interleave_high(v[0][w], v[1][w]), o01);
+        e2m1x8_to_f16(interleave_low(v[2][w], v[3][w]), e23);
+        e2m1x8_to_f16(interleave_high(v[2][w], v[3][w]), o23);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a0 = mul_f16x2(e01[j], s01), a1 = mul_f16x2(o01[j], s01);
+          const uint32_t a2 = mul_f16x2(e23[j], s23), a3 = mul_f16x2(o23[j], s23);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][4 * w + j], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {      // elements 2j, 2j + 1 of both keys
+          uint32_t e01, o01, e23, o23;
+          e4m3x4_to_f16(__byte_perm(v[0][w], v[1][w], j ? 0x7362 : 0x5140), e01, o01);
+          e4m3x4_to_f16(__byte_perm(v[2][w], v[3][w], j ? 0x7362 : 0x5140), e23, o23);
+          const uint32_t a0 = mul_f16x2(e01, s01), a1 = mul_f16x2(o01, s01);
+          const uint32_t a2 = mul_f16x2(e23, s23), a3 = mul_f16x2(o23, s23);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][2 * w + j], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        }
+      }
+    }
+  }
+}
+
 template <int FMT, int D, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kernel(const CacheAttnArgs a, int row_tiles,
                                                                                     int cluster_blocks) {
@@ -276,10 +562,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
   const int to0 = piece_at<RB>(lane / PR, lane % PR), to1 = piece_at<RB>(lane / PR + RPC, lane % PR) - RPC * RB;
   constexpr int LB = C::KE * RB / D;              // bytes of a lane's K run: 8, 16 or 32
   constexpr int VB = C::VE * RB / D;              // of its V run: 4, 8 or 16
-  const int ko = piece_at<RB>(key_of_row(g), t * LB / 16) + t * LB % 16;
-  const int vo0 = piece_at<RB>(t, g * VB / 16) + g * VB % 16, vo4 = piece_at<RB>(t + 4, g * VB / 16) + g * VB % 16;
-  const int kso = 2 * KT * RB + key_of_row(g) * NB + t * C::KE / 32;
-  const int vso = 2 * KT * RB + KT * NB + t * NB + g * C::VE / 32;
+  const Place place{lane, g, t, piece_at<RB>(key_of_row(g), t * LB / 16) + t * LB % 16,
+                    piece_at<RB>(t, g * VB / 16) + g * VB % 16, piece_at<RB>(t + 4, g * VB / 16) + g * VB % 16,
+                    2 * KT * RB + key_of_row(g) * NB + t * C::KE / 32,
+                    2 * KT * RB + KT * NB + t * NB + g * C::VE / 32};
   // pages of a multiple of 32 tokens: a tile lies in one page and is copied as a whole; else 16 keys at a time
   const bool one_page = page_size % KT == 0;
   const int sc_lanes = one_page ? 2 * NB : NB;    // pieces of scales per pool and copy
@@ -481,9 +767,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 
       uint8_t* const stage = ring + st_out * C::STAGE;
       st_out = st_out + 1 == C::STAGES ? 0 : st_out + 1;
-      uint8_t* const vrows = stage + KT * RB;
-      uint8_t* const ksc = stage + 2 * KT * RB;
-      uint8_t* const vsc = ksc + KT * NB;
+      const uint8_t* const ksc = stage + 2 * KT * RB;
+      const uint8_t* const vsc = ksc + KT * NB;
       const int k0 = k_first + tile * k_step;
 
       // ---- which keys the matrix path leaves out: `gone` (past the sequence, no page), `odd` (scales) ----
@@ -499,272 +784,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
                                 (uint32_t)reinterpret_cast<const uint16_t*>(vsc)[lane] << 16);
       }
       const uint32_t odd = __ballot_sync(0xFFFFFFFFu, !ok) & ~gone;
-      const uint32_t left_out = gone | odd;
-
-      // ---- scores ----
-      float s[NT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const uint32_t sa = scale_f16<C>(stage[kso + mt * 16 * NB]), sb = scale_f16<C>(stage[kso + (mt * 16 + 8) * NB]);
-        const uint8_t* const ra = stage + ko + mt * 16 * RB;
-        const uint8_t* const rb = ra + 8 * RB;
-        uint32_t wa[LB / 4], wb[LB / 4];
-        if (LB == 8) {
-          const uint2 ua = *reinterpret_cast<const uint2*>(ra), ub = *reinterpret_cast<const uint2*>(rb);
-          wa[0] = ua.x; wa[1] = ua.y; wb[0] = ub.x; wb[1] = ub.y;
-        } else {
-#pragma unroll
-          for (int i = 0; i < LB / 16; ++i) {   // the run's second piece is the first's neighbour: bit 4 of the offset
-            const int flip = i ? ((ko & 16) ? -16 : 16) : 0;
-            const uint4 ua = *reinterpret_cast<const uint4*>(ra + flip), ub = *reinterpret_cast<const uint4*>(rb + flip);
-            wa[4 * i] = ua.x; wa[4 * i + 1] = ua.y; wa[4 * i + 2] = ua.z; wa[4 * i + 3] = ua.w;
-            wb[4 * i] = ub.x; wb[4 * i + 1] = ub.y; wb[4 * i + 2] = ub.z; wb[4 * i + 3] = ub.w;
-          }
-        }
-        if (FMT == CACHE_FP4) {
-#pragma unroll
-          for (int i = 0; i < LB / 4; ++i) {
-            uint32_t ha[4], hb[4];
-            e2m1x8_to_f16(wa[i], ha);
-            e2m1x8_to_f16(wb[i], hb);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t a0 = mul_f16x2(ha[2 * j], sa), a1 = mul_f16x2(hb[2 * j], sb);
-              const uint32_t a2 = mul_f16x2(ha[2 * j + 1], sa), a3 = mul_f16x2(hb[2 * j + 1], sb);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint2 qb = q_frag(nt, 2 * i + j);
-                if (2 * i + j == 0) mma_f16_first(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
-                else mma_f16(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
-              }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < LB / 4; ++i) {
-            uint32_t ha[2], hb[2];
-            e4m3x4_to_f16(wa[i], ha[0], ha[1]);
-            e4m3x4_to_f16(wb[i], hb[0], hb[1]);
-            const uint32_t a0 = mul_f16x2(ha[0], sa), a1 = mul_f16x2(hb[0], sb);
-            const uint32_t a2 = mul_f16x2(ha[1], sa), a3 = mul_f16x2(hb[1], sb);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 qb = q_frag(nt, i);
-              if (i == 0) mma_f16_first(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
-              else mma_f16(s[nt][mt], a0, a1, a2, a3, qb.x, qb.y);
-            }
-          }
-        }
-      }
-
-      // ---- scores of the odd keys, one at a time in fp32; then the masks ----
-      for (uint32_t rest = odd; rest; rest &= rest - 1) {
-        const int k = __ffs(rest) - 1;
-        float dot[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) dot[nt] = 0.f;
-        const float sc = scale_value(ksc[k * NB + t * C::KE / 32]);
-#pragma unroll
-        for (int w = 0; w < LB / 4; ++w) {
-          constexpr int PW = FMT == CACHE_FP4 ? 2 : 1;      // k-steps per word
-          float e[4 * PW];
-          word_values<FMT, C>(stage, k, t * LB + 4 * w, sc, e);
-#pragma unroll
-          for (int j = 0; j < PW; ++j)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 qf = q_frag(nt, w * PW + j);
-              const float2 qa = f16x2_to_f32(qf.x), qb = f16x2_to_f32(qf.y);
-              dot[nt] += qa.x * e[4 * j] + qa.y * e[4 * j + 1] + qb.x * e[4 * j + 2] + qb.y * e[4 * j + 3];
-            }
-          in_order();
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          dot[nt] += __shfl_xor_sync(0xFFFFFFFFu, dot[nt], 1);
-          dot[nt] += __shfl_xor_sync(0xFFFFFFFFu, dot[nt], 2);
-          const float s0 = __shfl_sync(0xFFFFFFFFu, dot[nt], 8 * t), s1 = __shfl_sync(0xFFFFFFFFu, dot[nt], 8 * t + 4);
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              if (k == mt * 16 + half * 8 + key_of_row(g)) {
-                s[nt][mt][2 * half] = s0;
-                s[nt][mt][2 * half + 1] = s1;
-              }
-        }
-      }
-      if (gone != 0u || k0 + KT > min_lim) {
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int k = mt * 16 + half * 8 + key_of_row(g);
-            const bool away = (gone >> k) & 1u;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                if (away || k0 + k >= lim_of(nt, j)) s[nt][mt][2 * half + j] = -INFINITY;
-          }
-      }
-
-      // ---- the reference: moved for a row when one of its own scores is SLACK above it ----
-      float top[NT][2];
-      bool climb = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          top[nt][j] = c_of(nt, j) * fmaxf(fmaxf(s[nt][0][j], s[nt][0][2 + j]), fmaxf(s[nt][1][j], s[nt][1][2 + j]));
-          climb |= top[nt][j] + ref[nt][j] > LIFT + SLACK;
-        }
-      if (__any_sync(0xFFFFFFFFu, climb)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float mx = top[nt][j];
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-            if (mx + ref[nt][j] > LIFT + SLACK) {
-              const float keep = ex2_approx((LIFT - mx) - ref[nt][j]);   // 0 from UNSET
-              ref[nt][j] = LIFT - mx;
-              l[nt][j] *= keep;
-#pragma unroll
-              for (int i = 0; i < C::MT; ++i) {
-                acc[nt][i][j] *= keep;
-                acc[nt][i][2 + j] *= keep;
-              }
-            }
-          }
-      }
-
-      // ---- weights ----
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[nt][mt][i] = ex2_approx(fmaf(s[nt][mt][i], c_of(nt, i & 1), ref[nt][i & 1]));
-            l[nt][i & 1] += s[nt][mt][i];
-          }
-
-      // ---- odd keys' part of O in fp32, only for rows that see them; then they and absent keys become zeros ----
-      if (left_out != 0u) {
-        for (uint32_t rest = odd; rest; rest &= rest - 1) {
-          const int k = __ffs(rest) - 1;
-          // the lane that holds key k's weights for rows 2t, 2t + 1: row r of a 16-key tile with key_of_row(r) = k % 8
-          const int src = ((k & 3) * 2 + ((k >> 2) & 1)) * 4 + t;
-          const float sc = scale_value(vsc[k * NB + g * C::VE / 32]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float p[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float p0 = __shfl_sync(0xFFFFFFFFu, s[nt][0][j], src), p1 = __shfl_sync(0xFFFFFFFFu, s[nt][0][2 + j], src);
-              const float p2 = __shfl_sync(0xFFFFFFFFu, s[nt][1][j], src), p3 = __shfl_sync(0xFFFFFFFFu, s[nt][1][2 + j], src);
-              p[j] = k < 16 ? (k < 8 ? p0 : p1) : (k < 24 ? p2 : p3);
-            }
-            const bool sees0 = k0 + k < lim_of(nt, 0), sees1 = k0 + k < lim_of(nt, 1);
-#pragma unroll
-            for (int w = 0; w < VB / 4; ++w) {
-              constexpr int PW = FMT == CACHE_FP4 ? 4 : 2;  // 16-row tiles per word
-              float e[2 * PW];
-              word_values<FMT, C>(vrows, k, g * VB + 4 * w, sc, e);
-#pragma unroll
-              for (int i = 0; i < PW; ++i) {
-                if (sees0) {
-                  acc[nt][w * PW + i][0] += p[0] * e[2 * i];
-                  acc[nt][w * PW + i][2] += p[0] * e[2 * i + 1];
-                }
-                if (sees1) {
-                  acc[nt][w * PW + i][1] += p[1] * e[2 * i];
-                  acc[nt][w * PW + i][3] += p[1] * e[2 * i + 1];
-                }
-              }
-              in_order();
-            }
-          }
-        }
-        __syncwarp();
-        if ((left_out >> lane) & 1u) {
-#pragma unroll
-          for (int i = 0; i < RB / 16; ++i)
-            *reinterpret_cast<uint4*>(vrows + piece_at<RB>(lane, i)) = make_uint4(0, 0, 0, 0);
-          if (NB == 4)
-            reinterpret_cast<uint32_t*>(vsc)[lane] = 0u;
-          else
-            reinterpret_cast<uint16_t*>(vsc)[lane] = 0;
-        }
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            if ((left_out >> (mt * 16 + half * 8 + key_of_row(g))) & 1u) {
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) s[nt][mt][2 * half] = s[nt][mt][2 * half + 1] = 0.f;
-            }
-        __syncwarp();
-      }
-
-      // ---- O^T += V^T P^T ----
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          pb[nt][0] = transpose8(pack_f16x2(s[nt][mt][0], s[nt][mt][1]));
-          pb[nt][1] = transpose8(pack_f16x2(s[nt][mt][2], s[nt][mt][3]));
-        }
-        const uint8_t* const sv = stage + vso + mt * 16 * NB;
-        const uint32_t s01 = scales_f16x2<C>(sv[0], sv[4 * NB]), s23 = scales_f16x2<C>(sv[8 * NB], sv[12 * NB]);
-        uint32_t v[4][VB / 4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint8_t* src = vrows + (i & 1 ? vo4 : vo0) + (i >> 1) * 8 * RB + mt * 16 * RB;
-          if (VB == 4) {
-            v[i][0] = *reinterpret_cast<const uint32_t*>(src);
-          } else if (VB == 8) {
-            const uint2 y = *reinterpret_cast<const uint2*>(src);
-            v[i][0] = y.x; v[i][1] = y.y;
-          } else {
-            const uint4 y = *reinterpret_cast<const uint4*>(src);
-            v[i][0] = y.x; v[i][1] = y.y; v[i][2] = y.z; v[i][3] = y.w;
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < VB / 4; ++w) {
-          if (FMT == CACHE_FP4) {
-            // even elements of two keys per byte, then odd ones
-            uint32_t e01[4], o01[4], e23[4], o23[4];
-            e2m1x8_to_f16(interleave_low(v[0][w], v[1][w]), e01);
-            e2m1x8_to_f16(interleave_high(v[0][w], v[1][w]), o01);
-            e2m1x8_to_f16(interleave_low(v[2][w], v[3][w]), e23);
-            e2m1x8_to_f16(interleave_high(v[2][w], v[3][w]), o23);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t a0 = mul_f16x2(e01[j], s01), a1 = mul_f16x2(o01[j], s01);
-              const uint32_t a2 = mul_f16x2(e23[j], s23), a3 = mul_f16x2(o23[j], s23);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][4 * w + j], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {      // elements 2j, 2j + 1 of both keys
-              uint32_t e01, o01, e23, o23;
-              e4m3x4_to_f16(__byte_perm(v[0][w], v[1][w], j ? 0x7362 : 0x5140), e01, o01);
-              e4m3x4_to_f16(__byte_perm(v[2][w], v[3][w], j ? 0x7362 : 0x5140), e23, o23);
-              const uint32_t a0 = mul_f16x2(e01, s01), a1 = mul_f16x2(o01, s01);
-              const uint32_t a2 = mul_f16x2(e23, s23), a3 = mul_f16x2(o23, s23);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][2 * w + j], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-            }
-          }
-        }
-      }
+      if ((gone | odd) != 0u || k0 + KT > min_lim)
+        tile_work<FMT, D, NT, true>(stage, k0, gone, odd, place, acc, l, ref, q_frag, c_of, lim_of);
+      else
+        tile_work<FMT, D, NT, false>(stage, k0, 0u, 0u, place, acc, l, ref, q_frag, c_of, lim_of);
     }
 
     // ---- the four warps' parts joined in shared memory (over the rings, whose copies have all landed) ----
