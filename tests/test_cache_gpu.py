@@ -293,6 +293,8 @@ def test_read_into_strided_outputs_and_bad_pages(ops):
 
 
 # ----------------------------------------------------------------------------------------- attention
+# query heads over 2 KV heads: a few rows per KV head, two tiles of them, and many (the form that decodes once)
+HEADS = pytest.mark.parametrize("Hq", [4, 10, 40])
 SHAPES = [
     # lens, T, Hq, Hkv, D, page, dtype, layout
     ([1], 1, 1, 1, 128, 16, "bf16", 0),
@@ -304,6 +306,8 @@ SHAPES = [
     ([90, 33], 33, 5, 1, 128, 16, "bf16", 0),
     ([1500], 2, 7, 1, 64, 16, "bf16", 0),
     ([2100, 900], 1, 24, 1, 128, 128, "bf16", 0),
+    ([130, 64, 65, 1], 7, 15, 1, 64, 48, "fp16", 1),
+    ([1000, 63], 9, 8, 1, 128, 16, "fp16", 0),
 ]
 
 
@@ -317,33 +321,36 @@ def test_attn(ops, fmt, lens, T, Hq, Hkv, D, page, dtype, layout):
     check_attn(f, q, o, lse, [T] * len(lens), D ** -0.5, layout)
 
 
+@HEADS
 @pytest.mark.parametrize("fmt", [0, 1])
-def test_attn_sharp_scores(ops, fmt):
+def test_attn_sharp_scores(ops, fmt, Hq):
     """Scores so wide that the running maximum keeps climbing, and so sharp that one key takes all."""
     for mult, scale in ((6.0, 0.3), (1.0, 4.0)):
         f = Filled(ops, 31, [640, 35], 2, 128, fmt, 16, k_mult=mult)
-        q = make_q(6, 2, 2, 8, 128, "bf16", 0)
+        q = make_q(6, 2, 2, Hq, 128, "bf16", 0)
         o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, softmax_scale=scale)
         check_attn(f, q, o, lse, [2, 2], float(np.float32(scale)), 0)
 
 
+@HEADS
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("lo,hi", [(-20, 20), (-90, -60), (60, 90), (0, 30)])
-def test_attn_wide_magnitudes(ops, fmt, lo, hi):
+def test_attn_wide_magnitudes(ops, fmt, lo, hi, Hq):
     """V tokens (and 32-element blocks of them) of very unlike magnitudes, some of them zero; each
     32-column block is held to its own magnitude."""
     def mult(rng, n):
         m = np.exp2(rng.integers(lo, hi + 1, (n, 1, 4))).repeat(32, -1)
         return m * (rng.random((n, 1, 1)) > 0.1)
     f = Filled(ops, 41, [200, 33], 2, 128, fmt, 16, v_mult=mult)
-    q = make_q(7, 2, 3, 4, 128, "bf16", 0)
+    q = make_q(7, 2, 3, Hq, 128, "bf16", 0)
     o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
     for c in range(4):
         check_attn(f, q, o, lse, [3, 3], 128 ** -0.5, 0, cols=slice(32 * c, 32 * c + 32))
 
 
+@HEADS
 @pytest.mark.parametrize("fmt", [0, 1])
-def test_attn_wide_keys(ops, fmt):
+def test_attn_wide_keys(ops, fmt, Hq):
     """K blocks of very unlike magnitudes, scores kept moderate by the softmax scale."""
     rng = np.random.default_rng(3)
     f = Filled(ops, 43, [150, 48], 2, 128, fmt, 16)
@@ -353,14 +360,15 @@ def test_attn_wide_keys(ops, fmt):
     f.cache.k_sc.copy_(torch.where(sc == 255, sc, (sc + shift).clamp(0, 254)).to(torch.uint8))
     host_k, host_s = f.cache.k.cpu().numpy(), f.cache.k_sc.cpu().numpy()
     f.K = [C.gather(host_k, host_s, fmt, f.table[b].cpu().numpy(), n, 16) for b, n in enumerate(f.lens)]
-    q = make_q(8, 2, 2, 6, 128, "bf16", 0)
+    q = make_q(8, 2, 2, Hq, 128, "bf16", 0)
     o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, softmax_scale=2e-5)
     check_attn(f, q, o, lse, [2, 2], float(np.float32(2e-5)), 0)
 
 
-def test_attn_padded_and_empty_rows(ops):
+@HEADS
+def test_attn_padded_and_empty_rows(ops, Hq):
     f = Filled(ops, 51, [100, 0, 3, 50, 2], 2, 128, 1, 16)
-    q = make_q(9, 5, 4, 8, 128, "bf16", 0)
+    q = make_q(9, 5, 4, Hq, 128, "bf16", 0)
     new = [2, 0, 4, -3, 9]                 # 9 of T = 4: clamped; 2 held with 4 new: two rows before the start
     o = torch.full_like(q, 7.0)
     o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, new_lens=i32(new), o=o)
@@ -371,11 +379,12 @@ def test_attn_padded_and_empty_rows(ops):
     assert torch.all(o == 0) and torch.all(torch.isneginf(lse))
 
 
+@HEADS
 @pytest.mark.parametrize("fmt", [0, 1])
-def test_attn_absent_pages(ops, fmt):
+def test_attn_absent_pages(ops, fmt, Hq):
     """A page id outside the pool is not followed: its tokens take no part, and the status says so."""
     f = Filled(ops, 52, [100], 2, 128, fmt, 16)
-    q = make_q(9, 1, 2, 4, 128, "bf16", 0)
+    q = make_q(9, 1, 2, Hq, 128, "bf16", 0)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     for bad in (-1, f.cache.num_pages, 2147483647, -2147483648):
         f.table[0, 1], f.table[0, 6] = bad, bad       # 96.. is the tail page
@@ -388,11 +397,12 @@ def test_attn_absent_pages(ops, fmt):
     assert torch.all(o == 0) and torch.all(torch.isneginf(lse))
 
 
+@HEADS
 @pytest.mark.parametrize("fmt", [0, 1])
-def test_attn_length_past_the_table(ops, fmt):
+def test_attn_length_past_the_table(ops, fmt, Hq):
     """Queries that stand past the table's end see every key it has."""
     f = Filled(ops, 53, [64], 2, 128, fmt, 16)
-    q = make_q(9, 1, 2, 4, 128, "bf16", 0)
+    q = make_q(9, 1, 2, Hq, 128, "bf16", 0)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     o, lse = ops.mx_cache_attn(q, f.cache, f.table[:, :4].contiguous(), i32([80]), dev_status=st)
     assert int(st) == 0x202 and ops.bsc_read_device_status(st) == 7
@@ -400,13 +410,14 @@ def test_attn_length_past_the_table(ops, fmt):
         check_attn(f, q[:, t:t + 1], o[:, t:t + 1], lse[:, :, t:t + 1], [1], 128 ** -0.5, 0)
 
 
+@HEADS
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("n", [40, 45, 200])
-def test_attn_rows_do_not_see_later_tokens(ops, fmt, n):
+def test_attn_rows_do_not_see_later_tokens(ops, fmt, n, Hq):
     """Row t is bit-for-bit what it is whatever the tokens after it hold, NaN and infinities included."""
     T = 5
     f = Filled(ops, 61, [n], 2, 128, fmt, 16)
-    q = make_q(10, 1, T, 8, 128, "bf16", 0)
+    q = make_q(10, 1, T, Hq, 128, "bf16", 0)
     ref = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
     fills = [float("nan"), float("inf"), 0.0, 1e30, 1e-30, 3e4, None]
     for t in range(T - 1):
@@ -421,19 +432,20 @@ def test_attn_rows_do_not_see_later_tokens(ops, fmt, n):
         f = Filled(ops, 61, [n], 2, 128, fmt, 16)
 
 
+@HEADS
 @pytest.mark.parametrize("fmt", [0, 1])
-def test_attn_visible_nan(ops, fmt):
+def test_attn_visible_nan(ops, fmt, Hq):
     """A NaN block of V that a row sees makes that block of its output NaN, and no other; a NaN block of
     K makes the whole row NaN."""
     f = Filled(ops, 62, [90], 2, 128, fmt, 16)
-    q = make_q(11, 1, 3, 4, 128, "bf16", 0)
+    q = make_q(11, 1, 3, Hq, 128, "bf16", 0)
     clean, clean_lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
     pg, off = int(f.table[0, 88 // 16]), 88 % 16
     f.cache.v_sc[pg, 0, off, 1] = 255
     o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
-    nan = torch.isnan(o[0])                                  # [T, Hq, D]; KV head 0 serves query heads 0, 1
+    nan = torch.isnan(o[0])                                  # [T, Hq, D]; KV head 0 serves the first half of the query heads
     want = torch.zeros_like(nan)
-    want[1:, :2, 32:64] = True                               # rows at positions 88 and 89
+    want[1:, :Hq // 2, 32:64] = True                               # rows at positions 88 and 89
     assert torch.equal(nan, want)
     np.testing.assert_allclose(f64(lse), f64(clean_lse), atol=2.0 ** -16)
     keep = ~want[0]
@@ -441,8 +453,8 @@ def test_attn_visible_nan(ops, fmt):
     f = Filled(ops, 62, [90], 2, 128, fmt, 16)
     f.cache.k_sc[pg, 1, off, 2] = 255
     o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
-    assert torch.all(torch.isnan(o[0, 1:, 2:])) and torch.all(torch.isnan(lse[0, 2:, 1:]))
-    assert torch.equal(o[0, 0], clean[0, 0]) and torch.equal(o[0, :, :2], clean[0, :, :2])
+    assert torch.all(torch.isnan(o[0, 1:, Hq // 2:])) and torch.all(torch.isnan(lse[0, Hq // 2:, 1:]))
+    assert torch.equal(o[0, 0], clean[0, 0]) and torch.equal(o[0, :, :Hq // 2], clean[0, :, :Hq // 2])
 
 
 def test_attn_shared_prefix(ops):
@@ -476,11 +488,12 @@ def test_attn_strided_and_guarded(ops):
     assert torch.all(ws_buf[:2048] == 0xA5) and torch.all(ws_buf[2048 + ws:] == 0xA5)
 
 
-def test_streams_and_graphs(ops):
+@pytest.mark.parametrize("Hq", [8, 40])
+def test_streams_and_graphs(ops, Hq):
     """The same call on a side stream, twice at once on two streams, and captured and replayed on new
     inputs gives the eager call's bits; a second replay too."""
     f = Filled(ops, 65, [1200, 300], 2, 128, 1, 16)
-    q, q2 = (make_q(s, 2, 2, 8, 128, "bf16", 0) for s in (14, 15))
+    q, q2 = (make_q(s, 2, 2, Hq, 128, "bf16", 0) for s in (14, 15))
     ref, ref2 = (ops.mx_cache_attn(x, f.cache, f.table, f.seq) for x in (q, q2))
     torch.cuda.synchronize()
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
