@@ -457,40 +457,52 @@ def mx_cache_alloc(num_pages, page_size, Hkv, D=128, fmt=CACHE_MXFP4, device="cu
     return MxCache(k, k_sc, v, v_sc, fmt)
 
 
-def _act_dims(x, layout, H, D, cache, name):
+def _act_dims(x, layout, cache, name):
     """(B, T, H), element strides (b, t, h) and the dtype code of an activation of `cache`'s head size."""
     code = _ACT.get(x.dtype)
-    if code is None or x.device != cache.device or x.dim() != 4:
+    if code is None or x.dim() != 4 or x.device != cache.device:
         raise ValueError("%s must be a 4-D bfloat16 or float16 tensor on the cache's device" % name)
-    shape, st = x.shape, x.stride()
-    if layout == BSHD:
-        B, T, sb, s_t = shape[0], shape[1], st[0], st[1]
-    elif layout == SBHD:
-        T, B, s_t, sb = shape[0], shape[1], st[0], st[1]
-    else:
+    B, T, H, D = x.shape
+    sb, st, sh, sd = x.stride()
+    if layout == SBHD:
+        B, T, sb, st = T, B, st, sb
+    elif layout != BSHD:
         raise ValueError("layout must be BSHD or SBHD")
-    if shape[3] != D or (H is not None and shape[2] != H):
-        raise ValueError("%s does not have the cache's heads or head size" % name)
-    if st[3] != 1 and D > 1 and x.numel():
+    if D != cache.D:
+        raise ValueError("%s does not have the cache's head size" % name)
+    if sd != 1 and x.numel():
         raise ValueError("%s must be contiguous along D" % name)
-    return (B, T, shape[2]), (sb, s_t, st[2]), code
+    return (B, T, H), (sb, st, sh), code
 
 
-def _index(t, shape, cache, name):
-    """Pointer of an int32 index array of the given shape (None: NULL)."""
+def _dense(layout, B, T, H, D):
+    """Shape of a contiguous activation and its strides (b, t, h)."""
+    if layout == BSHD:
+        return (B, T, H, D), (T * H * D, H * D, D)
+    if layout == SBHD:
+        return (T, B, H, D), (H * D, B * H * D, D)
+    raise ValueError("layout must be BSHD or SBHD")
+
+
+def _index(t, B, cache, name):
+    """Pointer of an int32 index array of B entries (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != cache.device or t.shape != shape:
-        raise ValueError("%s must be an int32 tensor of shape %s on the cache's device" % (name, shape))
-    if len(shape) == 1 and shape[0] > 1 and t.stride(0) != 1:
+    if t.dtype is not torch.int32 or t.shape != (B,) or t.device != cache.device:
+        raise ValueError("%s must be an int32 tensor of shape (%d,) on the cache's device" % (name, B))
+    if B > 1 and t.stride(0) != 1:
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
 
 
-def _table(page_table, B, cache):
-    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be [B, max_pages] with contiguous rows")
-    return (_index(page_table, (B, page_table.shape[1]), cache, "page_table"), page_table.stride(0), page_table.shape[1])
+def _table(t, B, cache):
+    """Pointer, row stride and columns of a page table of B rows."""
+    if t.dim() != 2 or t.shape[0] != B or t.dtype is not torch.int32 or t.device != cache.device:
+        raise ValueError("page_table must be an int32 tensor [B, max_pages] on the cache's device")
+    row, col = t.stride()
+    if col != 1 and t.shape[1] > 1:
+        raise ValueError("page_table must have contiguous rows")
+    return t.data_ptr(), row, t.shape[1]
 
 
 def _status(t, cache):
@@ -524,13 +536,14 @@ def mx_cache_write(cache, k, v, page_table, seq_lens, new_lens=None, layout=BSHD
     if there is not None:
         with there:
             return mx_cache_write(cache, k, v, page_table, seq_lens, new_lens, layout, rule, dev_status)
-    (B, T, H), ks, dt = _act_dims(k, layout, cache.Hkv, cache.D, cache, "k")
-    dims, vs, dv = _act_dims(v, layout, cache.Hkv, cache.D, cache, "v")
-    if dims != (B, T, H) or dv != dt:
-        raise ValueError("k and v must have the same shape and dtype")
+    dims, ks, dt = _act_dims(k, layout, cache, "k")
+    dims_v, vs, dt_v = _act_dims(v, layout, cache, "v")
+    B, T, H = dims
+    if dims_v != dims or dt_v != dt or H != cache.Hkv:
+        raise ValueError("k and v must both have the cache's heads, one shape and one dtype")
     p = CacheWriteParams(cache.params, k.data_ptr(), v.data_ptr(), *ks, *vs, B, T, dt, rule,
-                         *_table(page_table, B, cache), _index(seq_lens, (B,), cache, "seq_lens"),
-                         _index(new_lens, (B,), cache, "new_lens"), _status(dev_status, cache))
+                         *_table(page_table, B, cache), _index(seq_lens, B, cache, "seq_lens"),
+                         _index(new_lens, B, cache, "new_lens"), _status(dev_status, cache))
     _check(lib.mx_cache_write(ctypes.byref(p), _raw_stream(cache.device.index)))
 
 
@@ -542,17 +555,27 @@ def mx_cache_read(cache, page_table, seq_lens, T, starts=None, layout=BSHD, dtyp
     if there is not None:
         with there:
             return mx_cache_read(cache, page_table, seq_lens, T, starts, layout, dtype, k_out, v_out, dev_status)
-    B = page_table.shape[0]
-    shape = (B, T, cache.Hkv, cache.D) if layout == BSHD else (T, B, cache.Hkv, cache.D)
-    k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
-    v_out = torch.empty(shape, dtype=dtype, device=cache.device) if v_out is None else v_out
-    dk, ks, dt = _act_dims(k_out, layout, cache.Hkv, cache.D, cache, "k_out")
-    dv, vs, dt_v = _act_dims(v_out, layout, cache.Hkv, cache.D, cache, "v_out")
-    if dk != (B, T, cache.Hkv) or dv != dk or dt != dt_v:
-        raise ValueError("k_out and v_out must both be [B, T, Hkv, D] in the layout, of one dtype")
+    B, Hkv = page_table.shape[0], cache.Hkv
+    shape, ks = _dense(layout, B, T, Hkv, cache.D)
+    vs, dt = ks, _ACT.get(dtype)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=cache.device)
+    else:
+        dims, ks, dt = _act_dims(k_out, layout, cache, "k_out")
+        if dims != (B, T, Hkv):
+            raise ValueError("k_out must be [B, T, Hkv, D] in the layout")
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=cache.device)
+        dt_v = _ACT.get(dtype)
+    else:
+        dims, vs, dt_v = _act_dims(v_out, layout, cache, "v_out")
+        if dims != (B, T, Hkv):
+            raise ValueError("v_out must be [B, T, Hkv, D] in the layout")
+    if dt is None or dt != dt_v:
+        raise ValueError("k_out and v_out must be bfloat16 or float16, of one dtype")
     p = CacheReadParams(cache.params, k_out.data_ptr(), v_out.data_ptr(), *ks, *vs, B, T, dt,
-                        *_table(page_table, B, cache), _index(seq_lens, (B,), cache, "seq_lens"),
-                        _index(starts, (B,), cache, "starts"), _status(dev_status, cache))
+                        *_table(page_table, B, cache), _index(seq_lens, B, cache, "seq_lens"),
+                        _index(starts, B, cache, "starts"), _status(dev_status, cache))
     _check(lib.mx_cache_read(ctypes.byref(p), _raw_stream(cache.device.index)))
     return k_out, v_out
 
@@ -576,16 +599,16 @@ def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, so
         with there:
             return mx_cache_attn(q, cache, page_table, seq_lens, new_lens, layout, softmax_scale, o, lse, workspace,
                                  dev_status)
-    (B, T, Hq), qs, dt = _act_dims(q, layout, None, cache.D, cache, "q")
+    dims, qs, dt = _act_dims(q, layout, cache, "q")
+    B, T, Hq = dims
     table = _table(page_table, B, cache)
     device = cache.device
     if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=device)
-        st = o.stride()
-        o_s = (st[0], st[1], st[2]) if layout == BSHD else (st[1], st[0], st[2])
+        _, o_s = _dense(layout, B, T, Hq, cache.D)
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
-        dims, o_s, dt_o = _act_dims(o, layout, Hq, cache.D, cache, "o")
-        if dims != (B, T, Hq) or dt_o != dt:
+        dims_o, o_s, dt_o = _act_dims(o, layout, cache, "o")
+        if dims_o != dims or dt_o != dt:
             raise ValueError("o must have q's shape and dtype")
     if lse is None:
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=device)
@@ -601,8 +624,8 @@ def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, so
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
         need = workspace.numel() * workspace.element_size()
     p = CacheAttnParams(cache.params, q.data_ptr(), o.data_ptr(), lse.data_ptr(), *qs, *o_s, B, T, Hq, dt,
-                        cache.D ** -0.5 if softmax_scale is None else softmax_scale, *table, _index(seq_lens, (B,), cache, "seq_lens"),
-                        _index(new_lens, (B,), cache, "new_lens"), _status(dev_status, cache),
+                        cache.D ** -0.5 if softmax_scale is None else softmax_scale, *table, _index(seq_lens, B, cache, "seq_lens"),
+                        _index(new_lens, B, cache, "new_lens"), _status(dev_status, cache),
                         workspace.data_ptr() if need else None, need)
     _check(lib.mx_cache_attn(ctypes.byref(p), _raw_stream(device.index)))
     return o, lse
