@@ -20,15 +20,16 @@ struct Piece {
   int b, t0, h, which;
 };
 __device__ __forceinline__ bool piece_of(const CacheRwArgs& a, Piece& p) {
-  long long i = (long long)blockIdx.x * RW_WARPS + (threadIdx.x >> 5);
-  const int tiles = (a.T + RW_TOKENS - 1) / RW_TOKENS;
-  if (i >= 2LL * a.B * tiles * a.c.Hkv) return false;
-  p.h = (int)(i % a.c.Hkv);
-  i /= a.c.Hkv;
-  p.which = (int)(i & 1);
-  i >>= 1;
-  p.t0 = (int)(i % tiles) * RW_TOKENS;
-  p.b = (int)(i / tiles);
+  uint32_t i = blockIdx.x * RW_WARPS + (threadIdx.x >> 5);          // fewer than 2^31 warps: checked by the host
+  const uint32_t tiles = (uint32_t)(a.T + RW_TOKENS - 1) / RW_TOKENS, H = a.c.Hkv;
+  if (i >= 2u * a.B * tiles * H) return false;
+  uint32_t next = i / H;
+  p.h = (int)(i - next * H);
+  p.which = (int)(next & 1u);
+  i = next >> 1;
+  next = i / tiles;
+  p.t0 = (int)(i - next * tiles) * RW_TOKENS;
+  p.b = (int)next;
   return true;
 }
 
@@ -62,12 +63,16 @@ __global__ void __launch_bounds__(RW_WARPS * 32) cache_write_kernel(const CacheR
   uint8_t* const pool = (w.which ? a.c.v : a.c.k) + col * (RB / LPR);
   uint8_t* const pool_sc = w.which ? a.c.v_sc : a.c.k_sc;
   const long long ps = w.which ? a.c.v_ps : a.c.k_ps, ps_sc = w.which ? a.c.v_sc_ps : a.c.k_sc_ps;
+  // the rows are mostly neighbours in one page: one address then, and constant steps
+  const int page0 = __shfl_sync(0xFFFFFFFFu, page, 0);
+  const uint32_t row0 = __shfl_sync(0xFFFFFFFFu, in_page, 0);
+  const bool together = page0 >= 0 && __all_sync(0xFFFFFFFFu, lane >= rows || (page == page0 && in_page == row0 + lane));
+  uint8_t* const dst0 = pool + page0 * ps + (unsigned long long)(row0 + sub) * RB;
+  uint8_t* const sc0 = pool_sc + page0 * ps_sc + (unsigned long long)(row0 + sub) * NB;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     if (i * RPI >= rows) break;
     const int r = i * RPI + sub;
-    const int pg = __shfl_sync(0xFFFFFFFFu, page, r);
-    const uint32_t row = __shfl_sync(0xFFFFFFFFu, in_page, r);
     // the block's maximum from bit patterns: without the sign they are in the values' order, NaN above Inf on top
     const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     uint32_t mx = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu), __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
@@ -87,23 +92,29 @@ __global__ void __launch_bounds__(RW_WARPS * 32) cache_write_kernel(const CacheR
       f[2 * j] = p.x;
       f[2 * j + 1] = p.y;
     }
-    if (pg >= 0) {
-      uint8_t* const dst = pool + pg * ps + (unsigned long long)row * RB;
-      if (FMT == CACHE_FP4) {
-        const uint32_t q = cvt_e2m1x8(f);
-        *reinterpret_cast<uint32_t*>(dst) = sb == 0xFFu ? 0x77777777u : q;
-      } else {
-        uint2 q;
-        q.x = cvt_e4m3x2(f[0], f[1]) | (uint32_t)cvt_e4m3x2(f[2], f[3]) << 16;
-        q.y = cvt_e4m3x2(f[4], f[5]) | (uint32_t)cvt_e4m3x2(f[6], f[7]) << 16;
-        *reinterpret_cast<uint2*>(dst) = sb == 0xFFu ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu) : q;
-      }
+    uint2 q;
+    if (FMT == CACHE_FP4) {
+      q.x = sb == 0xFFu ? 0x77777777u : cvt_e2m1x8(f);
+    } else {
+      q.x = cvt_e4m3x2(f[0], f[1]) | (uint32_t)cvt_e4m3x2(f[2], f[3]) << 16;
+      q.y = cvt_e4m3x2(f[4], f[5]) | (uint32_t)cvt_e4m3x2(f[6], f[7]) << 16;
+      if (sb == 0xFFu) q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    }
+    uint8_t *dst = dst0 + i * RPI * RB, *sc = sc0 + i * RPI * NB;
+    bool there = r < rows;
+    if (!together) {
+      const int pg = __shfl_sync(0xFFFFFFFFu, page, r);
+      const uint32_t row = __shfl_sync(0xFFFFFFFFu, in_page, r);
+      there = pg >= 0;
+      dst = pool + pg * ps + (unsigned long long)row * RB;
+      sc = pool_sc + pg * ps_sc + (unsigned long long)row * NB;
+    }
+    if (there) {
+      if (FMT == CACHE_FP4) *reinterpret_cast<uint32_t*>(dst) = q.x;
+      else *reinterpret_cast<uint2*>(dst) = q;
       if (col == 0) {
-        uint8_t* const sc = pool_sc + pg * ps_sc + (unsigned long long)row * NB;
-        if (NB == 4)
-          *reinterpret_cast<uint32_t*>(sc) = word;
-        else
-          *reinterpret_cast<uint16_t*>(sc) = (uint16_t)word;
+        if (NB == 4) *reinterpret_cast<uint32_t*>(sc) = word;
+        else *reinterpret_cast<uint16_t*>(sc) = (uint16_t)word;
       }
     }
     __syncwarp();
@@ -158,8 +169,8 @@ __global__ void __launch_bounds__(RW_WARPS * 32) cache_read_kernel(const CacheRw
   for (int i = 0; i < NI; ++i) {
     if (i * RPI >= rows) break;
     const int r = i * RPI + sub;
-    const uint32_t sw = __shfl_sync(0xFFFFFFFFu, word, r);
-    const float s = scale_value((sw >> (8 * (col >> 2))) & 0xFFu);
+    const float s = scale_value((__shfl_sync(0xFFFFFFFFu, word, r) >> (8 * (col >> 2))) & 0xFFu);
+    const float2 s2 = make_float2(s, s);
     uint32_t h[4];
     if (FMT == CACHE_FP4) {
       e2m1x8_to_f16(v[i].x, h);
@@ -170,8 +181,8 @@ __global__ void __launch_bounds__(RW_WARPS * 32) cache_read_kernel(const CacheRw
     uint32_t o[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 f = f16x2_to_f32(h[j]);
-      o[j] = f32_to_act<DT>(f.x * s, f.y * s);   // the product is exact in fp32: one rounding
+      const float2 f = __fmul2_rn(f16x2_to_f32(h[j]), s2);
+      o[j] = f32_to_act<DT>(f.x, f.y);           // the product is exact in fp32: one rounding
     }
     if (r < rows)
       __stcs(reinterpret_cast<uint4*>(x + (long long)(w.t0 + r) * xs.t),
