@@ -25,8 +25,8 @@
 //
 // Roundings.  Q is scaled per row by a power of two to [2^14, 2^15) and held in fp16: exact for 16-bit
 // inputs down to 2^-29 of the row's maximum.  Scores, weights' sums and O are fp32.  Weights are rounded to
-// fp16 for the second product (2^-12 relative at most, far under the output's own rounding), around 2^8
-// at the reference so that only weights under 2^-22 of the largest lose relative precision.
+// fp16 for the second product (2^-11 relative at most, and each weight on its own; the output's own rounding is
+// 2^-8 or 2^-11 of the result), around 2^8 at the reference so that only weights under 2^-22 of the largest lose relative precision.
 //
 // Work.  A warp takes 32 keys at a time through its own ring of shared-memory stages (cp.async, 16
 // bytes per lane, rows permuted so that both fragments read without bank conflicts); a block is 4 warps on
@@ -47,7 +47,7 @@ namespace cg = cooperative_groups;
 
 constexpr int KT = 32, WARPS = 4, CHUNK = KT * WARPS, THREADS = WARPS * 32;
 constexpr int SMS = 152;
-constexpr int MIN_CHUNKS = 2;
+constexpr int MIN_CHUNKS = 2;   // chunks a block takes at least, once there is one block per SM (see Share)
 constexpr float SLACK = 4.f;    // a reference moves when a score passes it by this much (log2)
 constexpr float LIFT = 8.f;     // a reference m gives weights 2^(x + r), r = LIFT - m
 constexpr float UNSET = 3e38f;  // r of a row without a score yet: 2^(-inf + r) = 0, and any score moves it
@@ -72,7 +72,10 @@ struct Cfg {
   static constexpr int MERGE = WARPS * ROWS * (D + 4) * 4 + WARPS * ROWS * 8;
   static constexpr int JOINED = MERGE + ROWS * D * 4 + ROWS * 8;   // and the block's own part, in the cluster form
   static constexpr int SMEM = RING + QBYTES > JOINED ? RING + QBYTES : JOINED;
-  static constexpr int OCC = NT == 1 ? (STAGE * STAGES * WARPS > 56 * 1024 ? 3 : 4) : 2;   // blocks per SM
+  // Blocks per SM.  One row tile: 3 blocks leave 168 registers, 4 leave 128 and fewer loads and conversions in flight.
+  // D = 128, G = 4, 4 bits, 4 blocks / 3: 64 x 6000 keys 50.3 / 48.1 us, 16 x 6000 20.2 / 19.1; but one sequence
+  // of 32K 12.7 / 13.7, whose 2048 chunks divide worse by 456.  In 8 bits shared memory holds 3 at most.
+  static constexpr int OCC = NT == 1 ? 3 : 2;
 };
 
 // Byte offset of 16-byte piece c of key k's row in a stage.  Rows of 32, 64 or 128 bytes lie in 128-byte
@@ -911,7 +914,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const CacheAttnArgs a, int row_tiles, int grid,
                                                                           int rows_pb) {
   constexpr int ROWS = 8 * NT, SLOT = ROWS * (D + 1), PL = D / 32;    // columns per lane
-  constexpr int MOST_PARTS = SMS * (NT == 1 ? 4 : 2);                 // blocks of the largest grid
+  constexpr int MOST_PARTS = SMS * (NT == 1 ? 3 : 2);                 // blocks of the largest grid
   __shared__ float zs[MOST_PARTS * (ROWS < JOIN_WARPS ? ROWS : JOIN_WARPS)];   // [row of the block][part]
   __shared__ __align__(16) float part_o[JOIN_WARPS][D];
   __shared__ float part_sum[JOIN_WARPS];
@@ -999,11 +1002,13 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
 // Short tables: a cluster of this many blocks per unit (1: a block), or 0 for the list.  A cluster joins its parts
 // through shared memory: one launch, no workspace.  But a unit then has 8 blocks at most, whatever the others'
 // lengths, so it is taken only where the longest sequence that the table allows is MOST_CLUSTER_CHUNKS chunks per
-// block.
+// block.  D = 128, Hkv = 8, 4 bits, cluster / list in us: G = 4, 1 x 500 tokens 5.6 / 7.3, 4 x 1000 6.4 / 8.2,
+// 16 x 2000 9.6 / 13.4, 64 x 512 8.2 / 13.1, 1 x 6000 9.9 / 10.5; G = 16, 4 x 1000 9.6 / 10.7, 1 x 4000 11.1 / 9.6
+// (from 3000 tokens on one sequence of 16 rows loses, and shorter tables win more often).
 constexpr int MOST_CLUSTER_CHUNKS = 6;
 int tile_rows(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 int cluster_size(long long B, long long rows, int Hkv, long long max_tokens) {
-  const int tile = tile_rows(rows), occ = tile == 8 ? 4 : 2;
+  const int tile = tile_rows(rows), occ = tile == 8 ? 3 : 2;
   const long long units = B * Hkv * ((rows + tile - 1) / tile), chunks = (max_tokens + CHUNK - 1) / CHUNK;
   int cs = 1;
   while (cs < 8 && cs < chunks && units * cs * 2 <= SMS * occ) cs *= 2;
@@ -1013,7 +1018,7 @@ int cluster_size(long long B, long long rows, int Hkv, long long max_tokens) {
 template <int FMT, int D, int NT>
 cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   using C = Cfg<FMT, D, NT>;
-  static_assert(C::OCC <= (NT == 1 ? 4 : 2), "the join's table of parts, and the workspace");
+  static_assert(C::OCC <= (NT == 1 ? 3 : 2), "the join's table of parts, and the workspace");
   const int rows = a.T * (a.Hq / a.c.Hkv), row_tiles = (rows + C::ROWS - 1) / C::ROWS;
   const long long units = (long long)a.B * a.c.Hkv * row_tiles;
   const long long chunks = ((long long)a.pt.max_pages * a.c.page_size + CHUNK - 1) / CHUNK;
@@ -1074,7 +1079,7 @@ size_t cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long lon
   const long long all = (long long)T * (Hq / Hkv);
   if (all <= 0 || cluster_size(B, all, Hkv, max_tokens)) return 0;
   // two slots per block of the largest grid of either format
-  const int rows = tile_rows(all), occ = rows == 8 ? 4 : 2;
+  const int rows = tile_rows(all), occ = rows == 8 ? 3 : 2;
   return (size_t)2 * SMS * occ * rows * (D + 1) * 4;
 }
 

@@ -198,7 +198,7 @@ def test_workspace_bytes(ops):
         assert ops.mx_cache_attn_workspace_bytes(*bad) == 0
     # short tables need none; long ones the same whatever their length, two slots of fp32 rows per block
     assert ops.mx_cache_attn_workspace_bytes(1, 1, 8, 4, 128, 1024) == 0
-    assert ops.mx_cache_attn_workspace_bytes(1, 1, 8, 4, 128, 1 << 20) == 2 * 608 * 8 * 129 * 4
+    assert ops.mx_cache_attn_workspace_bytes(1, 1, 8, 4, 128, 1 << 20) == 2 * 456 * 8 * 129 * 4
     assert ops.mx_cache_attn_workspace_bytes(8, 4, 8, 2, 64, 1 << 17) == 2 * 304 * 16 * 65 * 4
     assert ops.mx_cache_attn_workspace_bytes(8, 40, 8, 2, 64) == 2 * 304 * 32 * 65 * 4
 
