@@ -161,9 +161,9 @@ bsc_status check_cache(const bsc_mx_cache& c, int B, int T, int H, int dtype, lo
   if (c.Hkv == 0 || c.num_pages == 0 || c.page_size == 0) return BSC_ERR_SHAPE;
   if ((c.D != 64 && c.D != 128) || c.page_size % 16 != 0) return BSC_ERR_UNSUPPORTED;
   if (B > 1 && table_stride < max_pages) return BSC_ERR_SHAPE;
-  // positions are 32-bit, and the grids (at most one warp per 16 tokens and KV head, or one block per
-  // query row) must fit theirs
-  if ((long long)max_pages * c.page_size >= (1LL << 31)) return BSC_ERR_UNSUPPORTED;
+  // positions are 32-bit, with room above the last for a tile's end and the tiles after it, and the grids (at most
+  // one warp per 16 tokens and KV head, or one block per query row) must fit theirs
+  if ((long long)max_pages * c.page_size > BSC_CACHE_MAX_TOKENS) return BSC_ERR_UNSUPPORTED;
   if ((long long)B * T >= (1LL << 31) / H || (long long)B * ((T + 15LL) / 16) * 2 >= (1LL << 31) / c.Hkv)
     return BSC_ERR_UNSUPPORTED;
   // the attention addresses a page in 32-bit units of 16 bytes
@@ -449,7 +449,7 @@ bsc_status mx_cache_write(const bsc_mx_cache_write_params* p, bsc_stream_t strea
   bool empty;
   bsc_status s = check_cache(p->cache, p->B, p->T, p->cache.Hkv, p->dtype, p->table_stride, p->max_pages, &empty);
   if (s != BSC_OK || empty) return s;
-  if (!p->k || !p->v || !p->seq_lens || !p->page_table) return BSC_ERR_NULL;
+  if (!p->k || !p->v || !p->seq_lens || (p->max_pages > 0 && !p->page_table)) return BSC_ERR_NULL;
   if (!aligned16(p->k) || !aligned16(p->v) || !aligned4(p->page_table) || !aligned4(p->seq_lens) ||
       !aligned4(p->new_lens) || !aligned4(p->dev_status))
     return BSC_ERR_ALIGN;
@@ -478,7 +478,7 @@ bsc_status mx_cache_read(const bsc_mx_cache_read_params* p, bsc_stream_t stream)
   bool empty;
   bsc_status s = check_cache(p->cache, p->B, p->T, p->cache.Hkv, p->dtype, p->table_stride, p->max_pages, &empty);
   if (s != BSC_OK || empty) return s;
-  if (!p->k || !p->v || !p->seq_lens || !p->page_table) return BSC_ERR_NULL;
+  if (!p->k || !p->v || !p->seq_lens || (p->max_pages > 0 && !p->page_table)) return BSC_ERR_NULL;
   if (!aligned16(p->k) || !aligned16(p->v) || !aligned4(p->page_table) || !aligned4(p->seq_lens) ||
       !aligned4(p->starts) || !aligned4(p->dev_status))
     return BSC_ERR_ALIGN;
@@ -503,6 +503,8 @@ bsc_status mx_cache_read(const bsc_mx_cache_read_params* p, bsc_stream_t stream)
 
 size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long long max_tokens) {
   if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_tokens < 0) return 0;
+  if ((long long)B * T >= (1LL << 31) / Hq) return 0;       // refused by the call itself
+  if (max_tokens > BSC_CACHE_MAX_TOKENS) max_tokens = BSC_CACHE_MAX_TOKENS;
   return bsc::cache_attn_workspace_bytes(B, T, Hq, Hkv, D, max_tokens);
 }
 
@@ -515,7 +517,7 @@ bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream)
   if (!(std::isfinite(p->softmax_scale) && p->softmax_scale > 0.f)) return BSC_ERR_UNSUPPORTED;
   const size_t need = mx_cache_attn_workspace_bytes(p->B, p->T, p->Hq, p->cache.Hkv, p->cache.D,
                                                     (long long)p->max_pages * p->cache.page_size);
-  if (!p->q || !p->o || !p->seq_lens || !p->page_table || (need > 0 && !p->workspace)) return BSC_ERR_NULL;
+  if (!p->q || !p->o || !p->seq_lens || (p->max_pages > 0 && !p->page_table) || (need > 0 && !p->workspace)) return BSC_ERR_NULL;
   if (!aligned16(p->q) || !aligned16(p->o) || !aligned16(p->workspace) || !aligned4(p->page_table) ||
       !aligned4(p->seq_lens) || !aligned4(p->new_lens) || !aligned4(p->lse) || !aligned4(p->dev_status))
     return BSC_ERR_ALIGN;

@@ -21,7 +21,7 @@
 // range: scale exponents -16..11 (4 bits) or -19..2 (8 bits), block maxima from about 2^-14 or 2^-11
 // to 2^13 or 2^11.  A key with a scale outside of that (or a NaN block) takes the scalar path below in
 // fp32; keys are sorted one by one, by their own bytes, so a row never depends on a key it cannot see.
-// Scale byte 0 (a zero block, or a maximum under 2^-117) counts as zero.
+// Scale byte 0 (a zero block, or a maximum under 2^-118) counts as zero.
 //
 // Roundings.  Q is scaled per row by a power of two to [2^14, 2^15) and held in fp16: exact for 16-bit
 // inputs down to 2^-29 of the row's maximum.  Scores, weights' sums and O are fp32.  Weights are rounded to

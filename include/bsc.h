@@ -314,7 +314,16 @@ size_t bf16_attn_bwd_static_capacity(void);
  * attended; a position past max_pages * page_size is treated the same way, a negative length as 0.
  * If dev_status is given, it then receives 0x201 (page id) or 0x202 (length); it is left untouched
  * otherwise, and bsc_read_device_status returns BSC_ERR_DEVICE_PAGE for both.
+ *
+ * Outputs, workspace and dev_status overlap no other argument.  Refused as BSC_ERR_UNSUPPORTED, because
+ * positions, page rows and grids are counted in 32 bits: a page table of more than
+ * BSC_CACHE_MAX_TOKENS positions (max_pages * page_size), a page of Hkv * page_size * D >= 2^31, a page stride of
+ * 2^36 bytes or more, B * T * Hq (or B * T * Hkv / 8) >= 2^31, and for the attention
+ * B * Hkv * ceil(max_pages * page_size / 128) * R >= 2^31, R the tiles of 8, 16 or 32 rows (the smallest that is
+ * enough, else 32) that the T * (Hq/Hkv) query rows of a KV head take.  page_table may be NULL where
+ * max_pages is 0.
  */
+#define BSC_CACHE_MAX_TOKENS (1LL << 30)
 typedef enum { BSC_CACHE_MXFP8 = 0, BSC_CACHE_MXFP4 = 1 } bsc_cache_format;
 typedef enum { BSC_BF16 = 0, BSC_FP16 = 1 } bsc_dtype;
 typedef struct {
@@ -396,7 +405,8 @@ typedef struct {
  *   s_j = softmax_scale * q . Kc_j,  O = sum_j exp(s_j - LSE) Vc_j,  LSE = ln sum_j exp(s_j).
  * Rows that attend nothing (t >= n_b, p < 0, an empty sequence) get O = 0 and LSE = -inf.
  * Row p is bit-for-bit independent of what positions after p hold, NaN and infinities included.
- * Finite V is taken up to 2^100 in magnitude.  The result does not depend on the stream, on other calls
+ * Finite V is taken up to 2^100 in magnitude, and a block of scale byte 0 (a maximum under 2^-118) counts
+ * as zeros.  A NaN block of K makes the rows that attend it NaN, one of V their columns of that block.  The result does not depend on the stream, on other calls
  * or on timing (no atomics); it may differ in the last bits with the batch's lengths, which decide
  * how the keys are split.
  */

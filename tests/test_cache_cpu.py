@@ -129,6 +129,8 @@ POOL_CASES = [
     (dict(k_page_stride=4 * 16 * 64 - 16), 2),       # pages would overlap
     (dict(v_sc_page_stride=4 * 16 * 4 - 16), 2),
     (dict(k_page_stride=4 * 16 * 64 + 8), 3),
+    (dict(v_page_stride=1 << 36), 4),
+    (dict(page_size=1 << 22, k_page_stride=1 << 30, v_page_stride=1 << 30), 4),   # 2^31 elements a page
 ]
 COMMON = [
     (dict(B=-1), 2),
@@ -142,6 +144,7 @@ COMMON = [
     (dict(table_stride=31), 2),
     (dict(max_pages=-1), 2),
     (dict(max_pages=1 << 27, table_stride=1 << 27), 4),   # 2^31 positions
+    (dict(max_pages=(1 << 26) + 1, table_stride=1 << 27), 4),   # 2^30 + 16
     (dict(B=1 << 20, T=1 << 12), 4),
     (dict(T=0), 0),
     (dict(B=0, page_table=0), 0),
@@ -201,6 +204,9 @@ def test_workspace_bytes(ops):
     assert ops.mx_cache_attn_workspace_bytes(1, 1, 8, 4, 128, 1 << 20) == 2 * 456 * 8 * 129 * 4
     assert ops.mx_cache_attn_workspace_bytes(8, 4, 8, 2, 64, 1 << 17) == 2 * 304 * 16 * 65 * 4
     assert ops.mx_cache_attn_workspace_bytes(8, 40, 8, 2, 64) == 2 * 304 * 32 * 65 * 4
+    # sizes that no call takes: a table past the limit as one at the limit, a batch past it nothing
+    assert ops.mx_cache_attn_workspace_bytes(8, 40, 8, 2, 64, (1 << 63) - 1) == 2 * 304 * 32 * 65 * 4
+    assert ops.mx_cache_attn_workspace_bytes(1 << 30, 1 << 30, 1 << 30, 1, 128) == 0
 
 
 def test_binding_refuses_cpu_pools(ops):

@@ -3,6 +3,7 @@ values read back, attention within bounds derived below, and the calls a serving
 them: ragged and empty rows, shared and absent pages, garbage behind a sequence, other streams, graphs.
 """
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -511,6 +512,99 @@ def test_streams_and_graphs(ops, Hq):
         g.replay()
         torch.cuda.synchronize()
         assert same(out, want)
+
+
+def test_two_host_threads(ops):
+    """Calls of several host threads, each on its own stream, give the single call's bits."""
+    f = Filled(ops, 67, [700, 90, 0], 2, 64, 0, 32)
+    qs = [make_q(20 + i, 3, 1 + 8 * i, 8, 64, "fp16", 0) for i in range(3)]      # 4, 36 and 68 rows per KV head
+    want = [ops.mx_cache_attn(q, f.cache, f.table, f.seq) for q in qs]
+    torch.cuda.synchronize()
+    got = [[] for _ in qs]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got[i].append(ops.mx_cache_attn(qs[i], f.cache, f.table, f.seq, stream=s))
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for outs, ref in zip(got, want):
+        assert len(outs) == 20
+        for o in outs:
+            assert torch.equal(bits(o[0]), bits(ref[0])) and torch.equal(bits(o[1]), bits(ref[1]))
+
+
+def test_two_graphs_at_once(ops):
+    """Two captured calls with a workspace each, replayed at the same time on two streams."""
+    f = Filled(ops, 68, [900, 40], 2, 128, 1, 16)
+    xs = [make_q(30 + i, 2, 1, 8, 128, "bf16", 0) for i in range(2)]
+    want = [ops.mx_cache_attn(x, f.cache, f.table, f.seq) for x in xs]
+    need = max(16, ops.mx_cache_attn_workspace_bytes(2, 1, 8, 2, 128, f.table.shape[1] * 16))
+    ws = [torch.full((need,), 0xA5, dtype=torch.uint8, device="cuda") for _ in xs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x, w in zip(xs, ws):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ops.mx_cache_attn(x, f.cache, f.table, f.seq, workspace=w))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(bits(o[0]), bits(w[0])) and torch.equal(bits(o[1]), bits(w[1]))
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_extreme_lengths(ops, fmt):
+    """Lengths and starts at the ends of int32 are bad or empty positions, not addresses."""
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    f = Filled(ops, 69, [48, 48], 2, 128, fmt, 16)
+    table = f.table[:, :3].contiguous()
+    q = make_q(40, 2, 2, 4, 128, "bf16", 0)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = ops.mx_cache_attn(q, f.cache, table, i32([lo, hi]), dev_status=st)
+    assert torch.all(o[0] == 0) and torch.all(torch.isneginf(lse[0])) and int(st) == 0x202
+    f.lens = [0, 48]
+    for t in (0, 1):        # far behind the table: every key it has
+        check_attn(f, q[:, t:t + 1], o[:, t:t + 1], lse[:, :, t:t + 1], [1, 1], 128 ** -0.5, 0)
+    o, lse = ops.mx_cache_attn(q, f.cache, table, i32([48, 48]), i32([lo, hi]))
+    f.lens = [48, 48]
+    check_attn(f, q, o, lse, [0, 2], 128 ** -0.5, 0)
+    k, v = ops.mx_cache_read(f.cache, table, i32([hi, lo]), 20, starts=i32([lo, hi]))
+    assert not k.any() and not v.any()
+    before = [p.clone() for p in (f.cache.k, f.cache.k_sc, f.cache.v, f.cache.v_sc)]
+    x = make_q(41, 2, 2, 2, 128, "bf16", 0)
+    st.zero_()
+    ops.mx_cache_write(f.cache, x, x, table, i32([hi, lo]), i32([hi, hi]), dev_status=st)
+    assert int(st) == 0x202
+    for p, b in zip((f.cache.k, f.cache.k_sc, f.cache.v, f.cache.v_sc), before):
+        assert torch.equal(p, b)
+
+
+def test_table_without_pages(ops):
+    """A page table of no columns: nothing is held, and tokens that should be are reported."""
+    cache = ops.mx_cache_alloc(2, 16, 2, 128, 1)
+    table = torch.empty((3, 0), dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, x = make_q(42, 3, 1, 4, 128, "bf16", 0), make_q(43, 3, 1, 2, 128, "bf16", 0)
+    o, lse = ops.mx_cache_attn(q, cache, table, i32([0, 0, 0]), dev_status=st)
+    assert not o.any() and torch.all(torch.isneginf(lse)) and int(st) == 0
+    k, v = ops.mx_cache_read(cache, table, i32([0, 0, 0]), 5, dev_status=st)
+    assert not k.any() and not v.any() and int(st) == 0
+    ops.mx_cache_write(cache, x, x, table, i32([0, 1, 0]), dev_status=st)
+    assert int(st) == 0x202 and not cache.k.any()
+    st.zero_()
+    o, lse = ops.mx_cache_attn(q, cache, table, i32([0, 1, 0]), dev_status=st)
+    assert not o.any() and torch.all(torch.isneginf(lse)) and int(st) == 0x202
 
 
 def test_binding_refusals(ops):
