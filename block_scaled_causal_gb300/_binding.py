@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -427,7 +428,7 @@ class MxCache:
     free, so pools may be slices of one allocation.  The handle keeps the tensors alive and holds no
     other state.  `mx_cache_alloc` makes one with new pools."""
 
-    __slots__ = ("k", "k_sc", "v", "v_sc", "fmt", "num_pages", "page_size", "Hkv", "D", "device", "params")
+    __slots__ = ("k", "k_sc", "v", "v_sc", "fmt", "num_pages", "page_size", "Hkv", "D", "device", "params", "packed")
 
     def __init__(self, k, k_sc, v, v_sc, fmt=CACHE_MXFP4):
         if fmt not in (CACHE_MXFP8, CACHE_MXFP4):
@@ -447,6 +448,7 @@ class MxCache:
         self.device = k.device
         self.params = CachePools(*(t.data_ptr() for t in pools), *(t.stride(0) for t in pools), fmt, pages, page_size,
                                  Hkv, D)
+        self.packed = bytes(self.params)
 
 
 def mx_cache_alloc(num_pages, page_size, Hkv, D=128, fmt=CACHE_MXFP4, device="cuda"):
@@ -487,7 +489,7 @@ def _dense(layout, B, T, H, D):
 def _index(t, B, cache, name):
     """Pointer of an int32 index array of B entries (None: NULL)."""
     if t is None:
-        return None
+        return 0
     if t.dtype is not torch.int32 or t.shape != (B,) or t.device != cache.device:
         raise ValueError("%s must be an int32 tensor of shape (%d,) on the cache's device" % (name, B))
     if B > 1 and t.stride(0) != 1:
@@ -508,7 +510,7 @@ def _table(t, B, cache):
 def _status(t, cache):
     if t is not None and (t.dtype != torch.int32 or t.device != cache.device or t.numel() < 1):
         raise ValueError("dev_status must be an int32 tensor on the cache's device")
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def _elsewhere(cache, stream):
@@ -519,12 +521,29 @@ def _elsewhere(cache, stream):
         if stream.device != cache.device:
             raise ValueError("stream must be on the cache's device")
         return torch.cuda.stream(stream)
-    return None if torch.cuda.current_device() == cache.device.index else torch.cuda.device(cache.device)
+    return None if _current_device() == cache.device.index else torch.cuda.device(cache.device)
 
 
 # The current stream's handle without a Stream object around it (a call's largest host cost after the launches).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _packed_call(name, params, fields):
+    """The C call `name` taking its parameters as packed bytes, and the packer of what follows the cache in them
+    (native sizes and alignment, as ctypes lays `params` out): a quarter of a ctypes structure's time."""
+    f = lib[name]
+    f.restype, f.argtypes = ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]
+    packer = struct.Struct("@" + fields)
+    assert ctypes.sizeof(CachePools) + packer.size == ctypes.sizeof(params)
+    return f, packer.pack
+
+
+# pointers and strides, sizes and codes, then from page_table on
+_c_write, _pack_write = _packed_call("mx_cache_write", CacheWriteParams, "8q4i2qi3q")
+_c_read, _pack_read = _packed_call("mx_cache_read", CacheReadParams, "8q3i2qi3q")
+_c_attn, _pack_attn = _packed_call("mx_cache_attn", CacheAttnParams, "9q4if2qi5q")
 
 
 def mx_cache_write(cache, k, v, page_table, seq_lens, new_lens=None, layout=BSHD, rule=SCALE_FLOOR, dev_status=None,
@@ -541,10 +560,10 @@ def mx_cache_write(cache, k, v, page_table, seq_lens, new_lens=None, layout=BSHD
     B, T, H = dims
     if dims_v != dims or dt_v != dt or H != cache.Hkv:
         raise ValueError("k and v must both have the cache's heads, one shape and one dtype")
-    p = CacheWriteParams(cache.params, k.data_ptr(), v.data_ptr(), *ks, *vs, B, T, dt, rule,
+    p = cache.packed + _pack_write(k.data_ptr(), v.data_ptr(), *ks, *vs, B, T, dt, rule,
                          *_table(page_table, B, cache), _index(seq_lens, B, cache, "seq_lens"),
                          _index(new_lens, B, cache, "new_lens"), _status(dev_status, cache))
-    _check(lib.mx_cache_write(ctypes.byref(p), _raw_stream(cache.device.index)))
+    _check(_c_write(p, _raw_stream(cache.device.index)))
 
 
 def mx_cache_read(cache, page_table, seq_lens, T, starts=None, layout=BSHD, dtype=torch.bfloat16, k_out=None,
@@ -573,10 +592,10 @@ def mx_cache_read(cache, page_table, seq_lens, T, starts=None, layout=BSHD, dtyp
             raise ValueError("v_out must be [B, T, Hkv, D] in the layout")
     if dt is None or dt != dt_v:
         raise ValueError("k_out and v_out must be bfloat16 or float16, of one dtype")
-    p = CacheReadParams(cache.params, k_out.data_ptr(), v_out.data_ptr(), *ks, *vs, B, T, dt,
+    p = cache.packed + _pack_read(k_out.data_ptr(), v_out.data_ptr(), *ks, *vs, B, T, dt,
                         *_table(page_table, B, cache), _index(seq_lens, B, cache, "seq_lens"),
                         _index(starts, B, cache, "starts"), _status(dev_status, cache))
-    _check(lib.mx_cache_read(ctypes.byref(p), _raw_stream(cache.device.index)))
+    _check(_c_read(p, _raw_stream(cache.device.index)))
     return k_out, v_out
 
 
@@ -623,9 +642,9 @@ def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, so
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
         need = workspace.numel() * workspace.element_size()
-    p = CacheAttnParams(cache.params, q.data_ptr(), o.data_ptr(), lse.data_ptr(), *qs, *o_s, B, T, Hq, dt,
+    p = cache.packed + _pack_attn(q.data_ptr(), o.data_ptr(), lse.data_ptr(), *qs, *o_s, B, T, Hq, dt,
                         cache.D ** -0.5 if softmax_scale is None else softmax_scale, *table, _index(seq_lens, B, cache, "seq_lens"),
                         _index(new_lens, B, cache, "new_lens"), _status(dev_status, cache),
-                        workspace.data_ptr() if need else None, need)
-    _check(lib.mx_cache_attn(ctypes.byref(p), _raw_stream(device.index)))
+                        workspace.data_ptr() if need else 0, need)
+    _check(_c_attn(p, _raw_stream(device.index)))
     return o, lse
