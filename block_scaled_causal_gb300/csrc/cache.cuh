@@ -26,18 +26,18 @@ struct Elem {
 };
 
 // The scale byte of a block from its absolute maximum (0xFF for NaN/Inf), and 2^-(byte - 127): the
-// rule of e8m0_from_amax for either format.  fp32-subnormal maxima clamp to byte 0.
+// rule of e8m0_from_amax for either format.  `up` is ceil_carry's: 0 under the floor rule, else what carries a
+// fraction above the largest element's into the exponent.  fp32-subnormal maxima clamp to byte 0.
 template <int FMT>
-__device__ __forceinline__ uint32_t block_scale(float amax, int ceil_rule, float& inv) {
-  const uint32_t bits = __float_as_uint(amax), eb = bits >> 23;
-  if (eb == 0xFFu) {
-    inv = 0.f;
-    return 0xFFu;
-  }
-  const uint32_t up = (ceil_rule && eb > 0u && (bits & 0x7FFFFFu) > Elem<FMT>::top_frac) ? 1u : 0u;
-  const uint32_t sb = eb + up > Elem<FMT>::emax ? eb + up - Elem<FMT>::emax : 0u;
+__device__ __forceinline__ uint32_t ceil_carry(int ceil_rule) {
+  return ceil_rule ? 0x7FFFFFu - Elem<FMT>::top_frac : 0u;
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t block_scale(float amax, uint32_t up, float& inv) {
+  const uint32_t bits = __float_as_uint(amax);
+  const uint32_t sb = max((bits + up) >> 23, Elem<FMT>::emax) - Elem<FMT>::emax;
   inv = __uint_as_float((254u - sb) << 23);   // sb <= 253: a normal fp32
-  return sb;
+  return bits >= 0x7F800000u ? 0xFFu : sb;
 }
 
 // 2^(byte - 127) in fp32; byte 0 is the fp32-subnormal 2^-127, byte 255 NaN.
