@@ -52,6 +52,12 @@ constexpr float SLACK = 4.f;    // a reference moves when a score passes it by t
 constexpr float LIFT = 8.f;     // a reference m gives weights 2^(x + r), r = LIFT - m
 constexpr float UNSET = 3e38f;  // r of a row without a score yet: 2^(-inf + r) = 0, and any score moves it
 
+// Blocks per SM.  Tiles of 8 rows: 3 blocks leave 168 registers, 4 leave 128 and fewer loads and conversions in flight.
+// D = 128, G = 4, 4 bits, 4 blocks / 3: 64 x 6000 keys 50.3 / 48.1 us, 16 x 6000 20.2 / 19.1; but one sequence
+// of 32K 12.7 / 13.7, whose 1024 chunks divide worse by 456.  In 8 bits shared memory holds 3 at most.  Larger tiles
+// need 255 registers.
+constexpr int blocks_per_sm(int tile) { return tile == 8 ? 3 : 2; }
+
 template <int FMT, int D, int NT>
 struct Cfg {
   static constexpr int RB = row_bytes<FMT, D>(), NB = D / 32;
@@ -72,10 +78,7 @@ struct Cfg {
   static constexpr int MERGE = WARPS * ROWS * (D + 4) * 4 + WARPS * ROWS * 8;
   static constexpr int JOINED = MERGE + ROWS * D * 4 + ROWS * 8;   // and the block's own part, in the cluster form
   static constexpr int SMEM = RING + QBYTES > JOINED ? RING + QBYTES : JOINED;
-  // Blocks per SM.  One row tile: 3 blocks leave 168 registers, 4 leave 128 and fewer loads and conversions in flight.
-  // D = 128, G = 4, 4 bits, 4 blocks / 3: 64 x 6000 keys 50.3 / 48.1 us, 16 x 6000 20.2 / 19.1; but one sequence
-  // of 32K 12.7 / 13.7, whose 2048 chunks divide worse by 456.  In 8 bits shared memory holds 3 at most.
-  static constexpr int OCC = NT == 1 ? 3 : 2;
+  static constexpr int OCC = blocks_per_sm(ROWS);
 };
 
 // Byte offset of 16-byte piece c of key k's row in a stage.  Rows of 32, 64 or 128 bytes lie in 128-byte
@@ -914,7 +917,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const CacheAttnArgs a, int row_tiles, int grid,
                                                                           int rows_pb) {
   constexpr int ROWS = 8 * NT, SLOT = ROWS * (D + 1), PL = D / 32;    // columns per lane
-  constexpr int MOST_PARTS = SMS * (NT == 1 ? 3 : 2);                 // blocks of the largest grid
+  constexpr int MOST_PARTS = SMS * blocks_per_sm(ROWS);               // blocks of the largest grid
   __shared__ float zs[MOST_PARTS * (ROWS < JOIN_WARPS ? ROWS : JOIN_WARPS)];   // [row of the block][part]
   __shared__ __align__(16) float part_o[JOIN_WARPS][D];
   __shared__ float part_sum[JOIN_WARPS];
@@ -999,26 +1002,39 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
     a.lse[((long long)b * a.Hq + hq) * a.T + tq] = none ? -INFINITY : (m + __log2f(sum)) * 0.6931471805599453f;
 }
 
-// Short tables: a cluster of this many blocks per unit (1: a block), or 0 for the list.  A cluster joins its parts
-// through shared memory: one launch, no workspace.  But a unit then has 8 blocks at most, whatever the others'
-// lengths, so it is taken only where the longest sequence that the table allows is MOST_CLUSTER_CHUNKS chunks per
-// block.  D = 128, Hkv = 8, 4 bits, cluster / list in us: G = 4, 1 x 500 tokens 5.6 / 7.3, 4 x 1000 6.4 / 8.2,
-// 16 x 2000 9.6 / 13.4, 64 x 512 8.2 / 13.1, 1 x 6000 9.9 / 10.5; G = 16, 4 x 1000 9.6 / 10.7, 1 x 4000 11.1 / 9.6
-// (from 3000 tokens on one sequence of 16 rows loses, and shorter tables win more often).
-constexpr int MOST_CLUSTER_CHUNKS = 6;
-int tile_rows(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
-int cluster_size(long long B, long long rows, int Hkv, long long max_tokens) {
-  const int tile = tile_rows(rows), occ = tile == 8 ? 3 : 2;
-  const long long units = B * Hkv * ((rows + tile - 1) / tile), chunks = (max_tokens + CHUNK - 1) / CHUNK;
-  int cs = 1;
-  while (cs < 8 && cs < chunks && units * cs * 2 <= SMS * occ) cs *= 2;
-  return chunks <= (long long)cs * MOST_CLUSTER_CHUNKS ? cs : 0;
+// How a call is cut up: the rows of a tile, and the blocks of a unit's cluster (1: a block), or 0 for the list.
+struct Plan {
+  int tile, cluster;
+};
+// A cluster joins its parts through shared memory: one launch, no workspace.  But a unit then has 8 blocks at most,
+// whatever the others' lengths, so it is taken only where the longest sequence that the table allows is
+// MOST_CLUSTER_CHUNKS chunks per block.  D = 128, Hkv = 4, 4 bits, cluster / list in us: G = 4, 1 x 500 tokens
+// 5.6 / 7.3, 4 x 1000 6.4 / 8.2, 16 x 2000 9.6 / 13.4, 64 x 512 8.2 / 13.1, 1 x 6000 9.9 / 10.5.
+//
+// Rows.  The smallest tile that takes all rows decodes each key once and is the best for long work.  A smaller one
+// decodes keys again per tile, but each warp has fewer instructions per key tile and more warps fit, which
+// wins while the card is not full: the smallest tile whose clusters all run at once is taken, else the smallest
+// whose list has at most SMALL_LIST chunks.  D = 128, Hkv = 8, 4 bits, tiles of 8 / 16 / 32 in us: 16 rows, 4 x 1000
+// tokens 8.3 / 10.3 / 12.2, 4 x 4000 16.5 / 14.0 / 17.0, 1 x 16000 15.6 / 16.9 / 20.4, 16 x 8000 57.9 / 47.4 / 66.5; 64
+// rows, 4 x 512 8.5 / 11.2 / 14.8, 4 x 1000 17.2 / 13.7 / 16.1, 4 x 2000 23.1 / 21.9 / 20.3, 16 x 4000 112 / 85 / 72.
+constexpr int MOST_CLUSTER_CHUNKS = 6, SMALL_LIST = 2304;
+Plan plan(long long B, long long rows, int Hkv, long long max_tokens) {
+  const int whole = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  const long long chunks = (max_tokens + CHUNK - 1) / CHUNK;
+  for (int tile = 8; tile <= whole; tile *= 2) {
+    const long long units = B * Hkv * ((rows + tile - 1) / tile), slots = SMS * blocks_per_sm(tile);
+    int cs = 1;
+    while (cs < 8 && cs < chunks && units * cs * 2 <= slots) cs *= 2;
+    if (chunks <= (long long)cs * MOST_CLUSTER_CHUNKS && (tile == whole || units <= slots)) return {tile, cs};
+  }
+  for (int tile = 8; tile < whole; tile *= 2)
+    if (B * Hkv * ((rows + tile - 1) / tile) * chunks <= SMALL_LIST) return {tile, 0};
+  return {whole, 0};
 }
 
 template <int FMT, int D, int NT>
-cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
+cudaError_t launch(const CacheAttnArgs& a, int cs, cudaStream_t st) {
   using C = Cfg<FMT, D, NT>;
-  static_assert(C::OCC <= (NT == 1 ? 3 : 2), "the join's table of parts, and the workspace");
   const int rows = a.T * (a.Hq / a.c.Hkv), row_tiles = (rows + C::ROWS - 1) / C::ROWS;
   const long long units = (long long)a.B * a.c.Hkv * row_tiles;
   const long long chunks = ((long long)a.pt.max_pages * a.c.page_size + CHUNK - 1) / CHUNK;
@@ -1040,7 +1056,7 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   cfg.stream = st;
   cfg.attrs = attr;
-  if (const int cs = cluster_size(a.B, rows, a.c.Hkv, (long long)a.pt.max_pages * a.c.page_size)) {
+  if (cs) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)cs;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -1069,18 +1085,20 @@ cudaError_t launch(const CacheAttnArgs& a, cudaStream_t st) {
 
 template <int FMT, int D>
 cudaError_t pick(const CacheAttnArgs& a, cudaStream_t st) {
-  const int tile = tile_rows(a.T * (a.Hq / a.c.Hkv));
-  return tile == 8 ? launch<FMT, D, 1>(a, st) : tile == 16 ? launch<FMT, D, 2>(a, st) : launch<FMT, D, 4>(a, st);
+  const Plan p = plan(a.B, (long long)a.T * (a.Hq / a.c.Hkv), a.c.Hkv, (long long)a.pt.max_pages * a.c.page_size);
+  return p.tile == 8    ? launch<FMT, D, 1>(a, p.cluster, st)
+         : p.tile == 16 ? launch<FMT, D, 2>(a, p.cluster, st)
+                        : launch<FMT, D, 4>(a, p.cluster, st);
 }
 
 }  // namespace
 
 size_t cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long long max_tokens) {
   const long long all = (long long)T * (Hq / Hkv);
-  if (all <= 0 || cluster_size(B, all, Hkv, max_tokens)) return 0;
+  if (all <= 0) return 0;
+  const Plan p = plan(B, all, Hkv, max_tokens);
   // two slots per block of the largest grid of either format
-  const int rows = tile_rows(all), occ = rows == 8 ? 3 : 2;
-  return (size_t)2 * SMS * occ * rows * (D + 1) * 4;
+  return p.cluster ? 0 : (size_t)2 * SMS * blocks_per_sm(p.tile) * p.tile * (D + 1) * 4;
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int format, int D, cudaStream_t st) {

@@ -22,10 +22,11 @@ def ops():
     return _binding
 
 
-@pytest.fixture(autouse=True, params=[0, 8192], ids=["short", "wide"])
+@pytest.fixture(autouse=True, params=[0, 8192, 1 << 20], ids=["short", "wide", "long"])
 def table_width(request):
-    """Every test twice: page tables just wide enough (the attention's cluster form) and 8192 tokens wider
-    (its list form, with parts joined through the workspace)."""
+    """Every test three times, with page tables just wide enough (the attention's cluster form), 8192 tokens wider
+    (its list form, with parts joined through the workspace, mostly in tiles of 8 rows) and 2^20 tokens wider
+    (the list in tiles of 8, 16 or 32 rows)."""
     Filled.more = request.param
     yield
     Filled.more = 0
@@ -294,7 +295,7 @@ def test_read_into_strided_outputs_and_bad_pages(ops):
 
 
 # ----------------------------------------------------------------------------------------- attention
-# query heads over 2 KV heads: a few rows per KV head, two tiles of them, and many (the form that decodes once)
+# query heads over 2 KV heads: with the tests' token counts, up to 8, 16 and many rows per KV head
 HEADS = pytest.mark.parametrize("Hq", [4, 10, 40])
 SHAPES = [
     # lens, T, Hq, Hkv, D, page, dtype, layout
@@ -320,6 +321,26 @@ def test_attn(ops, fmt, lens, T, Hq, Hkv, D, page, dtype, layout):
     o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, layout=layout)
     torch.cuda.synchronize()
     check_attn(f, q, o, lse, [T] * len(lens), D ** -0.5, layout)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "fp16")])
+@pytest.mark.parametrize("T,G,extra", [(2, 8, 5120), (8, 4, 5120), (9, 5, 5120), (3, 4, 0), (5, 6, 0), (33, 1, 0)])
+def test_attn_cluster_tiles(ops, fmt, D, dtype, T, G, extra):
+    """Clusters of several blocks in tiles of 16 and 32 rows: more units than 8-row tiles could have at once, or
+    a table too long for their clusters; ragged, with new_lens, an absent page and NaN behind the sequence."""
+    few = [600, 33, 0, 1, 17, 250, 64, 5, 129, 40, 2, 100, 31, 7, 48]
+    lens = few if extra else few * 4                       # 30 or 120 (sequence, head) pairs
+    f = Filled(ops, 57, lens, 2, D, fmt, 16)
+    f.table = torch.nn.functional.pad(f.table, (0, extra // 16), value=-7)
+    f.table[5, 3] = -1
+    new = [T if b % 3 else T - 1 for b in range(len(lens))]
+    q = make_q(18, len(lens), T, 2 * G, D, dtype, 0)
+    o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, i32(new))
+    gone = set(range(48, 64))
+    for b in range(len(lens)):
+        one = type("F", (), dict(K=[f.K[b]], V=[f.V[b]], lens=[lens[b]]))
+        check_attn(one, q[b:b + 1], o[b:b + 1], lse[b:b + 1], [new[b]], D ** -0.5, 0, gone if b == 5 else None)
 
 
 @HEADS
