@@ -1007,9 +1007,12 @@ struct Plan {
   int tile, cluster;
 };
 // A cluster joins its parts through shared memory: one launch, no workspace.  But a unit then has 8 blocks at most,
-// whatever the others' lengths, so it is taken only where the longest sequence that the table allows is
-// MOST_CLUSTER_CHUNKS chunks per block.  D = 128, Hkv = 4, 4 bits, cluster / list in us: G = 4, 1 x 500 tokens
-// 5.6 / 7.3, 4 x 1000 6.4 / 8.2, 16 x 2000 9.6 / 13.4, 64 x 512 8.2 / 13.1, 1 x 6000 9.9 / 10.5.
+// whatever the others' lengths, so it is taken only where the longest sequence that the table allows is few
+// chunks per block: CLUSTER_CHUNKS where the clusters leave more than half of the card idle, which the list would
+// use, else CLUSTER_CHUNKS_FULL, or CLUSTER_CHUNKS_TILED where a larger tile would do.  D = 128, Hkv = 4, 4 bits,
+// cluster / list in us: 4 rows, 1 x 500 tokens 5.6 / 7.3, 4 x 1000 6.4 / 8.2, 1 x 6000 9.9 / 10.5, 1 x 8000 11.3 / 10.8,
+// 1 x 12000 14.1 / 9.9; 16 x 2000 9.6 / 13.4, 16 x 4000 13.5 / 16.3, 16 x 6000 17.8 / 19.4 (lengths spread from 1/8 of that:
+// 16.1 / 15.6), 64 x 512 8.2 / 13.1, 64 x 1500 16.1 / 19.6 (spread: 14.8 / 16.0), 64 x 2000 20.0 / 22.6.
 //
 // Rows.  The smallest tile that takes all rows decodes each key once and is the best for long work.  A smaller one
 // decodes keys again per tile, but each warp has fewer instructions per key tile and more warps fit, which
@@ -1017,7 +1020,7 @@ struct Plan {
 // whose list has at most SMALL_LIST chunks.  D = 128, Hkv = 8, 4 bits, tiles of 8 / 16 / 32 in us: 16 rows, 4 x 1000
 // tokens 8.3 / 10.3 / 12.2, 4 x 4000 16.5 / 14.0 / 17.0, 1 x 16000 15.6 / 16.9 / 20.4, 16 x 8000 57.9 / 47.4 / 66.5; 64
 // rows, 4 x 512 8.5 / 11.2 / 14.8, 4 x 1000 17.2 / 13.7 / 16.1, 4 x 2000 23.1 / 21.9 / 20.3, 16 x 4000 112 / 85 / 72.
-constexpr int MOST_CLUSTER_CHUNKS = 6, SMALL_LIST = 2304;
+constexpr int CLUSTER_CHUNKS = 6, CLUSTER_CHUNKS_TILED = 8, CLUSTER_CHUNKS_FULL = 12, SMALL_LIST = 2304;
 Plan plan(long long B, long long rows, int Hkv, long long max_tokens) {
   const int whole = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   const long long chunks = (max_tokens + CHUNK - 1) / CHUNK;
@@ -1025,7 +1028,8 @@ Plan plan(long long B, long long rows, int Hkv, long long max_tokens) {
     const long long units = B * Hkv * ((rows + tile - 1) / tile), slots = SMS * blocks_per_sm(tile);
     int cs = 1;
     while (cs < 8 && cs < chunks && units * cs * 2 <= slots) cs *= 2;
-    if (chunks <= (long long)cs * MOST_CLUSTER_CHUNKS && (tile == whole || units <= slots)) return {tile, cs};
+    const int most = units * cs * 2 <= slots ? CLUSTER_CHUNKS : tile < whole ? CLUSTER_CHUNKS_TILED : CLUSTER_CHUNKS_FULL;
+    if (chunks <= (long long)cs * most && (tile == whole || units <= slots)) return {tile, cs};
   }
   for (int tile = 8; tile < whole; tile *= 2)
     if (B * Hkv * ((rows + tile - 1) / tile) * chunks <= SMALL_LIST) return {tile, 0};
