@@ -601,8 +601,8 @@ def mx_cache_read(cache, page_table, seq_lens, T, starts=None, layout=BSHD, dtyp
 
 @functools.lru_cache(maxsize=256)
 def mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D=128, max_tokens=1 << 30):
-    """Bytes of scratch mx_cache_attn needs (the C call of the same name); max_tokens: page_table columns times
-    page size (left out: enough for any table)."""
+    """Bytes of scratch mx_cache_attn needs at these sizes (the C call of the same name); max_tokens: page_table
+    columns times page size (left out: enough for any table)."""
     return int(lib.mx_cache_attn_workspace_bytes(B, T, Hq, Hkv, D, max_tokens))
 
 

@@ -6,7 +6,10 @@
 // What bounds it.  A decode step reads every K and V byte once for the few query rows that share a KV
 // head, so it is bound by memory if the decoding of elements keeps up: at D = 128 a token of one head is
 // 136 bytes in 4 bits, so a full-rate stream leaves about 23 warp instructions per token and SM to decode
-// 256 elements and do both products.  The layout below spends them.
+// 256 elements and do both products.  The layout below spends 20 (8 of them conversions and fp16 scalings), but 12
+// warps per SM issue 2.2 per clock, so 4 bits run at half the copy rate (32 ragged sequences up to 16K, Hkv = 4:
+// 33 us for 116 MB) and 8 bits, with twice the bytes per key, at all of it (16 x 16K, Hkv = 16: 163 us for 1.1 GB).
+// Short work is bound by latency: 5.8 us for one sequence of 500 tokens, 13.7 us for one of 32K.
 //
 // Products.  Scores are taken transposed, S^T = K Q^T, and O^T = V^T P^T, with 16-bit MMAs
 // (mma.sync m16n8k16, fp32 accumulation): keys (then output columns) fill the 16-row side and 8 query
@@ -26,7 +29,8 @@
 // Roundings.  Q is scaled per row by a power of two to [2^14, 2^15) and held in fp16: exact for 16-bit
 // inputs down to 2^-29 of the row's maximum.  Scores, weights' sums and O are fp32.  Weights are rounded to
 // fp16 for the second product (2^-11 relative at most, and each weight on its own; the output's own rounding is
-// 2^-8 or 2^-11 of the result), around 2^8 at the reference so that only weights under 2^-22 of the largest lose relative precision.
+// 2^-8 or 2^-11 of the result), around 2^8 at the reference so that only weights under 2^-22 of the largest lose
+// relative precision.
 //
 // Work.  A warp takes 32 keys at a time through its own ring of shared-memory stages (cp.async, 16
 // bytes per lane, rows permuted so that both fragments read without bank conflicts); a block is 4 warps on
@@ -34,7 +38,7 @@
 // list, which the blocks split into equal runs: a long sequence spreads over the card and ragged batches stay
 // balanced, whatever the lengths, which only the device knows.  A run that covers a unit writes O; one
 // that covers part of it writes (O, log-sum-exp) to the workspace, two slots per block at most, and a second
-// kernel joins them in order.
+// kernel joins them in order.  Short tables take a cluster per unit instead (plan() has the rule and both sides).
 #include <atomic>
 #include <cooperative_groups.h>
 
@@ -231,7 +235,8 @@ __device__ __forceinline__ int seq_of_chunk(const CacheAttnArgs& a, uint32_t x, 
 }
 // How the list is shared: n blocks, the first `more` of them with each + 1 chunks, the others with `each`.
 // A block costs a prologue and a part to join, so a block per chunk is taken only while there are fewer chunks than
-// SMs, and then MIN_CHUNKS chunks each until the grid is full.
+// SMs, and then MIN_CHUNKS chunks each until the grid is full (2 chunks at least: one sequence of 32K 12.7 us; 3 to 6:
+// 14.5 and more).
 struct Share {
   uint32_t n, each, more;
   __device__ __forceinline__ Share(uint32_t total, uint32_t grid) {
@@ -911,7 +916,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 // are spread over the rows, and over the parts of a row where there are more warps than rows.  The log-sum-exps
 // come in first, all at once, then every part's O is loaded independently: two latencies, whatever the
 // number of parts.  It is launched while the first kernel still runs (programmatic dependence) and waits for
-// it before it touches the workspace or O.
+// it before it touches the workspace or O.  Alone and cold it takes 8 to 11 us, bound by latency; behind the first
+// kernel about 3 are left (one part after another instead: 22 us alone).
 constexpr int JOIN_WARPS = 16;
 template <int D, int NT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const CacheAttnArgs a, int row_tiles, int grid,

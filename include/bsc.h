@@ -406,15 +406,16 @@ typedef struct {
  * Rows that attend nothing (t >= n_b, p < 0, an empty sequence) get O = 0 and LSE = -inf.
  * Row p is bit-for-bit independent of what positions after p hold, NaN and infinities included.
  * Finite V is taken up to 2^100 in magnitude, and a block of scale byte 0 (a maximum under 2^-118) counts
- * as zeros.  A NaN block of K makes the rows that attend it NaN, one of V their columns of that block.  The result does not depend on the stream, on other calls
- * or on timing (no atomics); it may differ in the last bits with the batch's lengths, which decide
- * how the keys are split.
+ * as zeros.  A NaN block of K makes the rows that attend it NaN, one of V their columns of that block.
+ * The result does not depend on the stream, on other calls or on timing (no atomics); it may differ in the
+ * last bits with the batch's sizes, lengths and table, which decide how the keys are split.
  */
 bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream);
 
 /* Bytes of workspace mx_cache_attn needs at these sizes, whatever the lengths are; max_tokens =
  * max_pages * page_size.  0 where it needs none (short tables; then workspace may be NULL) and if a
- * size is not positive.  Host only, no CUDA call. */
+ * size is not positive.  Smaller sizes may need more than larger ones: ask for each that is used.
+ * Host only, no CUDA call. */
 size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long long max_tokens);
 
 /*
