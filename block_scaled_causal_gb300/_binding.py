@@ -426,7 +426,10 @@ class MxCache:
     k, v [num_pages, Hkv, page_size, D] (CACHE_MXFP8) or [..., D/2] (CACHE_MXFP4); k_sc, v_sc
     [num_pages, Hkv, page_size, D/32].  Dimensions after the first are contiguous; the page stride is
     free, so pools may be slices of one allocation.  The handle keeps the tensors alive and holds no
-    other state.  `mx_cache_alloc` makes one with new pools."""
+    other state.  `mx_cache_alloc` makes one with new pools.
+
+    The calls' `stream` works like torch.cuda.stream(stream) around them: the caller sees to it that what other
+    streams wrote is ready, and that the tensors live until the call has run."""
 
     __slots__ = ("k", "k_sc", "v", "v_sc", "fmt", "num_pages", "page_size", "Hkv", "D", "device", "params", "packed")
 

@@ -916,8 +916,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 // are spread over the rows, and over the parts of a row where there are more warps than rows.  The log-sum-exps
 // come in first, all at once, then every part's O is loaded independently: two latencies, whatever the
 // number of parts.  It is launched while the first kernel still runs (programmatic dependence) and waits for
-// it before it touches the workspace or O.  Alone and cold it takes 8 to 11 us, bound by latency; behind the first
-// kernel about 3 are left (one part after another instead: 22 us alone).
+// it before it touches the workspace or O.  Alone and cold it takes 8 to 11 us, bound by latency
+// (one part after another instead: 22 us).
 constexpr int JOIN_WARPS = 16;
 template <int D, int NT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const CacheAttnArgs a, int row_tiles, int grid,
