@@ -1,4 +1,4 @@
-// What the kernels of the key/value cache share: element formats, scale rule, addresses.
+// What the kernels of the key/value cache share: element formats, scale rule, addresses, launch.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -110,6 +110,34 @@ __device__ __forceinline__ int cache_page(const CachePools& c, const CacheTable&
     return -1;
   }
   return page;
+}
+
+// Programmatic dependence.  A cache kernel of at most one block per SM lets the next one of the stream be launched as soon
+// as its own blocks run, and every one touches no memory before the one ahead of it has finished: of a step's
+// write and attention, the second's launch is hidden behind the first.  (A token each, written and read
+// back: 4.55 -> 3.7 us.  With larger grids the next kernel's waiting blocks are in the way: 8 ragged prompts written
+// and read 35.0 -> 35.9 us, 368 blocks of attention 10.9 -> 11.4.)
+constexpr unsigned EARLY_BLOCKS = 152;
+__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A launch that may start early; cluster: blocks per cluster (1: none).
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, int block, size_t smem, cudaStream_t st, int cluster, const A&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace bsc

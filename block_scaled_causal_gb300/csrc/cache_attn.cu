@@ -553,12 +553,14 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
   const int G = a.Hq / a.c.Hkv, U = a.c.Hkv * row_tiles, page_size = a.c.page_size;
   const int R = a.T * G;
 
+  wait_for_last_kernel();
+  // the joining kernel comes next in the list form; not before the wait, as it reads the lengths ahead of its own
+  if (!CLUSTER || gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
   // List form (cs = 0): this block's run of the list.  Cluster form: unit blockIdx.x / cs, every cs-th chunk.
   uint32_t base = 0, x = 0, x_end = 1;
   const int unit = cs ? blockIdx.x / cs : 0, rank = cs ? blockIdx.x - unit * cs : 0;
   int b = cs ? unit / U : 0;
   if (cs == 0) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Share share(chunks_of_all(a, U, 0, base), gridDim.x);
     if (blockIdx.x >= share.n) return;
     x = share.first(blockIdx.x);
@@ -946,7 +948,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
   } else if (__ldg(a.pt.seq_lens + b) > 0 && threadIdx.x == 0 && a.dev_status) {
     *a.dev_status = CACHE_BAD_LEN;      // tokens, but a table without pages
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_last_kernel();
   if (!mine) return;
   // part i of a row: block i0 + i; the first one holds its share in its odd slot, the others in their even one
   const float* const ws = reinterpret_cast<const float*>(a.ws) + 2LL * i0 * SLOT;
@@ -1062,35 +1064,16 @@ cudaError_t launch(const CacheAttnArgs& a, int cs, cudaStream_t st) {
       opted.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
   }
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  cfg.stream = st;
-  cfg.attrs = attr;
-  if (cs) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cs;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(units * cs));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.numAttrs = cs > 1;
-    return cudaLaunchKernelEx(&cfg, cache_attn_kernel<FMT, D, NT, true>, a, row_tiles, cs);
-  }
+  if (cs) return launch_early(cache_attn_kernel<FMT, D, NT, true>, (unsigned)(units * cs), THREADS, C::SMEM, st, cs, a, row_tiles, cs);
   const long long grid = units * chunks < SMS * C::OCC ? units * chunks : SMS * C::OCC;
   if (grid > 0) {
-    cache_attn_kernel<FMT, D, NT, false><<<(unsigned)grid, THREADS, C::SMEM, st>>>(a, row_tiles, 0);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_early(cache_attn_kernel<FMT, D, NT, false>, (unsigned)grid, THREADS, C::SMEM, st, 1, a, row_tiles, 0);
     if (e != cudaSuccess) return e;
   }
   // few units have many parts each: as many blocks per unit as the card takes at once
   int rows_pb = C::ROWS < JOIN_WARPS ? C::ROWS : JOIN_WARPS;
   while (rows_pb > 1 && units * (C::ROWS / rows_pb) * 2 <= SMS * 2) rows_pb /= 2;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(units * (C::ROWS / rows_pb)));
-  cfg.blockDim = dim3(JOIN_WARPS * 32);
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, NT>, a, row_tiles, (int)grid, rows_pb);
+  return launch_early(cache_attn_join_kernel<D, NT>, (unsigned)(units * (C::ROWS / rows_pb)), JOIN_WARPS * 32, 0, st, 1, a, row_tiles, (int)grid, rows_pb);
 }
 
 template <int FMT, int D>

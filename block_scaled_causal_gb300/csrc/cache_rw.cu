@@ -58,8 +58,11 @@ template <int FMT, int D, int DT>
 __global__ void __launch_bounds__(RW_WARPS * 32) cache_write_kernel(const CacheRwArgs a) {
   constexpr int LPR = D / 16, RPI = 32 / LPR, NI = RW_TOKENS / RPI;   // lanes per row, rows per access, accesses
   constexpr int RB = row_bytes<FMT, D>(), NB = D / 32;
+  if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
   Piece w;
-  if (!piece_of(a, w)) return;
+  const bool mine = piece_of(a, w);
+  wait_for_last_kernel();
+  if (!mine) return;
   const int lane = threadIdx.x & 31, sub = lane / LPR, blk = lane % LPR >> 1, half = lane & 1;
   const long long len = __ldg(a.pt.seq_lens + w.b);
   const int n = a.first ? min(max(__ldg(a.first + w.b), 0), a.T) : a.T;
@@ -156,8 +159,11 @@ template <int FMT, int D, int DT>
 __global__ void __launch_bounds__(RW_WARPS * 32) cache_read_kernel(const CacheRwArgs a) {
   constexpr int LPR = D / 16, RPI = 32 / LPR, NI = RW_TOKENS / RPI;
   constexpr int RB = row_bytes<FMT, D>(), NB = D / 32, PB = RB / (D / 8);
+  if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
   Piece w;
-  if (!piece_of(a, w)) return;
+  const bool mine = piece_of(a, w);
+  wait_for_last_kernel();
+  if (!mine) return;
   const int lane = threadIdx.x & 31, sub = lane / LPR, blk = lane % LPR >> 1, half = lane & 1;
   const long long len = __ldg(a.pt.seq_lens + w.b), start = a.first ? __ldg(a.first + w.b) : 0;
   const int rows = min(a.T - w.t0, RW_TOKENS);
@@ -233,8 +239,7 @@ __global__ void __launch_bounds__(RW_WARPS * 32) cache_read_kernel(const CacheRw
 using Kernel = void (*)(CacheRwArgs);
 cudaError_t launch(Kernel k, const CacheRwArgs& a, cudaStream_t st) {
   const long long warps = 2LL * a.B * ((a.T + RW_TOKENS - 1) / RW_TOKENS) * a.c.Hkv;
-  k<<<(unsigned)((warps + RW_WARPS - 1) / RW_WARPS), RW_WARPS * 32, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(k, (unsigned)((warps + RW_WARPS - 1) / RW_WARPS), RW_WARPS * 32, 0, st, 1, a);
 }
 
 }  // namespace

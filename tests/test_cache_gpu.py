@@ -535,6 +535,86 @@ def test_streams_and_graphs(ops, Hq):
         assert same(out, want)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_in_a_row_keep_their_order(ops, captured):
+    """Launches may start early, but every call sees what is ahead of it in its stream and nothing behind it: inputs,
+    lengths and cache changed by slow kernels and by other calls between two attentions, across two streams too."""
+    B, Hq, Hkv, D, n = 3, 8, 2, 128, 300
+    f = Filled(ops, 71, [n] * B, Hkv, D, 1, 16)
+    kv = [make_q(50 + i, B, 1, Hkv, D, "bf16", 0) for i in range(4)]
+    qs = [make_q(60 + i, B, 1, Hq, D, "bf16", 0) for i in range(2)]
+    lens2 = f.seq - 7
+    x, lens = torch.zeros_like(qs[0]), f.seq.clone()
+    side = torch.cuda.Stream()
+
+    def steps(slow):
+        outs = []
+        main = torch.cuda.current_stream()
+        for i in range(2):
+            if slow:
+                torch.cuda._sleep(200000)
+            x.copy_(qs[i])
+            lens.copy_(lens2 if i else f.seq)
+            ops.mx_cache_write(f.cache, kv[2 * i], kv[2 * i + 1], f.table, lens)
+            outs += ops.mx_cache_attn(x, f.cache, f.table, lens)
+            x.zero_()                                         # behind the call that reads it
+            lens.zero_()
+            lens.copy_(f.seq)
+            ops.mx_cache_write(f.cache, kv[3 - 2 * i], kv[2 - 2 * i], f.table, lens)      # and behind the attention
+            outs += ops.mx_cache_read(f.cache, f.table, lens, 3, starts=lens - 3)
+            side.wait_stream(main)
+            if slow:
+                torch.cuda._sleep(200000)
+            x.copy_(qs[1 - i])
+            with torch.cuda.stream(side):
+                if slow:
+                    torch.cuda._sleep(300000)
+                ops.mx_cache_write(f.cache, kv[0], kv[1], f.table, lens)
+            main.wait_stream(side)
+            outs += ops.mx_cache_attn(x, f.cache, f.table, lens)
+        return outs
+
+    steps(False)             # leaves the two slots that every pass writes as every later pass finds them
+    want = steps(False)
+    torch.cuda.synchronize()
+    want = [o.clone() for o in want]
+    again = steps(False)
+    torch.cuda.synchronize()
+    for o, w in zip(again, want):
+        assert torch.equal(o.view(torch.uint8), w.view(torch.uint8))
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = steps(True)
+        for _ in range(5):
+            g.replay()
+    else:
+        for _ in range(5):
+            got = steps(True)
+    torch.cuda.synchronize()
+    for o, w in zip(got, want):
+        assert torch.equal(o.view(torch.uint8), w.view(torch.uint8))
+    # against separate, synchronised calls
+    for i in range(2):
+        lens.copy_(lens2 if i else f.seq)
+        ops.mx_cache_write(f.cache, kv[2 * i], kv[2 * i + 1], f.table, lens)
+        torch.cuda.synchronize()
+        o, lse = ops.mx_cache_attn(qs[i], f.cache, f.table, lens)
+        torch.cuda.synchronize()
+        assert torch.equal(bits(o), bits(want[6 * i])) and torch.equal(bits(lse), bits(want[6 * i + 1]))
+        lens.copy_(f.seq)
+        ops.mx_cache_write(f.cache, kv[3 - 2 * i], kv[2 - 2 * i], f.table, lens)
+        torch.cuda.synchronize()
+        k, v = ops.mx_cache_read(f.cache, f.table, lens, 3, starts=lens - 3)
+        torch.cuda.synchronize()
+        assert torch.equal(bits(k), bits(want[6 * i + 2])) and torch.equal(bits(v), bits(want[6 * i + 3]))
+        ops.mx_cache_write(f.cache, kv[0], kv[1], f.table, lens)
+        torch.cuda.synchronize()
+        o, lse = ops.mx_cache_attn(qs[1 - i], f.cache, f.table, lens)
+        torch.cuda.synchronize()
+        assert torch.equal(bits(o), bits(want[6 * i + 4])) and torch.equal(bits(lse), bits(want[6 * i + 5]))
+
+
 def test_two_host_threads(ops):
     """Calls of several host threads, each on its own stream, give the single call's bits."""
     f = Filled(ops, 67, [700, 90, 0], 2, 64, 0, 32)
