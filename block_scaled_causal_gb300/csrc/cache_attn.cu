@@ -9,7 +9,7 @@
 // 256 elements and do both products.  The layout below spends 20 (8 of them conversions and fp16 scalings), but 12
 // warps per SM issue 2.2 per clock, so 4 bits run at half the copy rate (32 ragged sequences up to 16K, Hkv = 4:
 // 33 us for 116 MB) and 8 bits, with twice the bytes per key, at all of it (16 x 16K, Hkv = 16: 163 us for 1.1 GB).
-// Short work is bound by latency: 5.8 us for one sequence of 500 tokens, 13.7 us for one of 32K.
+// Short work is bound by latency: 5.6 us for one sequence of 500 tokens, 13.4 us for one of 32K.
 //
 // Products.  Scores are taken transposed, S^T = K Q^T, and O^T = V^T P^T, with 16-bit MMAs
 // (mma.sync m16n8k16, fp32 accumulation): keys (then output columns) fill the 16-row side and 8 query

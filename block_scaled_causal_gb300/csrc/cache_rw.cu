@@ -10,15 +10,16 @@
 // What bounds them.  Memory, once the instructions are few enough: 8 elements per lane and access (4 lanes to a
 // block) took 950 warp instructions per warp in the write and 724 in the read, and both ran at the issue
 // rate (22 and 17 us for 32K tokens of 4 heads, 85 MB); 16 elements per lane share the block's scale, addresses and
-// shuffles.  Write then read of those, 4 bits, captured together: 34.6 -> 29.1 us (5.8 TB/s of 170 MB); of 8
-// ragged prompts in 8 bits 38.9 -> 35.0 us; a read alone of 4 x 16K tokens of 16 heads 100.8 us (6.7 TB/s).
+// shuffles.  Write then read of those, 4 bits, captured together: 34.6 -> 28.5 us (6.0 TB/s of 170 MB); of 8
+// ragged prompts in 8 bits 38.9 -> 35.1 us; a read alone of 4 x 16K tokens of 16 heads 100.7 us (6.7 TB/s).
 #include "cache.cuh"
 
 namespace bsc {
 namespace {
 
-constexpr int RW_TOKENS = 16;   // tokens per warp
-constexpr int RW_WARPS = 4;
+// Tokens per warp, warps per block: 32 tokens, or 2 or 8 warps, are within 2% on long prompts; 8 ragged prompts take
+// 35.0 us with 16 and 4, 35.7 with 32, 37.1 and 35.8 with 2 and 8 warps.
+constexpr int RW_TOKENS = 16, RW_WARPS = 4;
 
 // Which piece of the work a warp has.
 struct Piece {
