@@ -123,7 +123,8 @@ __device__ __forceinline__ void wait_for_last_kernel() { asm volatile("griddepco
 
 // A launch that may start early; cluster: blocks per cluster (1: none).
 template <class... P, class... A>
-cudaError_t launch_early(void (*kernel)(P...), unsigned grid, int block, size_t smem, cudaStream_t st, int cluster, const A&... args) {
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, int block, size_t smem, cudaStream_t st, int cluster,
+                         const A&... args) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

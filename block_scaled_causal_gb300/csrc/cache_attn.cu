@@ -1064,16 +1064,20 @@ cudaError_t launch(const CacheAttnArgs& a, int cs, cudaStream_t st) {
       opted.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
   }
-  if (cs) return launch_early(cache_attn_kernel<FMT, D, NT, true>, (unsigned)(units * cs), THREADS, C::SMEM, st, cs, a, row_tiles, cs);
+  if (cs)
+    return launch_early(cache_attn_kernel<FMT, D, NT, true>, (unsigned)(units * cs), THREADS, C::SMEM, st, cs, a, row_tiles,
+                        cs);
   const long long grid = units * chunks < SMS * C::OCC ? units * chunks : SMS * C::OCC;
   if (grid > 0) {
-    const cudaError_t e = launch_early(cache_attn_kernel<FMT, D, NT, false>, (unsigned)grid, THREADS, C::SMEM, st, 1, a, row_tiles, 0);
+    const cudaError_t e =
+        launch_early(cache_attn_kernel<FMT, D, NT, false>, (unsigned)grid, THREADS, C::SMEM, st, 1, a, row_tiles, 0);
     if (e != cudaSuccess) return e;
   }
   // few units have many parts each: as many blocks per unit as the card takes at once
   int rows_pb = C::ROWS < JOIN_WARPS ? C::ROWS : JOIN_WARPS;
   while (rows_pb > 1 && units * (C::ROWS / rows_pb) * 2 <= SMS * 2) rows_pb /= 2;
-  return launch_early(cache_attn_join_kernel<D, NT>, (unsigned)(units * (C::ROWS / rows_pb)), JOIN_WARPS * 32, 0, st, 1, a, row_tiles, (int)grid, rows_pb);
+  return launch_early(cache_attn_join_kernel<D, NT>, (unsigned)(units * (C::ROWS / rows_pb)), JOIN_WARPS * 32, 0, st, 1, a,
+                      row_tiles, (int)grid, rows_pb);
 }
 
 template <int FMT, int D>
