@@ -104,7 +104,7 @@ __device__ __forceinline__ int cache_page(const CachePools& c, const CacheTable&
   }
   const uint32_t lp = (uint32_t)pos / (uint32_t)c.page_size;
   row = (uint32_t)h * c.page_size + (uint32_t)pos - lp * c.page_size;
-  const int page = __ldg(pt.table + b * pt.stride + lp);
+  const int page = __ldca(pt.table + b * pt.stride + lp);
   if (page < 0 || page >= c.num_pages) {
     bad = CACHE_BAD_PAGE;
     return -1;
@@ -117,6 +117,11 @@ __device__ __forceinline__ int cache_page(const CachePools& c, const CacheTable&
 // write and attention, the second's launch is hidden behind the first.  (A token each, written and read
 // back: 4.55 -> 3.7 us.  With larger grids the next kernel's waiting blocks are in the way: 8 ragged prompts written
 // and read 35.0 -> 35.9 us, 368 blocks of attention 10.9 -> 11.4.)
+//
+// A kernel gives the signal after its own wait, never before: then all but one of the kernels ahead of a resident block have
+// finished, and that one loads nothing that it stores, so no L1 can hold an old copy of what the block reads once
+// its wait is over.  Nor is anything read by ld.global.nc (__ldg), which may take it for constant while a kernel lives and
+// promises nothing of stores made meanwhile: lengths, page ids, queries and scales come by ordinary loads (__ldca).
 constexpr unsigned EARLY_BLOCKS = 152;
 __device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

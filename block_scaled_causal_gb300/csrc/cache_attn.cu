@@ -195,7 +195,7 @@ __device__ __forceinline__ const uint8_t* unit_at(const uint8_t* pool, uint32_t 
 // has checked that the longest list the page table allows has fewer than 2^31 chunks.
 __device__ __forceinline__ int seq_len(const CacheAttnArgs& a, int b) {
   const int cap = a.pt.max_pages * a.c.page_size;   // < 2^31
-  return min(max(__ldg(a.pt.seq_lens + b), 0), cap);
+  return min(max(__ldca(a.pt.seq_lens + b), 0), cap);
 }
 __device__ __forceinline__ uint32_t chunks_of(const CacheAttnArgs& a, int b, int U) {
   return b < a.B ? (uint32_t)((seq_len(a, b) + (CHUNK - 1)) / CHUNK) * U : 0u;
@@ -604,8 +604,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
       count = min(n_chunks - c0, (int)(x_end - x));
     }
     const int h = u / row_tiles, rt = u - h * row_tiles;
-    const int raw_len = max(__ldg(a.pt.seq_lens + b), 0);
-    const int n_new = a.new_lens ? min(max(__ldg(a.new_lens + b), 0), a.T) : a.T;
+    const int raw_len = max(__ldca(a.pt.seq_lens + b), 0);
+    const int n_new = a.new_lens ? min(max(__ldca(a.new_lens + b), 0), a.T) : a.T;
     if (raw_len > len && tid == 0 && a.dev_status) *a.dev_status = CACHE_BAD_LEN;
 
     // ---- Q's loads start: lane (g, t) has elements KE t .. KE t + KE - 1 of query row g of each 8-row tile ----
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
       const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + b * a.qs.b + tq * a.qs.t + hq * a.qs.h + t * C::KE;
 #pragma unroll
       for (int i = 0; i < C::KE / 8; ++i)
-        q_in[nt][i] = r < R ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+        q_in[nt][i] = r < R ? __ldca(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
     }
 
     // ---- the warp's tiles: keys (c0 + i step) CHUNK + warp KT + [0, KT); only the last can be past the end ----
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
           if (i < n_tiles && key < len) {
             const int lp = key / page_size;
             w_row = (uint32_t)(h * page_size + key - lp * page_size);
-            w_page = __ldg(a.pt.table + b * a.pt.stride + lp);
+            w_page = __ldca(a.pt.table + b * a.pt.stride + lp);
             if (w_page < 0 || w_page >= a.c.num_pages) {
               w_page = -1;
               if (a.dev_status) *a.dev_status = CACHE_BAD_PAGE;
@@ -945,7 +945,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
     i0 = share.block(x0);
     parts = (int)(share.block(x0 + n_chunks - 1) - i0) + 1;
     if (parts == 1) mine = false;       // one block had the whole unit and wrote it
-  } else if (__ldg(a.pt.seq_lens + b) > 0 && threadIdx.x == 0 && a.dev_status) {
+  } else if (__ldca(a.pt.seq_lens + b) > 0 && threadIdx.x == 0 && a.dev_status) {
     *a.dev_status = CACHE_BAD_LEN;      // tokens, but a table without pages
   }
   wait_for_last_kernel();

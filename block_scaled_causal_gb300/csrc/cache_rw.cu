@@ -59,14 +59,14 @@ template <int FMT, int D, int DT>
 __global__ void __launch_bounds__(RW_WARPS * 32) cache_write_kernel(const CacheRwArgs a) {
   constexpr int LPR = D / 16, RPI = 32 / LPR, NI = RW_TOKENS / RPI;   // lanes per row, rows per access, accesses
   constexpr int RB = row_bytes<FMT, D>(), NB = D / 32;
-  if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
   Piece w;
   const bool mine = piece_of(a, w);
   wait_for_last_kernel();
+  if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
   if (!mine) return;
   const int lane = threadIdx.x & 31, sub = lane / LPR, blk = lane % LPR >> 1, half = lane & 1;
-  const long long len = __ldg(a.pt.seq_lens + w.b);
-  const int n = a.first ? min(max(__ldg(a.first + w.b), 0), a.T) : a.T;
+  const long long len = __ldca(a.pt.seq_lens + w.b);
+  const int n = a.first ? min(max(__ldca(a.first + w.b), 0), a.T) : a.T;
   const int rows = min(n - w.t0, RW_TOKENS);
   if (rows <= 0) return;
 
@@ -160,13 +160,13 @@ template <int FMT, int D, int DT>
 __global__ void __launch_bounds__(RW_WARPS * 32) cache_read_kernel(const CacheRwArgs a) {
   constexpr int LPR = D / 16, RPI = 32 / LPR, NI = RW_TOKENS / RPI;
   constexpr int RB = row_bytes<FMT, D>(), NB = D / 32, PB = RB / (D / 8);
-  if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
   Piece w;
   const bool mine = piece_of(a, w);
   wait_for_last_kernel();
+  if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
   if (!mine) return;
   const int lane = threadIdx.x & 31, sub = lane / LPR, blk = lane % LPR >> 1, half = lane & 1;
-  const long long len = __ldg(a.pt.seq_lens + w.b), start = a.first ? __ldg(a.first + w.b) : 0;
+  const long long len = __ldca(a.pt.seq_lens + w.b), start = a.first ? __ldca(a.first + w.b) : 0;
   const int rows = min(a.T - w.t0, RW_TOKENS);
   Rows at{-1, -1, 0, 0, false};
   int32_t bad = 0;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(RW_WARPS * 32) cache_read_kernel(const CacheRw
   uint2 v[NI][2];                                 // the two pieces' bytes
   uint32_t sb[NI];
   auto load = [&](int i, const uint8_t* src, const uint8_t* sc) {
-    sb[i] = __ldg(sc);
+    sb[i] = __ldca(sc);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (FMT == CACHE_FP4) v[i][k].x = __ldcs(reinterpret_cast<const uint32_t*>(src + 2 * k * PB));
