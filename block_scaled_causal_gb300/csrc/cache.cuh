@@ -113,10 +113,10 @@ __device__ __forceinline__ int cache_page(const CachePools& c, const CacheTable&
 }
 
 // Programmatic dependence.  A cache kernel of at most one block per SM lets the next one of the stream be launched as soon
-// as its own blocks run, and every one touches no memory before the one ahead of it has finished: of a step's
-// write and attention, the second's launch is hidden behind the first.  (A token each, written and read
-// back: 4.55 -> 3.7 us.  With larger grids the next kernel's waiting blocks are in the way: 8 ragged prompts written
-// and read 35.0 -> 35.9 us, 368 blocks of attention 10.9 -> 11.4.)
+// as its own blocks run, and every one touches no memory before the one ahead of it has finished (but for the lengths
+// that an attention's join reads, see there): of a step's write and attention, the second's launch is hidden behind
+// the first.  (A token each, written and read back: 4.55 -> 3.7 us.  With larger grids the next kernel's waiting blocks
+// are in the way: 8 ragged prompts written and read 35.0 -> 35.9 us, 368 blocks of attention 10.9 -> 11.4.)
 //
 // A kernel gives the signal after its own wait, never before: then all but one of the kernels ahead of a resident block have
 // finished, and that one loads nothing that it stores, so no L1 can hold an old copy of what the block reads once

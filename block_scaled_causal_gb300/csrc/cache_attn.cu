@@ -918,7 +918,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 // are spread over the rows, and over the parts of a row where there are more warps than rows.  The log-sum-exps
 // come in first, all at once, then every part's O is loaded independently: two latencies, whatever the
 // number of parts.  It is launched while the first kernel still runs (programmatic dependence) and waits for
-// it before it touches the workspace or O.  Alone and cold it takes 8 to 11 us, bound by latency
+// it before it touches the workspace or O; the lengths it reads ahead of that, which the first kernel allows by its signal:
+// that comes after its own wait for whoever wrote them.  Alone and cold it takes 8 to 11 us, bound by latency
 // (one part after another instead: 22 us).
 constexpr int JOIN_WARPS = 16;
 template <int D, int NT>
@@ -945,8 +946,6 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
     i0 = share.block(x0);
     parts = (int)(share.block(x0 + n_chunks - 1) - i0) + 1;
     if (parts == 1) mine = false;       // one block had the whole unit and wrote it
-  } else if (__ldca(a.pt.seq_lens + b) > 0 && threadIdx.x == 0 && a.dev_status) {
-    *a.dev_status = CACHE_BAD_LEN;      // tokens, but a table without pages
   }
   wait_for_last_kernel();
   if (!mine) return;
@@ -1067,12 +1066,10 @@ cudaError_t launch(const CacheAttnArgs& a, int cs, cudaStream_t st) {
   if (cs)
     return launch_early(cache_attn_kernel<FMT, D, NT, true>, (unsigned)(units * cs), THREADS, C::SMEM, st, cs, a, row_tiles,
                         cs);
-  const long long grid = units * chunks < SMS * C::OCC ? units * chunks : SMS * C::OCC;
-  if (grid > 0) {
-    const cudaError_t e =
-        launch_early(cache_attn_kernel<FMT, D, NT, false>, (unsigned)grid, THREADS, C::SMEM, st, 1, a, row_tiles, 0);
-    if (e != cudaSuccess) return e;
-  }
+  const long long grid = units * chunks < SMS * C::OCC ? units * chunks : SMS * C::OCC;   // no list without chunks: plan()
+  const cudaError_t e =
+      launch_early(cache_attn_kernel<FMT, D, NT, false>, (unsigned)grid, THREADS, C::SMEM, st, 1, a, row_tiles, 0);
+  if (e != cudaSuccess) return e;
   // few units have many parts each: as many blocks per unit as the card takes at once
   int rows_pb = C::ROWS < JOIN_WARPS ? C::ROWS : JOIN_WARPS;
   while (rows_pb > 1 && units * (C::ROWS / rows_pb) * 2 <= SMS * 2) rows_pb /= 2;
