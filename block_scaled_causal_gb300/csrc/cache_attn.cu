@@ -22,8 +22,9 @@
 //   * P: the score fragment (keys x queries) becomes the P^T operand by one 8x8 transpose per 8 keys.
 // E2M1 and E4M3 are exact in fp16, and so is their product with 2^(scale + OFF) while that is in fp16's
 // range: scale exponents -16..11 (4 bits) or -19..2 (8 bits), block maxima from about 2^-14 or 2^-11
-// to 2^13 or 2^11.  A key with a scale outside of that (or a NaN block) takes the scalar path below in
-// fp32; keys are sorted one by one, by their own bytes, so a row never depends on a key it cannot see.
+// to 2^13 or 2^11.  A key with a scale outside of that (or a NaN block, or, in tiles with keys that some row does
+// not see, an E4M3 NaN code in V) takes the scalar path below in fp32; keys are sorted one by one, by their own
+// bytes, so a row never depends on a key it cannot see.
 // Scale byte 0 (a zero block, or a maximum under 2^-118) counts as zero.
 //
 // Roundings.  Q is scaled per row by a power of two to [2^14, 2^15) and held in fp16: exact for 16-bit
@@ -144,6 +145,19 @@ __device__ __forceinline__ bool scales_in_range(uint32_t w) {
   const uint32_t beyond = add4(w, ((127u - C::HI) & 0xFFu) * 0x01010101u);    // top bit: byte > HI, or 0
   const uint32_t nonzero = ((w & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | w;             // top bit: byte != 0
   return (((above & ~beyond) | ~nonzero) & 0x80808080u) == 0x80808080u;
+}
+
+// Whether a row of E4M3 in shared memory has a NaN code (0x7F under the sign).
+template <int RB>
+__device__ __forceinline__ bool row_has_nan(const uint8_t* rows, int k) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < RB / 16; ++i) {
+    const uint4 w = *reinterpret_cast<const uint4*>(rows + piece_at<RB>(k, i));
+    any |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
+           ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+  }
+  return (any & 0x80808080u) != 0u;
 }
 
 // 2^(byte - 127 + OFF) in fp16 for bytes in range, 0 for byte 0: in both halves / for two bytes.
@@ -796,8 +810,11 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
         ok = scales_in_range<C>(reinterpret_cast<const uint16_t*>(ksc)[lane] |
                                 (uint32_t)reinterpret_cast<const uint16_t*>(vsc)[lane] << 16);
       }
+      // a hidden key weighs 0, and 0 * NaN is NaN: where rows see different keys, NaN codes of V leave the matrix path too
+      const bool masked = k0 + KT > min_lim;
+      if (FMT == CACHE_FP8 && masked) ok &= !row_has_nan<RB>(stage + KT * RB, lane);
       const uint32_t odd = __ballot_sync(0xFFFFFFFFu, !ok) & ~gone;
-      if ((gone | odd) != 0u || k0 + KT > min_lim)
+      if ((gone | odd) != 0u || masked)
         tile_work<FMT, D, NT, true>(stage, k0, gone, odd, place, acc, l, ref, q_frag, c_of, lim_of);
       else
         tile_work<FMT, D, NT, false>(stage, k0, 0u, 0u, place, acc, l, ref, q_frag, c_of, lim_of);

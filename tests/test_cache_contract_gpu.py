@@ -54,3 +54,51 @@ def test_read_write_read_with_nothing_between(ops, fmt, captured):
                 assert torch.equal(bits(x), bits(w)), i
             for x in got:
                 x.zero_()
+
+
+def fill_v(f, b, first, last, code, scale):
+    """Element codes `code` under scale byte `scale` in V of positions first..last of sequence b, straight in the pool."""
+    for p in range(first, last + 1):
+        pg, off = int(f.table[b, p // f.page]), p % f.page
+        f.cache.v[pg, :, off] = code
+        f.cache.v_sc[pg, :, off] = scale
+
+
+@HEADS
+@pytest.mark.parametrize("D,n,extra", [(128, 45, 0), (64, 200, 0), (128, 200, 5120)])
+@pytest.mark.parametrize("code,scale", [(0x7F, 127), (0xFF, 127), (0x7F, 0), (0xFF, 200)])
+def test_rows_do_not_see_later_nan_codes(ops, D, n, extra, code, scale, Hq):
+    """E4M3's NaN codes in V under a scale of their own (mx_cache_write gives such a block scale 0xFF, but the pools are
+    the caller's): rows that may not see the token keep their bits, rows that see it are NaN in every column."""
+    T = 5
+    # the key's score may come from the other path: each within D 2^-23 sum |q||K| scale + 2^-16 of the formula's
+    # (here sum |q||K| scale < 40), so the two within 2^-9
+    tol = 2.0 ** -9
+    f = Filled(ops, 81, [n], 2, D, 0, 16)
+    f.table = torch.nn.functional.pad(f.table, (0, extra // 16), value=-7)
+    q = make_q(31, 1, T, Hq, D, "bf16", 0)
+    ref = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
+    for t in range(T - 2, -1, -1):
+        fill_v(f, 0, n - T + t + 1, n - T + t + 1, code, scale)
+        o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
+        assert torch.equal(bits(o[:, :t + 1]), bits(ref[0][:, :t + 1])), t
+        assert torch.equal(bits(lse[:, :, :t + 1]), bits(ref[1][:, :, :t + 1]))
+        assert torch.all(torch.isnan(o[:, t + 1:]))
+        np.testing.assert_allclose(f64(lse), f64(ref[1]), rtol=0, atol=tol)
+
+
+@pytest.mark.parametrize("T,G", [(2, 4), (3, 8), (12, 4)])
+def test_one_nan_code_is_one_column(ops, T, G):
+    """A single NaN code: its column alone, in the rows that see its token."""
+    n, D = 70, 128
+    f = Filled(ops, 82, [n], 2, D, 0, 16)
+    q = make_q(32, 1, T, 2 * G, D, "fp16", 0)
+    ref = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
+    p = n - 1
+    f.cache.v[int(f.table[0, p // 16]), 1, p % 16, 37] = 0x7F
+    o, _ = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
+    nan = torch.isnan(o[0])
+    want = torch.zeros_like(nan)
+    want[T - 1, G:, 37] = True
+    assert torch.equal(nan, want)
+    assert torch.equal(bits(o[:, :T - 1]), bits(ref[0][:, :T - 1]))
