@@ -56,6 +56,7 @@ constexpr int MIN_CHUNKS = 2;   // chunks a block takes at least, once there is 
 constexpr float SLACK = 4.f;    // a reference moves when a score passes it by this much (log2)
 constexpr float LIFT = 8.f;     // a reference m gives weights 2^(x + r), r = LIFT - m
 constexpr float UNSET = 3e38f;  // r of a row without a score yet: 2^(-inf + r) = 0, and any score moves it
+constexpr float FAR = 1048576.f;   // |r| from which products are rounded first (tile_work): a unit is 1/8 there
 
 // Blocks per SM.  Tiles of 8 rows: 3 blocks leave 168 registers, 4 leave 128 and fewer loads and conversions in flight.
 // D = 128, G = 4, 4 bits, 4 blocks / 3: 64 x 6000 keys 50.3 / 48.1 us, 16 x 6000 20.2 / 19.1; but one sequence
@@ -187,6 +188,8 @@ __device__ __forceinline__ void word_values(const uint8_t* rows, int k, int at, 
     v[2 * i + 1] = y.y * scale * f;
   }
 }
+// Whether a reference is one whose scores' products are rounded before they are compared (tile_work).
+__device__ __forceinline__ bool is_far(float r) { return fabsf(r) >= FAR && r != UNSET; }
 // Keeps the loads of a rarely taken loop from being gathered in registers ahead of it.
 __device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
 
@@ -275,12 +278,13 @@ struct Place {
   int lane, g, t, ko, vo0, vo4, kso, vso;
 };
 // One tile of 32 keys: scores, weights, and both products into acc, l and the references.  SPECIAL: some keys
-// are left out (`gone`), need the scalar path (`odd`) or are hidden from some row; a plain tile's code has none of
-// that.  Both add the same things in the same order for the keys that a row sees.
+// are left out (`gone`), need the scalar path (`odd`) or are hidden from some row, or some row's reference is `far`; a
+// plain tile's code has none of that, and returns false with nothing changed but `far` where a reference gets there.  Both
+// add the same things in the same order for the keys that a row sees.
 template <int FMT, int D, int NT, bool SPECIAL, class QFrag, class COf, class LimOf>
-__device__ __forceinline__ void tile_work(uint8_t* const stage, const int k0, const uint32_t gone, const uint32_t odd,
+__device__ __forceinline__ bool tile_work(uint8_t* const stage, const int k0, const uint32_t gone, const uint32_t odd,
                                           const Place& at, float (&acc)[NT][D / 16][4], float (&l)[NT][2],
-                                          float (&ref)[NT][2], QFrag q_frag, COf c_of, LimOf lim_of) {
+                                          float (&ref)[NT][2], bool& far, QFrag q_frag, COf c_of, LimOf lim_of) {
   using C = Cfg<FMT, D, NT>;
   constexpr int RB = C::RB, NB = C::NB;
   constexpr int LB = C::KE * RB / D, VB = C::VE * RB / D;   // bytes of a lane's K run and of its V run
@@ -405,10 +409,11 @@ __device__ __forceinline__ void tile_work(uint8_t* const stage, const int k0, co
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      top[nt][j] = c_of(nt, j) * fmaxf(fmaxf(s[nt][0][j], s[nt][0][2 + j]), fmaxf(s[nt][1][j], s[nt][1][2 + j]));
+      top[nt][j] = __fmul_rn(c_of(nt, j), fmaxf(fmaxf(s[nt][0][j], s[nt][0][2 + j]), fmaxf(s[nt][1][j], s[nt][1][2 + j])));
       climb |= top[nt][j] + ref[nt][j] > LIFT + SLACK;
     }
   if (__any_sync(0xFFFFFFFFu, climb)) {
+    bool away = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -417,9 +422,19 @@ __device__ __forceinline__ void tile_work(uint8_t* const stage, const int k0, co
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-        if (mx + ref[nt][j] > LIFT + SLACK) {
-          const float keep = ex2_approx((LIFT - mx) - ref[nt][j]);   // 0 from UNSET
-          ref[nt][j] = LIFT - mx;
+        // from here on the new reference; mx + it <= LIFT also where bits are lost
+        top[nt][j] = mx + ref[nt][j] > LIFT + SLACK ? __fsub_rd(LIFT, mx) : ref[nt][j];
+        away |= is_far(top[nt][j]);
+      }
+    far = __any_sync(0xFFFFFFFFu, away);
+    if (!SPECIAL && far) return false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (top[nt][j] != ref[nt][j]) {
+          const float keep = ex2_approx(top[nt][j] - ref[nt][j]);   // 0 from UNSET
+          ref[nt][j] = top[nt][j];
           l[nt][j] *= keep;
 #pragma unroll
           for (int i = 0; i < C::MT; ++i) {
@@ -427,19 +442,25 @@ __device__ __forceinline__ void tile_work(uint8_t* const stage, const int k0, co
             acc[nt][i][2 + j] *= keep;
           }
         }
-      }
   }
 
   // ---- weights ----
+  // A reference holds its row's largest product as rounded, which is up to half a unit off.  Far out, where a unit is many
+  // powers of two, that alone would take 2^(s c - round(s c)) out of fp16's range: there all products are rounded first.
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int j = 0; j < 2; ++j) {
+      const bool rounded = SPECIAL && is_far(ref[nt][j]);
+      const float c = rounded ? 1.f : c_of(nt, j), r = rounded ? 0.f : ref[nt][j];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[nt][mt][i] = ex2_approx(fmaf(s[nt][mt][i], c_of(nt, i & 1), ref[nt][i & 1]));
-        l[nt][i & 1] += s[nt][mt][i];
+        float& x = s[nt][i >> 1][2 * (i & 1) + j];
+        if (rounded) x = __fadd_rn(__fmul_rn(x, c_of(nt, j)), ref[nt][j]);
+        x = ex2_approx(fmaf(x, c, r));
+        l[nt][j] += x;
       }
+    }
 
   // ---- odd keys' part of O in fp32, only for rows that see them; then they and absent keys become zeros ----
   if constexpr (SPECIAL) if (left_out != 0u) {
@@ -554,6 +575,7 @@ __device__ __forceinline__ void tile_work(uint8_t* const stage, const int k0, co
       }
     }
   }
+  return true;
 }
 
 template <int FMT, int D, int NT, bool CLUSTER>
@@ -779,6 +801,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
     auto lim_of = [&](int nt, int j) { return C::QS ? lims[nt * 8 + 2 * t + j] : lim_own[C::QS ? 0 : nt][j]; };
 
     float acc[NT][C::MT][4], l[NT][2], ref[NT][2];   // weights are 2^(c s + ref)
+    bool far = false;                                // some row's reference is FAR or more
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -810,14 +833,14 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
         ok = scales_in_range<C>(reinterpret_cast<const uint16_t*>(ksc)[lane] |
                                 (uint32_t)reinterpret_cast<const uint16_t*>(vsc)[lane] << 16);
       }
-      // a hidden key weighs 0, and 0 * NaN is NaN: where rows see different keys, NaN codes of V leave the matrix path too
+      uint32_t odd = __ballot_sync(0xFFFFFFFFu, !ok) & ~gone;
       const bool masked = k0 + KT > min_lim;
-      if (FMT == CACHE_FP8 && masked) ok &= !row_has_nan<RB>(stage + KT * RB, lane);
-      const uint32_t odd = __ballot_sync(0xFFFFFFFFu, !ok) & ~gone;
-      if ((gone | odd) != 0u || masked)
-        tile_work<FMT, D, NT, true>(stage, k0, gone, odd, place, acc, l, ref, q_frag, c_of, lim_of);
-      else
-        tile_work<FMT, D, NT, false>(stage, k0, 0u, 0u, place, acc, l, ref, q_frag, c_of, lim_of);
+      if ((gone | odd) != 0u || masked || far ||
+          !tile_work<FMT, D, NT, false>(stage, k0, 0u, 0u, place, acc, l, ref, far, q_frag, c_of, lim_of)) {
+        // a hidden key weighs 0, and 0 * NaN is NaN: where rows see different keys, NaN codes of V leave the matrix path too
+        if (FMT == CACHE_FP8 && masked) odd |= __ballot_sync(0xFFFFFFFFu, row_has_nan<RB>(stage + KT * RB, lane)) & ~gone;
+        tile_work<FMT, D, NT, true>(stage, k0, gone, odd, place, acc, l, ref, far, q_frag, c_of, lim_of);
+      }
     }
 
     // ---- the four warps' parts joined in shared memory (over the rings, whose copies have all landed) ----

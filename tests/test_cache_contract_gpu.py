@@ -102,3 +102,40 @@ def test_one_nan_code_is_one_column(ops, T, G):
     want[T - 1, G:, 37] = True
     assert torch.equal(nan, want)
     assert torch.equal(bits(o[:, :T - 1]), bits(ref[0][:, :T - 1]))
+
+
+@HEADS
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("power", [12, 18, 20, 23, 25, 28, 31, 40, 100])
+def test_large_scores(ops, fmt, power, Hq):
+    """Scores so far from 0 that one fp32 step of them is many powers of e: finite, and the oracle's within what fp32
+    scores allow (its bounds grow with them; the log-sum-exp is held to 2^-21 of itself)."""
+    f = Filled(ops, 83, [300, 20], 2, 128, fmt, 16)
+    q = make_q(33, 2, 2, Hq, 128, "bf16", 0)
+    o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, softmax_scale=2.0 ** power)
+    assert torch.all(torch.isfinite(o)) and torch.all(torch.isfinite(lse))
+    check_attn(f, q, o, lse, [2, 2], 2.0 ** power, 0)
+
+
+@HEADS
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("power", [10, 20, 24, 30, 60])
+def test_large_scores_take_the_largest(ops, power, sign, Hq):
+    """Keys that are powers of two times one vector: scores are exact, the largest is far above the others, and O is its V
+    rounded once (sign -1: all scores negative, the smallest key is the largest score)."""
+    n, T = 200, 2
+    f = Filled(ops, 84, [n], 2, 128, 1, 16)
+    best = [17, 150]                                     # per KV head; seen by every row
+    k = torch.full((1, n, 2, 128), 1.0, dtype=torch.bfloat16)
+    for h in range(2):
+        k[0, best[h], h] = 4.0 if sign > 0 else 0.25
+    v = make_q(34, 1, n, 2, 128, "bf16", 0)
+    ops.mx_cache_write(f.cache, k.cuda(), v, f.table, f.seq)
+    _, vv = ops.mx_cache_read(f.cache, f.table, f.seq, n)
+    q = torch.full((1, T, Hq, 128), sign, dtype=torch.bfloat16, device="cuda")
+    o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, softmax_scale=2.0 ** power)
+    for h in range(2):
+        want = vv[0, best[h], h].expand(T, Hq // 2, 128)
+        np.testing.assert_allclose(f64(o[0, :, h * Hq // 2:(h + 1) * Hq // 2]), f64(want), rtol=2.0 ** -8, atol=0)
+    s = 128.0 * 2.0 ** power * (4.0 if sign > 0 else -0.25)
+    np.testing.assert_allclose(f64(lse), s, rtol=2.0 ** -21)
