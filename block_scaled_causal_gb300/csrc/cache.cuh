@@ -93,6 +93,11 @@ __device__ __forceinline__ uint32_t f32_to_act(float lo, float hi, int fp16) {
   return fp16 ? f32_to_act<1>(lo, hi) : f32_to_act<0>(lo, hi);
 }
 
+// Reports a code.  The status word keeps the first one it is given, whichever of the library's calls gave it.
+__device__ __forceinline__ void report(int32_t* dev_status, int32_t code) {
+  if (dev_status) atomicCAS(dev_status, 0, code);
+}
+
 // The page that holds position `pos` of sequence `b`, or -1 where there is none, and the row of that position and
 // head in the page's [Hkv][page_size]; `bad` collects a status code.
 __device__ __forceinline__ int cache_page(const CachePools& c, const CacheTable& pt, int b, long long pos, int h,

@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
     const int h = u / row_tiles, rt = u - h * row_tiles;
     const int raw_len = max(__ldca(a.pt.seq_lens + b), 0);
     const int n_new = a.new_lens ? min(max(__ldca(a.new_lens + b), 0), a.T) : a.T;
-    if (raw_len > len && tid == 0 && a.dev_status) *a.dev_status = CACHE_BAD_LEN;
+    if (raw_len > len && tid == 0) report(a.dev_status, CACHE_BAD_LEN);
 
     // ---- Q's loads start: lane (g, t) has elements KE t .. KE t + KE - 1 of query row g of each 8-row tile ----
     // (of all tiles, or each warp of its own where Q goes to shared memory)
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
             w_page = __ldca(a.pt.table + b * a.pt.stride + lp);
             if (w_page < 0 || w_page >= a.c.num_pages) {
               w_page = -1;
-              if (a.dev_status) *a.dev_status = CACHE_BAD_PAGE;
+              report(a.dev_status, CACHE_BAD_PAGE);
             }
           }
           present = __ballot_sync(0xFFFFFFFFu, w_page >= 0);

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(RW_WARPS * 32) cache_write_kernel(const CacheR
   Rows at{-1, -1, 0, 0, false};
   int32_t bad = 0;
   if (lane < rows) at.page = cache_page(a.c, a.pt, w.b, (len < 0 ? 0 : len) - n + w.t0 + lane, w.h, at.row, bad);
-  if (bad && a.dev_status) *a.dev_status = bad;
+  if (bad) report(a.dev_status, bad);
   at.settle(lane, rows);
 
   constexpr int PB = RB / (D / 8);               // bytes of a piece: 4 or 8
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(RW_WARPS * 32) cache_read_kernel(const CacheRw
   int32_t bad = 0;
   const long long pos = start + w.t0 + lane;
   if (lane < rows && pos < len) at.page = cache_page(a.c, a.pt, w.b, pos, w.h, at.row, bad);
-  if (bad && a.dev_status) *a.dev_status = bad;
+  if (bad) report(a.dev_status, bad);
   at.settle(lane, rows);
 
   const uint8_t* const pool = (w.which ? a.c.v : a.c.k) + blk * 4 * PB + half * PB;

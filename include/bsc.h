@@ -312,8 +312,9 @@ size_t bf16_attn_bwd_static_capacity(void);
  * Lengths and page ids live on the device and cannot be checked before the launch.  A page id
  * outside [0, num_pages) is never followed: its tokens are not written, read as zeros, and are not
  * attended; a position past max_pages * page_size is treated the same way, a negative length as 0.
- * If dev_status is given, it then receives 0x201 (page id) or 0x202 (length); it is left untouched
- * otherwise, and bsc_read_device_status returns BSC_ERR_DEVICE_PAGE for both.
+ * If dev_status is given and holds 0, it then receives 0x201 (page id) or 0x202 (length; either one where a call meets
+ * both); it is left untouched otherwise, so a word shared by several calls keeps the first code.
+ * bsc_read_device_status returns BSC_ERR_DEVICE_PAGE for both.
  *
  * Outputs, workspace and dev_status overlap no other argument.  Refused as BSC_ERR_UNSUPPORTED, because
  * positions, page rows and grids are counted in 32 bits: a page table of more than

@@ -139,3 +139,26 @@ def test_large_scores_take_the_largest(ops, power, sign, Hq):
         np.testing.assert_allclose(f64(o[0, :, h * Hq // 2:(h + 1) * Hq // 2]), f64(want), rtol=2.0 ** -8, atol=0)
     s = 128.0 * 2.0 ** power * (4.0 if sign > 0 else -0.25)
     np.testing.assert_allclose(f64(lse), s, rtol=2.0 ** -21)
+
+
+def test_status_keeps_the_first_code(ops):
+    """One status word over a step's calls: a code that is there, another kernel's time-out among them, stays."""
+    f = Filled(ops, 85, [20], 2, 128, 1, 16)
+    q, x = make_q(35, 1, 1, 8, 128, "bf16", 0), make_q(36, 1, 1, 2, 128, "bf16", 0)
+    bad_page = f.table.clone()
+    bad_page[0, 1] = f.cache.num_pages
+    short = f.table[:, :1].contiguous()                  # 16 positions of 20
+    calls = [lambda t, st: ops.mx_cache_write(f.cache, x, x, t, f.seq, dev_status=st),
+             lambda t, st: ops.mx_cache_read(f.cache, t, f.seq, 20, dev_status=st),
+             lambda t, st: ops.mx_cache_attn(q, f.cache, t, f.seq, dev_status=st)]
+    for call in calls:
+        for first in (0, 0x103, 0x201, 0x202):
+            for table, code in ((bad_page, 0x201), (short, 0x202)):
+                st = i32([first])
+                call(table, st)
+                assert int(st) == (first or code)
+                assert ops.bsc_read_device_status(st) == (6 if first == 0x103 else 7)
+    st = i32([0])
+    for call, table in zip(calls, (bad_page, short, short)):
+        call(table, st)
+    assert int(st) == 0x201
