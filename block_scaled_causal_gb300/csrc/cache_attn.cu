@@ -765,7 +765,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
         q[nt][i][1] = pack_f16x2(f[4 * i + 2] * up, f[4 * i + 3] * up);
       }
       const int ex_back = max(ex - 14 - C::OFF, -126);
-      const float cg = fmaxf(a.scale_log2e * __uint_as_float((uint32_t)(ex_back + 127) << 23), 1.17549435e-38f);
+      // above 0, so that -inf stays -inf; in fp32's subnormals it is off by 2^-150 at most, scores then by under 2^-22
+      const float cg = fmaxf(a.scale_log2e * __uint_as_float((uint32_t)(ex_back + 127) << 23), 1.4e-45f);
       // first key past the row: position raw_len - n_new + tq sees itself
       int lg = len;
       if (r < R && tq < n_new) {

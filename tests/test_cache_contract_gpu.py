@@ -162,3 +162,24 @@ def test_status_keeps_the_first_code(ops):
     for call, table in zip(calls, (bad_page, short, short)):
         call(table, st)
     assert int(st) == 0x201
+
+
+@HEADS
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_tiny_queries_and_scale_over_large_keys(ops, fmt, Hq):
+    """Query exponents and softmax scale together under fp32's normal range, keys that bring the scores back to 2^-5: one key
+    weighs a little more than the zeros beside it."""
+    n = 12
+    f = Filled(ops, 87, [n], 2, 128, fmt, 16)
+    sign = torch.where(torch.arange(128) % 3 == 0, -1.0, 1.0)
+    k = torch.zeros((1, n, 2, 128), dtype=torch.bfloat16)
+    k[0, 5] = sign * 2.0 ** 100
+    v = make_q(38, 1, n, 2, 128, "bf16", 0)
+    ops.mx_cache_write(f.cache, k.cuda(), v, f.table, f.seq)
+    host = [x.cpu().numpy() for x in (f.cache.k, f.cache.k_sc, f.cache.v, f.cache.v_sc)]
+    f.K = [C.gather(host[0], host[1], fmt, f.table[0].cpu().numpy(), n, 16)]
+    f.V = [C.gather(host[2], host[3], fmt, f.table[0].cpu().numpy(), n, 16)]
+    for qp, sp in ((-96, -16), (-88, -24), (-100, -12), (0, -112)):
+        q = (sign * 2.0 ** qp).to(torch.bfloat16).cuda().expand(1, 1, Hq, 128)
+        o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, softmax_scale=2.0 ** sp)
+        check_attn(f, q, o, lse, [1], 2.0 ** sp, 0)
