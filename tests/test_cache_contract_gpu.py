@@ -166,6 +166,19 @@ def test_status_keeps_the_first_code(ops):
 
 @HEADS
 @pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("qp,kp,scale", [(-98, 97, 128 ** -0.5), (0, 97, 2.0 ** -96), (0, 97, 128 ** -0.5), (90, 0, 2.0 ** -90)])
+def test_keys_up_to_the_bound(ops, fmt, qp, kp, scale, Hq):
+    """Visible K up to 2^100 in magnitude, with q or the scale to match or scores as large as that makes them."""
+    f = Filled(ops, 86, [200, 33], 2, 128, fmt, 16, k_mult=2.0 ** kp)
+    assert kp == 0 or 2.0 ** 98 < max(np.abs(k).max() for k in f.K) <= 2.0 ** 100
+    q = make_q(37, 2, 3, Hq, 128, "bf16", 0, mult=2.0 ** qp)
+    o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, softmax_scale=scale)
+    assert torch.all(torch.isfinite(o)) and torch.all(torch.isfinite(lse))
+    check_attn(f, q, o, lse, [3, 3], float(np.float32(scale)), 0)
+
+
+@HEADS
+@pytest.mark.parametrize("fmt", [0, 1])
 def test_tiny_queries_and_scale_over_large_keys(ops, fmt, Hq):
     """Query exponents and softmax scale together under fp32's normal range, keys that bring the scores back to 2^-5: one key
     weighs a little more than the zeros beside it."""
@@ -183,3 +196,24 @@ def test_tiny_queries_and_scale_over_large_keys(ops, fmt, Hq):
         q = (sign * 2.0 ** qp).to(torch.bfloat16).cuda().expand(1, 1, Hq, 128)
         o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, softmax_scale=2.0 ** sp)
         check_attn(f, q, o, lse, [1], 2.0 ** sp, 0)
+
+
+@HEADS
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("n,power", [(1024, 100), (4500, 80)])
+def test_values_up_to_the_bound(ops, fmt, n, power, Hq):
+    """V of 2^100 over 1024 keys and of 2^80 over more, all but the first key nearly 2^4 above the reference that the first one
+    sets (the most that weights and their sums grow to)."""
+    f = Filled(ops, 88, [n], 2, 128, fmt, 16)
+    k = torch.zeros((1, n, 2, 128), dtype=torch.bfloat16)
+    k[:, 1:, :, 0] = 1.0
+    v = torch.full((1, n, 2, 128), 2.0 ** power, dtype=torch.bfloat16)
+    v[..., 64:] *= -0.5
+    ops.mx_cache_write(f.cache, k.cuda(), v.cuda(), f.table, f.seq)
+    q = torch.zeros((1, 1, Hq, 128), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, softmax_scale=2.7)      # 3.895 in powers of two
+    np.testing.assert_allclose(f64(o[..., :64]), 2.0 ** power, rtol=2.0 ** -8 + 2.0 ** -10)
+    np.testing.assert_allclose(f64(o[..., 64:]), -0.5 * 2.0 ** power, rtol=2.0 ** -8 + 2.0 ** -10)
+    s = float(np.float32(2.7))
+    np.testing.assert_allclose(f64(lse), np.log(1 + (n - 1) * np.exp(s)), rtol=2.0 ** -14)
