@@ -2,6 +2,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include <cuda.h>
@@ -146,6 +147,24 @@ bsc_status quant_v_common(const void* v, int B, int S, int H, int D, bsc_layout 
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Whether a product of sizes (each at least 1 and below 2^31) reaches 2^31.
+bool reaches_2_31(std::initializer_list<long long> sizes) {
+  long long product = 1;
+  for (const long long s : sizes)
+    if ((product *= s) >= (1LL << 31)) return true;
+  return false;
+}
+
+// What the attention's grids and row numbers cannot hold: the rows of all tiles (the smallest of 8, 16 and 32 rows that takes
+// a KV head's, else 32), or the chunks of 128 tokens of all tiles.  max_tokens 0: rows alone.
+bool cache_attn_too_large(int B, int T, int Hq, int Hkv, long long max_tokens) {
+  const long long rows = (long long)T * (Hq / Hkv);
+  const int tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  if (rows >= (1LL << 31)) return true;
+  const long long tiles = (rows + tile - 1) / tile, chunks = (max_tokens + 127) / 128;
+  return reaches_2_31({B, Hkv, tiles, tile}) || (chunks > 0 && reaches_2_31({B, Hkv, tiles, chunks}));
+}
+
 // The checks that the three cache calls share.  *empty: a problem without sequences, tokens or heads.
 bsc_status check_cache(const bsc_mx_cache& c, int B, int T, int H, int dtype, long long table_stride, int max_pages,
                        bool* empty) {
@@ -161,11 +180,8 @@ bsc_status check_cache(const bsc_mx_cache& c, int B, int T, int H, int dtype, lo
   if (c.Hkv == 0 || c.num_pages == 0 || c.page_size == 0) return BSC_ERR_SHAPE;
   if ((c.D != 64 && c.D != 128) || c.page_size % 16 != 0) return BSC_ERR_UNSUPPORTED;
   if (B > 1 && table_stride < max_pages) return BSC_ERR_SHAPE;
-  // positions are 32-bit, with room above the last for a tile's end and the tiles after it, and the grids (at most
-  // one warp per 16 tokens and KV head, or one block per query row) must fit theirs
+  // positions are 32-bit, with room above the last for a tile's end and the tiles after it
   if ((long long)max_pages * c.page_size > BSC_CACHE_MAX_TOKENS) return BSC_ERR_UNSUPPORTED;
-  if ((long long)B * T >= (1LL << 31) / H || (long long)B * ((T + 15LL) / 16) * 2 >= (1LL << 31) / c.Hkv)
-    return BSC_ERR_UNSUPPORTED;
   // the attention addresses a page in 32-bit units of 16 bytes
   if ((long long)c.Hkv * c.page_size >= (1LL << 31) / c.D) return BSC_ERR_UNSUPPORTED;
   if (!c.k || !c.k_sc || !c.v || !c.v_sc) return BSC_ERR_NULL;
@@ -449,6 +465,7 @@ bsc_status mx_cache_write(const bsc_mx_cache_write_params* p, bsc_stream_t strea
   bool empty;
   bsc_status s = check_cache(p->cache, p->B, p->T, p->cache.Hkv, p->dtype, p->table_stride, p->max_pages, &empty);
   if (s != BSC_OK || empty) return s;
+  if (reaches_2_31({2, p->B, (p->T + 15LL) / 16, p->cache.Hkv})) return BSC_ERR_UNSUPPORTED;   // warps
   if (!p->k || !p->v || !p->seq_lens || (p->max_pages > 0 && !p->page_table)) return BSC_ERR_NULL;
   if (!aligned16(p->k) || !aligned16(p->v) || !aligned4(p->page_table) || !aligned4(p->seq_lens) ||
       !aligned4(p->new_lens) || !aligned4(p->dev_status))
@@ -478,6 +495,7 @@ bsc_status mx_cache_read(const bsc_mx_cache_read_params* p, bsc_stream_t stream)
   bool empty;
   bsc_status s = check_cache(p->cache, p->B, p->T, p->cache.Hkv, p->dtype, p->table_stride, p->max_pages, &empty);
   if (s != BSC_OK || empty) return s;
+  if (reaches_2_31({2, p->B, (p->T + 15LL) / 16, p->cache.Hkv})) return BSC_ERR_UNSUPPORTED;   // warps
   if (!p->k || !p->v || !p->seq_lens || (p->max_pages > 0 && !p->page_table)) return BSC_ERR_NULL;
   if (!aligned16(p->k) || !aligned16(p->v) || !aligned4(p->page_table) || !aligned4(p->seq_lens) ||
       !aligned4(p->starts) || !aligned4(p->dev_status))
@@ -503,7 +521,7 @@ bsc_status mx_cache_read(const bsc_mx_cache_read_params* p, bsc_stream_t stream)
 
 size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long long max_tokens) {
   if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_tokens < 0) return 0;
-  if ((long long)B * T >= (1LL << 31) / Hq) return 0;       // refused by the call itself
+  if (cache_attn_too_large(B, T, Hq, Hkv, 0)) return 0;     // refused by the call itself
   if (max_tokens > BSC_CACHE_MAX_TOKENS) max_tokens = BSC_CACHE_MAX_TOKENS;
   return bsc::cache_attn_workspace_bytes(B, T, Hq, Hkv, D, max_tokens);
 }
@@ -515,6 +533,8 @@ bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream)
   if (s != BSC_OK || empty) return s;
   if (p->Hq % p->cache.Hkv != 0) return BSC_ERR_SHAPE;
   if (!(std::isfinite(p->softmax_scale) && p->softmax_scale > 0.f)) return BSC_ERR_UNSUPPORTED;
+  if (cache_attn_too_large(p->B, p->T, p->Hq, p->cache.Hkv, (long long)p->max_pages * p->cache.page_size))
+    return BSC_ERR_UNSUPPORTED;
   const size_t need = mx_cache_attn_workspace_bytes(p->B, p->T, p->Hq, p->cache.Hkv, p->cache.D,
                                                     (long long)p->max_pages * p->cache.page_size);
   if (!p->q || !p->o || !p->seq_lens || (p->max_pages > 0 && !p->page_table) || (need > 0 && !p->workspace)) return BSC_ERR_NULL;

@@ -1084,13 +1084,14 @@ Plan plan(long long B, long long rows, int Hkv, long long max_tokens) {
   return {whole, 0};
 }
 
+// units * ROWS and units * chunks are below 2^31: checked with the arguments for the tile that takes all rows, and a smaller
+// one is chosen for few units or few chunks only.
 template <int FMT, int D, int NT>
 cudaError_t launch(const CacheAttnArgs& a, int cs, cudaStream_t st) {
   using C = Cfg<FMT, D, NT>;
   const int rows = a.T * (a.Hq / a.c.Hkv), row_tiles = (rows + C::ROWS - 1) / C::ROWS;
   const long long units = (long long)a.B * a.c.Hkv * row_tiles;
   const long long chunks = ((long long)a.pt.max_pages * a.c.page_size + CHUNK - 1) / CHUNK;
-  if (units * chunks >= (1LL << 31) || units * C::ROWS >= (1LL << 31)) return cudaErrorNotSupported;
   {  // the opt-in to more than 48 KB of shared memory, once per device
     static std::atomic<uint64_t> opted{0};
     int dev = 0;

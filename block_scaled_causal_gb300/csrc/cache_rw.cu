@@ -27,7 +27,7 @@ struct Piece {
 };
 __device__ __forceinline__ bool piece_of(const CacheRwArgs& a, Piece& p) {
   uint32_t i = blockIdx.x * RW_WARPS + (threadIdx.x >> 5);          // fewer than 2^31 warps: checked by the host
-  const uint32_t tiles = (uint32_t)(a.T + RW_TOKENS - 1) / RW_TOKENS, H = a.c.Hkv;
+  const uint32_t tiles = ((uint32_t)a.T + RW_TOKENS - 1) / RW_TOKENS, H = a.c.Hkv;
   if (i >= 2u * a.B * tiles * H) return false;
   uint32_t next = i / H;
   p.h = (int)(i - next * H);
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(RW_WARPS * 32) cache_read_kernel(const CacheRw
 
 using Kernel = void (*)(CacheRwArgs);
 cudaError_t launch(Kernel k, const CacheRwArgs& a, cudaStream_t st) {
-  const long long warps = 2LL * a.B * ((a.T + RW_TOKENS - 1) / RW_TOKENS) * a.c.Hkv;
+  const long long warps = 2LL * a.B * ((a.T + RW_TOKENS - 1LL) / RW_TOKENS) * a.c.Hkv;
   return launch_early(k, (unsigned)((warps + RW_WARPS - 1) / RW_WARPS), RW_WARPS * 32, 0, st, 1, a);
 }
 

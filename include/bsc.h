@@ -319,9 +319,9 @@ size_t bf16_attn_bwd_static_capacity(void);
  * Outputs, workspace and dev_status overlap no other argument.  Refused as BSC_ERR_UNSUPPORTED, because
  * positions, page rows and grids are counted in 32 bits: a page table of more than
  * BSC_CACHE_MAX_TOKENS positions (max_pages * page_size), a page of Hkv * page_size * D >= 2^31, a page stride of
- * 2^36 bytes or more, B * T * Hq (or B * T * Hkv / 8) >= 2^31, and for the attention
- * B * Hkv * ceil(max_pages * page_size / 128) * R >= 2^31, R the tiles of 8, 16 or 32 rows (the smallest that is
- * enough, else 32) that the T * (Hq/Hkv) query rows of a KV head take.  page_table may be NULL where
+ * 2^36 bytes or more; for writing and reading 2 * B * Hkv * ceil(T / 16) >= 2^31; for the attention
+ * B * Hkv * ceil(T * (Hq/Hkv) / r) * max(r, ceil(max_pages * page_size / 128)) >= 2^31, r the smallest of 8, 16
+ * and 32 rows that takes the T * (Hq/Hkv) query rows of a KV head, else 32.  page_table may be NULL where
  * max_pages is 0.
  */
 #define BSC_CACHE_MAX_TOKENS (1LL << 30)
