@@ -125,9 +125,7 @@ bool encode_vt_map(CUtensorMap* m, const void* base, long long rows, int S) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bsc_status from_cuda(cudaError_t e) {
-  return e == cudaSuccess ? BSC_OK : e == cudaErrorNotSupported ? BSC_ERR_UNSUPPORTED : BSC_ERR_CUDA;
-}
+bsc_status from_cuda(cudaError_t e) { return e == cudaSuccess ? BSC_OK : BSC_ERR_CUDA; }
 
 bsc_status quant_v_common(const void* v, int B, int S, int H, int D, bsc_layout layout, uint8_t* vt, uint8_t* vsc,
                           uint8_t* vtn, uint8_t* vtn_sc, bsc_stream_t stream, bool want_col, bool want_tn,
