@@ -217,3 +217,30 @@ def test_values_up_to_the_bound(ops, fmt, n, power, Hq):
     np.testing.assert_allclose(f64(o[..., 64:]), -0.5 * 2.0 ** power, rtol=2.0 ** -8 + 2.0 ** -10)
     s = float(np.float32(2.7))
     np.testing.assert_allclose(f64(lse), np.log(1 + (n - 1) * np.exp(s)), rtol=2.0 ** -14)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("Hq", [2, 6])
+@pytest.mark.parametrize("n", [70, 400])
+def test_many_rows_do_not_see_later_tokens(ops, fmt, Hq, n):
+    """A chunk of 70 tokens, a tile of rows spread over several tiles of keys: what later tokens hold may send the tile's
+    other rows through every rare path (far references, scalar keys, NaN codes), the earlier rows keep their bits."""
+    T, D = 70, 128
+    f = Filled(ops, 89, [n], 2, D, fmt, 16)
+    q = make_q(39, 1, T, Hq, D, "bf16", 0)
+    ref = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
+    check_attn(f, q, *ref, [T], D ** -0.5, 0)
+    for t in (60, 40, 33, 9, 0):
+        m = T - 1 - t
+        for fill in (1e30, 1e9, 1e6, float("nan"), 1e-30, "codes"):
+            if fill == "codes":
+                if fmt:
+                    continue
+                for p in range(n - m, n, 3):
+                    fill_v(f, 0, p, p, 0xFF, 127)
+            else:
+                x = (torch.randn((1, m, 2, D), generator=torch.Generator().manual_seed(m)) * fill).to(torch.bfloat16).cuda()
+                ops.mx_cache_write(f.cache, x, x.flip(1).contiguous(), f.table, f.seq)
+            o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
+            assert torch.equal(bits(o[:, :t + 1]), bits(ref[0][:, :t + 1])), (t, fill)
+            assert torch.equal(bits(lse[:, :, :t + 1]), bits(ref[1][:, :, :t + 1])), (t, fill)
