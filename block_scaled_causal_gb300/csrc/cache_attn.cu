@@ -6,10 +6,10 @@
 // What bounds it.  A decode step reads every K and V byte once for the few query rows that share a KV
 // head, so it is bound by memory if the decoding of elements keeps up: at D = 128 a token of one head is
 // 136 bytes in 4 bits, so a full-rate stream leaves about 23 warp instructions per token and SM to decode
-// 256 elements and do both products.  The layout below spends 20 (8 of them conversions and fp16 scalings), but 12
+// 256 elements and do both products.  The layout below spends 21 (8 of them conversions and fp16 scalings), but 12
 // warps per SM issue 2.2 per clock, so 4 bits run at half the copy rate (32 ragged sequences up to 16K, Hkv = 4:
-// 33 us for 116 MB) and 8 bits, with twice the bytes per key, at all of it (16 x 16K, Hkv = 16: 163 us for 1.1 GB).
-// Short work is bound by latency: 5.6 us for one sequence of 500 tokens, 13.4 us for one of 32K.
+// 34 us for 116 MB) and 8 bits, with twice the bytes per key, at all of it (16 x 16K, Hkv = 16: 162 to 165 us for 1.1
+// GB).  Short work is bound by latency: 5.7 us for one sequence of 500 tokens, 13.4 us for one of 32K.
 //
 // Products.  Scores are taken transposed, S^T = K Q^T, and O^T = V^T P^T, with 16-bit MMAs
 // (mma.sync m16n8k16, fp32 accumulation): keys (then output columns) fill the 16-row side and 8 query
@@ -61,7 +61,7 @@ constexpr float FAR = 1048576.f;   // |r| from which products are rounded first 
 // Blocks per SM.  Tiles of 8 rows: 3 blocks leave 168 registers, 4 leave 128 and fewer loads and conversions in flight.
 // D = 128, G = 4, 4 bits, 4 blocks / 3: 64 x 6000 keys 50.3 / 48.1 us, 16 x 6000 20.2 / 19.1; but one sequence
 // of 32K 12.7 / 13.7, whose 1024 chunks divide worse by 456.  In 8 bits shared memory holds 3 at most.  Larger tiles
-// need 255 registers.
+// need up to 255 registers, and those of 32 rows at D = 128 spill 24 to 60 bytes beside.
 constexpr int blocks_per_sm(int tile) { return tile == 8 ? 3 : 2; }
 
 template <int FMT, int D, int NT>
@@ -1061,6 +1061,7 @@ struct Plan {
 // cluster / list in us: 4 rows, 1 x 500 tokens 5.6 / 7.3, 4 x 1000 6.4 / 8.2, 1 x 6000 9.9 / 10.5, 1 x 8000 11.3 / 10.8,
 // 1 x 12000 14.1 / 9.9; 16 x 2000 9.6 / 13.4, 16 x 4000 13.5 / 16.3, 16 x 6000 17.8 / 19.4 (lengths spread from 1/8 of that:
 // 16.1 / 15.6), 64 x 512 8.2 / 13.1, 64 x 1500 16.1 / 19.6 (spread: 14.8 / 16.0), 64 x 2000 20.0 / 22.6.
+// 8 bits and heads of 64 take the same thresholds; they were not measured apart.
 //
 // Rows.  The smallest tile that takes all rows decodes each key once and is the best for long work.  A smaller one
 // decodes keys again per tile, but each warp has fewer instructions per key tile and more warps fit, which

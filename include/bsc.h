@@ -60,7 +60,7 @@ typedef enum {
   BSC_ERR_NULL = 1,           /* a required pointer is NULL */
   BSC_ERR_SHAPE = 2,          /* negative size, Hq not a multiple of Hkv, bad layout code */
   BSC_ERR_ALIGN = 3,          /* a pointer is not 16-byte aligned */
-  BSC_ERR_UNSUPPORTED = 4,    /* D != 128, S % 32 != 0, wrong device, unsupported option */
+  BSC_ERR_UNSUPPORTED = 4,    /* D != 128 (the cache calls: nor 64), S % 32 != 0, wrong device, unsupported option or size */
   BSC_ERR_CUDA = 5,           /* a CUDA runtime/driver call failed (launch, tensor map) */
   BSC_ERR_DEVICE_TIMEOUT = 6, /* a device-side wait gave up (see bsc_read_device_status) */
   BSC_ERR_DEVICE_PAGE = 7     /* a cache call met a page id or a length its page table does not have */
@@ -411,7 +411,7 @@ typedef struct {
  * may come out infinite or NaN.  A block of scale byte 0 (a maximum under 2^-118, or 2^-124 in 4 bits) may count as zeros,
  * and so do elements of q under 2^-39 of their row's largest (under 2^-29 of it they lose low bits).
  * A NaN block of K makes the rows that attend it NaN, one of V their columns of that block, a NaN code its column.
- * The result does not depend on the stream, on other calls or on timing (no atomics); it may differ in the
+ * The result does not depend on the stream, on other calls or on timing (no atomics in it); it may differ in the
  * last bits with the batch's sizes, lengths and table, which decide how the keys are split.
  */
 bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream);
