@@ -1,6 +1,8 @@
 """The cache calls' contract on the GPU where a caller can lean on it hardest: calls with nothing between them, bytes that
 mx_cache_write never writes, magnitudes and scores at the ends of what is taken, a status word with a history.
 Bounds as in test_cache_gpu.py, whose helpers (and its three table widths) are used here."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -244,3 +246,68 @@ def test_many_rows_do_not_see_later_tokens(ops, fmt, Hq, n):
             o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
             assert torch.equal(bits(o[:, :t + 1]), bits(ref[0][:, :t + 1])), (t, fill)
             assert torch.equal(bits(lse[:, :, :t + 1]), bits(ref[1][:, :, :t + 1])), (t, fill)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_write_every_fp16_value(ops, fmt):
+    """All 65536 fp16 patterns: alone in a block, and as elements under a larger one."""
+    pat = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.float16)
+    lone = torch.zeros((2048, 32, 32), dtype=torch.float16)
+    lone[:, torch.arange(32), (torch.arange(32) * 11) % 32] = pat.view(2048, 32)
+    x = torch.cat((lone.view(-1, 1, 64), pat.view(-1, 1, 64)))
+    n = x.shape[0]
+    cache = ops.mx_cache_alloc(-(-n // 256), 256, 1, 64, fmt)
+    table = widened(torch.arange(cache.num_pages, dtype=torch.int32, device="cuda").view(1, -1), 256)
+    xs = x.cuda().view(1, n, 1, 64)
+    for rule, name in ((0, "floor"), (1, "ceil")):
+        ops.mx_cache_write(cache, xs, xs.flip(1).contiguous(), table, i32([n]), rule=rule)
+        torch.cuda.synchronize()
+        data, sb = C.quantize(f64(x.view(n, 64)), fmt, name)
+        np.testing.assert_array_equal(cache.k_sc.view(-1, 2)[:n].cpu().numpy(), sb)
+        np.testing.assert_array_equal(cache.k.view(cache.num_pages * 256, -1)[:n].cpu().numpy(), data)
+        np.testing.assert_array_equal(cache.v.view(cache.num_pages * 256, -1)[:n].cpu().numpy(), data[::-1])
+
+
+@HEADS
+def test_attention_without_lse(ops, Hq):
+    """The C call with lse = NULL gives the same O."""
+    f = Filled(ops, 90, [700, 31, 0], 2, 128, 1, 16)
+    q = make_q(40, 3, 2, Hq, 128, "bf16", 0)
+    ref, _ = ops.mx_cache_attn(q, f.cache, f.table, f.seq)
+    o = torch.full_like(q, 7.0)
+    width = f.table.shape[1]
+    ws = torch.empty(max(16, ops.mx_cache_attn_workspace_bytes(3, 2, Hq, 2, 128, width * 16)), dtype=torch.uint8, device="cuda")
+    sb, st, sh, _ = q.stride()
+    p = ops.CacheAttnParams(cache=f.cache.params, q=q.data_ptr(), o=o.data_ptr(), lse=0, B=3, T=2, Hq=Hq, dtype=0,
+                            softmax_scale=128 ** -0.5, page_table=f.table.data_ptr(), table_stride=f.table.stride(0),
+                            max_pages=width, seq_lens=f.seq.data_ptr(), workspace=ws.data_ptr(), workspace_bytes=ws.numel(),
+                            q_stride_b=sb, q_stride_t=st, q_stride_h=sh, o_stride_b=sb, o_stride_t=st, o_stride_h=sh)
+    assert ops.lib.mx_cache_attn(ctypes.byref(p), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(bits(o), bits(ref))
+
+
+@pytest.mark.parametrize("fmt,dtype,layout", [(0, "bf16", 1), (1, "fp16", 0)])
+def test_long_chunks(ops, fmt, dtype, layout):
+    """A chunk of a prompt behind cached prefixes: more query tokens than a tile of keys has keys, some of them padding."""
+    T, lens, new = 300, [300, 437, 90, 1001], [300, 211, 90, 3]
+    f = Filled(ops, 91, lens, 1, 64, fmt, 48)
+    q = make_q(41, 4, T, 3, 64, dtype, layout)
+    o, lse = ops.mx_cache_attn(q, f.cache, f.table, f.seq, i32(new), layout=layout)
+    check_attn(f, q, o, lse, new, 64 ** -0.5, layout)
+
+
+def test_sizes_of_nothing(ops):
+    """No sequences, no tokens, no heads: accepted, nothing is launched, outputs of that shape."""
+    cache = ops.mx_cache_alloc(2, 16, 2, 64, 1)
+    e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    for B, T, Hq in ((0, 3, 4), (2, 0, 4), (2, 1, 0)):
+        table, lens = torch.zeros((B, 1), dtype=torch.int32, device="cuda"), torch.ones(B, dtype=torch.int32, device="cuda")
+        o, lse = ops.mx_cache_attn(e(B, T, Hq, 64), cache, table, lens)
+        assert o.shape == (B, T, Hq, 64) and lse.shape == (B, Hq, T)
+        if Hq:
+            ops.mx_cache_write(cache, e(B, T, 2, 64), e(B, T, 2, 64), table, lens)
+            k, v = ops.mx_cache_read(cache, table, lens, T)
+            assert k.shape == v.shape == (B, T, 2, 64)
+    torch.cuda.synchronize()
+    assert not cache.k.any() and not cache.k_sc.any()
