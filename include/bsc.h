@@ -408,7 +408,8 @@ typedef struct {
  * Row p is bit-for-bit independent of what positions after p hold, NaN and infinities included.
  * Sums run in fp32 over values that are lifted by powers of two, so finite Kc is taken up to 2^100 in magnitude, Vc
  * up to 2^100 where a row attends at most 1024 keys and up to 2^80 at any length, and s_j up to 2^120; beyond that rows
- * may come out infinite or NaN.  A block of scale byte 0 (a maximum under 2^-118, or 2^-124 in 4 bits) may count as zeros,
+ * may come out infinite or NaN.  Scores, and the log-sum-exps by which the parts of a long sequence are weighed, are as
+ * exact as fp32 is at their size.  A block of scale byte 0 (a maximum under 2^-118, or 2^-124 in 4 bits) may count as zeros,
  * and so do elements of q under 2^-39 of their row's largest (under 2^-29 of it they lose low bits).
  * A NaN block of K makes the rows that attend it NaN, one of V their columns of that block, a NaN code its column.
  * The result does not depend on the stream, on other calls or on timing (no atomics in it); it may differ in the
