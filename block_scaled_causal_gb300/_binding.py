@@ -58,6 +58,20 @@ def _load():
         f.argtypes = [ctypes.POINTER(params), vp]
     lib.mx_cache_attn_workspace_bytes.restype = ctypes.c_size_t
     lib.mx_cache_attn_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, ctypes.c_longlong]
+    for name, params in (("rms_norm", RmsNormParams), ("rms_norm_bwd", RmsNormBwdParams), ("rope", RopeParams),
+                         ("mxfp8_rope_quantize_qk", RopeQuantParams), ("mx_cache_write_rope", CacheWriteRopeParams),
+                         ("mx_cache_bounds", CacheBoundsParams), ("mx_cache_sparse_attn", CacheSparseAttnParams)):
+        f = getattr(lib, name)
+        f.restype = i32
+        f.argtypes = [ctypes.POINTER(params), vp]
+    lib.rms_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.rms_norm_bwd_workspace_bytes.argtypes = [ctypes.c_longlong, i32]
+    lib.mx_cache_sparse_attn_workspace_bytes.restype = ctypes.c_size_t
+    lib.mx_cache_sparse_attn_workspace_bytes.argtypes = [i32] * 8
+    lib.mxfp8_dequantize.restype = i32
+    lib.mxfp8_dequantize.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.bsc_rope_turns.restype = i32
+    lib.bsc_rope_turns.argtypes = [ctypes.POINTER(RopeConfig), vp, ctypes.POINTER(ctypes.c_float)]
     lib.bsc_read_device_status.restype = i32
     lib.bsc_read_device_status.argtypes = [vp, vp]
     return lib
@@ -157,6 +171,81 @@ class CacheAttnParams(ctypes.Structure):
          ("max_pages", ctypes.c_int), ("seq_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p),
          ("dev_status", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
+
+_TABLE = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong), ("max_pages", ctypes.c_int),
+          ("seq_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
+
+
+def _row_strides(*names):
+    return [(n + d, ctypes.c_longlong) for n in names for d in ("_stride", "_inner_stride")]
+
+
+class RmsNormParams(ctypes.Structure):
+    """Mirror of bsc_rms_norm_params."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "residual", "weight", "y", "sum", "rstd", "y_e4m3", "y_sc")] + \
+        [("rows", ctypes.c_longlong)] + _row_strides("x", "residual", "y", "sum") + \
+        [(n, ctypes.c_int) for n in ("inner", "N", "dtype", "weight_dtype", "rule")] + [("eps", ctypes.c_float)]
+
+
+class RmsNormBwdParams(ctypes.Structure):
+    """Mirror of bsc_rms_norm_bwd_params."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dy", "s", "weight", "rstd", "d_sum", "dx", "dweight")] + \
+        [("rows", ctypes.c_longlong)] + _row_strides("dy", "s", "d_sum", "dx") + \
+        [(n, ctypes.c_int) for n in ("inner", "N", "dtype", "weight_dtype")] + \
+        [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class RopeConfig(ctypes.Structure):
+    """Mirror of bsc_rope_config."""
+    _fields_ = [("rot", ctypes.c_int), ("scaling", ctypes.c_int)] + \
+        [(n, ctypes.c_double) for n in ("base", "factor", "original_length", "low_turns", "high_turns")]
+
+
+class RopeAngles(ctypes.Structure):
+    """Mirror of bsc_rope_angles."""
+    _fields_ = [("turns", ctypes.c_void_p), ("magnitude", ctypes.c_float), ("rot", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
+_POSITIONS = [("positions", ctypes.c_void_p), ("position_stride_b", ctypes.c_longlong),
+              ("position_stride_t", ctypes.c_longlong)]
+
+
+class RopeParams(ctypes.Structure):
+    """Mirror of bsc_rope_params."""
+    _fields_ = [("angles", RopeAngles)] + [(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out")] + \
+        _strides("q", "k", "q_out", "k_out") + _POSITIONS + \
+        [(n, ctypes.c_int) for n in ("B", "T", "Hq", "Hkv", "D", "dtype", "inverse")]
+
+
+class RopeQuantParams(ctypes.Structure):
+    """Mirror of bsc_rope_quant_params."""
+    _fields_ = [("angles", RopeAngles), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p)] + _strides("q", "k") + \
+        [(n, ctypes.c_void_p) for n in ("q_e4m3", "q_sc", "k_e4m3", "k_sc")] + _POSITIONS + \
+        [(n, ctypes.c_int) for n in ("B", "T", "Hq", "Hkv", "D", "dtype", "layout", "rule")]
+
+
+class CacheWriteRopeParams(ctypes.Structure):
+    """Mirror of bsc_mx_cache_write_rope_params."""
+    _fields_ = [("cache", CachePools), ("angles", RopeAngles)] + [(n, ctypes.c_void_p) for n in ("q", "k", "v", "q_out")] + \
+        _strides("q", "k", "v", "q_out") + [(n, ctypes.c_int) for n in ("B", "T", "Hq", "dtype", "rule")] + _TABLE
+
+
+class CacheBoundsParams(ctypes.Structure):
+    """Mirror of bsc_mx_cache_bounds_params."""
+    _fields_ = [("cache", CachePools), ("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p), ("B", ctypes.c_int),
+                ("T", ctypes.c_int)] + _TABLE
+
+
+class CacheSparseAttnParams(ctypes.Structure):
+    """Mirror of bsc_mx_cache_sparse_attn_params."""
+    _fields_ = [("cache", CachePools)] + [(n, ctypes.c_void_p) for n in ("codes", "exps", "q", "o", "lse", "blocks")] + \
+        _strides("q", "o") + [(n, ctypes.c_int) for n in ("B", "T", "Hq", "dtype")] + [("softmax_scale", ctypes.c_float)] + \
+        [(n, ctypes.c_int) for n in ("top", "first", "last")] + _TABLE + \
+        [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BY_PARTS = 0, 1, 2, 3
 
 CACHE_MXFP8, CACHE_MXFP4 = 0, 1
 _ACT = {torch.bfloat16: 0, torch.float16: 1}
@@ -296,13 +385,26 @@ def bsc_read_device_status(dev_status, stream=None):
     return lib.bsc_read_device_status(_ptr(dev_status), _stream(stream))
 
 
+def _operands(q, k, v, layout, token_norm, rope, positions, stream):
+    """The eight operands of the attention: Q and K rotated where `rope` is given."""
+    if rope is None:
+        if positions is not None:
+            raise ValueError("positions are for rope")
+        return mxfp8_quantize_qkv(q, k, v, layout, token_norm=token_norm, stream=stream)
+    qk = mxfp8_rope_quantize_qk(q, k, rope, positions, layout, stream=stream)
+    if token_norm:
+        return qk + tuple(mxfp8_quantize_v_fused(v, layout, stream=stream))
+    return qk + tuple(mxfp8_quantize_v_colwise(v, layout, stream=stream)) + (None, None)
+
+
 def forward(q, k, v, layout=BSHD, softmax_scale=None, p_terms=2, leaky=0, o=None, lse=None, stream=None,
-            o8_out=False, bf16_out=True):
+            o8_out=False, bf16_out=True, rope=None, positions=None):
     """The whole hot path on bf16 inputs: quantise Q, K rowwise, V columnwise + token-normalised,
     then the leak-free causal attention forward.  Returns (O bf16, LSE fp32); `o` and `lse` may be
     given (laid out like q and [B, Hq, S]).  With o8_out=True the MXFP8 O is returned as well, as
-    in mxfp8_causal_attn_fwd."""
-    qq, qs, kq, ks, vt, vsc, vtn, vtn_sc = mxfp8_quantize_qkv(q, k, v, layout, token_norm=not leaky, stream=stream)
+    in mxfp8_causal_attn_fwd.  With `rope` (a Rope) Q and K are rotated on their way into MXFP8, at
+    `positions` as in mxfp8_rope_quantize_qk; attention is causal by the tokens' order all the same."""
+    qq, qs, kq, ks, vt, vsc, vtn, vtn_sc = _operands(q, k, v, layout, not leaky, rope, positions, stream)
     return mxfp8_causal_attn_fwd(qq, qs, kq, ks, vt, vsc, vtn, vtn_sc, layout, softmax_scale, p_terms, leaky,
                                  o=o, lse=lse, stream=stream, o8_out=o8_out, bf16_out=bf16_out)
 
@@ -362,12 +464,15 @@ def bf16_attn_bwd_static_capacity():
     return int(lib.bf16_attn_bwd_static_capacity())
 
 
-def forward_backward(q, k, v, do, layout=BSHD, softmax_scale=None, p_terms=2, stream=None):
-    """Forward then the backward on decoded operands; returns (O, LSE, dQ, dK, dV)."""
-    qq, qs, kq, ks, vt, vsc, vtn, vtn_sc = mxfp8_quantize_qkv(q, k, v, layout, stream=stream)
+def forward_backward(q, k, v, do, layout=BSHD, softmax_scale=None, p_terms=2, stream=None, rope=None, positions=None):
+    """Forward then the backward on decoded operands; returns (O, LSE, dQ, dK, dV).  With `rope` (see forward) dQ and
+    dK are those of the unrotated q and k."""
+    qq, qs, kq, ks, vt, vsc, vtn, vtn_sc = _operands(q, k, v, layout, True, rope, positions, stream)
     o, lse = mxfp8_causal_attn_fwd(qq, qs, kq, ks, vt, vsc, vtn, vtn_sc, layout, softmax_scale, p_terms,
                                    stream=stream)
     dq, dk, dv = bf16_attn_bwd(qq, qs, kq, ks, vtn, vtn_sc, o, lse, do, layout, softmax_scale, stream=stream)
+    if rope is not None:
+        apply_rope(dq, dk, rope, positions, layout, inverse=True, q_out=dq, k_out=dk, stream=stream)
     return o, lse, dq, dk, dv
 
 
@@ -463,7 +568,7 @@ def mx_cache_alloc(num_pages, page_size, Hkv, D=128, fmt=CACHE_MXFP4, device="cu
 
 
 def _act_dims(x, layout, cache, name):
-    """(B, T, H), element strides (b, t, h) and the dtype code of an activation of `cache`'s head size."""
+    """(B, T, H), element strides (b, t, h) and the dtype code of an activation of `cache`'s head size (and device)."""
     code = _ACT.get(x.dtype)
     if code is None or x.dim() != 4 or x.device != cache.device:
         raise ValueError("%s must be a 4-D bfloat16 or float16 tensor on the cache's device" % name)
@@ -533,13 +638,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _packed_call(name, params, fields):
-    """The C call `name` taking its parameters as packed bytes, and the packer of what follows the cache in them
-    (native sizes and alignment, as ctypes lays `params` out): a quarter of a ctypes structure's time."""
+def _packed_call(name, params, fields, ahead=ctypes.sizeof(CachePools)):
+    """The C call `name` taking its parameters as packed bytes, and the packer of what follows the cache (`ahead` bytes)
+    in them (native sizes and alignment, as ctypes lays `params` out): a quarter of a ctypes structure's time."""
     f = lib[name]
     f.restype, f.argtypes = ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]
     packer = struct.Struct("@" + fields)
-    assert ctypes.sizeof(CachePools) + packer.size == ctypes.sizeof(params)
+    assert ahead + packer.size == ctypes.sizeof(params)
     return f, packer.pack
 
 
@@ -651,3 +756,464 @@ def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, so
                         workspace.data_ptr() if need else 0, need)
     _check(_c_attn(p, _raw_stream(device.index)))
     return o, lse
+
+
+# ------------------------------------------------------------------------------- norm and rotary positions
+_WEIGHT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_ANGLES = ctypes.sizeof(RopeAngles)
+_c_norm, _pack_norm = _packed_call("rms_norm", RmsNormParams, "8q9q5if", 0)
+_c_norm_bwd, _pack_norm_bwd = _packed_call("rms_norm_bwd", RmsNormBwdParams, "7q9q4i2q", 0)
+_c_rope, _pack_rope = _packed_call("rope", RopeParams, "4q12q3q7i0q", _ANGLES)
+_c_rope_quant, _pack_rope_quant = _packed_call("mxfp8_rope_quantize_qk", RopeQuantParams, "2q6q4q3q8i", _ANGLES)
+_c_write_rope, _pack_write_rope = _packed_call("mx_cache_write_rope", CacheWriteRopeParams, "4q12q5i2qi3q",
+                                               ctypes.sizeof(CachePools) + _ANGLES)
+_c_bounds, _pack_bounds = _packed_call("mx_cache_bounds", CacheBoundsParams, "2q2i2qi3q")
+_c_sparse, _pack_sparse = _packed_call("mx_cache_sparse_attn", CacheSparseAttnParams, "12q4if3i2qi5q")
+
+
+def _same_rows(x, t, name, dtype=None):
+    if t.shape != x.shape or t.dtype != (dtype or x.dtype) or t.device != x.device:
+        raise ValueError("%s must have the first tensor's shape, device and dtype" % name)
+
+
+def _row_layout(tensors):
+    """(rows, inner, [(stride, inner stride)]) of tensors [..., N] of one shape (None: (0, 0)): one split of the leading
+    dimensions into two groups, within each of which every tensor's rows are evenly spaced."""
+    first = tensors[0]
+    lead = first.shape[:-1]
+    rows = 1
+    for n in lead:
+        rows *= n
+    if all(t is None or t.is_contiguous() for t in tensors):
+        pair = (first.shape[-1], 0)
+        return rows, 1, [pair if t is not None else (0, 0) for t in tensors]
+
+    def even(t, dims):
+        """Stride of rows numbered over `dims`, or None."""
+        step = None
+        for d in reversed(dims):
+            if t.shape[d] == 1:
+                continue
+            if step is None:
+                step, count = t.stride(d), t.shape[d]
+            elif t.stride(d) == step * count:
+                count *= t.shape[d]
+            else:
+                return None
+        return step or 0
+
+    if rows == 0:
+        return 0, 1, [(0, 0)] * len(tensors)
+    for cut in range(len(lead), -1, -1):
+        outer, inner = range(cut), range(cut, len(lead))
+        pairs = [(0, 0) if t is None else (even(t, outer), even(t, inner)) for t in tensors]
+        if all(a is not None and b is not None for a, b in pairs):
+            n = 1
+            for d in inner:
+                n *= lead[d]
+            return rows, n, pairs
+    raise ValueError("the rows of every tensor must be spaced by at most two strides")
+
+
+def _on_cuda(x, name):
+    if not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+
+
+def _norm_args(x, weight):
+    dt, wt = _ACT.get(x.dtype), _WEIGHT.get(weight.dtype)
+    if dt is None or x.dim() < 1:
+        raise ValueError("expected a bfloat16 or float16 tensor [..., N]")
+    N = x.shape[-1]
+    if weight.shape != (N,) or weight.device != x.device or not weight.is_contiguous() or \
+            weight.dtype not in (x.dtype, torch.float32):
+        raise ValueError("weight must be a contiguous [N] tensor of the activations' dtype or float32")
+    return dt, wt, N
+
+
+def _d_contiguous(t, name):
+    if t is not None and t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
+        raise ValueError("%s must be contiguous along its last dimension" % name)
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, y=None, sum_out=None, rstd=None, y8_out=False, y_out=True, y8=None,
+             y_sc=None, rule=SCALE_FLOOR, stream=None):
+    """Root-mean-square norm of the rows of x [..., N] (bf16 or fp16), with the residual's addition.
+
+    s = x + residual (held in x's dtype), rstd = (mean s^2 + eps)^-1/2, y = s * rstd * weight.  Returns (y, s, rstd), s being
+    x itself without a residual and rstd float32 [...]; with y8_out=True, (y or None, s, rstd, y as E4M3 bytes [..., N], its
+    scales [..., N/32]).  weight: [N], x's dtype or float32.  y, sum_out and rstd may be given; y and sum_out may be x or
+    residual themselves."""
+    _on_cuda(x, "x")
+    there = _elsewhere(x, stream)
+    if there is not None:
+        with there:
+            return rms_norm(x, weight, eps, residual, y, sum_out, rstd, y8_out, y_out, y8, y_sc, rule)
+    dt, wt, N = _norm_args(x, weight)
+    if residual is not None:
+        _same_rows(x, residual, "residual")
+    if not y_out:
+        if not y8_out:
+            raise ValueError("y_out=False needs y8_out=True")
+        y = None
+    elif y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        _same_rows(x, y, "y")
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out is for a residual")
+    elif sum_out is None:
+        sum_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        _same_rows(x, sum_out, "sum_out")
+    if rstd is None:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    elif rstd.shape != x.shape[:-1] or rstd.dtype != torch.float32 or rstd.device != x.device or not rstd.is_contiguous():
+        raise ValueError("rstd must be a contiguous float32 tensor of x's leading dimensions")
+    if y8_out:
+        shapes = (x.shape, x.shape[:-1] + (N // 32,))
+        y8, y_sc = (torch.empty(n, dtype=torch.uint8, device=x.device) if t is None else t for t, n in zip((y8, y_sc), shapes))
+        for t, n in ((y8, shapes[0]), (y_sc, shapes[1])):
+            if t.dtype != torch.uint8 or t.shape != n or t.device != x.device or not t.is_contiguous():
+                raise ValueError("y8 and y_sc must be contiguous uint8 tensors [..., N] and [..., N/32]")
+    for t, n in ((x, "x"), (residual, "residual"), (y, "y"), (sum_out, "sum_out")):
+        _d_contiguous(t, n)
+    rows, inner, (xs, rs, ys, ss) = _row_layout((x, residual, y, sum_out))
+    p = _pack_norm(x.data_ptr(), 0 if residual is None else residual.data_ptr(), weight.data_ptr(),
+                   0 if y is None else y.data_ptr(), 0 if sum_out is None else sum_out.data_ptr(), rstd.data_ptr(),
+                   y8.data_ptr() if y8_out else 0, y_sc.data_ptr() if y8_out else 0, rows, *xs, *rs, *ys, *ss, inner, N, dt,
+                   wt, rule, eps)
+    _check(_c_norm(p, _raw_stream(x.device.index)))
+    s = x if residual is None else sum_out
+    return (y, s, rstd, y8, y_sc) if y8_out else (y, s, rstd)
+
+
+def rms_norm_bwd_workspace_bytes(rows, N):
+    """Bytes of scratch rms_norm_bwd needs (the C call of the same name)."""
+    return int(lib.rms_norm_bwd_workspace_bytes(rows, N))
+
+
+def rms_norm_bwd(dy, s, weight, rstd, ds=None, dx=None, dweight=None, workspace=None, stream=None):
+    """Gradients of rms_norm at s (its second output) with its rstd: (dx, dweight).  dx is the gradient of x and of the
+    residual alike, with `ds`, the gradient that reaches s by the residual stream, added; dweight has weight's dtype.
+    dx may be dy, s or ds themselves.  `workspace`: a device tensor of rms_norm_bwd_workspace_bytes(rows, N) bytes that no
+    other running call uses, else one is allocated here."""
+    _on_cuda(s, "s")
+    there = _elsewhere(s, stream)
+    if there is not None:
+        with there:
+            return rms_norm_bwd(dy, s, weight, rstd, ds, dx, dweight, workspace)
+    dt, wt, N = _norm_args(s, weight)
+    _same_rows(s, dy, "dy")
+    if ds is not None:
+        _same_rows(s, ds, "ds")
+    if rstd.shape != s.shape[:-1] or rstd.dtype != torch.float32 or rstd.device != s.device or not rstd.is_contiguous():
+        raise ValueError("rstd must be a contiguous float32 tensor of s's leading dimensions")
+    if dx is None:
+        dx = torch.empty_like(s, memory_format=torch.contiguous_format)
+    else:
+        _same_rows(s, dx, "dx")
+    rows, inner, (dys, ss, dss, dxs) = _row_layout((dy, s, ds, dx))
+    for t, n in ((dy, "dy"), (s, "s"), (ds, "ds"), (dx, "dx")):
+        _d_contiguous(t, n)
+    if dweight is None:
+        dweight = torch.empty_like(weight) if rows else torch.zeros_like(weight)
+    elif dweight.shape != weight.shape or dweight.dtype != weight.dtype or dweight.device != s.device or \
+            not dweight.is_contiguous():
+        raise ValueError("dweight must be a contiguous tensor like weight")
+    if workspace is None:
+        need = rms_norm_bwd_workspace_bytes(rows, N)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=s.device)
+    else:
+        if workspace.device != s.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the activations' device")
+        need = workspace.numel() * workspace.element_size()
+    p = _pack_norm_bwd(dy.data_ptr(), s.data_ptr(), weight.data_ptr(), rstd.data_ptr(), 0 if ds is None else ds.data_ptr(),
+                       dx.data_ptr(), dweight.data_ptr(), rows, *dys, *ss, *dss, *dxs, inner, N, dt, wt, workspace.data_ptr(),
+                       need)
+    _check(_c_norm_bwd(p, _raw_stream(s.device.index)))
+    return dx, dweight
+
+
+def mxfp8_dequantize(x, sc, layout=BSHD, dtype=torch.bfloat16, out=None, stream=None):
+    """MXFP8 rows back to values: x uint8 [B, S, H, D] (SBHD: [S, B, H, D]) with sc [B, H, S, D/32], as the rowwise
+    quantisers return them, or [..., N] with sc [..., N/32], as rms_norm does (x not 4-D, or 4-D with such scales and
+    layout=None)."""
+    _on_cuda(x, "x")
+    there = _elsewhere(x, stream)
+    if there is not None:
+        with there:
+            return mxfp8_dequantize(x, sc, layout, dtype, out)
+    code = _ACT.get(dtype)
+    if code is None:
+        raise ValueError("dtype must be bfloat16 or float16")
+    for t, n in ((x, "x"), (sc, "sc")):
+        if not t.is_cuda or t.dtype != torch.uint8 or not t.is_contiguous() or t.device != x.device:
+            raise ValueError("%s must be a contiguous CUDA uint8 tensor on one device with the other" % n)
+    if x.dim() == 4 and layout is not None:
+        if layout not in (BSHD, SBHD):
+            raise ValueError("layout must be BSHD or SBHD")
+        B, S, H, D = _bshd_dims(x, layout)
+        want = (B, H, S, D // 32)
+    elif x.dim() >= 1:
+        B, H, D = 1, 1, x.shape[-1]
+        S, want, layout = x.numel() // D if D else 0, x.shape[:-1] + (D // 32,), BSHD
+    else:
+        raise ValueError("x must have at least one dimension")
+    if tuple(sc.shape) != tuple(want):
+        raise ValueError("sc must have the shape %s" % (tuple(want),))
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != dtype or out.device != x.device or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor shaped like x, of dtype")
+    _check(lib.mxfp8_dequantize(x.data_ptr(), sc.data_ptr(), B, S, H, D, layout, code, out.data_ptr(),
+                                _raw_stream(x.device.index)))
+    return out
+
+
+class Rope:
+    """Rotary positions' frequencies: one per pair of the first `rot` elements of a head, on the device, in turns per token
+    (bsc_rope_turns and bsc_rope_angles in bsc.h).  Any 32-bit position may be rotated by it; it holds no other state.
+
+    interleaved: pairs are neighbours (x_2i, x_2i+1), else (x_i, x_{i + rot/2}).  scaling: ROPE_PLAIN; ROPE_LINEAR (positions
+    / factor); ROPE_BASE (base * factor^(rot/(rot-2))); ROPE_BY_PARTS (pairs of fewer than low_turns turns in
+    original_length tokens are interpolated by factor, those of more than high_turns are kept, what lies between is mixed).
+    magnitude: the factor on what is rotated (None: 0.1 ln(factor) + 1 by parts, else 1)."""
+
+    __slots__ = ("rot", "interleaved", "magnitude", "turns", "device", "params", "packed")
+
+    def __init__(self, rot, base=10000.0, interleaved=False, scaling=ROPE_PLAIN, factor=1.0, original_length=0,
+                 low_turns=1.0, high_turns=32.0, magnitude=None, device="cuda"):
+        config = RopeConfig(rot, scaling, base, factor, original_length, low_turns, high_turns)
+        host, m = (ctypes.c_ulonglong * 128)(), ctypes.c_float()
+        _check(lib.bsc_rope_turns(ctypes.byref(config), host, ctypes.byref(m)))
+        signed = (ctypes.c_longlong * (rot // 2)).from_buffer(host)
+        self.turns = torch.tensor(list(signed), dtype=torch.int64).to(device)
+        self.rot, self.interleaved = rot, bool(interleaved)
+        self.magnitude = m.value if magnitude is None else float(magnitude)
+        self.device = self.turns.device
+        self.params = RopeAngles(self.turns.data_ptr(), self.magnitude, rot, int(self.interleaved))
+        self.packed = bytes(self.params)
+
+
+def _positions(t, B, T, rope):
+    """Pointer and strides (b, t) of positions: None, [B] (of the first tokens) or [B, T] int32."""
+    if t is None:
+        return 0, 0, 0
+    if t.dtype is not torch.int32 or t.device != rope.device or t.shape not in ((B,), (B, T)):
+        raise ValueError("positions must be an int32 tensor of shape (%d,) or (%d, %d) on rope's device" % (B, B, T))
+    if t.dim() == 1:
+        return t.data_ptr(), t.stride(0), 0
+    if T > 1 and t.stride(1) == 0:
+        raise ValueError("positions must not be expanded along the tokens")
+    return t.data_ptr(), t.stride(0), t.stride(1) or 1
+
+
+class _Heads:
+    """A head size and a device, for _act_dims."""
+    __slots__ = ("D", "device")
+
+    def __init__(self, x):
+        self.D, self.device = x.shape[-1] if x.dim() else 0, x.device
+
+
+def _on_device(x, rope):
+    if not x.is_cuda or x.device != rope.device:
+        raise ValueError("q must be on rope's device")
+
+
+def apply_rope(q, k, rope, positions=None, layout=BSHD, inverse=False, q_out=None, k_out=None, stream=None):
+    """Q and K (or None) rotated by a Rope in one launch; returns (q, k) of the same shapes and dtype.
+
+    q [B, T, Hq, D] and k [B, T, Hkv, D] (SBHD: [T, B, H, D]), bf16 or fp16, any strides with D contiguous.  positions: None
+    (token t is at t), int32 [B] (of each sequence's first token) or [B, T].  inverse=True turns back: gradients of q and k
+    from those of the outputs.  q_out and k_out may be q and k themselves."""
+    _on_device(q, rope)
+    there = _elsewhere(q, stream)
+    if there is not None:
+        with there:
+            return apply_rope(q, k, rope, positions, layout, inverse, q_out, k_out)
+    like = _Heads(q)
+    dims, qs, dt = _act_dims(q, layout, like, "q")
+    B, T, Hq = dims
+    D, Hkv, ks, k_os = like.D, 0, (0, 0, 0), (0, 0, 0)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        _, q_os = _dense(layout, B, T, Hq, D)
+    else:
+        dims_o, q_os, dt_o = _act_dims(q_out, layout, like, "q_out")
+        if dims_o != dims or dt_o != dt:
+            raise ValueError("q_out must have q's shape and dtype")
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out is for k")
+    else:
+        (Bk, Tk, Hkv), ks, dt_k = _act_dims(k, layout, like, "k")
+        if (Bk, Tk) != (B, T) or dt_k != dt:
+            raise ValueError("k must have q's batch, tokens and dtype")
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            _, k_os = _dense(layout, B, T, Hkv, D)
+        else:
+            dims_o, k_os, dt_o = _act_dims(k_out, layout, like, "k_out")
+            if dims_o != (B, T, Hkv) or dt_o != dt:
+                raise ValueError("k_out must have k's shape and dtype")
+    p = rope.packed + _pack_rope(q.data_ptr(), 0 if k is None else k.data_ptr(), q_out.data_ptr(),
+                                 0 if k is None else k_out.data_ptr(), *qs, *ks, *q_os, *k_os, *_positions(positions, B, T, rope),
+                                 B, T, Hq, Hkv, D, dt, int(bool(inverse)))
+    _check(_c_rope(p, _raw_stream(q.device.index)))
+    return q_out, k_out
+
+
+rope = apply_rope      # the C call's name; `rope` is also what the calls name their Rope argument
+
+
+def mxfp8_rope_quantize_qk(q, k, rope, positions=None, layout=BSHD, rule=SCALE_FLOOR, stream=None):
+    """Q and K rotated (as in `rope`) and quantised rowwise to MXFP8 in one launch, from the rotated fp32 values:
+    (q_e4m3, q_sc, k_e4m3, k_sc), bytes dense in `layout` and scales [B, H, T, D/32]; D = 128."""
+    _on_device(q, rope)
+    there = _elsewhere(q, stream)
+    if there is not None:
+        with there:
+            return mxfp8_rope_quantize_qk(q, k, rope, positions, layout, rule)
+    like = _Heads(q)
+    (B, T, Hq), qs, dt = _act_dims(q, layout, like, "q")
+    (Bk, Tk, Hkv), ks, dt_k = _act_dims(k, layout, like, "k")
+    if (Bk, Tk) != (B, T) or dt_k != dt:
+        raise ValueError("k must have q's batch, tokens and dtype")
+    u8 = dict(dtype=torch.uint8, device=q.device)
+    q8, q_sc = torch.empty(q.shape, **u8), torch.empty((B, Hq, T, like.D // 32), **u8)
+    k8, k_sc = torch.empty(k.shape, **u8), torch.empty((B, Hkv, T, like.D // 32), **u8)
+    p = rope.packed + _pack_rope_quant(q.data_ptr(), k.data_ptr(), *qs, *ks, q8.data_ptr(), q_sc.data_ptr(), k8.data_ptr(),
+                                       k_sc.data_ptr(), *_positions(positions, B, T, rope), B, T, Hq, Hkv, like.D, dt, layout,
+                                       rule)
+    _check(_c_rope_quant(p, _raw_stream(q.device.index)))
+    return q8, q_sc, k8, k_sc
+
+
+def mx_cache_write_rope(cache, q, k, v, rope, page_table, seq_lens, new_lens=None, layout=BSHD, rule=SCALE_FLOOR, q_out=None,
+                        dev_status=None, stream=None):
+    """mx_cache_write with K rotated on its way in, and q's rows of the same tokens rotated: returns q_out, shaped and typed
+    like q.  Positions are those of the write: token t < new_lens[b] of sequence b is at seq_lens[b] - new_lens[b] + t; rows of
+    q_out of other tokens are zeros.  q_out may be q itself."""
+    there = _elsewhere(cache, stream)
+    if there is not None:
+        with there:
+            return mx_cache_write_rope(cache, q, k, v, rope, page_table, seq_lens, new_lens, layout, rule, q_out, dev_status)
+    _on_device(q, rope)
+    dims, qs, dt = _act_dims(q, layout, cache, "q")
+    dims_k, ks, dt_k = _act_dims(k, layout, cache, "k")
+    dims_v, vs, dt_v = _act_dims(v, layout, cache, "v")
+    B, T, Hq = dims
+    if dims_k != (B, T, cache.Hkv) or dims_v != dims_k or dt_k != dt or dt_v != dt:
+        raise ValueError("k and v must have q's batch, tokens and dtype and the cache's heads")
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        _, q_os = _dense(layout, B, T, Hq, cache.D)
+    else:
+        dims_o, q_os, dt_o = _act_dims(q_out, layout, cache, "q_out")
+        if dims_o != dims or dt_o != dt:
+            raise ValueError("q_out must have q's shape and dtype")
+    p = cache.packed + rope.packed + _pack_write_rope(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), *qs, *ks, *vs, *q_os, B, T, Hq, dt, rule,
+        *_table(page_table, B, cache), _index(seq_lens, B, cache, "seq_lens"), _index(new_lens, B, cache, "new_lens"),
+        _status(dev_status, cache))
+    _check(_c_write_rope(p, _raw_stream(cache.device.index)))
+    return q_out
+
+
+# ----------------------------------------------------------------------------- reading less of a long cache
+class MxBounds:
+    """Bounds of a cache's pages: codes int8 [num_pages, Hkv, 2, D] (minima, maxima along D) and exps uint8 [num_pages, Hkv],
+    the caller's two buffers (mx_cache_bounds_alloc makes new ones).  The handle holds no other state."""
+
+    __slots__ = ("codes", "exps")
+
+    def __init__(self, cache, codes, exps):
+        shape = (cache.num_pages, cache.Hkv)
+        for t, n, d, want in ((codes, "codes", torch.int8, shape + (2, cache.D)), (exps, "exps", torch.uint8, shape)):
+            if t.dtype != d or tuple(t.shape) != want or t.device != cache.device or not t.is_contiguous():
+                raise ValueError("%s must be a contiguous %s tensor %s on the cache's device" % (n, d, want))
+        self.codes, self.exps = codes, exps
+
+
+def mx_cache_bounds_alloc(cache):
+    """MxBounds with new buffers for `cache`; mx_cache_bounds fills in the pages that hold tokens."""
+    shape = (cache.num_pages, cache.Hkv)
+    return MxBounds(cache, torch.zeros(shape + (2, cache.D), dtype=torch.int8, device=cache.device),
+                    torch.zeros(shape, dtype=torch.uint8, device=cache.device))
+
+
+def _bounds_of(bounds, cache):
+    if bounds.codes.shape != (cache.num_pages, cache.Hkv, 2, cache.D) or bounds.codes.device != cache.device:
+        raise ValueError("bounds are not this cache's")
+    return bounds.codes.data_ptr(), bounds.exps.data_ptr()
+
+
+def mx_cache_bounds(cache, bounds, page_table, seq_lens, T, new_lens=None, dev_status=None, stream=None):
+    """Brings up to date the bounds of the pages that hold the last new_lens[b] (None: T; at most T) tokens of every
+    sequence: after a write, with the write's lengths."""
+    there = _elsewhere(cache, stream)
+    if there is not None:
+        with there:
+            return mx_cache_bounds(cache, bounds, page_table, seq_lens, T, new_lens, dev_status)
+    B = page_table.shape[0]
+    p = cache.packed + _pack_bounds(*_bounds_of(bounds, cache), B, T, *_table(page_table, B, cache),
+                                    _index(seq_lens, B, cache, "seq_lens"), _index(new_lens, B, cache, "new_lens"),
+                                    _status(dev_status, cache))
+    _check(_c_bounds(p, _raw_stream(cache.device.index)))
+
+
+@functools.lru_cache(maxsize=256)
+def mx_cache_sparse_attn_workspace_bytes(B, T, Hq, Hkv, D, page_size, max_pages, top):
+    """Bytes of scratch mx_cache_sparse_attn needs at these sizes (the C call of the same name)."""
+    return int(lib.mx_cache_sparse_attn_workspace_bytes(B, T, Hq, Hkv, D, page_size, max_pages, top))
+
+
+def mx_cache_sparse_attn(q, cache, bounds, page_table, seq_lens, top, first=1, last=1, new_lens=None, layout=BSHD,
+                         softmax_scale=None, o=None, lse=None, blocks=None, workspace=None, dev_status=None, stream=None):
+    """mx_cache_attn over `top` pages for every query and KV head: the first `first`, the last `last` (the query's own among
+    them), and those whose bounds score highest against the KV head's queries (bsc.h has the score).  Returns (O shaped and
+    typed like q, LSE fp32 [B, Hq, T], blocks int32 [B, T, Hkv, top]: the pages' numbers, ascending, then -1).  Bounds must
+    be up to date (mx_cache_bounds).  `workspace`: a device tensor of mx_cache_sparse_attn_workspace_bytes(...) bytes that
+    no other running call uses, else one is allocated here."""
+    there = _elsewhere(cache, stream)
+    if there is not None:
+        with there:
+            return mx_cache_sparse_attn(q, cache, bounds, page_table, seq_lens, top, first, last, new_lens, layout,
+                                        softmax_scale, o, lse, blocks, workspace, dev_status)
+    dims, qs, dt = _act_dims(q, layout, cache, "q")
+    B, T, Hq = dims
+    table = _table(page_table, B, cache)
+    device = cache.device
+    if o is None:
+        _, o_s = _dense(layout, B, T, Hq, cache.D)
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        dims_o, o_s, dt_o = _act_dims(o, layout, cache, "o")
+        if dims_o != dims or dt_o != dt:
+            raise ValueError("o must have q's shape and dtype")
+    if lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=device)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T) or lse.device != device or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 tensor [B, Hq, T] on the cache's device")
+    if blocks is None:
+        blocks = torch.empty((B, T, cache.Hkv, max(top, 0)), dtype=torch.int32, device=device)
+    elif blocks.dtype != torch.int32 or tuple(blocks.shape) != (B, T, cache.Hkv, top) or blocks.device != device or \
+            not blocks.is_contiguous():
+        raise ValueError("blocks must be a contiguous int32 tensor [B, T, Hkv, top] on the cache's device")
+    if workspace is None:
+        need = mx_cache_sparse_attn_workspace_bytes(B, T, Hq, cache.Hkv, cache.D, cache.page_size, table[2], top)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    else:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        need = workspace.numel() * workspace.element_size()
+    p = cache.packed + _pack_sparse(*_bounds_of(bounds, cache), q.data_ptr(), o.data_ptr(), lse.data_ptr(), blocks.data_ptr(),
+                                    *qs, *o_s, B, T, Hq, dt, cache.D ** -0.5 if softmax_scale is None else softmax_scale, top,
+                                    first, last, *table, _index(seq_lens, B, cache, "seq_lens"),
+                                    _index(new_lens, B, cache, "new_lens"), _status(dev_status, cache), workspace.data_ptr(),
+                                    need)
+    _check(_c_sparse(p, _raw_stream(device.index)))
+    return o, lse, blocks

@@ -14,6 +14,8 @@
 
 namespace {
 
+constexpr long long ROPE_MOST_HEADS = 1 << 20;   // of q, k and v together
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Device capability check, cached per device ordinal.
@@ -219,6 +221,78 @@ bsc::CachePools cache_pools(const bsc_mx_cache& c) {
   p.page_size = c.page_size;
   p.Hkv = c.Hkv;
   return p;
+}
+
+// The counting strides of a row layout: 16-byte rows, and no two output rows in one place.
+bsc_status check_rows(long long outer, long long inner_stride, long long rows, int inner, bool output) {
+  const bool many = rows > inner, grouped = inner > 1 && rows > 1;
+  if ((many && outer % 8 != 0) || (grouped && inner_stride % 8 != 0)) return BSC_ERR_ALIGN;
+  if (output && ((many && outer == 0) || (grouped && inner_stride == 0))) return BSC_ERR_SHAPE;
+  return BSC_OK;
+}
+
+// Sizes and types that rms_norm and its gradients share.
+bsc_status check_norm(long long rows, int N, int inner, int dtype, int weight_dtype, bool* empty) {
+  *empty = false;
+  if (rows < 0 || N < 0 || inner < 1) return BSC_ERR_SHAPE;
+  if (dtype != BSC_BF16 && dtype != BSC_FP16) return BSC_ERR_UNSUPPORTED;
+  if (weight_dtype != dtype && weight_dtype != BSC_FP32) return BSC_ERR_UNSUPPORTED;
+  if (rows == 0 || N == 0) {
+    *empty = true;
+    return BSC_OK;
+  }
+  if (N % 8 != 0 || N > BSC_NORM_MAX_N || rows >= (1LL << 40)) return BSC_ERR_UNSUPPORTED;
+  return BSC_OK;
+}
+
+// What the rotary calls share.  rot counts for a problem that is not empty.
+bsc_status check_angles(const bsc_rope_angles& a, int D) {
+  if (a.rot < 16 || a.rot % 16 != 0 || a.rot > D) return BSC_ERR_UNSUPPORTED;
+  if ((a.interleaved != 0 && a.interleaved != 1) || !std::isfinite(a.magnitude)) return BSC_ERR_UNSUPPORTED;
+  if (!a.turns) return BSC_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(a.turns) & 7u) != 0) return BSC_ERR_ALIGN;
+  return BSC_OK;
+}
+bsc_status check_rope(int B, int T, int Hq, int Hkv, int D, int dtype, bool* empty) {
+  *empty = false;
+  if (B < 0 || T < 0 || Hq < 0 || Hkv < 0 || D < 0) return BSC_ERR_SHAPE;
+  if (dtype != BSC_BF16 && dtype != BSC_FP16) return BSC_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0 || Hq == 0) {
+    *empty = true;
+    return BSC_OK;
+  }
+  if (D == 0 || D % 16 != 0 || D > 256) return BSC_ERR_UNSUPPORTED;
+  // blocks, and rows of a block's 16 tokens
+  if (reaches_2_31({B, T}) || (long long)Hq + 2LL * Hkv > ROPE_MOST_HEADS) return BSC_ERR_UNSUPPORTED;
+  return BSC_OK;
+}
+
+// A cache whose pages are the (page, head) slices of another's, numbered page * per_page + head: 0 where they cannot be.
+int slices_per_page(const bsc_mx_cache& c) {
+  if (c.num_pages == 1) return c.Hkv;
+  const long long data = (long long)c.page_size * (c.format == BSC_CACHE_MXFP4 ? c.D / 2 : c.D);
+  const long long scales = (long long)c.page_size * (c.D / 32), n = c.k_page_stride / data;
+  if (c.k_page_stride != n * data || c.v_page_stride != n * data || c.k_sc_page_stride != n * scales ||
+      c.v_sc_page_stride != n * scales || n * c.num_pages >= (1LL << 31))
+    return 0;
+  return (int)n;
+}
+
+// The parts of mx_cache_sparse_attn's workspace, in bytes from its start; false where the sizes are refused.
+struct SparseParts {
+  size_t table, lens, attn, all;
+};
+bool sparse_parts(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int top, SparseParts* w) {
+  if (reaches_2_31({B, T, Hkv, max_pages > 128 ? max_pages : 128}) || reaches_2_31({B, T, Hkv, top})) return false;
+  const int rows = B * T * Hkv, cols = top < max_pages ? top : max_pages;
+  const long long tokens = (long long)cols * page_size;
+  if (tokens > BSC_CACHE_MAX_TOKENS || cache_attn_too_large(rows, 1, Hq / Hkv, 1, tokens)) return false;
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  w->table = max_pages > top ? up((size_t)rows * max_pages * 4) : 0;
+  w->lens = w->table + up((size_t)rows * cols * 4);
+  w->attn = w->lens + up((size_t)rows * 4);
+  w->all = w->attn + bsc::cache_attn_workspace_bytes(rows, 1, Hq / Hkv, 1, D, tokens);
+  return true;
 }
 
 }  // namespace
@@ -560,6 +634,365 @@ bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream)
   a.ws = p->workspace;
   a.fp16 = p->dtype == BSC_FP16;
   return from_cuda(bsc::launch_cache_attn(a, p->cache.format, p->cache.D, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bsc_status rms_norm(const bsc_rms_norm_params* p, bsc_stream_t stream) {
+  if (!p) return BSC_ERR_NULL;
+  if (p->rule != BSC_SCALE_FLOOR && p->rule != BSC_SCALE_CEIL) return BSC_ERR_UNSUPPORTED;
+  if (!(std::isfinite(p->eps) && p->eps >= 0.f)) return BSC_ERR_UNSUPPORTED;
+  bool empty;
+  bsc_status s = check_norm(p->rows, p->N, p->inner, p->dtype, p->weight_dtype, &empty);
+  if (s != BSC_OK || empty) return s;
+  if (p->y_e4m3 && p->N % 32 != 0) return BSC_ERR_UNSUPPORTED;
+  if (!p->x || !p->weight || (!p->y && !p->y_e4m3) || (p->y_e4m3 && !p->y_sc)) return BSC_ERR_NULL;
+  for (const void* q : {p->x, p->residual, p->weight, (const void*)p->y, (const void*)p->sum, (const void*)p->y_e4m3})
+    if (!aligned16(q)) return BSC_ERR_ALIGN;
+  if (!aligned4(p->rstd)) return BSC_ERR_ALIGN;
+  if ((s = check_rows(p->x_stride, p->x_inner_stride, p->rows, p->inner, false)) != BSC_OK) return s;
+  if (p->residual && (s = check_rows(p->residual_stride, p->residual_inner_stride, p->rows, p->inner, false)) != BSC_OK)
+    return s;
+  if (p->y && (s = check_rows(p->y_stride, p->y_inner_stride, p->rows, p->inner, true)) != BSC_OK) return s;
+  if (p->sum && (s = check_rows(p->sum_stride, p->sum_inner_stride, p->rows, p->inner, true)) != BSC_OK) return s;
+  if ((s = check_device()) != BSC_OK) return s;
+  bsc::NormArgs a{};
+  a.x = p->x;
+  a.r = p->residual;
+  a.w = p->weight;
+  a.y = p->y;
+  a.s = p->sum;
+  a.rstd = p->rstd;
+  a.y8 = p->y_e4m3;
+  a.ysc = p->y_sc;
+  a.xs = {p->x_stride, p->x_inner_stride};
+  a.rs = {p->residual_stride, p->residual_inner_stride};
+  a.ys = {p->y_stride, p->y_inner_stride};
+  a.ss = {p->sum_stride, p->sum_inner_stride};
+  a.rows = p->rows;
+  a.inner = p->inner;
+  a.N = p->N;
+  a.rule = p->rule;
+  a.eps = p->eps;
+  return from_cuda(bsc::launch_norm(a, p->dtype, p->weight_dtype == BSC_FP32, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t rms_norm_bwd_workspace_bytes(long long rows, int N) {
+  if (rows <= 0 || N <= 0 || N % 8 != 0 || N > BSC_NORM_MAX_N) return 0;
+  return bsc::norm_bwd_workspace_bytes(rows, N);
+}
+
+bsc_status rms_norm_bwd(const bsc_rms_norm_bwd_params* p, bsc_stream_t stream) {
+  if (!p) return BSC_ERR_NULL;
+  bool empty;
+  bsc_status s = check_norm(p->rows, p->N, p->inner, p->dtype, p->weight_dtype, &empty);
+  if (s != BSC_OK || empty) return s;
+  if (!p->dy || !p->s || !p->weight || !p->rstd || !p->dx || !p->dweight || !p->workspace) return BSC_ERR_NULL;
+  for (const void* q : {p->dy, p->s, p->weight, p->d_sum, (const void*)p->dx, (const void*)p->dweight,
+                        (const void*)p->workspace})
+    if (!aligned16(q)) return BSC_ERR_ALIGN;
+  if (!aligned4(p->rstd)) return BSC_ERR_ALIGN;
+  if ((s = check_rows(p->dy_stride, p->dy_inner_stride, p->rows, p->inner, false)) != BSC_OK) return s;
+  if ((s = check_rows(p->s_stride, p->s_inner_stride, p->rows, p->inner, false)) != BSC_OK) return s;
+  if (p->d_sum && (s = check_rows(p->d_sum_stride, p->d_sum_inner_stride, p->rows, p->inner, false)) != BSC_OK) return s;
+  if ((s = check_rows(p->dx_stride, p->dx_inner_stride, p->rows, p->inner, true)) != BSC_OK) return s;
+  if (p->workspace_bytes < rms_norm_bwd_workspace_bytes(p->rows, p->N)) return BSC_ERR_SHAPE;
+  if ((s = check_device()) != BSC_OK) return s;
+  bsc::NormBwdArgs a{};
+  a.dy = p->dy;
+  a.s = p->s;
+  a.w = p->weight;
+  a.rstd = p->rstd;
+  a.ds = p->d_sum;
+  a.dx = p->dx;
+  a.dw = p->dweight;
+  a.partial = reinterpret_cast<float*>(p->workspace);
+  a.dys = {p->dy_stride, p->dy_inner_stride};
+  a.ss = {p->s_stride, p->s_inner_stride};
+  a.dss = {p->d_sum_stride, p->d_sum_inner_stride};
+  a.dxs = {p->dx_stride, p->dx_inner_stride};
+  a.rows = p->rows;
+  a.inner = p->inner;
+  a.N = p->N;
+  return from_cuda(bsc::launch_norm_bwd(a, p->dtype, p->weight_dtype == BSC_FP32, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bsc_status mxfp8_dequantize(const uint8_t* x, const uint8_t* sc, int B, int S, int H, int D, bsc_layout layout, int dtype,
+                            void* y, bsc_stream_t stream) {
+  if (B < 0 || S < 0 || H < 0 || D < 0) return BSC_ERR_SHAPE;
+  if (layout != BSC_BSHD && layout != BSC_SBHD) return BSC_ERR_SHAPE;
+  if (dtype != BSC_BF16 && dtype != BSC_FP16) return BSC_ERR_UNSUPPORTED;
+  if (B == 0 || S == 0 || H == 0 || D == 0) return BSC_OK;
+  if (D % 32 != 0 || reaches_2_31({B, S, H}) || (long long)B * S * H >= (1LL << 40) / D) return BSC_ERR_UNSUPPORTED;
+  if (!x || !sc || !y) return BSC_ERR_NULL;
+  if (!aligned16(x) || !aligned16(y)) return BSC_ERR_ALIGN;
+  bsc_status s = check_device();
+  if (s != BSC_OK) return s;
+  return from_cuda(bsc::launch_dequantize(x, sc, y, B, S, H, D, layout, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bsc_status bsc_rope_turns(const bsc_rope_config* c, unsigned long long* turns, float* magnitude) {
+  if (!c || !turns || !magnitude) return BSC_ERR_NULL;
+  if (c->rot < 16 || c->rot % 16 != 0 || c->rot > 256) return BSC_ERR_UNSUPPORTED;
+  if (c->scaling < BSC_ROPE_PLAIN || c->scaling > BSC_ROPE_BY_PARTS) return BSC_ERR_UNSUPPORTED;
+  const bool parts = c->scaling == BSC_ROPE_BY_PARTS;
+  const double factor = c->scaling == BSC_ROPE_PLAIN ? 1.0 : c->factor;
+  if (!(std::isfinite(c->base) && c->base > 0.0 && std::isfinite(factor) && factor > 0.0)) return BSC_ERR_UNSUPPORTED;
+  if (parts && !(factor >= 1.0 && std::isfinite(c->original_length) && c->original_length > 0.0 && c->low_turns >= 0.0 &&
+                 std::isfinite(c->high_turns) && c->low_turns < c->high_turns))
+    return BSC_ERR_UNSUPPORTED;
+  const double two_pi = 6.283185307179586476925;
+  const double base = c->scaling == BSC_ROPE_BASE ? c->base * std::pow(factor, c->rot / (c->rot - 2.0)) : c->base;
+  if (!(std::isfinite(base) && base > 0.0)) return BSC_ERR_UNSUPPORTED;
+  for (int i = 0; i < c->rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / c->rot) / two_pi;      // turns per token
+    if (c->scaling == BSC_ROPE_LINEAR) f /= factor;
+    if (parts) {
+      double k = (c->original_length * f - c->low_turns) / (c->high_turns - c->low_turns);
+      k = k < 0.0 ? 0.0 : k > 1.0 ? 1.0 : k;
+      f *= k + (1.0 - k) / factor;
+    }
+    if (!std::isfinite(f)) return BSC_ERR_UNSUPPORTED;
+    f -= std::floor(f);                                         // whole turns change nothing
+    const double x = std::nearbyint(std::ldexp(f, 64));
+    turns[i] = x >= 18446744073709551616.0 ? 0ull : (unsigned long long)x;
+  }
+  *magnitude = parts ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  return BSC_OK;
+}
+
+bsc_status rope(const bsc_rope_params* p, bsc_stream_t stream) {
+  if (!p) return BSC_ERR_NULL;
+  if (p->inverse != 0 && p->inverse != 1) return BSC_ERR_UNSUPPORTED;
+  const int Hkv = p->k ? p->Hkv : 0;
+  bool empty;
+  bsc_status s = check_rope(p->B, p->T, p->Hq, Hkv, p->D, p->dtype, &empty);
+  if (s != BSC_OK || empty) return s;
+  if ((s = check_angles(p->angles, p->D)) != BSC_OK) return s;
+  if (!p->q || !p->q_out || (Hkv > 0 && !p->k_out)) return BSC_ERR_NULL;
+  if (!aligned16(p->q) || !aligned16(p->q_out) || !aligned4(p->positions)) return BSC_ERR_ALIGN;
+  if ((s = check_strides(p->q_stride_b, p->q_stride_t, p->q_stride_h, p->B, p->T, p->Hq, false)) != BSC_OK) return s;
+  if ((s = check_strides(p->q_out_stride_b, p->q_out_stride_t, p->q_out_stride_h, p->B, p->T, p->Hq, true)) != BSC_OK) return s;
+  if (Hkv > 0) {
+    if (!aligned16(p->k) || !aligned16(p->k_out)) return BSC_ERR_ALIGN;
+    if ((s = check_strides(p->k_stride_b, p->k_stride_t, p->k_stride_h, p->B, p->T, Hkv, false)) != BSC_OK) return s;
+    if ((s = check_strides(p->k_out_stride_b, p->k_out_stride_t, p->k_out_stride_h, p->B, p->T, Hkv, true)) != BSC_OK) return s;
+  }
+  if ((s = check_device()) != BSC_OK) return s;
+  bsc::RopeArgs a{};
+  a.x[0] = p->q;
+  a.x[1] = p->k;
+  a.xs[0] = {p->q_stride_b, p->q_stride_t, p->q_stride_h};
+  a.xs[1] = {p->k_stride_b, p->k_stride_t, p->k_stride_h};
+  a.y[0] = p->q_out;
+  a.y[1] = p->k_out;
+  a.ys[0] = {p->q_out_stride_b, p->q_out_stride_t, p->q_out_stride_h};
+  a.ys[1] = {p->k_out_stride_b, p->k_out_stride_t, p->k_out_stride_h};
+  a.turns = p->angles.turns;
+  a.magnitude = p->angles.magnitude;
+  a.rot = p->angles.rot;
+  a.inverse = p->inverse;
+  a.pos = p->positions;
+  a.pos_b = p->position_stride_b;
+  a.pos_t = p->position_stride_t;
+  a.B = p->B;
+  a.T = p->T;
+  a.Hq = p->Hq;
+  a.Hkv = Hkv;
+  a.D = p->D;
+  return from_cuda(bsc::launch_rope(a, p->dtype, p->angles.interleaved, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bsc_status mxfp8_rope_quantize_qk(const bsc_rope_quant_params* p, bsc_stream_t stream) {
+  if (!p) return BSC_ERR_NULL;
+  if (p->layout != BSC_BSHD && p->layout != BSC_SBHD) return BSC_ERR_SHAPE;
+  if (p->rule != BSC_SCALE_FLOOR && p->rule != BSC_SCALE_CEIL) return BSC_ERR_UNSUPPORTED;
+  const int Hkv = p->k ? p->Hkv : 0;
+  bool empty;
+  bsc_status s = check_rope(p->B, p->T, p->Hq, Hkv, p->D, p->dtype, &empty);
+  if (s != BSC_OK || empty) return s;
+  if (p->D != 128) return BSC_ERR_UNSUPPORTED;
+  if ((s = check_angles(p->angles, p->D)) != BSC_OK) return s;
+  if (!p->q || !p->q_e4m3 || !p->q_sc || (Hkv > 0 && (!p->k_e4m3 || !p->k_sc))) return BSC_ERR_NULL;
+  if (!aligned16(p->q) || !aligned16(p->q_e4m3) || !aligned16(p->q_sc) || !aligned4(p->positions)) return BSC_ERR_ALIGN;
+  if ((s = check_strides(p->q_stride_b, p->q_stride_t, p->q_stride_h, p->B, p->T, p->Hq, false)) != BSC_OK) return s;
+  if (Hkv > 0) {
+    if (!aligned16(p->k) || !aligned16(p->k_e4m3) || !aligned16(p->k_sc)) return BSC_ERR_ALIGN;
+    if ((s = check_strides(p->k_stride_b, p->k_stride_t, p->k_stride_h, p->B, p->T, Hkv, false)) != BSC_OK) return s;
+  }
+  if ((s = check_device()) != BSC_OK) return s;
+  bsc::RopeArgs a{};
+  a.x[0] = p->q;
+  a.x[1] = p->k;
+  a.xs[0] = {p->q_stride_b, p->q_stride_t, p->q_stride_h};
+  a.xs[1] = {p->k_stride_b, p->k_stride_t, p->k_stride_h};
+  a.y[0] = p->q_e4m3;
+  a.y[1] = p->k_e4m3;
+  a.sc[0] = p->q_sc;
+  a.sc[1] = p->k_sc;
+  for (int i = 0; i < 2; ++i) {                                 // bytes, dense in the layout
+    const long long row = (long long)(i ? Hkv : p->Hq) * p->D;
+    a.ys[i] = p->layout == BSC_BSHD ? bsc::RowStrides{p->T * row, row, p->D} : bsc::RowStrides{row, p->B * row, p->D};
+  }
+  a.turns = p->angles.turns;
+  a.magnitude = p->angles.magnitude;
+  a.rot = p->angles.rot;
+  a.pos = p->positions;
+  a.pos_b = p->position_stride_b;
+  a.pos_t = p->position_stride_t;
+  a.B = p->B;
+  a.T = p->T;
+  a.Hq = p->Hq;
+  a.Hkv = Hkv;
+  a.D = p->D;
+  a.rule = p->rule;
+  return from_cuda(bsc::launch_rope_mx(a, p->dtype, p->angles.interleaved, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bsc_status mx_cache_write_rope(const bsc_mx_cache_write_rope_params* p, bsc_stream_t stream) {
+  if (!p) return BSC_ERR_NULL;
+  if (p->rule != BSC_SCALE_FLOOR && p->rule != BSC_SCALE_CEIL) return BSC_ERR_UNSUPPORTED;
+  bool empty;
+  bsc_status s = check_cache(p->cache, p->B, p->T, p->Hq, p->dtype, p->table_stride, p->max_pages, &empty);
+  if (s != BSC_OK || empty) return s;
+  const int Hkv = p->cache.Hkv;
+  if (p->Hq % Hkv != 0) return BSC_ERR_SHAPE;
+  if ((s = check_rope(p->B, p->T, p->Hq, Hkv, p->cache.D, p->dtype, &empty)) != BSC_OK) return s;
+  if ((s = check_angles(p->angles, p->cache.D)) != BSC_OK) return s;
+  if (!p->q || !p->k || !p->v || !p->q_out || !p->seq_lens || (p->max_pages > 0 && !p->page_table)) return BSC_ERR_NULL;
+  if (!aligned16(p->q) || !aligned16(p->k) || !aligned16(p->v) || !aligned16(p->q_out) || !aligned4(p->page_table) ||
+      !aligned4(p->seq_lens) || !aligned4(p->new_lens) || !aligned4(p->dev_status))
+    return BSC_ERR_ALIGN;
+  if ((s = check_strides(p->q_stride_b, p->q_stride_t, p->q_stride_h, p->B, p->T, p->Hq, false)) != BSC_OK) return s;
+  if ((s = check_strides(p->k_stride_b, p->k_stride_t, p->k_stride_h, p->B, p->T, Hkv, false)) != BSC_OK) return s;
+  if ((s = check_strides(p->v_stride_b, p->v_stride_t, p->v_stride_h, p->B, p->T, Hkv, false)) != BSC_OK) return s;
+  if ((s = check_strides(p->q_out_stride_b, p->q_out_stride_t, p->q_out_stride_h, p->B, p->T, p->Hq, true)) != BSC_OK) return s;
+  if ((s = check_device()) != BSC_OK) return s;
+  bsc::RopeArgs a{};
+  a.x[0] = p->q;
+  a.x[1] = p->k;
+  a.x[2] = p->v;
+  a.xs[0] = {p->q_stride_b, p->q_stride_t, p->q_stride_h};
+  a.xs[1] = {p->k_stride_b, p->k_stride_t, p->k_stride_h};
+  a.xs[2] = {p->v_stride_b, p->v_stride_t, p->v_stride_h};
+  a.y[0] = p->q_out;
+  a.ys[0] = {p->q_out_stride_b, p->q_out_stride_t, p->q_out_stride_h};
+  a.turns = p->angles.turns;
+  a.magnitude = p->angles.magnitude;
+  a.rot = p->angles.rot;
+  a.B = p->B;
+  a.T = p->T;
+  a.Hq = p->Hq;
+  a.Hkv = Hkv;
+  a.D = p->cache.D;
+  a.rule = p->rule;
+  a.c = cache_pools(p->cache);
+  a.pt = {p->page_table, p->table_stride, p->max_pages, p->seq_lens};
+  a.new_lens = p->new_lens;
+  a.dev_status = p->dev_status;
+  return from_cuda(bsc::launch_rope_cache(a, p->cache.format, p->dtype, p->angles.interleaved,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bsc_status mx_cache_bounds(const bsc_mx_cache_bounds_params* p, bsc_stream_t stream) {
+  if (!p) return BSC_ERR_NULL;
+  bool empty;
+  bsc_status s = check_cache(p->cache, p->B, p->T, p->cache.Hkv, BSC_BF16, p->table_stride, p->max_pages, &empty);
+  if (s != BSC_OK || empty) return s;
+  if (reaches_2_31({p->B, (p->T - 1LL) / p->cache.page_size + 2, p->cache.Hkv})) return BSC_ERR_UNSUPPORTED;   // blocks
+  if (!p->codes || !p->exps || !p->seq_lens || (p->max_pages > 0 && !p->page_table)) return BSC_ERR_NULL;
+  if (!aligned16(p->codes) || !aligned4(p->page_table) || !aligned4(p->seq_lens) || !aligned4(p->new_lens) ||
+      !aligned4(p->dev_status))
+    return BSC_ERR_ALIGN;
+  if ((s = check_device()) != BSC_OK) return s;
+  bsc::BoundsArgs a{};
+  a.c = cache_pools(p->cache);
+  a.pt = {p->page_table, p->table_stride, p->max_pages, p->seq_lens};
+  a.codes = p->codes;
+  a.exps = p->exps;
+  a.B = p->B;
+  a.T = p->T;
+  a.new_lens = p->new_lens;
+  a.dev_status = p->dev_status;
+  return from_cuda(bsc::launch_cache_bounds(a, p->cache.format, p->cache.D, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mx_cache_sparse_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int top) {
+  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || page_size <= 0 || max_pages < 0 || top <= 0) return 0;
+  SparseParts w;
+  return sparse_parts(B, T, Hq, Hkv, D, page_size, max_pages, top, &w) ? w.all : 0;
+}
+
+bsc_status mx_cache_sparse_attn(const bsc_mx_cache_sparse_attn_params* p, bsc_stream_t stream) {
+  if (!p) return BSC_ERR_NULL;
+  bool empty;
+  const bsc_mx_cache& c = p->cache;
+  bsc_status s = check_cache(c, p->B, p->T, p->Hq, p->dtype, p->table_stride, p->max_pages, &empty);
+  if (s != BSC_OK || empty) return s;
+  if (p->Hq % c.Hkv != 0) return BSC_ERR_SHAPE;
+  if (p->last < 1 || p->first < 0 || p->top < 1 || p->first > p->top - p->last) return BSC_ERR_SHAPE;
+  if (!(std::isfinite(p->softmax_scale) && p->softmax_scale > 0.f)) return BSC_ERR_UNSUPPORTED;
+  const int slices = slices_per_page(c);
+  SparseParts w;
+  if (slices == 0 || !sparse_parts(p->B, p->T, p->Hq, c.Hkv, c.D, c.page_size, p->max_pages, p->top, &w))
+    return BSC_ERR_UNSUPPORTED;
+  if (!p->codes || !p->exps || !p->q || !p->o || !p->seq_lens || (p->max_pages > 0 && !p->page_table) || !p->workspace)
+    return BSC_ERR_NULL;
+  if (!aligned16(p->codes) || !aligned16(p->q) || !aligned16(p->o) || !aligned16(p->workspace) || !aligned4(p->page_table) ||
+      !aligned4(p->seq_lens) || !aligned4(p->new_lens) || !aligned4(p->lse) || !aligned4(p->blocks) || !aligned4(p->dev_status))
+    return BSC_ERR_ALIGN;
+  if ((s = check_strides(p->q_stride_b, p->q_stride_t, p->q_stride_h, p->B, p->T, p->Hq, false)) != BSC_OK) return s;
+  if ((s = check_strides(p->o_stride_b, p->o_stride_t, p->o_stride_h, p->B, p->T, p->Hq, true)) != BSC_OK) return s;
+  if (p->workspace_bytes < w.all) return BSC_ERR_SHAPE;
+  if ((s = check_device()) != BSC_OK) return s;
+  uint8_t* const ws = reinterpret_cast<uint8_t*>(p->workspace);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  bsc::SelectArgs a{};
+  a.pt = {p->page_table, p->table_stride, p->max_pages, p->seq_lens};
+  a.codes = p->codes;
+  a.exps = p->exps;
+  a.q = p->q;
+  a.qs = {p->q_stride_b, p->q_stride_t, p->q_stride_h};
+  a.B = p->B;
+  a.T = p->T;
+  a.Hq = p->Hq;
+  a.Hkv = c.Hkv;
+  a.num_pages = c.num_pages;
+  a.page_size = c.page_size;
+  a.new_lens = p->new_lens;
+  a.dev_status = p->dev_status;
+  a.top = p->top;
+  a.first = p->first;
+  a.last = p->last;
+  a.pages_per_page = slices;
+  a.blocks = p->blocks;
+  a.scores = reinterpret_cast<float*>(ws);
+  a.table = reinterpret_cast<int32_t*>(ws + w.table);
+  a.lens = reinterpret_cast<int32_t*>(ws + w.lens);
+  if ((s = from_cuda(bsc::launch_cache_select(a, c.D, p->dtype, st))) != BSC_OK) return s;
+
+  const int cols = p->top < p->max_pages ? p->top : p->max_pages;
+  const long long slots = c.page_size;
+  bsc::CacheAttnArgs t{};
+  t.c = cache_pools(c);
+  t.c.k_ps = t.c.v_ps = slots * (c.format == BSC_CACHE_MXFP4 ? c.D / 2 : c.D);
+  t.c.k_sc_ps = t.c.v_sc_ps = slots * (c.D / 32);
+  t.c.num_pages = (c.num_pages - 1) * slices + c.Hkv;
+  t.c.Hkv = 1;
+  t.pt = {a.table, cols, cols, a.lens};
+  t.q = p->q;
+  t.o = p->o;
+  t.lse = p->lse;
+  t.qs = a.qs;
+  t.os = {p->o_stride_b, p->o_stride_t, p->o_stride_h};
+  t.B = p->B * p->T * c.Hkv;
+  t.T = 1;
+  t.Hq = p->Hq / c.Hkv;
+  t.fp16 = p->dtype == BSC_FP16;
+  t.dev_status = p->dev_status;
+  t.scale_log2e = (float)((double)p->softmax_scale * 1.4426950408889634);
+  t.ws = ws + w.attn;
+  t.sel_H = c.Hkv;
+  t.sel_T = p->T;
+  return from_cuda(bsc::launch_cache_attn(t, c.format, c.D, st));
 }
 
 bsc_status bsc_read_device_status(const int32_t* dev_status, bsc_stream_t stream) {

@@ -120,6 +120,98 @@ struct CacheRwArgs {
 cudaError_t launch_cache_write(const CacheRwArgs& a, int format, int D, int dtype, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheRwArgs& a, int format, int D, int dtype, cudaStream_t st);
 
+// Root-mean-square norm.  Row r of a tensor starts at (r / inner) * outer + (r % inner) * NormRows::inner elements.
+struct NormRows {
+  long long outer, inner;
+};
+struct NormArgs {
+  const void* x;
+  const void* r;           // residual, or nullptr
+  const void* w;
+  void* y;                 // 16-bit output, or nullptr
+  void* s;                 // x + residual, or nullptr
+  float* rstd;             // or nullptr
+  uint8_t* y8;             // MXFP8 output [rows][N], or nullptr
+  uint8_t* ysc;            // [rows][N/32]
+  NormRows xs, rs, ys, ss;
+  long long rows;
+  int inner, N, rule;
+  float eps;
+};
+cudaError_t launch_norm(const NormArgs& a, int dtype, int w32, cudaStream_t st);
+struct NormBwdArgs {
+  const void* dy;
+  const void* s;
+  const void* w;
+  const float* rstd;
+  const void* ds;          // gradient that reaches s by another way, or nullptr
+  void* dx;
+  void* dw;
+  float* partial;          // workspace [blocks][N]
+  NormRows dys, ss, dss, dxs;
+  long long rows;
+  int inner, N;
+};
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int w32, cudaStream_t st);
+size_t norm_bwd_workspace_bytes(long long rows, int N);
+
+// MXFP8 rows back to values: codes in `layout`, scales [B][H][S][N/32].
+cudaError_t launch_dequantize(const uint8_t* x, const uint8_t* sc, void* y, int B, int S, int H, int N, int layout, int dtype,
+                              cudaStream_t st);
+
+// Rotary positions.
+struct RopeArgs {
+  const void* x[3];        // q, k (nullptr: none), and v of the cache form
+  RowStrides xs[3];
+  void* y[2];              // 16-bit q and k (the cache form: q), or the E4M3 of the MXFP8 form
+  RowStrides ys[2];
+  uint8_t* sc[2];          // MXFP8 form: scales [B][H][T][D/32]
+  const unsigned long long* turns;   // [rot/2], turns per token times 2^64
+  float magnitude;
+  int rot, inverse;
+  const int32_t* pos;      // nullptr: token t is at position t
+  long long pos_b, pos_t;  // its strides; pos_t 0: of the first token
+  int B, T, Hq, Hkv, D;    // Hkv 0: no k
+  int tt;                  // tokens per block, set by the launcher
+  int rule;
+  CachePools c;            // cache form
+  CacheTable pt;
+  const int32_t* new_lens;
+  int32_t* dev_status;
+};
+cudaError_t launch_rope(const RopeArgs& a, int dtype, int interleaved, cudaStream_t st);
+cudaError_t launch_rope_mx(const RopeArgs& a, int dtype, int interleaved, cudaStream_t st);
+cudaError_t launch_rope_cache(const RopeArgs& a, int format, int dtype, int interleaved, cudaStream_t st);
+
+// Bounds of the cache's pages, and the pages that every query and KV head attends.
+struct BoundsArgs {
+  CachePools c;
+  CacheTable pt;
+  int8_t* codes;           // [num_pages][Hkv][2][D]
+  uint8_t* exps;           // [num_pages][Hkv]
+  int B, T;
+  const int32_t* new_lens; // may be nullptr
+  int32_t* dev_status;
+};
+cudaError_t launch_cache_bounds(const BoundsArgs& a, int format, int D, cudaStream_t st);
+struct SelectArgs {
+  CacheTable pt;
+  const int8_t* codes;
+  const uint8_t* exps;
+  const void* q;
+  RowStrides qs;
+  int B, T, Hq, Hkv, num_pages, page_size;
+  const int32_t* new_lens; // may be nullptr
+  int32_t* dev_status;
+  int top, first, last;
+  int pages_per_page;      // head slices of the pools from page to page: page p, head h is slice p * this + h
+  int32_t* blocks;         // [B][T][Hkv][top], or nullptr
+  float* scores;           // workspace [B T Hkv][max_pages]
+  int32_t* table;          // workspace [B T Hkv][top]: slices, in order
+  int32_t* lens;           // workspace [B T Hkv]: tokens of the listed slices
+};
+cudaError_t launch_cache_select(const SelectArgs& a, int D, int dtype, cudaStream_t st);
+
 struct CacheAttnArgs {
   CachePools c;
   CacheTable pt;
@@ -133,6 +225,9 @@ struct CacheAttnArgs {
   int32_t* dev_status;     // may be nullptr
   float scale_log2e;
   void* ws;
+  // Selected pages: 0, or the KV heads; then "sequence" (b sel_T + t) sel_H + h has the pages of one query and KV head, T and
+  // the cache's Hkv are 1, Hq counts the query heads of a KV head, and q, o and lse are addressed by (b, t, h).
+  int sel_H, sel_T;
 };
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int format, int D, cudaStream_t st);
 size_t cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long long max_tokens);

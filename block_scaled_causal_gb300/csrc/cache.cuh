@@ -73,6 +73,13 @@ __device__ __forceinline__ float2 f16x2_to_f32(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// Eight fp32 of a block with scale byte sb -> eight E4M3.
+__device__ __forceinline__ uint2 quant8_e4m3(const float (&f)[8], float inv, uint32_t sb) {
+  if (sb == 0xFFu) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  return make_uint2(cvt_e4m3x2(f[0] * inv, f[1] * inv) | (uint32_t)cvt_e4m3x2(f[2] * inv, f[3] * inv) << 16,
+                    cvt_e4m3x2(f[4] * inv, f[5] * inv) | (uint32_t)cvt_e4m3x2(f[6] * inv, f[7] * inv) << 16);
+}
+
 // Activations: bf16 (DT = 0) or fp16 (DT = 1), two to a word.
 template <int DT>
 __device__ __forceinline__ float2 act_to_f32(uint32_t w) {

@@ -269,6 +269,18 @@ struct Share {
   }
 };
 
+// Where the rows of "sequence" b and query head 0 start in an activation, and in lse.
+__device__ __forceinline__ long long rows_at(const CacheAttnArgs& a, const RowStrides& s, int b) {
+  if (a.sel_H == 0) return b * s.b;
+  const int x = b / a.sel_H, h = b - x * a.sel_H, bb = x / a.sel_T, t = x - bb * a.sel_T;
+  return bb * s.b + t * s.t + (long long)h * a.Hq * s.h;
+}
+__device__ __forceinline__ long long lse_at(const CacheAttnArgs& a, int b, int hq, int tq) {
+  if (a.sel_H == 0) return ((long long)b * a.Hq + hq) * a.T + tq;
+  const int x = b / a.sel_H, h = b - x * a.sel_H, bb = x / a.sel_T, t = x - bb * a.sel_T;
+  return (((long long)bb * a.sel_H + h) * a.Hq + hq) * a.sel_T + t;
+}
+
 // A workspace slot: ROWS x D of O, then ROWS log-sum-exps (log2).
 template <class C, int D>
 constexpr int slot_floats() { return C::ROWS * (D + 1); }
@@ -652,7 +664,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
 #pragma unroll
     for (int nt = 0; nt < NQ; ++nt) {
       const int r = rt * C::ROWS + (nt0 + nt) * 8 + g, tq = r / G, hq = h * G + r - tq * G;
-      const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + b * a.qs.b + tq * a.qs.t + hq * a.qs.h + t * C::KE;
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + rows_at(a, a.qs, b) + tq * a.qs.t + hq * a.qs.h + t * C::KE;
 #pragma unroll
       for (int i = 0; i < C::KE / 8; ++i)
         q_in[nt][i] = r < R ? __ldca(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
@@ -882,10 +894,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<FMT, D, NT>::OCC) cache_attn_kern
       for (int j = 0; j < 8; ++j) o[j] = none ? 0.f : o[j] * inv;
       if (whole || cs) {
         const int hq = h * G + r - tq * G;
-        uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + b * a.os.b + tq * a.os.t + hq * a.os.h + d;
+        uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + rows_at(a, a.os, b) + tq * a.os.t + hq * a.os.h + d;
         *reinterpret_cast<uint4*>(dst) = make_uint4(f32_to_act(o[0], o[1], a.fp16), f32_to_act(o[2], o[3], a.fp16),
                                                     f32_to_act(o[4], o[5], a.fp16), f32_to_act(o[6], o[7], a.fp16));
-        if (d == 0 && a.lse) a.lse[((long long)b * a.Hq + hq) * a.T + tq] = z * 0.6931471805599453f;
+        if (d == 0 && a.lse) a.lse[lse_at(a, b, hq, tq)] = z * 0.6931471805599453f;
       } else {
         float4* dst = reinterpret_cast<float4*>(slot + row * D + d);
         dst[0] = make_float4(o[0], o[1], o[2], o[3]);
@@ -1039,7 +1051,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
   if (row >= live) return;
   const int r = rt * ROWS + first_row + row, tq = r / G, hq = h * G + r - tq * G;
   const bool none = sum == 0.f;
-  uint16_t* const dst = reinterpret_cast<uint16_t*>(a.o) + b * a.os.b + tq * a.os.t + hq * a.os.h + lane * PL;
+  uint16_t* const dst = reinterpret_cast<uint16_t*>(a.o) + rows_at(a, a.os, b) + tq * a.os.t + hq * a.os.h + lane * PL;
   const float inv = 1.f / sum;
   uint32_t w[PL / 2];
 #pragma unroll
@@ -1047,7 +1059,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
   if (PL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[PL / 2 - 1]);
   else *reinterpret_cast<uint32_t*>(dst) = w[0];
   if (lane == 0 && a.lse)
-    a.lse[((long long)b * a.Hq + hq) * a.T + tq] = none ? -INFINITY : (m + __log2f(sum)) * 0.6931471805599453f;
+    a.lse[lse_at(a, b, hq, tq)] = none ? -INFINITY : (m + __log2f(sum)) * 0.6931471805599453f;
 }
 
 // How a call is cut up: the rows of a tile, and the blocks of a unit's cluster (1: a block), or 0 for the list.

@@ -1,0 +1,74 @@
+// MXFP8 rows back to values: element * 2^(scale - 127), exact in fp32 and rounded once to 16 bits.
+//
+// Memory-bound: 1 byte in, 2 out per element.  A thread takes 16 elements of one scale block at a time, DQ_ITEMS of
+// them with all loads ahead of the first use.
+#include "cache.cuh"
+
+namespace bsc {
+namespace {
+
+constexpr int DQ_THREADS = 256, DQ_ITEMS = 4;
+
+// Row r of the codes (in memory's order) has the scales of row scale_row(r).
+__device__ __forceinline__ uint32_t scale_row(uint32_t r, int B, int S, int H, int layout) {
+  const uint32_t x = r / H, h = r - x * H;
+  uint32_t b, s;
+  if (layout == 0) {
+    b = x / S;
+    s = x - b * S;
+  } else {
+    s = x / B;
+    b = x - s * B;
+  }
+  return (b * H + h) * S + s;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(DQ_THREADS) dequantize_kernel(const uint8_t* x, const uint8_t* sc, void* y, int B, int S,
+                                                                int H, int N, int layout, long long pieces) {
+  wait_for_last_kernel();
+  if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
+  const int per_row = N / 16;
+  uint4 v[DQ_ITEMS];
+  float f[DQ_ITEMS];
+  long long i0 = (long long)blockIdx.x * (DQ_THREADS * DQ_ITEMS) + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < DQ_ITEMS; ++k) {
+    const long long i = i0 + k * DQ_THREADS;
+    if (i >= pieces) break;
+    v[k] = __ldcs(reinterpret_cast<const uint4*>(x) + i);
+    const uint32_t r = (uint32_t)(i / per_row), p = (uint32_t)(i - (long long)r * per_row);   // fewer than 2^31 rows
+    const uint32_t sr = H == 1 && (B == 1 || layout == 0) ? r : scale_row(r, B, S, H, layout);
+    f[k] = scale_value(__ldca(sc + (long long)sr * (N / 32) + (p >> 1)));
+  }
+#pragma unroll
+  for (int k = 0; k < DQ_ITEMS; ++k) {
+    const long long i = i0 + k * DQ_THREADS;
+    if (i >= pieces) break;
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t h0, h1;
+      e4m3x4_to_f16(w[j], h0, h1);
+      const float2 a = f16x2_to_f32(h0), b = f16x2_to_f32(h1);
+      o[2 * j] = f32_to_act<DT>(a.x * f[k], a.y * f[k]);
+      o[2 * j + 1] = f32_to_act<DT>(b.x * f[k], b.y * f[k]);
+    }
+    uint4* const dst = reinterpret_cast<uint4*>(y) + 2 * i;
+    __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
+    __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_dequantize(const uint8_t* x, const uint8_t* sc, void* y, int B, int S, int H, int N, int layout, int dtype,
+                              cudaStream_t st) {
+  const long long pieces = (long long)B * S * H * (N / 16);
+  const unsigned grid = (unsigned)((pieces + DQ_THREADS * DQ_ITEMS - 1) / (DQ_THREADS * DQ_ITEMS));
+  return launch_early(dtype ? dequantize_kernel<1> : dequantize_kernel<0>, grid, DQ_THREADS, 0, st, 1, x, sc, y, B, S, H, N,
+                      layout, pieces);
+}
+
+}  // namespace bsc

@@ -326,7 +326,7 @@ size_t bf16_attn_bwd_static_capacity(void);
  */
 #define BSC_CACHE_MAX_TOKENS (1LL << 30)
 typedef enum { BSC_CACHE_MXFP8 = 0, BSC_CACHE_MXFP4 = 1 } bsc_cache_format;
-typedef enum { BSC_BF16 = 0, BSC_FP16 = 1 } bsc_dtype;
+typedef enum { BSC_BF16 = 0, BSC_FP16 = 1, BSC_FP32 = 2 } bsc_dtype;   /* BSC_FP32: weights of the norm only */
 typedef struct {
   uint8_t* k;             /* [num_pages][Hkv][page_size][D or D/2] */
   uint8_t* k_sc;          /* [num_pages][Hkv][page_size][D/32] */
@@ -422,6 +422,265 @@ bsc_status mx_cache_attn(const bsc_mx_cache_attn_params* p, bsc_stream_t stream)
  * size is not positive.  Smaller sizes may need more than larger ones: ask for each that is used.
  * Host only, no CUDA call. */
 size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long long max_tokens);
+
+/*
+ * What stands ahead of the attention: the norm before the projections that make Q, K and V, and rotary positions.
+ * The pages end at the attention's operands (PR #3865, Description); these calls make them.
+ *
+ * Root-mean-square norm of rows of N elements, with the residual's addition:
+ *   s = x + residual, rounded to `dtype` (s = x where residual is NULL): the residual stream, which the next layer adds to
+ *   rstd = (mean_n s_n^2 + eps)^(-1/2),  y_n = s_n * rstd * weight_n
+ * in fp32 (a sum of squares beyond 3.4e38 is infinite: rows up to 2^56 in magnitude are taken), each output rounded once.
+ * y goes out in `dtype` (y), as MXFP8 rows (y_e4m3 [rows][N] and y_sc [rows][N/32], the quantisation rule at the top of
+ * this file applied to the fp32 y), or both.  A row with a NaN or an infinity comes out as NaN where the formula says so.
+ *
+ * Row r of x starts at element (r / inner) * stride + (r % inner) * inner_stride, and so for residual, y and sum: inner = 1
+ * for evenly spaced rows, inner = the heads for the heads of a slice of a fused projection.  Strides are multiples of 8
+ * (ignored where they do not count: a single row or group), an output's not 0.  N is a multiple of 8 (of 32 with
+ * y_e4m3) and at most BSC_NORM_MAX_N.  Pointers are 16-byte aligned, rstd 4-byte.
+ * y or sum may be x or residual itself (same strides); no other outputs overlap.  rows or N of 0: BSC_OK, nothing is done.
+ */
+#define BSC_NORM_MAX_N 16384
+typedef struct {
+  const void* x;          /* [in] `dtype` */
+  const void* residual;   /* [in] `dtype`, or NULL */
+  const void* weight;     /* [in] [N], `weight_dtype`: `dtype` or BSC_FP32 */
+  void* y;                /* [out] `dtype`, or NULL */
+  void* sum;              /* [out] s, or NULL */
+  float* rstd;            /* [out] [rows], or NULL */
+  uint8_t* y_e4m3;        /* [out] [rows][N], or NULL */
+  uint8_t* y_sc;          /* [out] [rows][N/32], with y_e4m3 */
+  long long rows;
+  long long x_stride, x_inner_stride, residual_stride, residual_inner_stride, y_stride, y_inner_stride, sum_stride,
+      sum_inner_stride;
+  int inner;              /* at least 1 */
+  int N;
+  int dtype;              /* bsc_dtype: BSC_BF16 or BSC_FP16 */
+  int weight_dtype;
+  int rule;               /* bsc_scale_rule of y_e4m3 */
+  float eps;              /* finite and >= 0 */
+} bsc_rms_norm_params;
+bsc_status rms_norm(const bsc_rms_norm_params* p, bsc_stream_t stream);
+
+/*
+ * Gradients of rms_norm at s (the sum output, or x where there was no residual), with rstd of the forward call:
+ *   g = dy * weight,  dx = rstd (g - s rstd mean_n(g s rstd)) + d_sum,  dweight_n = sum over rows of dy_n s_n rstd
+ * dx is the gradient of x and of residual alike; d_sum (or NULL) is the gradient that reaches s by the residual stream.  fp32
+ * inside; dx is `dtype`, dweight `weight_dtype`.  The rows are summed in an order that depends on rows and N alone: the
+ * same inputs give the same bits.  dx may be dy, s or d_sum itself (same strides).  rows of 0 with N > 0: dweight is
+ * not written.  workspace: rms_norm_bwd_workspace_bytes(rows, N) bytes, 16-byte aligned, used by this call alone until
+ * it has run.  Strides and sizes as above.
+ */
+typedef struct {
+  const void* dy;         /* [in] `dtype` */
+  const void* s;          /* [in] `dtype` */
+  const void* weight;
+  const float* rstd;      /* [in] [rows] */
+  const void* d_sum;      /* [in] `dtype`, or NULL */
+  void* dx;               /* [out] `dtype` */
+  void* dweight;          /* [out] [N], `weight_dtype` */
+  long long rows;
+  long long dy_stride, dy_inner_stride, s_stride, s_inner_stride, d_sum_stride, d_sum_inner_stride, dx_stride,
+      dx_inner_stride;
+  int inner, N, dtype, weight_dtype;
+  void* workspace;
+  size_t workspace_bytes;
+} bsc_rms_norm_bwd_params;
+bsc_status rms_norm_bwd(const bsc_rms_norm_bwd_params* p, bsc_stream_t stream);
+
+/* Bytes of workspace rms_norm_bwd needs; 0 if a size is not positive or N is refused.  Host only, no CUDA call. */
+size_t rms_norm_bwd_workspace_bytes(long long rows, int N);
+
+/*
+ * MXFP8 rows back to values: y = element * 2^(scale - 127), rounded once to nearest even in `dtype`; NaN where the scale is
+ * 0xFF.  The way back from mxfp8_quantize_qk_rowwise, mxfp8_rope_quantize_qk and rms_norm's MXFP8 output (B = H = 1).
+ *   x_e4m3 [in] [..][D] in `layout`, dense;  x_sc [in] [B][H][S][D/32];  y [out] `dtype`, laid out like x_e4m3.
+ * D is a multiple of 32; any S.  B * S * H below 2^31, B * S * H * D below 2^40.
+ */
+bsc_status mxfp8_dequantize(const uint8_t* x_e4m3, const uint8_t* x_sc, int B, int S, int H, int D, bsc_layout layout, int dtype,
+                            void* y, bsc_stream_t stream);
+
+/*
+ * Rotary positions.  The first `rot` elements of a head are rot/2 pairs; pair i of the token at position p turns by p f_i:
+ *   (a, b) -> magnitude * (a cos(p f_i) - b sin(p f_i), a sin(p f_i) + b cos(p f_i))
+ * Pairs are (x_i, x_{i + rot/2}), or (x_2i, x_{2i+1}) where `interleaved` is 1.  Elements from rot on pass through.
+ *
+ * f_i is given as turns per token, times 2^64 and rounded: a 64-bit fraction, so that the angle of any 32-bit position is
+ * exact to 2^-33 turns without a table of positions.  bsc_rope_turns fills them in (host only, no CUDA call; the caller copies
+ * them to the device once):
+ *   BSC_ROPE_PLAIN      f_i = base^(-2i/rot)
+ *   BSC_ROPE_LINEAR     f_i / factor: positions are interpolated
+ *   BSC_ROPE_BASE       base * factor^(rot/(rot-2)) in the place of base: the slowest pair is interpolated by factor, the
+ *                       fastest not at all (rot = 2: plain)
+ *   BSC_ROPE_BY_PARTS   f_i (k + (1 - k) / factor), k = clamp((original_length f_i / 2 pi - low_turns) / (high_turns -
+ *                       low_turns), 0, 1): pairs that turn often in the trained length stay, slow ones are interpolated
+ *                       (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models", 3.2); magnitude
+ *                       0.1 ln(factor) + 1 (3.4), for every factor >= 1
+ * magnitude is 1 for the others.  base > 0, factor > 0 (>= 1 by parts), finite; by parts original_length > 0,
+ * 0 <= low_turns < high_turns: else BSC_ERR_UNSUPPORTED.  rot is a multiple of 16 from 16 to 256.
+ */
+typedef enum { BSC_ROPE_PLAIN = 0, BSC_ROPE_LINEAR = 1, BSC_ROPE_BASE = 2, BSC_ROPE_BY_PARTS = 3 } bsc_rope_scaling;
+typedef struct {
+  int rot;
+  int scaling;            /* bsc_rope_scaling */
+  double base, factor;
+  double original_length, low_turns, high_turns;   /* BSC_ROPE_BY_PARTS only */
+} bsc_rope_config;
+bsc_status bsc_rope_turns(const bsc_rope_config* c, unsigned long long* turns, float* magnitude);
+
+/* What a call rotates by. */
+typedef struct {
+  const unsigned long long* turns;   /* [in] device, [rot/2] */
+  float magnitude;        /* finite */
+  int rot;                /* a multiple of 16, at most D */
+  int interleaved;        /* 0 or 1 */
+} bsc_rope_angles;
+
+/*
+ * Q and K rotated in one launch.  Token t of sequence b is at position t (positions NULL), positions[b * position_stride_b]
+ * + t (position_stride_t 0), or positions[b * position_stride_b + t * position_stride_t]; positions may be negative.
+ * inverse 1 turns back: the gradients of q and k from those of the outputs.  fp32 inside, one rounding.
+ * q, k: strides as in the cache calls (elements, multiples of 8), D a multiple of 16, at most 256.  k may be NULL (k_out
+ * too), Hkv is then ignored.  q_out may be q and k_out k (same strides); no other overlap.  positions 4-byte aligned,
+ * turns 8-byte.
+ */
+typedef struct {
+  bsc_rope_angles angles;
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  long long q_stride_b, q_stride_t, q_stride_h, k_stride_b, k_stride_t, k_stride_h;
+  long long q_out_stride_b, q_out_stride_t, q_out_stride_h, k_out_stride_b, k_out_stride_t, k_out_stride_h;
+  const int32_t* positions;
+  long long position_stride_b, position_stride_t;
+  int B, T, Hq, Hkv, D;
+  int dtype;              /* bsc_dtype */
+  int inverse;
+} bsc_rope_params;
+bsc_status rope(const bsc_rope_params* p, bsc_stream_t stream);
+
+/*
+ * Q and K rotated and quantised rowwise to MXFP8 in one launch: the operands of mxfp8_causal_attn_fwd from the projections'
+ * outputs.  The rotated values are quantised from fp32, without a rounding to 16 bits between (so a byte can differ
+ * from that of rope followed by mxfp8_quantize_qk_rowwise).  D = 128; any T.
+ *   q_e4m3, k_e4m3 [out] dense in `layout`;  q_sc [B][Hq][T][D/32], k_sc [B][Hkv][T][D/32].  Else as rope.
+ */
+typedef struct {
+  bsc_rope_angles angles;
+  const void* q;
+  const void* k;
+  long long q_stride_b, q_stride_t, q_stride_h, k_stride_b, k_stride_t, k_stride_h;
+  uint8_t* q_e4m3;
+  uint8_t* q_sc;
+  uint8_t* k_e4m3;
+  uint8_t* k_sc;
+  const int32_t* positions;
+  long long position_stride_b, position_stride_t;
+  int B, T, Hq, Hkv, D;
+  int dtype;
+  int layout;             /* bsc_layout of the outputs */
+  int rule;               /* bsc_scale_rule */
+} bsc_rope_quant_params;
+bsc_status mxfp8_rope_quantize_qk(const bsc_rope_quant_params* p, bsc_stream_t stream);
+
+/*
+ * mx_cache_write with K rotated on the way in, and the same tokens' Q rotated beside it, in one launch: what a decode step or
+ * a chunk of a prompt needs ahead of mx_cache_attn.  Token t < n_b of sequence b is at position seq_lens[b] - n_b + t, where
+ * its K and V are written and by which its Q and K turn.  K is quantised from the rotated fp32 values.  Rows of q_out with
+ * t >= n_b or a negative position are zeros.  q_out may be q (same strides).  Checks and refusals as mx_cache_write, with
+ * Hq a multiple of Hkv and B * T below 2^31.
+ */
+typedef struct {
+  bsc_mx_cache cache;     /* [out] */
+  bsc_rope_angles angles;
+  const void* q;          /* [in] T tokens of each sequence, `dtype`, Hq heads */
+  const void* k;          /* [in] likewise, Hkv heads */
+  const void* v;
+  void* q_out;            /* [out] `dtype`, Hq heads */
+  long long q_stride_b, q_stride_t, q_stride_h, k_stride_b, k_stride_t, k_stride_h, v_stride_b, v_stride_t, v_stride_h;
+  long long q_out_stride_b, q_out_stride_t, q_out_stride_h;
+  int B, T, Hq;
+  int dtype;
+  int rule;
+  const int32_t* page_table;
+  long long table_stride;
+  int max_pages;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int32_t* dev_status;
+} bsc_mx_cache_write_rope_params;
+bsc_status mx_cache_write_rope(const bsc_mx_cache_write_rope_params* p, bsc_stream_t stream);
+
+/*
+ * Reading less of a long cache.  Beside the pools the caller keeps bounds of every page's keys:
+ *   codes [num_pages][Hkv][2][D]  int8, the minima and then the maxima along d, rounded outward
+ *   exps  [num_pages][Hkv]        one byte e + 127 per page and head: a code stands for code * 2^e
+ * with e = clamp(floor(log2 max|K|) - 6, -100, ...).  A page and head with a NaN, or a magnitude of 2^107 or more, has exps
+ * 0xFF and codes 0.
+ *
+ * mx_cache_bounds makes the bounds of the pages that hold positions [seq_lens[b] - n_b, seq_lens[b]) of every sequence, from
+ * all of a page's tokens below seq_lens[b]: after each write, with the write's lengths.  Nothing else changes.  It does not
+ * read earlier bounds.  codes 16-byte aligned.
+ */
+typedef struct {
+  bsc_mx_cache cache;     /* [in]; k and k_sc are read */
+  int8_t* codes;          /* [out] */
+  uint8_t* exps;          /* [out] */
+  int B, T;
+  const int32_t* page_table;
+  long long table_stride;
+  int max_pages;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;    /* [in] [B], clamped to [0, T]; NULL: T */
+  int32_t* dev_status;        /* optional */
+} bsc_mx_cache_bounds_params;
+bsc_status mx_cache_bounds(const bsc_mx_cache_bounds_params* p, bsc_stream_t stream);
+
+/*
+ * Attention of T new queries per sequence over `top` pages each, chosen for every query and KV head by a score of the
+ * pages' bounds.  Query t < n_b at position p sees the tokens at and before p, which lie in the pages 0 .. p / page_size.
+ * With top pages or fewer all are attended: the result is mx_cache_attn's.  Else the first `first` and the last `last`
+ * (the page of p among them), and of the others those with the largest
+ *   score = 2^e (sum_d u_d max_d - l_d min_d),  u = sum over the KV head's query heads of max(q_d, 0), l of max(-q_d, 0),
+ * u and l rounded to 0..127 with one power of two per query and KV head (the largest in [64, 128), 127 at most).  Scores are
+ * exact in fp32; equal ones are taken in the pages' order.  A page whose exps is 0xFF scores above all others; one whose
+ * id is out of range comes last and is not attended (0x201).  A query with a NaN or an infinity scores every page 0.
+ * O and LSE are those of mx_cache_attn over the tokens of the chosen pages.
+ *   blocks [out] int32 [B][T][Hkv][top], or NULL: the chosen pages' numbers (position / page_size) in ascending order,
+ *     then -1.
+ * 1 <= last, 0 <= first, first + last <= top: else BSC_ERR_SHAPE.  The page strides of the four pools are the same whole
+ * number of heads (page_size rows), num_pages times that number below 2^31: dense pools and slices of one [pages][2][Hkv]
+ * allocation are; else BSC_ERR_UNSUPPORTED.  Also refused so: B * T * Hkv * max(max_pages, 128) or B * T * Hkv * top of
+ * 2^31 or more, and what mx_cache_attn refuses at B * T * Hkv sequences of top pages.  Else as mx_cache_attn.
+ */
+typedef struct {
+  bsc_mx_cache cache;     /* [in] */
+  const int8_t* codes;    /* [in] */
+  const uint8_t* exps;    /* [in] */
+  const void* q;
+  void* o;
+  float* lse;             /* may be NULL */
+  int32_t* blocks;        /* may be NULL */
+  long long q_stride_b, q_stride_t, q_stride_h, o_stride_b, o_stride_t, o_stride_h;
+  int B, T, Hq;
+  int dtype;
+  float softmax_scale;
+  int top, first, last;
+  const int32_t* page_table;
+  long long table_stride;
+  int max_pages;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int32_t* dev_status;
+  void* workspace;        /* [scratch] 16-byte aligned, mx_cache_sparse_attn_workspace_bytes(...) bytes, of this call alone */
+  size_t workspace_bytes;
+} bsc_mx_cache_sparse_attn_params;
+bsc_status mx_cache_sparse_attn(const bsc_mx_cache_sparse_attn_params* p, bsc_stream_t stream);
+
+/* Bytes of workspace mx_cache_sparse_attn needs; 0 if a size is not positive or the sizes are refused.  Host only, no CUDA
+ * call. */
+size_t mx_cache_sparse_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int top);
 
 /*
  * Synchronises `stream`, reads the int32 at `dev_status` and returns BSC_OK (0),
