@@ -73,11 +73,41 @@ __device__ __forceinline__ float2 f16x2_to_f32(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// Eight fp32 of a block with scale byte sb -> eight E4M3.
-__device__ __forceinline__ uint2 quant8_e4m3(const float (&f)[8], float inv, uint32_t sb) {
+// The largest magnitude of values, NaN if any is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float amax8(const float2 (&f)[4]) {
+  const float a = max3_nan(fabsf(f[0].x), fabsf(f[0].y), fabsf(f[1].x)), b = max3_nan(fabsf(f[1].y), fabsf(f[2].x), fabsf(f[2].y));
+  return max_nan(max3_nan(a, b, fabsf(f[3].x)), fabsf(f[3].y));
+}
+// Eight fp32 of a block with scale byte sb, whose inverse is inv, as elements.
+__device__ __forceinline__ uint2 quant8_e4m3(const float2 (&f)[4], float inv, uint32_t sb) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = __fmul2_rn(f[i], make_float2(inv, inv));
+    r[i] = cvt_e4m3x2(y.x, y.y);
+  }
   if (sb == 0xFFu) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  return make_uint2(cvt_e4m3x2(f[0] * inv, f[1] * inv) | (uint32_t)cvt_e4m3x2(f[2] * inv, f[3] * inv) << 16,
-                    cvt_e4m3x2(f[4] * inv, f[5] * inv) | (uint32_t)cvt_e4m3x2(f[6] * inv, f[7] * inv) << 16);
+  return make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
+}
+__device__ __forceinline__ uint32_t quant8_e2m1(const float2 (&f)[4], float inv, uint32_t sb) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = __fmul2_rn(f[i], make_float2(inv, inv));
+    y[2 * i] = p.x;
+    y[2 * i + 1] = p.y;
+  }
+  return sb == 0xFFu ? 0x77777777u : cvt_e2m1x8(y);
 }
 
 // Activations: bf16 (DT = 0) or fp16 (DT = 1), two to a word.
@@ -140,7 +170,7 @@ __device__ __forceinline__ void wait_for_last_kernel() { asm volatile("griddepco
 
 // A launch that may start early; cluster: blocks per cluster (1: none).
 template <class... P, class... A>
-cudaError_t launch_early(void (*kernel)(P...), unsigned grid, int block, size_t smem, cudaStream_t st, int cluster,
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int block, size_t smem, cudaStream_t st, int cluster,
                          const A&... args) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -149,7 +179,7 @@ cudaError_t launch_early(void (*kernel)(P...), unsigned grid, int block, size_t 
   attr[1].val.clusterDim.x = (unsigned)cluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -28,18 +28,23 @@ __global__ void __launch_bounds__(DQ_THREADS) dequantize_kernel(const uint8_t* x
                                                                 int H, int N, int layout, long long pieces) {
   wait_for_last_kernel();
   if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
-  const int per_row = N / 16;
+  const uint32_t per_row = N / 16;
+  const bool in_order = H == 1 && (B == 1 || layout == 0);        // scales lie as their elements do
   uint4 v[DQ_ITEMS];
   float f[DQ_ITEMS];
-  long long i0 = (long long)blockIdx.x * (DQ_THREADS * DQ_ITEMS) + threadIdx.x;
+  const long long block = (long long)blockIdx.x * (DQ_THREADS * DQ_ITEMS), i0 = block + threadIdx.x;
+  const uint32_t row0 = (uint32_t)(block / per_row), p0 = (uint32_t)(block - (long long)row0 * per_row);   // below 2^31 rows
 #pragma unroll
   for (int k = 0; k < DQ_ITEMS; ++k) {
     const long long i = i0 + k * DQ_THREADS;
     if (i >= pieces) break;
     v[k] = __ldcs(reinterpret_cast<const uint4*>(x) + i);
-    const uint32_t r = (uint32_t)(i / per_row), p = (uint32_t)(i - (long long)r * per_row);   // fewer than 2^31 rows
-    const uint32_t sr = H == 1 && (B == 1 || layout == 0) ? r : scale_row(r, B, S, H, layout);
-    f[k] = scale_value(__ldca(sc + (long long)sr * (N / 32) + (p >> 1)));
+    long long at = i >> 1;
+    if (!in_order) {
+      const uint32_t p = p0 + threadIdx.x + k * DQ_THREADS, r = p / per_row;
+      at = (long long)scale_row(row0 + r, B, S, H, layout) * (N / 32) + ((p - r * per_row) >> 1);
+    }
+    f[k] = scale_value(__ldca(sc + at));
   }
 #pragma unroll
   for (int k = 0; k < DQ_ITEMS; ++k) {

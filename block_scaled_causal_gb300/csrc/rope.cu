@@ -5,195 +5,216 @@
 // pass through.
 //
 // Angles.  f_i is held as a 64-bit fraction of a turn, so p * f_i mod 2^64 is the angle's fraction of a turn, exactly,
-// whatever the position; its upper 32 bits (a step of 1.5e-9 radians) become an fp32 in [-1, 1) half turns for
-// sincospif.  No table of positions is read and there is no longest one.  A block works out each of its tokens' cosines
-// once, in shared memory, for all heads.
+// whatever the position: no table of positions is read and there is no longest one (turned()).
 //
-// What bounds it: memory, once those are shared by enough heads.  A lane has 8 neighbouring elements of one head (16
-// bytes); D / 8 lanes are a head, and half pairs exchange their packed elements with the lane rot / 16 away.  Four
-// neighbouring lanes are an MX block.  All loads of ROPE_BATCH heads are issued ahead of the first use.
+// Work.  A warp has one token: its cosines and sines are worked out once by its lanes and pass through shared memory into
+// registers, then all heads of the token (or a share of them, where there are few tokens) go by.  A lane has 8 neighbouring
+// elements of a head (16 bytes), D / 8 lanes are a head, and half pairs exchange their packed elements with the lane rot / 16
+// away; four neighbouring lanes are an MX block.  From head to head an address moves by one addition.
+//
+// What bounds it: memory, with the loads of ROPE_BATCH heads ahead of the first use.
 #include "cache.cuh"
 
 namespace bsc {
 namespace {
 
-constexpr int ROPE_THREADS = 128, ROPE_WARPS = ROPE_THREADS / 32, ROPE_BATCH = 4;
-constexpr int MOST_TOKENS = 16, MOST_ANGLES = 1024;   // of a block
+constexpr int ROPE_WARPS = 4, ROPE_BATCH = 4, MOST_PAIRS = 128;
 enum { TO_ACT, TO_MX, TO_CACHE };
 
-template <int DT, bool INTER, int OUT, int FMT, int DC>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeArgs a) {
-  __shared__ __align__(16) float cosines[MOST_ANGLES], sines[MOST_ANGLES];
-  __shared__ int page_of[MOST_TOKENS];           // TO_CACHE: the token's page, -1 where it has none; -2: not a token
-  __shared__ uint32_t slot_of[MOST_TOKENS];
-  wait_for_last_kernel();
-  if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
-  const int tiles = (a.T + a.tt - 1) / a.tt, b = blockIdx.x / tiles, t0 = (blockIdx.x - b * tiles) * a.tt;
-  const int tokens = min(a.tt, a.T - t0), P = a.rot / 2;
-  // ---- the tokens' positions, pages and angles ----
-  int n = 0;
-  long long len = 0;
-  if (OUT == TO_CACHE) {
-    len = __ldca(a.pt.seq_lens + b);
-    if (len < 0) len = 0;
-    n = a.new_lens ? min(max(__ldca(a.new_lens + b), 0), a.T) : a.T;
-    if (threadIdx.x < tokens) {
-      const int t = t0 + threadIdx.x;
-      const long long pos = len - n + t;
-      uint32_t row = 0;
-      int32_t bad = 0;
-      int page = -2;
-      if (t < n && pos >= 0) page = cache_page(a.c, a.pt, b, pos, 0, row, bad);
-      if (bad) report(a.dev_status, bad);
-      page_of[threadIdx.x] = page;
-      slot_of[threadIdx.x] = row;
-    }
-  }
-  for (int i = threadIdx.x; i < tokens * P; i += ROPE_THREADS) {
-    const int tl = i / P, p = i - tl * P;
-    long long pos = t0 + tl;
-    if (OUT == TO_CACHE) pos += len - n;
-    else if (a.pos) pos = a.pos_t ? __ldca(a.pos + b * a.pos_b + pos * a.pos_t) : __ldca(a.pos + b * a.pos_b) + pos;
-    const unsigned long long turn = (unsigned long long)pos * __ldca(a.turns + p);
-    float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-    cosines[i] = c * a.magnitude;
-    sines[i] = (a.inverse ? -s : s) * a.magnitude;
-  }
-  __syncthreads();
+// Cosine and sine of 2 pi x / 2^64, times m.  The upper 24 bits are half turns in [-1, 1), exact in fp32; the rest, delta <
+// 2^-21 radians, turns their cosine and sine by its first order (delta^2 / 2 < 2^-43).
+__device__ __forceinline__ void turned(unsigned long long x, float m, float& c, float& s) {
+  const float half_turns = (float)((int)(x >> 32) & ~0xFF) * 0x1p-31f;
+  const float delta = (float)(uint32_t)(x >> 8) * (6.2831853f * 0x1p-56f);
+  float c0, s0;
+  sincospif(half_turns, &s0, &c0);
+  c = fmaf(-s0, delta, c0) * m;
+  s = fmaf(c0, delta, s0) * m;
+}
 
-  // ---- the heads of all tokens, in memory's order: `heads` rows per token, q's then k's (then v's) ----
-  const int D = DC ? DC : a.D, lpr = D / 8, rpw = 32 / lpr;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / lpr, chunk = lane - sub * lpr;
-  const bool act = sub < rpw;
-  const int heads = a.Hq + (OUT == TO_CACHE ? 2 : 1) * a.Hkv, rows = tokens * heads;
-  const int half = a.rot / 16;                   // chunks of half the rotated part
-  const bool turned = chunk < 2 * half, low = chunk < half;
-  const int other = turned && !INTER ? (low ? lane + half : lane - half) : lane;
-  const int angle = INTER ? chunk * 4 : (low ? chunk : chunk - half) * 8;
-  const uint32_t up = OUT == TO_ACT ? 0u : ceil_carry<FMT>(a.rule);
-  constexpr int STEP = ROPE_WARPS * ROPE_BATCH;
-  for (int r0 = 0; r0 < rows; r0 += STEP * rpw) {
-    uint4 x[ROPE_BATCH];
-    int tok[ROPE_BATCH], head[ROPE_BATCH];
+// What a lane turns its 8 elements by: y = x c + o s, o being the partner chunk (or the pair's other element), signs in s.
+template <bool INTER>
+struct Turn {
+  float2 c[4], s[4];
+  __device__ __forceinline__ void load(const float* cosines, const float* sines, int angle, bool low) {
+    if (INTER) {
+      const float4 a = *reinterpret_cast<const float4*>(cosines + angle), b = *reinterpret_cast<const float4*>(sines + angle);
+      c[0] = make_float2(a.x, a.x); c[1] = make_float2(a.y, a.y); c[2] = make_float2(a.z, a.z); c[3] = make_float2(a.w, a.w);
+      s[0] = make_float2(-b.x, b.x); s[1] = make_float2(-b.y, b.y); s[2] = make_float2(-b.z, b.z); s[3] = make_float2(-b.w, b.w);
+    } else {
+      const float sign = low ? -1.f : 1.f;
 #pragma unroll
-    for (int k = 0; k < ROPE_BATCH; ++k) {
-      const int r = r0 + (k * ROPE_WARPS + warp) * rpw + sub;
-      x[k] = make_uint4(0, 0, 0, 0);
-      tok[k] = -1;
-      head[k] = 0;
-      if (act && r < rows) {
-        tok[k] = r / heads;
-        head[k] = r - tok[k] * heads;
-        if (OUT == TO_CACHE && page_of[tok[k]] == -2 && head[k] >= a.Hq) tok[k] = -1;
-      }
-      if (tok[k] >= 0) {
-        const int which = head[k] < a.Hq ? 0 : OUT == TO_CACHE && head[k] >= a.Hq + a.Hkv ? 2 : 1;
-        const int h = head[k] - (which == 0 ? 0 : which == 1 ? a.Hq : a.Hq + a.Hkv);
-        const RowStrides& s = a.xs[which];
-        x[k] = __ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x[which]) + b * s.b +
-                                                     (t0 + tok[k]) * s.t + h * s.h) + chunk);
+      for (int i = 0; i < 2; ++i) {
+        const float4 a = reinterpret_cast<const float4*>(cosines + angle)[i], b = reinterpret_cast<const float4*>(sines + angle)[i];
+        c[2 * i] = make_float2(a.x, a.y); c[2 * i + 1] = make_float2(a.z, a.w);
+        s[2 * i] = make_float2(sign * b.x, sign * b.y); s[2 * i + 1] = make_float2(sign * b.z, sign * b.w);
       }
     }
+  }
+};
+
+// One tensor's heads h0, h0 + rpw, ... below h1 of a token, for this lane: `emit(head, values)` for each.  Whole warps call
+// it with the same h0 and h1 (heads of lane group `sub` are h0 + sub + k rpw).
+template <int DT, bool INTER, bool TURN, class Emit>
+__device__ __forceinline__ void heads_of(const uint16_t* x, long long step, int first, int h1, int rounds, int rpw, bool act,
+                                         int other, bool in_rot, const Turn<INTER>& turn, Emit emit) {
+  for (int k0 = 0; k0 < rounds; k0 += ROPE_BATCH) {
+    uint4 v[ROPE_BATCH];
 #pragma unroll
     for (int k = 0; k < ROPE_BATCH; ++k) {
-      uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, o[4];
-      if (!INTER)
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (act && first + (k0 + k) * rpw < h1) v[k] = __ldcs(reinterpret_cast<const uint4*>(x + k * step));
+    }
+    x += ROPE_BATCH * step;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = __shfl_sync(0xFFFFFFFFu, u[j], other);
-      const int h = head[k], which = h < a.Hq ? 0 : OUT == TO_CACHE && h >= a.Hq + a.Hkv ? 2 : 1;
-      const bool there = tok[k] >= 0;
-      float f[8];
+    for (int k = 0; k < ROPE_BATCH; ++k) {
+      if (k0 + k >= rounds) break;
+      const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      float2 f[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 p = act_to_f32<DT>(u[j]);
-        f[2 * j] = p.x;
-        f[2 * j + 1] = p.y;
+      for (int j = 0; j < 4; ++j) f[j] = act_to_f32<DT>(u[j]);
+      if (TURN) {
+        float2 o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = INTER ? make_float2(f[j].y, f[j].x) : act_to_f32<DT>(__shfl_sync(0xFFFFFFFFu, u[j], other));
+        if (in_rot)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = __ffma2_rn(f[j], turn.c[j], __fmul2_rn(o[j], turn.s[j]));
       }
-      if (there && turned && which != 2) {
-        const float* const cs = cosines + tok[k] * P + angle;
-        const float* const sn = sines + tok[k] * P + angle;
-        if (INTER) {
-          const float4 c = *reinterpret_cast<const float4*>(cs), s = *reinterpret_cast<const float4*>(sn);
-          const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float p = f[2 * j], q = f[2 * j + 1];
-            f[2 * j] = p * cc[j] - q * ss[j];
-            f[2 * j + 1] = p * ss[j] + q * cc[j];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float4 c = reinterpret_cast<const float4*>(cs)[i], s = reinterpret_cast<const float4*>(sn)[i];
-            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 pair = act_to_f32<DT>(o[2 * i + j / 2]);
-              const float q = j & 1 ? pair.y : pair.x;
-              f[4 * i + j] = f[4 * i + j] * cc[j] + (low ? -q : q) * ss[j];
-            }
-          }
-        }
-      }
-      if (there && (OUT == TO_ACT || (OUT == TO_CACHE && which == 0))) {
-        const RowStrides& s = a.ys[which];
-        uint4 v = make_uint4(f32_to_act<DT>(f[0], f[1]), f32_to_act<DT>(f[2], f[3]), f32_to_act<DT>(f[4], f[5]),
-                             f32_to_act<DT>(f[6], f[7]));
-        if (OUT == TO_CACHE && page_of[tok[k]] == -2) v = make_uint4(0, 0, 0, 0);
-        __stcs(reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.y[which]) + b * s.b + (t0 + tok[k]) * s.t +
-                                        (h - (which ? a.Hq : 0)) * s.h) + chunk, v);
-      }
-      if (OUT != TO_ACT) {
-        uint32_t am = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-        float inv;
-        const uint32_t sb = block_scale<FMT>(__uint_as_float(am), up, inv);
-        if (OUT == TO_MX && there) {
-          const int H = which ? a.Hkv : a.Hq, hh = h - (which ? a.Hq : 0);
-          const RowStrides& s = a.ys[which];
-          __stcs(reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.y[which]) + b * s.b + (t0 + tok[k]) * s.t + hh * s.h) +
-                     chunk, quant8_e4m3(f, inv, sb));
-          if ((chunk & 3) == 0)
-            a.sc[which][(((long long)b * H + hh) * a.T + t0 + tok[k]) * (D / 32) + (chunk >> 2)] = (uint8_t)sb;
-        }
-        if (OUT == TO_CACHE && there && which != 0) {
-          const int page = page_of[tok[k]];
-          if (page >= 0) {
-            const int hh = h - a.Hq - (which == 2 ? a.Hkv : 0);
-            const unsigned long long row = (unsigned long long)hh * a.c.page_size + slot_of[tok[k]];
-            uint8_t* const dst = which == 2 ? a.c.v + page * a.c.v_ps : a.c.k + page * a.c.k_ps;
-            uint8_t* const sc = which == 2 ? a.c.v_sc + page * a.c.v_sc_ps : a.c.k_sc + page * a.c.k_sc_ps;
-            if (FMT == CACHE_FP4) {
-              float y[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = f[i] * inv;
-              reinterpret_cast<uint32_t*>(dst + row * (D / 2))[chunk] = sb == 0xFFu ? 0x77777777u : cvt_e2m1x8(y);
-            } else {
-              reinterpret_cast<uint2*>(dst + row * D)[chunk] = quant8_e4m3(f, inv, sb);
-            }
-            if ((chunk & 3) == 0) sc[row * (D / 32) + (chunk >> 2)] = (uint8_t)sb;
-          }
-        }
-      }
+      const int h = first + (k0 + k) * rpw;
+      emit(h, act && h < h1, f);
     }
   }
 }
 
-using Kernel = void (*)(RopeArgs);
-// Tokens per block: enough for two batches of every thread, so that a block's angles and start are spread over its rows.
-cudaError_t launch(Kernel k, RopeArgs a, int heads, cudaStream_t st) {
-  const long long lanes = (long long)heads * (a.D / 8);
-  long long tt = (2 * ROPE_BATCH * ROPE_THREADS + lanes - 1) / lanes;
-  if (tt > MOST_TOKENS) tt = MOST_TOKENS;
-  if (tt > MOST_ANGLES / (a.rot / 2)) tt = MOST_ANGLES / (a.rot / 2);
-  if (tt > a.T) tt = a.T;
-  a.tt = (int)tt;
-  const long long grid = (long long)a.B * ((a.T + tt - 1) / tt);
-  return launch_early(k, (unsigned)grid, ROPE_THREADS, 0, st, 1, a);
+// The scale byte of a block of four neighbouring lanes' elements.
+template <int FMT>
+__device__ __forceinline__ uint32_t chunk_scale(const float2 (&f)[4], uint32_t up, float& inv) {
+  float am = amax8(f);
+  am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+  am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+  return block_scale<FMT>(am, up, inv);
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack(const float2 (&f)[4]) {
+  return make_uint4(f32_to_act<DT>(f[0].x, f[0].y), f32_to_act<DT>(f[1].x, f[1].y), f32_to_act<DT>(f[2].x, f[2].y),
+                    f32_to_act<DT>(f[3].x, f[3].y));
+}
+
+// blockIdx.x: ROPE_WARPS tokens of the B x T, a warp each; blockIdx.y: a share of `per` heads of each token's list (q's, k's,
+// then v's).
+template <int DT, bool INTER, int OUT, int FMT, int DC>
+__global__ void __launch_bounds__(ROPE_WARPS * 32, 8) rope_kernel(const RopeArgs a, int per) {
+  __shared__ __align__(16) float cosines[ROPE_WARPS][MOST_PAIRS], sines[ROPE_WARPS][MOST_PAIRS];
+  wait_for_last_kernel();
+  if (gridDim.x * gridDim.y <= EARLY_BLOCKS) next_kernel_may_start();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t token = blockIdx.x * ROPE_WARPS + warp;
+  if (token >= (uint32_t)a.B * a.T) return;
+  const int b = token / a.T, t = token - b * a.T;
+
+  // ---- the token's position and page, its angles ----
+  long long pos = t;
+  bool real = true;                              // TO_CACHE: a token of the sequence
+  int page = -1;
+  uint32_t slot = 0;
+  if (OUT == TO_CACHE) {
+    const long long len = max(__ldca(a.pt.seq_lens + b), 0);
+    const int n = a.new_lens ? min(max(__ldca(a.new_lens + b), 0), a.T) : a.T;
+    pos = len - n + t;
+    real = t < n && pos >= 0;
+    if (real) {
+      int32_t bad = 0;
+      page = cache_page(a.c, a.pt, b, pos, 0, slot, bad);
+      if (bad && lane == 0) report(a.dev_status, bad);
+    }
+  } else if (a.pos) {
+    pos = a.pos_t ? __ldca(a.pos + b * a.pos_b + t * a.pos_t) : __ldca(a.pos + b * a.pos_b) + (long long)t;
+  }
+  const int P = a.rot / 2;
+  for (int p = lane; p < P; p += 32) {
+    float c, s;
+    turned((unsigned long long)pos * __ldca(a.turns + p), a.magnitude, c, s);
+    cosines[warp][p] = c;
+    sines[warp][p] = a.inverse ? -s : s;
+  }
+  __syncwarp();
+
+  const int D = DC ? DC : a.D, lpr = D / 8, rpw = 32 / lpr, sub = lane / lpr, chunk = lane - sub * lpr;
+  const bool act = sub < rpw;
+  const int half = a.rot / 16;                   // chunks of half the rotated part
+  const bool in_rot = chunk < 2 * half, low = chunk < half;
+  const int other = in_rot ? (low ? lane + half : lane - half) : lane;
+  Turn<INTER> turn;
+  turn.load(cosines[warp], sines[warp], !in_rot ? 0 : INTER ? chunk * 4 : (low ? chunk : chunk - half) * 8, low);
+
+  // ---- the heads: this block's share of [0, Hq + Hkv (+ Hkv)) ----
+  const int total = a.Hq + (OUT == TO_CACHE ? 2 : 1) * a.Hkv, from = blockIdx.y * per, to = min(from + per, total);
+  const uint32_t up = OUT == TO_ACT ? 0u : ceil_carry<FMT>(a.rule);
+  auto source = [&](int i, int h) {
+    return reinterpret_cast<const uint16_t*>(a.x[i]) + b * a.xs[i].b + t * a.xs[i].t + h * a.xs[i].h + chunk * 8;
+  };
+#pragma unroll
+  for (int i = 0; i < (OUT == TO_CACHE ? 3 : 2); ++i) {
+    const int base = i == 0 ? 0 : i == 1 ? a.Hq : a.Hq + a.Hkv, H = i == 0 ? a.Hq : a.Hkv;
+    const int h0 = max(from - base, 0), h1 = min(to - base, H);
+    if (h0 >= h1 || (OUT == TO_CACHE && i != 0 && page < 0)) continue;
+    const int first = h0 + sub, rounds = (h1 - h0 + rpw - 1) / rpw;
+    const uint16_t* const x = source(i, first);
+    const long long step = rpw * a.xs[i].h;
+    if (OUT == TO_ACT || (OUT == TO_CACHE && i == 0)) {
+      uint16_t* const y = reinterpret_cast<uint16_t*>(a.y[i]) + b * a.ys[i].b + t * a.ys[i].t + chunk * 8;
+      const long long ysh = a.ys[i].h;
+      heads_of<DT, INTER, true>(x, step, first, h1, rounds, rpw, act, other, in_rot, turn,
+                                [&](int h, bool there, const float2 (&f)[4]) {
+        if (there) __stcs(reinterpret_cast<uint4*>(y + h * ysh), real ? pack<DT>(f) : make_uint4(0, 0, 0, 0));
+      });
+    } else if (OUT == TO_MX) {
+      uint8_t* const y = reinterpret_cast<uint8_t*>(a.y[i]) + b * a.ys[i].b + t * a.ys[i].t + chunk * 8;
+      uint8_t* const sc = a.sc[i] + ((long long)b * H * a.T + t) * (D / 32) + (chunk >> 2);
+      const long long ysh = a.ys[i].h, sch = (long long)a.T * (D / 32);
+      heads_of<DT, INTER, true>(x, step, first, h1, rounds, rpw, act, other, in_rot, turn,
+                                [&](int h, bool there, const float2 (&f)[4]) {
+        float inv;
+        const uint32_t sb = chunk_scale<FMT>(f, up, inv);
+        if (there) {
+          __stcs(reinterpret_cast<uint2*>(y + h * ysh), quant8_e4m3(f, inv, sb));
+          if ((chunk & 3) == 0) sc[h * sch] = (uint8_t)sb;
+        }
+      });
+    } else if constexpr (OUT == TO_CACHE) {
+      constexpr int RB = row_bytes<FMT, DC>();
+      uint8_t* const y = (i == 2 ? a.c.v + page * a.c.v_ps : a.c.k + page * a.c.k_ps) + (unsigned long long)slot * RB + chunk * (RB / lpr);
+      uint8_t* const sc = (i == 2 ? a.c.v_sc + page * a.c.v_sc_ps : a.c.k_sc + page * a.c.k_sc_ps) +
+                          (unsigned long long)slot * (D / 32) + (chunk >> 2);
+      const long long ysh = (long long)a.c.page_size * RB, sch = (long long)a.c.page_size * (D / 32);
+      auto emit = [&](int h, bool there, const float2 (&f)[4]) {
+        float inv;
+        const uint32_t sb = chunk_scale<FMT>(f, up, inv);
+        if (there) {
+          if (FMT == CACHE_FP4) *reinterpret_cast<uint32_t*>(y + h * ysh) = quant8_e2m1(f, inv, sb);
+          else *reinterpret_cast<uint2*>(y + h * ysh) = quant8_e4m3(f, inv, sb);
+          if ((chunk & 3) == 0) sc[h * sch] = (uint8_t)sb;
+        }
+      };
+      if (i == 1) heads_of<DT, INTER, true>(x, step, first, h1, rounds, rpw, act, other, in_rot, turn, emit);
+      else heads_of<DT, INTER, false>(x, step, first, h1, rounds, rpw, act, other, in_rot, turn, emit);
+    }
+  }
+}
+
+using Kernel = void (*)(RopeArgs, int);
+// Heads of a token are shared by several warps while there are fewer tokens than the card takes warps at once.
+cudaError_t launch(Kernel k, const RopeArgs& a, int heads, cudaStream_t st) {
+  const long long tokens = (long long)a.B * a.T;
+  const int rpw = 32 / (a.D / 8);
+  int shares = 1;
+  while (shares * 2 <= heads / rpw && tokens * shares * 2 <= 152 * 16) shares *= 2;
+  int per = (heads + shares - 1) / shares;
+  per = (per + rpw - 1) / rpw * rpw;
+  const dim3 grid((unsigned)((tokens + ROPE_WARPS - 1) / ROPE_WARPS), (unsigned)((heads + per - 1) / per));
+  return launch_early(k, grid, ROPE_WARPS * 32, 0, st, 1, a, per);
 }
 
 }  // namespace
