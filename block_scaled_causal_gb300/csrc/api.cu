@@ -672,7 +672,8 @@ bsc_status rms_norm(const bsc_rms_norm_params* p, bsc_stream_t stream) {
   a.N = p->N;
   a.rule = p->rule;
   a.eps = p->eps;
-  return from_cuda(bsc::launch_norm(a, p->dtype, p->weight_dtype == BSC_FP32, reinterpret_cast<cudaStream_t>(stream)));
+  a.w32 = p->weight_dtype == BSC_FP32;
+  return from_cuda(bsc::launch_norm(a, p->dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t rms_norm_bwd_workspace_bytes(long long rows, int N) {
@@ -712,7 +713,8 @@ bsc_status rms_norm_bwd(const bsc_rms_norm_bwd_params* p, bsc_stream_t stream) {
   a.rows = p->rows;
   a.inner = p->inner;
   a.N = p->N;
-  return from_cuda(bsc::launch_norm_bwd(a, p->dtype, p->weight_dtype == BSC_FP32, reinterpret_cast<cudaStream_t>(stream)));
+  a.w32 = p->weight_dtype == BSC_FP32;
+  return from_cuda(bsc::launch_norm_bwd(a, p->dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 bsc_status mxfp8_dequantize(const uint8_t* x, const uint8_t* sc, int B, int S, int H, int D, bsc_layout layout, int dtype,

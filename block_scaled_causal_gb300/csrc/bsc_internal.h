@@ -136,9 +136,10 @@ struct NormArgs {
   NormRows xs, rs, ys, ss;
   long long rows;
   int inner, N, rule;
+  int w32;                 // weights: 0 the activations' type, 1 fp32
   float eps;
 };
-cudaError_t launch_norm(const NormArgs& a, int dtype, int w32, cudaStream_t st);
+cudaError_t launch_norm(const NormArgs& a, int dtype, cudaStream_t st);
 struct NormBwdArgs {
   const void* dy;
   const void* s;
@@ -151,8 +152,9 @@ struct NormBwdArgs {
   NormRows dys, ss, dss, dxs;
   long long rows;
   int inner, N;
+  int w32;
 };
-cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int w32, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, cudaStream_t st);
 size_t norm_bwd_workspace_bytes(long long rows, int N);
 
 // MXFP8 rows back to values: codes in `layout`, scales [B][H][S][N/32].
