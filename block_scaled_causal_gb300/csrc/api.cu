@@ -288,7 +288,7 @@ bool sparse_parts(int B, int T, int Hq, int Hkv, int D, int page_size, int max_p
   const long long tokens = (long long)cols * page_size;
   if (tokens > BSC_CACHE_MAX_TOKENS || cache_attn_too_large(rows, 1, Hq / Hkv, 1, tokens)) return false;
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  w->table = max_pages > top ? up((size_t)rows * max_pages * 4) : 0;
+  w->table = up(bsc::cache_select_scores_bytes(rows, max_pages, top));
   w->lens = w->table + up((size_t)rows * cols * 4);
   w->attn = w->lens + up((size_t)rows * 4);
   w->all = w->attn + bsc::cache_attn_workspace_bytes(rows, 1, Hq / Hkv, 1, D, tokens);

@@ -208,11 +208,12 @@ struct SelectArgs {
   int top, first, last;
   int pages_per_page;      // head slices of the pools from page to page: page p, head h is slice p * this + h
   int32_t* blocks;         // [B][T][Hkv][top], or nullptr
-  float* scores;           // workspace [B T Hkv][max_pages]
+  float* scores;           // workspace of cache_select_scores_bytes(): [B T Hkv][max_pages], or unused
   int32_t* table;          // workspace [B T Hkv][top]: slices, in order
   int32_t* lens;           // workspace [B T Hkv]: tokens of the listed slices
 };
 cudaError_t launch_cache_select(const SelectArgs& a, int D, int dtype, cudaStream_t st);
+size_t cache_select_scores_bytes(int rows, int max_pages, int top);
 
 struct CacheAttnArgs {
   CachePools c;

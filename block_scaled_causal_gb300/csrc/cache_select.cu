@@ -15,10 +15,14 @@
 //
 // What bounds it: latency for one sequence, else reading the bounds (2 D + 1 bytes per page and head against the
 // page_size * 2 * (D / 2 + D / 32) or more of the page itself).
+#include <cooperative_groups.h>
+
 #include "cache.cuh"
 
 namespace bsc {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int BOUNDS_THREADS = 128;
 
@@ -134,223 +138,257 @@ __device__ __forceinline__ Seen seen_by(const SelectArgs& a, int b, int t) {
   return s;
 }
 
-// Scores of SCORE_PAGES pages for one query and KV head.  D / 16 lanes are a page: 16 minima and 16 maxima each.
-constexpr int SCORE_THREADS = 128, SCORE_PAGES = 128;
-template <int D, int DT>
-__global__ void __launch_bounds__(SCORE_THREADS) cache_score_kernel(const SelectArgs a, int tiles) {
-  constexpr int LPP = D / 16, PPW = 32 / LPP, WARPS = SCORE_THREADS / 32;
-  __shared__ __align__(16) uint8_t codes[2][D];
-  __shared__ float tops[WARPS];
-  wait_for_last_kernel();
-  if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
-  const uint32_t row = blockIdx.x / tiles, tile = blockIdx.x - row * tiles;
-  const uint32_t bt = row / a.Hkv, h = row - bt * a.Hkv, b = bt / a.T, t = bt - b * a.T;
-  const Seen seen = seen_by(a, b, t);
-  const int first = tile * SCORE_PAGES, last = min(first + SCORE_PAGES, seen.pages);
-  if (first >= last || seen.pages <= a.top) return;      // every page is taken: no score is read
-  // ---- the row's codes ----
-  const int G = a.Hq / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float u = 0.f, l = 0.f;
-  if (threadIdx.x < D) {
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) + b * a.qs.b + t * a.qs.t + (long long)h * G * a.qs.h + threadIdx.x;
-    for (int g = 0; g < G; ++g) {
-      const float f = act_to_f32<DT>((uint32_t)__ldca(q + g * a.qs.h)).x;
-      u += f > 0.f ? f : 0.f;
-      l += f < 0.f ? -f : 0.f;
-      if (!(fabsf(f) < INFINITY)) u = INFINITY;
+// The pages of one query and KV head: a cluster of blocks scores them, each block a run of pages, and the first block chooses.
+//
+// The scores pass through the first block's shared memory, or the workspace where a table has more pages than that holds.
+// The threshold, the score of the last page taken, is found by histograms: the scores in question are spread evenly
+// over 256 bins between their least and their largest, and those of the bin that holds the threshold are the next round's,
+// until they are all equal.  Scores that are spread by chance take two or three rounds (a bin of 512 has a few); a round takes
+// at least the largest or the least away, and a bin is 1/255 of its round's range, so that no values of fp32 take more than
+// 32.  (Two bits of the threshold at a time, sixteen counts of all scores, took 8 us for 512 pages.)  A thread then has a
+// run of neighbouring pages, so that a scan over the threads gives the list's order.
+constexpr int CHOOSE_THREADS = 256, CHOOSE_WARPS = CHOOSE_THREADS / 32, BINS = 256;
+constexpr int HELD_PAGES = 10240;                // scores in shared memory at most: 40 KB
+constexpr float FIRST_SCORE = 0x1p126f, LAST_SCORE = -0x1p126f;   // of a page with a NaN, of one that is not there
+
+// Exclusive sums over the threads of two counts, and their totals.
+__device__ __forceinline__ void block_scan(int& x, int& y, int (&sums)[2][CHOOSE_WARPS], int& all_x) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, own_x = x, own_y = y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int ux = __shfl_up_sync(0xFFFFFFFFu, x, o), uy = __shfl_up_sync(0xFFFFFFFFu, y, o);
+    if (lane >= o) {
+      x += ux;
+      y += uy;
     }
   }
-  float top = fmaxf(u, l);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  if (lane == 0) tops[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < WARPS; ++k) top = fmaxf(top, tops[k]);
-  // 2^(6 - floor(log2 top)); rows of nothing, and those with a NaN or an infinity, score 0 everywhere
-  const int e = (int)(__float_as_uint(top) >> 23);
-  const float f = e == 0 || e == 255 ? 0.f : __uint_as_float((uint32_t)min(max(260 - e, 1), 254) << 23);
-  if (threadIdx.x < D) {
-    codes[0][threadIdx.x] = f == 0.f ? 0 : (uint8_t)min(__float2int_rn(u * f), 127);
-    codes[1][threadIdx.x] = f == 0.f ? 0 : (uint8_t)min(__float2int_rn(l * f), 127);
+  if (lane == 31) {
+    sums[0][warp] = x;
+    sums[1][warp] = y;
   }
   __syncthreads();
-  const int part = lane % LPP;
-  const uint4 cu = *reinterpret_cast<const uint4*>(codes[0] + part * 16), cl = *reinterpret_cast<const uint4*>(codes[1] + part * 16);
-  // ---- the pages: all loads of a batch first ----
-  constexpr int BATCH = 4;
-  float* const out = a.scores + (long long)row * a.pt.max_pages;
-  const int32_t* const table = a.pt.table + (long long)b * a.pt.stride;
-  for (int p0 = first + warp * PPW; p0 < last; p0 += BATCH * WARPS * PPW) {
-    int page[BATCH];
-    uint32_t e8[BATCH];
-    uint4 lo[BATCH], hi[BATCH];
+  x -= own_x;
+  y -= own_y;
+  all_x = 0;
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int p = p0 + k * WARPS * PPW + lane / LPP;
-      page[k] = p < last ? __ldca(table + p) : -1;
+  for (int k = 0; k < CHOOSE_WARPS; ++k) {
+    if (k < warp) {
+      x += sums[0][k];
+      y += sums[1][k];
     }
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      lo[k] = hi[k] = make_uint4(0, 0, 0, 0);
-      e8[k] = 0;
-      if (page[k] >= 0 && page[k] < a.num_pages) {
-        const long long at = (long long)page[k] * a.Hkv + h;
-        lo[k] = __ldca(reinterpret_cast<const uint4*>(a.codes + at * (2 * D)) + part);
-        hi[k] = __ldca(reinterpret_cast<const uint4*>(a.codes + at * (2 * D) + D) + part);
-        e8[k] = __ldca(a.exps + at);
-      } else {
-        page[k] = -1;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int p = p0 + k * WARPS * PPW + lane / LPP;
-      int d = __dp4a((int)hi[k].x, (int)cu.x, 0), m = __dp4a((int)lo[k].x, (int)cl.x, 0);
-      d = __dp4a((int)hi[k].y, (int)cu.y, d);
-      m = __dp4a((int)lo[k].y, (int)cl.y, m);
-      d = __dp4a((int)hi[k].z, (int)cu.z, d);
-      m = __dp4a((int)lo[k].z, (int)cl.z, m);
-      d = __dp4a((int)hi[k].w, (int)cu.w, d);
-      m = __dp4a((int)lo[k].w, (int)cl.w, m);
-      d -= m;
-#pragma unroll
-      for (int o = LPP / 2; o; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-      if (part == 0 && p < last) {
-        if (page[k] < 0) report(a.dev_status, CACHE_BAD_PAGE);
-        // a page that is not there comes last, one with a NaN first, so that it is met as it would be by reading all
-        out[p] = page[k] < 0 ? -INFINITY : e8[k] == 0xFFu ? INFINITY : (float)d * scale_value(e8[k]);
-      }
-    }
+    all_x += sums[0][k];
   }
 }
-
-// The pages of one query and KV head.  A thread has a run of neighbouring pages, so that a scan over the threads gives
-// the list's order.  The threshold, the key of the last page taken, is found two bits at a time: three counts of the
-// keys at or above a trial value, over the block.
-constexpr int SELECT_THREADS = 256, SELECT_WARPS = SELECT_THREADS / 32, HELD = 16;
-__device__ __forceinline__ uint32_t key_of(float s) {                     // in the order of the floats
+// Floats as unsigned integers of the same order, and back.
+__device__ __forceinline__ uint32_t key_of(float s) {
   const uint32_t u = __float_as_uint(s);
   return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
-__device__ __forceinline__ int block_scan(int v, int* sums, int& all) {   // exclusive; sums[SELECT_WARPS] of its own
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, s, o);
-    if (lane >= o) s += y;
-  }
-  if (lane == 31) sums[warp] = s;
-  __syncthreads();
-  int before = 0;
-  all = 0;
-#pragma unroll
-  for (int k = 0; k < SELECT_WARPS; ++k) {
-    const int y = sums[k];
-    if (k < warp) before += y;
-    all += y;
-  }
-  return before + s - v;
-}
-__global__ void __launch_bounds__(SELECT_THREADS) cache_select_kernel(const SelectArgs a, int cols) {
-  __shared__ int counts[2][SELECT_WARPS][3], scan[2][SELECT_WARPS];
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
+
+template <int D, int DT>
+__global__ void __launch_bounds__(CHOOSE_THREADS) cache_choose_kernel(const SelectArgs a, int cols, int cs) {
+  constexpr int LPP = D / 16, PPW = 32 / LPP;    // lanes per page (16 minima and 16 maxima each), pages per warp
+  extern __shared__ float held[];                // scores, if they fit
+  __shared__ __align__(16) uint8_t codes[2][D];
+  __shared__ float tops[CHOOSE_WARPS];
+  __shared__ uint32_t ends[2][CHOOSE_WARPS];
+  __shared__ int bins[2][BINS], sums[2][CHOOSE_WARPS];
   wait_for_last_kernel();
   if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
-  const uint32_t row = blockIdx.x, bt = row / a.Hkv, h = row - bt * a.Hkv, b = bt / a.T, t = bt - b * a.T;
+  const uint32_t row = blockIdx.x / cs, rank = blockIdx.x - row * cs;
+  const uint32_t bt = row / a.Hkv, h = row - bt * a.Hkv, b = bt / a.T, t = bt - b * a.T;
   const Seen seen = seen_by(a, b, t);
   const int32_t* const table = a.pt.table + (long long)b * a.pt.stride;
+  const int n = seen.pages, k = min(n, a.top), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool fits = a.pt.max_pages <= HELD_PAGES;
+  float* scores = fits ? held : a.scores + (long long)row * a.pt.max_pages;
+
+  // ---- scores: this block's run of the pages (where all are taken, none is needed) ----
+  if (n > k) {
+    const int G = a.Hq / a.Hkv;
+    float u = 0.f, l = 0.f;
+    if (threadIdx.x < D) {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q) + b * a.qs.b + t * a.qs.t + (long long)h * G * a.qs.h + threadIdx.x;
+      for (int g = 0; g < G; ++g) {
+        const float f = act_to_f32<DT>((uint32_t)__ldca(q + g * a.qs.h)).x;
+        u += f > 0.f ? f : 0.f;
+        l += f < 0.f ? -f : 0.f;
+        if (!(fabsf(f) < INFINITY)) u = INFINITY;
+      }
+    }
+    float top = fmaxf(u, l);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) top = fmaxf(top, tops[i]);
+    // 2^(6 - floor(log2 top)); rows of nothing, and those with a NaN or an infinity, score 0 everywhere
+    const int e = (int)(__float_as_uint(top) >> 23);
+    const float f = e == 0 || e == 255 ? 0.f : __uint_as_float((uint32_t)min(max(260 - e, 1), 254) << 23);
+    if (threadIdx.x < D) {
+      codes[0][threadIdx.x] = f == 0.f ? 0 : (uint8_t)min(__float2int_rn(u * f), 127);
+      codes[1][threadIdx.x] = f == 0.f ? 0 : (uint8_t)min(__float2int_rn(l * f), 127);
+    }
+    if (cs > 1) cg::this_cluster().sync();       // and the first block is there to be written to
+    else __syncthreads();
+    float* const out = fits && cs > 1 ? cg::this_cluster().map_shared_rank(held, 0) : scores;
+    const int part = lane % LPP, each = (n + cs - 1) / cs, p_first = min((int)rank * each, n), p_last = min(p_first + each, n);
+    const uint4 cu = *reinterpret_cast<const uint4*>(codes[0] + part * 16), cl = *reinterpret_cast<const uint4*>(codes[1] + part * 16);
+    constexpr int BATCH = 4;                     // pages of a lane whose loads are all ahead of the first use
+    for (int p0 = p_first + warp * PPW; p0 < p_last; p0 += BATCH * CHOOSE_WARPS * PPW) {
+      int page[BATCH];
+      uint32_t e8[BATCH];
+      uint4 lo[BATCH], hi[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int p = p0 + i * CHOOSE_WARPS * PPW + lane / LPP;
+        page[i] = p < p_last ? __ldca(table + p) : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+        e8[i] = 0;
+        if (page[i] >= 0 && page[i] < a.num_pages) {
+          const long long at = (long long)page[i] * a.Hkv + h;
+          lo[i] = __ldca(reinterpret_cast<const uint4*>(a.codes + at * (2 * D)) + part);
+          hi[i] = __ldca(reinterpret_cast<const uint4*>(a.codes + at * (2 * D) + D) + part);
+          e8[i] = __ldca(a.exps + at);
+        } else {
+          page[i] = -1;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int p = p0 + i * CHOOSE_WARPS * PPW + lane / LPP;
+        int d = __dp4a((int)hi[i].x, (int)cu.x, 0), m = __dp4a((int)lo[i].x, (int)cl.x, 0);
+        d = __dp4a((int)hi[i].y, (int)cu.y, d);
+        m = __dp4a((int)lo[i].y, (int)cl.y, m);
+        d = __dp4a((int)hi[i].z, (int)cu.z, d);
+        m = __dp4a((int)lo[i].z, (int)cl.z, m);
+        d = __dp4a((int)hi[i].w, (int)cu.w, d);
+        m = __dp4a((int)lo[i].w, (int)cl.w, m);
+        d -= m;
+#pragma unroll
+        for (int o = LPP / 2; o; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+        if (part == 0 && p < p_last) {
+          if (page[i] < 0) report(a.dev_status, CACHE_BAD_PAGE);
+          out[p] = page[i] < 0 ? LAST_SCORE : e8[i] == 0xFFu ? FIRST_SCORE : (float)d * scale_value(e8[i]);
+        }
+      }
+    }
+  }
+  if (cs > 1) cg::this_cluster().sync();
+  else __syncthreads();
+  if (rank != 0) return;
+
   int32_t* const list = a.table + (long long)row * cols;
   int32_t* const blocks = a.blocks ? a.blocks + (long long)row * a.top : nullptr;
-  const int n = seen.pages, k = min(n, a.top), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0 && seen.past) report(a.dev_status, CACHE_BAD_LEN);
-  if (threadIdx.x == 0) a.lens[row] = k > 0 ? (k - 1) * a.page_size + seen.tokens - (n - 1) * a.page_size : 0;
+  if (threadIdx.x == 0) {
+    if (seen.past) report(a.dev_status, CACHE_BAD_LEN);
+    a.lens[row] = k > 0 ? (k - 1) * a.page_size + seen.tokens - (n - 1) * a.page_size : 0;   // the last page is always listed
+  }
   auto put = [&](int at, int p) {
     const int page = __ldca(table + p);
     list[at] = page >= 0 && page < a.num_pages ? page * a.pages_per_page + (int)h : -1;
     if (blocks) blocks[at] = p;
   };
   if (blocks)
-    for (int i = k + threadIdx.x; i < a.top; i += SELECT_THREADS) blocks[i] = -1;
+    for (int i = k + threadIdx.x; i < a.top; i += CHOOSE_THREADS) blocks[i] = -1;
   if (n == k) {
-    for (int i = threadIdx.x; i < k; i += SELECT_THREADS) put(i, i);
+    for (int i = threadIdx.x; i < k; i += CHOOSE_THREADS) put(i, i);
     return;
   }
-  const float* const scores = a.scores + (long long)row * a.pt.max_pages;
-  const int run = (n + SELECT_THREADS - 1) / SELECT_THREADS, p0 = threadIdx.x * run, p1 = min(p0 + run, n);
-  auto key_at = [&](int p) {
-    return p < a.first || p >= n - a.last ? 0xFFFFFFFFu : key_of(__ldca(scores + p));
-  };
-  uint32_t held[HELD];
-  const bool fits = run <= HELD;
-#pragma unroll
-  for (int j = 0; j < HELD; ++j) held[j] = fits && p0 + j < p1 ? key_at(p0 + j) : 0u;
-  // keys at or above x among the thread's; no page has key 0 (that of a NaN)
-  auto count3 = [&](uint32_t x1, uint32_t x2, uint32_t x3, int& c1, int& c2, int& c3) {
-    c1 = c2 = c3 = 0;
-    if (fits) {
-#pragma unroll
-      for (int j = 0; j < HELD; ++j) {
-        c1 += held[j] >= x1;
-        c2 += held[j] >= x2;
-        c3 += held[j] >= x3;
-      }
-    } else {
-      for (int p = p0; p < p1; ++p) {
-        const uint32_t y = key_at(p);
-        c1 += y >= x1;
-        c2 += y >= x2;
-        c3 += y >= x3;
+
+  // ---- the threshold among pages [first, n - last): `want` of those with score `cut`, and all above it ----
+  const int from = a.first, to = n - a.last;
+  int want = k - a.first - a.last;
+  float cut = INFINITY, base = 0.f, per = 0.f;   // the round before: bins of (score - base) * per
+  float lo = -INFINITY, hi = INFINITY;
+  int bin = 0, turn = 0;
+  auto bin_of = [](float s, float base, float per) { return min((int)((s - base) * per), BINS - 1); };
+  for (; want > 0; turn ^= 1) {
+    uint32_t least = 0xFFFFFFFFu, most = 0u;
+    for (int p = from + threadIdx.x; p < to; p += CHOOSE_THREADS) {
+      const float s = scores[p];
+      if (s >= lo && s <= hi && bin_of(s, base, per) == bin) {
+        least = min(least, key_of(s));
+        most = max(most, key_of(s));
       }
     }
-  };
-  uint32_t cut = 0;                              // the largest value that at least k keys reach
-  for (int bit = 30, turn = 0; bit >= 0; bit -= 2, turn ^= 1) {
-    const uint32_t one = 1u << bit;
-    int c1, c2, c3;
-    count3(cut + one, cut + 2 * one, cut + 3 * one, c1, c2, c3);
-    c1 = __reduce_add_sync(0xFFFFFFFFu, c1);
-    c2 = __reduce_add_sync(0xFFFFFFFFu, c2);
-    c3 = __reduce_add_sync(0xFFFFFFFFu, c3);
+    least = __reduce_min_sync(0xFFFFFFFFu, least);
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
     if (lane == 0) {
-      counts[turn][warp][0] = c1;
-      counts[turn][warp][1] = c2;
-      counts[turn][warp][2] = c3;
+      ends[0][warp] = least;
+      ends[1][warp] = most;
+    }
+    bins[turn][threadIdx.x] = 0;               // last read two rounds ago
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < CHOOSE_WARPS; ++w) {
+      least = min(least, ends[0][w]);
+      most = max(most, ends[1][w]);
+    }
+    lo = of_key(least);
+    hi = of_key(most);
+    if (least == most) {
+      cut = lo;
+      break;
+    }
+    base = lo;
+    per = (float)(BINS - 1) / (hi - lo);
+    for (int p = from + threadIdx.x; p < to; p += CHOOSE_THREADS) {
+      const float s = scores[p];
+      if (s >= lo && s <= hi) atomicAdd(&bins[turn][bin_of(s, base, per)], 1);
     }
     __syncthreads();
-    c1 = c2 = c3 = 0;
+    // the bin of the want-th largest: every warp on its own, a lane with 8 bins, lane 0 the uppermost
+    int c[8], mine = 0;
 #pragma unroll
-    for (int w = 0; w < SELECT_WARPS; ++w) {
-      c1 += counts[turn][w][0];
-      c2 += counts[turn][w][1];
-      c3 += counts[turn][w][2];
+    for (int i = 0; i < 8; ++i) {
+      c[i] = bins[turn][BINS - 1 - (lane * 8 + i)];
+      mine += c[i];
     }
-    cut += c3 >= k ? 3 * one : c2 >= k ? 2 * one : c1 >= k ? one : 0u;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int who = __ffs(__ballot_sync(0xFFFFFFFFu, upto >= want)) - 1;
+    int above = upto - mine, which = 0;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!found) {
+        if (above + c[i] >= want) {
+          which = BINS - 1 - (lane * 8 + i);
+          found = true;
+        } else {
+          above += c[i];
+        }
+      }
+    bin = __shfl_sync(0xFFFFFFFFu, which, who);
+    want -= __shfl_sync(0xFFFFFFFFu, above, who);
   }
-  // ---- those above the cut, and the lowest of those at it ----
-  int above = 0, equal = 0;
-  auto each = [&](auto f) {
-    if (fits) {
-#pragma unroll
-      for (int j = 0; j < HELD; ++j)
-        if (p0 + j < p1) f(p0 + j, held[j]);
-    } else {
-      for (int p = p0; p < p1; ++p) f(p, key_at(p));
-    }
-  };
-  each([&](int, uint32_t y) {
-    above += y > cut;
-    equal += y == cut;
-  });
-  int all_above, all;
-  const int above_before = block_scan(above, scan[0], all_above);
-  const int equal_before = block_scan(equal, scan[1], all);
-  const int want = k - all_above;                // of those at the cut
-  int at = above_before + min(equal_before, want), ties = equal_before;
-  each([&](int p, uint32_t y) {
-    if (y > cut || (y == cut && ties < want)) put(at++, p);
-    ties += y == cut;
-  });
+
+  // ---- the list ----
+  const int run = (n + CHOOSE_THREADS - 1) / CHOOSE_THREADS, p0 = min((int)threadIdx.x * run, n), p1 = min(p0 + run, n);
+  auto taken = [&](int p) { return p < from || p >= to || scores[p] > cut; };
+  int at = 0, ties = 0;
+  for (int p = p0; p < p1; ++p) {
+    if (taken(p)) ++at;
+    else ties += scores[p] == cut;
+  }
+  int all;
+  block_scan(at, ties, sums, all);
+  at += min(ties, want);
+  for (int p = p0; p < p1; ++p) {
+    const bool t1 = taken(p), tie = !t1 && scores[p] == cut;
+    if (t1 || (tie && ties < want)) put(at++, p);
+    ties += tie;
+  }
 }
 
 }  // namespace
@@ -363,17 +401,21 @@ cudaError_t launch_cache_bounds(const BoundsArgs& a, int format, int D, cudaStre
   return launch_early(k, grid, BOUNDS_THREADS, 0, st, 1, a, per_seq);
 }
 
+size_t cache_select_scores_bytes(int rows, int max_pages, int top) {
+  return max_pages > top && max_pages > HELD_PAGES ? (size_t)rows * max_pages * 4 : 0;
+}
+
 cudaError_t launch_cache_select(const SelectArgs& a, int D, int dtype, cudaStream_t st) {
-  const unsigned rows = (unsigned)a.B * a.T * a.Hkv;
-  const int cols = a.top < a.pt.max_pages ? a.top : a.pt.max_pages;
-  if (a.pt.max_pages > a.top) {
-    const int tiles = (a.pt.max_pages + SCORE_PAGES - 1) / SCORE_PAGES;
-    const auto k = D == 128 ? (dtype ? cache_score_kernel<128, 1> : cache_score_kernel<128, 0>)
-                            : (dtype ? cache_score_kernel<64, 1> : cache_score_kernel<64, 0>);
-    const cudaError_t e = launch_early(k, rows * tiles, SCORE_THREADS, 0, st, 1, a, tiles);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_early(cache_select_kernel, rows, SELECT_THREADS, 0, st, 1, a, cols);
+  const int rows = a.B * a.T * a.Hkv, cols = a.top < a.pt.max_pages ? a.top : a.pt.max_pages;
+  const bool scored = a.pt.max_pages > a.top;
+  // blocks of a row's cluster: while they all run at once (two to an SM) and each has CLUSTER_PAGES pages
+  constexpr int CLUSTER_PAGES = 64, SMS = 152;
+  int cs = 1;
+  while (scored && cs < 8 && (long long)rows * cs * 2 <= 2 * SMS && a.pt.max_pages >= cs * 2 * CLUSTER_PAGES) cs *= 2;
+  const size_t smem = scored && a.pt.max_pages <= HELD_PAGES ? (size_t)a.pt.max_pages * 4 : 0;
+  const auto k = D == 128 ? (dtype ? cache_choose_kernel<128, 1> : cache_choose_kernel<128, 0>)
+                          : (dtype ? cache_choose_kernel<64, 1> : cache_choose_kernel<64, 0>);
+  return launch_early(k, (unsigned)(rows * cs), CHOOSE_THREADS, smem, st, cs, a, cols, cs);
 }
 
 }  // namespace bsc

@@ -157,9 +157,11 @@ def repeated(ops, entries, page, Hkv, D, fmt, distinct, seed, tail=0):
 
 
 @pytest.mark.parametrize("entries,top,first,last", [(257, 64, 0, 1), (1000, 200, 1, 2), (4096, 33, 1, 1), (4097, 33, 1, 1),
-                                                    (9000, 700, 2, 4)])
+                                                    (9000, 700, 2, 4), (10240, 50, 1, 1), (10241, 50, 1, 1),
+                                                    (12000, 300, 0, 300)])
 def test_ties_and_long_tables(ops, entries, top, first, last):
-    """Tables past what a block holds in registers (4096 pages), equal scores in the pages' order."""
+    """Tables up to and past what a block holds of scores (10240 pages), equal scores in the pages' order; a choice of which
+    nothing is left to the scores."""
     f, b = repeated(ops, entries, 16, 2, 64, 1, 9, 11, tail=5)
     q = make_q(3, 1, 1, 4, 64, "bf16", 0)
     out = ops.mx_cache_sparse_attn(q, f.cache, b, f.table, f.seq, top, first, last)
