@@ -536,7 +536,7 @@ class MxCache:
     The calls' `stream` works like torch.cuda.stream(stream) around them: the caller sees to it that what other
     streams wrote is ready, and that the tensors live until the call has run."""
 
-    __slots__ = ("k", "k_sc", "v", "v_sc", "fmt", "num_pages", "page_size", "Hkv", "D", "device", "params", "packed")
+    __slots__ = ("k", "k_sc", "v", "v_sc", "fmt", "num_pages", "page_size", "Hkv", "D", "device", "index", "params", "packed")
 
     def __init__(self, k, k_sc, v, v_sc, fmt=CACHE_MXFP4):
         if fmt not in (CACHE_MXFP8, CACHE_MXFP4):
@@ -553,7 +553,7 @@ class MxCache:
             raise ValueError("k, v must be [pages, Hkv, page_size, row] and k_sc, v_sc [pages, Hkv, page_size, D/32]")
         self.k, self.k_sc, self.v, self.v_sc = pools
         self.fmt, self.num_pages, self.page_size, self.Hkv, self.D = fmt, pages, page_size, Hkv, D
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self.params = CachePools(*(t.data_ptr() for t in pools), *(t.stride(0) for t in pools), fmt, pages, page_size,
                                  Hkv, D)
         self.packed = bytes(self.params)
@@ -567,18 +567,19 @@ def mx_cache_alloc(num_pages, page_size, Hkv, D=128, fmt=CACHE_MXFP4, device="cu
     return MxCache(k, k_sc, v, v_sc, fmt)
 
 
-def _act_dims(x, layout, cache, name):
-    """(B, T, H), element strides (b, t, h) and the dtype code of an activation of `cache`'s head size (and device)."""
-    code = _ACT.get(x.dtype)
-    if code is None or x.dim() != 4 or x.device != cache.device:
+def _act_dims(x, layout, cache, name, D=None):
+    """(B, T, H), element strides (b, t, h) and the dtype code of an activation of head size D (None: the cache's) on the
+    device of `cache` (or of a Rope)."""
+    code, shape = _ACT.get(x.dtype), x.shape
+    if code is None or len(shape) != 4 or x.get_device() != cache.index:
         raise ValueError("%s must be a 4-D bfloat16 or float16 tensor on the cache's device" % name)
-    B, T, H, D = x.shape
+    B, T, H, width = shape
     sb, st, sh, sd = x.stride()
     if layout == SBHD:
         B, T, sb, st = T, B, st, sb
     elif layout != BSHD:
         raise ValueError("layout must be BSHD or SBHD")
-    if D != cache.D:
+    if width != (cache.D if D is None else D):
         raise ValueError("%s does not have the cache's head size" % name)
     if sd != 1 and x.numel():
         raise ValueError("%s must be contiguous along D" % name)
@@ -594,42 +595,69 @@ def _dense(layout, B, T, H, D):
     raise ValueError("layout must be BSHD or SBHD")
 
 
+def _out_like(x, out, dims, layout, cache, name, dtype, D=None):
+    """An output of the shape and dtype of activation x (dims, dtype code): `out` if given, else a new contiguous one; and its
+    element strides (b, t, h)."""
+    if out is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format), _dense(layout, *dims, x.shape[3])[1]
+    dims_o, strides, dtype_o = _act_dims(out, layout, cache, name, D)
+    if dims_o != dims or dtype_o != dtype:
+        raise ValueError("%s must have its input's shape and dtype" % name)
+    return out, strides
+
+
 def _index(t, B, cache, name):
     """Pointer of an int32 index array of B entries (None: NULL)."""
     if t is None:
         return 0
-    if t.dtype is not torch.int32 or t.shape != (B,) or t.device != cache.device:
+    if t.dtype is not torch.int32 or t.shape != (B,) or t.get_device() != cache.index:
         raise ValueError("%s must be an int32 tensor of shape (%d,) on the cache's device" % (name, B))
-    if B > 1 and t.stride(0) != 1:
+    if B > 1 and not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
 
 
 def _table(t, B, cache):
     """Pointer, row stride and columns of a page table of B rows."""
-    if t.dim() != 2 or t.shape[0] != B or t.dtype is not torch.int32 or t.device != cache.device:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != B or t.dtype is not torch.int32 or t.get_device() != cache.index:
         raise ValueError("page_table must be an int32 tensor [B, max_pages] on the cache's device")
     row, col = t.stride()
-    if col != 1 and t.shape[1] > 1:
+    if col != 1 and shape[1] > 1:
         raise ValueError("page_table must have contiguous rows")
-    return t.data_ptr(), row, t.shape[1]
+    return t.data_ptr(), row, shape[1]
 
 
 def _status(t, cache):
-    if t is not None and (t.dtype != torch.int32 or t.device != cache.device or t.numel() < 1):
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or t.device != cache.device or t.numel() < 1:
         raise ValueError("dev_status must be an int32 tensor on the cache's device")
-    return 0 if t is None else t.data_ptr()
+    return t.data_ptr()
 
 
 def _elsewhere(cache, stream):
     """The context a call has to enter before it allocates and launches: None where the current device is the
     cache's and no stream is given; else the stream's (memory allocated inside belongs to the stream that
     uses it) or the device's."""
+    if stream is None and _current_device() == cache.index:
+        return None
     if stream is not None:
         if stream.device != cache.device:
             raise ValueError("stream must be on the cache's device")
         return torch.cuda.stream(stream)
-    return None if _current_device() == cache.device.index else torch.cuda.device(cache.device)
+    return torch.cuda.device(cache.device)
+
+
+def _elsewhere_of(x, name, stream):
+    """_elsewhere for a call whose device is that of tensor x."""
+    if not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if stream is not None:
+        if stream.device != x.device:
+            raise ValueError("stream must be on %s's device" % name)
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(x.device)
 
 
 # The current stream's handle without a Stream object around it (a call's largest host cost after the launches).
@@ -671,7 +699,7 @@ def mx_cache_write(cache, k, v, page_table, seq_lens, new_lens=None, layout=BSHD
     p = cache.packed + _pack_write(k.data_ptr(), v.data_ptr(), *ks, *vs, B, T, dt, rule,
                          *_table(page_table, B, cache), _index(seq_lens, B, cache, "seq_lens"),
                          _index(new_lens, B, cache, "new_lens"), _status(dev_status, cache))
-    _check(_c_write(p, _raw_stream(cache.device.index)))
+    _check(_c_write(p, _raw_stream(cache.index)))
 
 
 def mx_cache_read(cache, page_table, seq_lens, T, starts=None, layout=BSHD, dtype=torch.bfloat16, k_out=None,
@@ -703,7 +731,7 @@ def mx_cache_read(cache, page_table, seq_lens, T, starts=None, layout=BSHD, dtyp
     p = cache.packed + _pack_read(k_out.data_ptr(), v_out.data_ptr(), *ks, *vs, B, T, dt,
                         *_table(page_table, B, cache), _index(seq_lens, B, cache, "seq_lens"),
                         _index(starts, B, cache, "starts"), _status(dev_status, cache))
-    _check(_c_read(p, _raw_stream(cache.device.index)))
+    _check(_c_read(p, _raw_stream(cache.index)))
     return k_out, v_out
 
 
@@ -730,13 +758,7 @@ def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, so
     B, T, Hq = dims
     table = _table(page_table, B, cache)
     device = cache.device
-    if o is None:
-        _, o_s = _dense(layout, B, T, Hq, cache.D)
-        o = torch.empty_like(q, memory_format=torch.contiguous_format)
-    else:
-        dims_o, o_s, dt_o = _act_dims(o, layout, cache, "o")
-        if dims_o != dims or dt_o != dt:
-            raise ValueError("o must have q's shape and dtype")
+    o, o_s = _out_like(q, o, dims, layout, cache, "o", dt)
     if lse is None:
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=device)
     elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T) or lse.device != device or \
@@ -754,7 +776,7 @@ def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, so
                         cache.D ** -0.5 if softmax_scale is None else softmax_scale, *table, _index(seq_lens, B, cache, "seq_lens"),
                         _index(new_lens, B, cache, "new_lens"), _status(dev_status, cache),
                         workspace.data_ptr() if need else 0, need)
-    _check(_c_attn(p, _raw_stream(device.index)))
+    _check(_c_attn(p, _raw_stream(cache.index)))
     return o, lse
 
 
@@ -767,12 +789,12 @@ _c_rope, _pack_rope = _packed_call("rope", RopeParams, "4q12q3q7i0q", _ANGLES)
 _c_rope_quant, _pack_rope_quant = _packed_call("mxfp8_rope_quantize_qk", RopeQuantParams, "2q6q4q3q8i", _ANGLES)
 _c_write_rope, _pack_write_rope = _packed_call("mx_cache_write_rope", CacheWriteRopeParams, "4q12q5i2qi3q",
                                                ctypes.sizeof(CachePools) + _ANGLES)
-_c_bounds, _pack_bounds = _packed_call("mx_cache_bounds", CacheBoundsParams, "2q2i2qi3q")
-_c_sparse, _pack_sparse = _packed_call("mx_cache_sparse_attn", CacheSparseAttnParams, "12q4if3i2qi5q")
+_c_bounds, _pack_bounds = _packed_call("mx_cache_bounds", CacheBoundsParams, "2i2qi3q", ctypes.sizeof(CachePools) + 16)
+_c_sparse, _pack_sparse = _packed_call("mx_cache_sparse_attn", CacheSparseAttnParams, "10q4if3i2qi5q", ctypes.sizeof(CachePools) + 16)
 
 
-def _same_rows(x, t, name, dtype=None):
-    if t.shape != x.shape or t.dtype != (dtype or x.dtype) or t.device != x.device:
+def _same_rows(x, t, name):
+    if t.shape != x.shape or t.dtype is not x.dtype or t.get_device() != x.get_device():
         raise ValueError("%s must have the first tensor's shape, device and dtype" % name)
 
 
@@ -780,13 +802,15 @@ def _row_layout(tensors):
     """(rows, inner, [(stride, inner stride)]) of tensors [..., N] of one shape (None: (0, 0)): one split of the leading
     dimensions into two groups, within each of which every tensor's rows are evenly spaced."""
     first = tensors[0]
-    lead = first.shape[:-1]
+    lead, N = first.shape[:-1], first.shape[-1]
     rows = 1
     for n in lead:
         rows *= n
-    if all(t is None or t.is_contiguous() for t in tensors):
-        pair = (first.shape[-1], 0)
-        return rows, 1, [pair if t is not None else (0, 0) for t in tensors]
+    if all([t is None or t.is_contiguous() for t in tensors]):
+        return rows, 1, [(0, 0) if t is None else (N, 0) for t in tensors]
+    for t in tensors:
+        if t is not None and t.stride(-1) != 1 and N > 1 and t.numel():
+            raise ValueError("rows must be contiguous")
 
     def even(t, dims):
         """Stride of rows numbered over `dims`, or None."""
@@ -815,25 +839,16 @@ def _row_layout(tensors):
     raise ValueError("the rows of every tensor must be spaced by at most two strides")
 
 
-def _on_cuda(x, name):
-    if not x.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-
-
-def _norm_args(x, weight):
-    dt, wt = _ACT.get(x.dtype), _WEIGHT.get(weight.dtype)
-    if dt is None or x.dim() < 1:
-        raise ValueError("expected a bfloat16 or float16 tensor [..., N]")
-    N = x.shape[-1]
-    if weight.shape != (N,) or weight.device != x.device or not weight.is_contiguous() or \
-            weight.dtype not in (x.dtype, torch.float32):
+def _weight_code(weight, x, N):
+    if weight.shape != (N,) or weight.get_device() != x.get_device() or not weight.is_contiguous() or \
+            (weight.dtype is not x.dtype and weight.dtype is not torch.float32):
         raise ValueError("weight must be a contiguous [N] tensor of the activations' dtype or float32")
-    return dt, wt, N
+    return _WEIGHT[weight.dtype]
 
 
-def _d_contiguous(t, name):
-    if t is not None and t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
-        raise ValueError("%s must be contiguous along its last dimension" % name)
+def _rstd_of(rstd, lead, x):
+    if rstd.shape != lead or rstd.dtype is not torch.float32 or rstd.get_device() != x.get_device() or not rstd.is_contiguous():
+        raise ValueError("rstd must be a contiguous float32 tensor of the activations' leading dimensions")
 
 
 def rms_norm(x, weight, eps=1e-6, residual=None, y=None, sum_out=None, rstd=None, y8_out=False, y_out=True, y8=None,
@@ -844,47 +859,58 @@ def rms_norm(x, weight, eps=1e-6, residual=None, y=None, sum_out=None, rstd=None
     x itself without a residual and rstd float32 [...]; with y8_out=True, (y or None, s, rstd, y as E4M3 bytes [..., N], its
     scales [..., N/32]).  weight: [N], x's dtype or float32.  y, sum_out and rstd may be given; y and sum_out may be x or
     residual themselves."""
-    _on_cuda(x, "x")
-    there = _elsewhere(x, stream)
-    if there is not None:
-        with there:
+    if stream is not None or not x.is_cuda or _current_device() != x.get_device():
+        with _elsewhere_of(x, "x", stream):
             return rms_norm(x, weight, eps, residual, y, sum_out, rstd, y8_out, y_out, y8, y_sc, rule)
-    dt, wt, N = _norm_args(x, weight)
-    if residual is not None:
-        _same_rows(x, residual, "residual")
-    if not y_out:
-        if not y8_out:
-            raise ValueError("y_out=False needs y8_out=True")
-        y = None
-    elif y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    dt, shape = _ACT.get(x.dtype), x.shape
+    if dt is None or not shape:
+        raise ValueError("x must be a bfloat16 or float16 tensor [..., N]")
+    N, lead = shape[-1], shape[:-1]
+    wt = _weight_code(weight, x, N)
+    fresh = x.is_contiguous()                  # an output that is allocated here is laid out like x
+    if y_out:
+        if y is None:
+            y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        else:
+            _same_rows(x, y, "y")
+            fresh = False
+        y_ptr = y.data_ptr()
+    elif y8_out:
+        y, y_ptr = None, 0
     else:
-        _same_rows(x, y, "y")
+        raise ValueError("y_out=False needs y8_out=True")
     if residual is None:
         if sum_out is not None:
             raise ValueError("sum_out is for a residual")
-    elif sum_out is None:
-        sum_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        r_ptr = s_ptr = 0
     else:
-        _same_rows(x, sum_out, "sum_out")
+        _same_rows(x, residual, "residual")
+        fresh = fresh and residual.is_contiguous()
+        if sum_out is None:
+            sum_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        else:
+            _same_rows(x, sum_out, "sum_out")
+            fresh = False
+        r_ptr, s_ptr = residual.data_ptr(), sum_out.data_ptr()
     if rstd is None:
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    elif rstd.shape != x.shape[:-1] or rstd.dtype != torch.float32 or rstd.device != x.device or not rstd.is_contiguous():
-        raise ValueError("rstd must be a contiguous float32 tensor of x's leading dimensions")
+        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
+    else:
+        _rstd_of(rstd, lead, x)
+    y8_ptr = sc_ptr = 0
     if y8_out:
-        shapes = (x.shape, x.shape[:-1] + (N // 32,))
+        shapes = (shape, lead + (N // 32,))
         y8, y_sc = (torch.empty(n, dtype=torch.uint8, device=x.device) if t is None else t for t, n in zip((y8, y_sc), shapes))
         for t, n in ((y8, shapes[0]), (y_sc, shapes[1])):
             if t.dtype != torch.uint8 or t.shape != n or t.device != x.device or not t.is_contiguous():
                 raise ValueError("y8 and y_sc must be contiguous uint8 tensors [..., N] and [..., N/32]")
-    for t, n in ((x, "x"), (residual, "residual"), (y, "y"), (sum_out, "sum_out")):
-        _d_contiguous(t, n)
-    rows, inner, (xs, rs, ys, ss) = _row_layout((x, residual, y, sum_out))
-    p = _pack_norm(x.data_ptr(), 0 if residual is None else residual.data_ptr(), weight.data_ptr(),
-                   0 if y is None else y.data_ptr(), 0 if sum_out is None else sum_out.data_ptr(), rstd.data_ptr(),
-                   y8.data_ptr() if y8_out else 0, y_sc.data_ptr() if y8_out else 0, rows, *xs, *rs, *ys, *ss, inner, N, dt,
-                   wt, rule, eps)
-    _check(_c_norm(p, _raw_stream(x.device.index)))
+        y8_ptr, sc_ptr = y8.data_ptr(), y_sc.data_ptr()
+    if fresh:
+        rows, inner, xs, rs, ys, ss = x.numel() // max(N, 1), 1, (N, 0), (N, 0), (N, 0), (N, 0)
+    else:
+        rows, inner, (xs, rs, ys, ss) = _row_layout((x, residual, y, sum_out))
+    p = _pack_norm(x.data_ptr(), r_ptr, weight.data_ptr(), y_ptr, s_ptr, rstd.data_ptr(), y8_ptr, sc_ptr, rows, *xs, *rs, *ys,
+                   *ss, inner, N, dt, wt, rule, eps)
+    _check(_c_norm(p, _raw_stream(x.get_device())))
     s = x if residual is None else sum_out
     return (y, s, rstd, y8, y_sc) if y8_out else (y, s, rstd)
 
@@ -899,24 +925,23 @@ def rms_norm_bwd(dy, s, weight, rstd, ds=None, dx=None, dweight=None, workspace=
     residual alike, with `ds`, the gradient that reaches s by the residual stream, added; dweight has weight's dtype.
     dx may be dy, s or ds themselves.  `workspace`: a device tensor of rms_norm_bwd_workspace_bytes(rows, N) bytes that no
     other running call uses, else one is allocated here."""
-    _on_cuda(s, "s")
-    there = _elsewhere(s, stream)
-    if there is not None:
-        with there:
+    if stream is not None or not s.is_cuda or _current_device() != s.get_device():
+        with _elsewhere_of(s, "s", stream):
             return rms_norm_bwd(dy, s, weight, rstd, ds, dx, dweight, workspace)
-    dt, wt, N = _norm_args(s, weight)
+    dt, shape = _ACT.get(s.dtype), s.shape
+    if dt is None or not shape:
+        raise ValueError("s must be a bfloat16 or float16 tensor [..., N]")
+    N = shape[-1]
+    wt = _weight_code(weight, s, N)
     _same_rows(s, dy, "dy")
     if ds is not None:
         _same_rows(s, ds, "ds")
-    if rstd.shape != s.shape[:-1] or rstd.dtype != torch.float32 or rstd.device != s.device or not rstd.is_contiguous():
-        raise ValueError("rstd must be a contiguous float32 tensor of s's leading dimensions")
+    _rstd_of(rstd, shape[:-1], s)
     if dx is None:
         dx = torch.empty_like(s, memory_format=torch.contiguous_format)
     else:
         _same_rows(s, dx, "dx")
     rows, inner, (dys, ss, dss, dxs) = _row_layout((dy, s, ds, dx))
-    for t, n in ((dy, "dy"), (s, "s"), (ds, "ds"), (dx, "dx")):
-        _d_contiguous(t, n)
     if dweight is None:
         dweight = torch.empty_like(weight) if rows else torch.zeros_like(weight)
     elif dweight.shape != weight.shape or dweight.dtype != weight.dtype or dweight.device != s.device or \
@@ -932,7 +957,7 @@ def rms_norm_bwd(dy, s, weight, rstd, ds=None, dx=None, dweight=None, workspace=
     p = _pack_norm_bwd(dy.data_ptr(), s.data_ptr(), weight.data_ptr(), rstd.data_ptr(), 0 if ds is None else ds.data_ptr(),
                        dx.data_ptr(), dweight.data_ptr(), rows, *dys, *ss, *dss, *dxs, inner, N, dt, wt, workspace.data_ptr(),
                        need)
-    _check(_c_norm_bwd(p, _raw_stream(s.device.index)))
+    _check(_c_norm_bwd(p, _raw_stream(s.get_device())))
     return dx, dweight
 
 
@@ -940,10 +965,8 @@ def mxfp8_dequantize(x, sc, layout=BSHD, dtype=torch.bfloat16, out=None, stream=
     """MXFP8 rows back to values: x uint8 [B, S, H, D] (SBHD: [S, B, H, D]) with sc [B, H, S, D/32], as the rowwise
     quantisers return them, or [..., N] with sc [..., N/32], as rms_norm does (x not 4-D, or 4-D with such scales and
     layout=None)."""
-    _on_cuda(x, "x")
-    there = _elsewhere(x, stream)
-    if there is not None:
-        with there:
+    if stream is not None or not x.is_cuda or _current_device() != x.get_device():
+        with _elsewhere_of(x, "x", stream):
             return mxfp8_dequantize(x, sc, layout, dtype, out)
     code = _ACT.get(dtype)
     if code is None:
@@ -968,7 +991,7 @@ def mxfp8_dequantize(x, sc, layout=BSHD, dtype=torch.bfloat16, out=None, stream=
     elif out.shape != x.shape or out.dtype != dtype or out.device != x.device or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor shaped like x, of dtype")
     _check(lib.mxfp8_dequantize(x.data_ptr(), sc.data_ptr(), B, S, H, D, layout, code, out.data_ptr(),
-                                _raw_stream(x.device.index)))
+                                _raw_stream(x.get_device())))
     return out
 
 
@@ -981,7 +1004,7 @@ class Rope:
     original_length tokens are interpolated by factor, those of more than high_turns are kept, what lies between is mixed).
     magnitude: the factor on what is rotated (None: 0.1 ln(factor) + 1 by parts, else 1)."""
 
-    __slots__ = ("rot", "interleaved", "magnitude", "turns", "device", "params", "packed")
+    __slots__ = ("rot", "interleaved", "magnitude", "turns", "device", "index", "params", "packed")
 
     def __init__(self, rot, base=10000.0, interleaved=False, scaling=ROPE_PLAIN, factor=1.0, original_length=0,
                  low_turns=1.0, high_turns=32.0, magnitude=None, device="cuda"):
@@ -992,7 +1015,7 @@ class Rope:
         self.turns = torch.tensor(list(signed), dtype=torch.int64).to(device)
         self.rot, self.interleaved = rot, bool(interleaved)
         self.magnitude = m.value if magnitude is None else float(magnitude)
-        self.device = self.turns.device
+        self.device, self.index = self.turns.device, self.turns.get_device()
         self.params = RopeAngles(self.turns.data_ptr(), self.magnitude, rot, int(self.interleaved))
         self.packed = bytes(self.params)
 
@@ -1001,26 +1024,22 @@ def _positions(t, B, T, rope):
     """Pointer and strides (b, t) of positions: None, [B] (of the first tokens) or [B, T] int32."""
     if t is None:
         return 0, 0, 0
-    if t.dtype is not torch.int32 or t.device != rope.device or t.shape not in ((B,), (B, T)):
+    shape = t.shape
+    if t.dtype is not torch.int32 or t.get_device() != rope.index or (shape != (B, T) and shape != (B,)):
         raise ValueError("positions must be an int32 tensor of shape (%d,) or (%d, %d) on rope's device" % (B, B, T))
-    if t.dim() == 1:
-        return t.data_ptr(), t.stride(0), 0
-    if T > 1 and t.stride(1) == 0:
+    stride = t.stride()
+    if len(shape) == 1:
+        return t.data_ptr(), stride[0], 0
+    if T > 1 and stride[1] == 0:
         raise ValueError("positions must not be expanded along the tokens")
-    return t.data_ptr(), t.stride(0), t.stride(1) or 1
+    return t.data_ptr(), stride[0], stride[1] or 1
 
 
-class _Heads:
-    """A head size and a device, for _act_dims."""
-    __slots__ = ("D", "device")
-
-    def __init__(self, x):
-        self.D, self.device = x.shape[-1] if x.dim() else 0, x.device
-
-
-def _on_device(x, rope):
-    if not x.is_cuda or x.device != rope.device:
-        raise ValueError("q must be on rope's device")
+def _elsewhere_with(rope, q, stream):
+    """_elsewhere for a call on q by a Rope."""
+    if q.get_device() != rope.index or not q.is_cuda:
+        raise ValueError("q must be on rope's device, a CUDA device")
+    return None if stream is None and _current_device() == rope.index else _elsewhere(rope, stream)
 
 
 def apply_rope(q, k, rope, positions=None, layout=BSHD, inverse=False, q_out=None, k_out=None, stream=None):
@@ -1029,40 +1048,28 @@ def apply_rope(q, k, rope, positions=None, layout=BSHD, inverse=False, q_out=Non
     q [B, T, Hq, D] and k [B, T, Hkv, D] (SBHD: [T, B, H, D]), bf16 or fp16, any strides with D contiguous.  positions: None
     (token t is at t), int32 [B] (of each sequence's first token) or [B, T].  inverse=True turns back: gradients of q and k
     from those of the outputs.  q_out and k_out may be q and k themselves."""
-    _on_device(q, rope)
-    there = _elsewhere(q, stream)
+    there = _elsewhere_with(rope, q, stream)
     if there is not None:
         with there:
             return apply_rope(q, k, rope, positions, layout, inverse, q_out, k_out)
-    like = _Heads(q)
-    dims, qs, dt = _act_dims(q, layout, like, "q")
+    D = q.shape[-1]
+    dims, qs, dt = _act_dims(q, layout, rope, "q", D)
     B, T, Hq = dims
-    D, Hkv, ks, k_os = like.D, 0, (0, 0, 0), (0, 0, 0)
-    if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _, q_os = _dense(layout, B, T, Hq, D)
-    else:
-        dims_o, q_os, dt_o = _act_dims(q_out, layout, like, "q_out")
-        if dims_o != dims or dt_o != dt:
-            raise ValueError("q_out must have q's shape and dtype")
+    q_out, q_os = _out_like(q, q_out, dims, layout, rope, "q_out", dt, D)
     if k is None:
         if k_out is not None:
             raise ValueError("k_out is for k")
+        Hkv, ks, k_os, k_ptr, k_out_ptr = 0, (0, 0, 0), (0, 0, 0), 0, 0
     else:
-        (Bk, Tk, Hkv), ks, dt_k = _act_dims(k, layout, like, "k")
-        if (Bk, Tk) != (B, T) or dt_k != dt:
+        dims_k, ks, dt_k = _act_dims(k, layout, rope, "k", D)
+        Bk, Tk, Hkv = dims_k
+        if Bk != B or Tk != T or dt_k != dt:
             raise ValueError("k must have q's batch, tokens and dtype")
-        if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-            _, k_os = _dense(layout, B, T, Hkv, D)
-        else:
-            dims_o, k_os, dt_o = _act_dims(k_out, layout, like, "k_out")
-            if dims_o != (B, T, Hkv) or dt_o != dt:
-                raise ValueError("k_out must have k's shape and dtype")
-    p = rope.packed + _pack_rope(q.data_ptr(), 0 if k is None else k.data_ptr(), q_out.data_ptr(),
-                                 0 if k is None else k_out.data_ptr(), *qs, *ks, *q_os, *k_os, *_positions(positions, B, T, rope),
-                                 B, T, Hq, Hkv, D, dt, int(bool(inverse)))
-    _check(_c_rope(p, _raw_stream(q.device.index)))
+        k_out, k_os = _out_like(k, k_out, dims_k, layout, rope, "k_out", dt, D)
+        k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
+    p = rope.packed + _pack_rope(q.data_ptr(), k_ptr, q_out.data_ptr(), k_out_ptr, *qs, *ks, *q_os, *k_os,
+                                 *_positions(positions, B, T, rope), B, T, Hq, Hkv, D, dt, 1 if inverse else 0)
+    _check(_c_rope(p, _raw_stream(rope.index)))
     return q_out, k_out
 
 
@@ -1072,23 +1079,21 @@ rope = apply_rope      # the C call's name; `rope` is also what the calls name t
 def mxfp8_rope_quantize_qk(q, k, rope, positions=None, layout=BSHD, rule=SCALE_FLOOR, stream=None):
     """Q and K rotated (as in `rope`) and quantised rowwise to MXFP8 in one launch, from the rotated fp32 values:
     (q_e4m3, q_sc, k_e4m3, k_sc), bytes dense in `layout` and scales [B, H, T, D/32]; D = 128."""
-    _on_device(q, rope)
-    there = _elsewhere(q, stream)
+    there = _elsewhere_with(rope, q, stream)
     if there is not None:
         with there:
             return mxfp8_rope_quantize_qk(q, k, rope, positions, layout, rule)
-    like = _Heads(q)
-    (B, T, Hq), qs, dt = _act_dims(q, layout, like, "q")
-    (Bk, Tk, Hkv), ks, dt_k = _act_dims(k, layout, like, "k")
-    if (Bk, Tk) != (B, T) or dt_k != dt:
+    D = q.shape[-1]
+    (B, T, Hq), qs, dt = _act_dims(q, layout, rope, "q", D)
+    (Bk, Tk, Hkv), ks, dt_k = _act_dims(k, layout, rope, "k", D)
+    if Bk != B or Tk != T or dt_k != dt:
         raise ValueError("k must have q's batch, tokens and dtype")
     u8 = dict(dtype=torch.uint8, device=q.device)
-    q8, q_sc = torch.empty(q.shape, **u8), torch.empty((B, Hq, T, like.D // 32), **u8)
-    k8, k_sc = torch.empty(k.shape, **u8), torch.empty((B, Hkv, T, like.D // 32), **u8)
+    q8, q_sc = torch.empty(q.shape, **u8), torch.empty((B, Hq, T, D // 32), **u8)
+    k8, k_sc = torch.empty(k.shape, **u8), torch.empty((B, Hkv, T, D // 32), **u8)
     p = rope.packed + _pack_rope_quant(q.data_ptr(), k.data_ptr(), *qs, *ks, q8.data_ptr(), q_sc.data_ptr(), k8.data_ptr(),
-                                       k_sc.data_ptr(), *_positions(positions, B, T, rope), B, T, Hq, Hkv, like.D, dt, layout,
-                                       rule)
-    _check(_c_rope_quant(p, _raw_stream(q.device.index)))
+                                       k_sc.data_ptr(), *_positions(positions, B, T, rope), B, T, Hq, Hkv, D, dt, layout, rule)
+    _check(_c_rope_quant(p, _raw_stream(rope.index)))
     return q8, q_sc, k8, k_sc
 
 
@@ -1101,25 +1106,20 @@ def mx_cache_write_rope(cache, q, k, v, rope, page_table, seq_lens, new_lens=Non
     if there is not None:
         with there:
             return mx_cache_write_rope(cache, q, k, v, rope, page_table, seq_lens, new_lens, layout, rule, q_out, dev_status)
-    _on_device(q, rope)
+    if rope.index != cache.index:
+        raise ValueError("rope must be on the cache's device")
     dims, qs, dt = _act_dims(q, layout, cache, "q")
     dims_k, ks, dt_k = _act_dims(k, layout, cache, "k")
     dims_v, vs, dt_v = _act_dims(v, layout, cache, "v")
     B, T, Hq = dims
     if dims_k != (B, T, cache.Hkv) or dims_v != dims_k or dt_k != dt or dt_v != dt:
         raise ValueError("k and v must have q's batch, tokens and dtype and the cache's heads")
-    if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _, q_os = _dense(layout, B, T, Hq, cache.D)
-    else:
-        dims_o, q_os, dt_o = _act_dims(q_out, layout, cache, "q_out")
-        if dims_o != dims or dt_o != dt:
-            raise ValueError("q_out must have q's shape and dtype")
+    q_out, q_os = _out_like(q, q_out, dims, layout, cache, "q_out", dt)
     p = cache.packed + rope.packed + _pack_write_rope(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), *qs, *ks, *vs, *q_os, B, T, Hq, dt, rule,
         *_table(page_table, B, cache), _index(seq_lens, B, cache, "seq_lens"), _index(new_lens, B, cache, "new_lens"),
         _status(dev_status, cache))
-    _check(_c_write_rope(p, _raw_stream(cache.device.index)))
+    _check(_c_write_rope(p, _raw_stream(cache.index)))
     return q_out
 
 
@@ -1128,14 +1128,15 @@ class MxBounds:
     """Bounds of a cache's pages: codes int8 [num_pages, Hkv, 2, D] (minima, maxima along D) and exps uint8 [num_pages, Hkv],
     the caller's two buffers (mx_cache_bounds_alloc makes new ones).  The handle holds no other state."""
 
-    __slots__ = ("codes", "exps")
+    __slots__ = ("codes", "exps", "of", "packed")
 
     def __init__(self, cache, codes, exps):
         shape = (cache.num_pages, cache.Hkv)
         for t, n, d, want in ((codes, "codes", torch.int8, shape + (2, cache.D)), (exps, "exps", torch.uint8, shape)):
             if t.dtype != d or tuple(t.shape) != want or t.device != cache.device or not t.is_contiguous():
                 raise ValueError("%s must be a contiguous %s tensor %s on the cache's device" % (n, d, want))
-        self.codes, self.exps = codes, exps
+        self.codes, self.exps, self.of = codes, exps, shape + (cache.D, cache.index)
+        self.packed = struct.pack("@2q", codes.data_ptr(), exps.data_ptr())
 
 
 def mx_cache_bounds_alloc(cache):
@@ -1146,9 +1147,9 @@ def mx_cache_bounds_alloc(cache):
 
 
 def _bounds_of(bounds, cache):
-    if bounds.codes.shape != (cache.num_pages, cache.Hkv, 2, cache.D) or bounds.codes.device != cache.device:
+    if bounds.of != (cache.num_pages, cache.Hkv, cache.D, cache.index):
         raise ValueError("bounds are not this cache's")
-    return bounds.codes.data_ptr(), bounds.exps.data_ptr()
+    return cache.packed + bounds.packed
 
 
 def mx_cache_bounds(cache, bounds, page_table, seq_lens, T, new_lens=None, dev_status=None, stream=None):
@@ -1159,10 +1160,10 @@ def mx_cache_bounds(cache, bounds, page_table, seq_lens, T, new_lens=None, dev_s
         with there:
             return mx_cache_bounds(cache, bounds, page_table, seq_lens, T, new_lens, dev_status)
     B = page_table.shape[0]
-    p = cache.packed + _pack_bounds(*_bounds_of(bounds, cache), B, T, *_table(page_table, B, cache),
+    p = _bounds_of(bounds, cache) + _pack_bounds(B, T, *_table(page_table, B, cache),
                                     _index(seq_lens, B, cache, "seq_lens"), _index(new_lens, B, cache, "new_lens"),
                                     _status(dev_status, cache))
-    _check(_c_bounds(p, _raw_stream(cache.device.index)))
+    _check(_c_bounds(p, _raw_stream(cache.index)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -1187,13 +1188,7 @@ def mx_cache_sparse_attn(q, cache, bounds, page_table, seq_lens, top, first=1, l
     B, T, Hq = dims
     table = _table(page_table, B, cache)
     device = cache.device
-    if o is None:
-        _, o_s = _dense(layout, B, T, Hq, cache.D)
-        o = torch.empty_like(q, memory_format=torch.contiguous_format)
-    else:
-        dims_o, o_s, dt_o = _act_dims(o, layout, cache, "o")
-        if dims_o != dims or dt_o != dt:
-            raise ValueError("o must have q's shape and dtype")
+    o, o_s = _out_like(q, o, dims, layout, cache, "o", dt)
     if lse is None:
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=device)
     elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T) or lse.device != device or not lse.is_contiguous():
@@ -1210,10 +1205,10 @@ def mx_cache_sparse_attn(q, cache, bounds, page_table, seq_lens, top, first=1, l
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
         need = workspace.numel() * workspace.element_size()
-    p = cache.packed + _pack_sparse(*_bounds_of(bounds, cache), q.data_ptr(), o.data_ptr(), lse.data_ptr(), blocks.data_ptr(),
+    p = _bounds_of(bounds, cache) + _pack_sparse(q.data_ptr(), o.data_ptr(), lse.data_ptr(), blocks.data_ptr(),
                                     *qs, *o_s, B, T, Hq, dt, cache.D ** -0.5 if softmax_scale is None else softmax_scale, top,
                                     first, last, *table, _index(seq_lens, B, cache, "seq_lens"),
                                     _index(new_lens, B, cache, "new_lens"), _status(dev_status, cache), workspace.data_ptr(),
                                     need)
-    _check(_c_sparse(p, _raw_stream(device.index)))
+    _check(_c_sparse(p, _raw_stream(cache.index)))
     return o, lse, blocks
