@@ -56,26 +56,37 @@ __global__ void __launch_bounds__(BOUNDS_THREADS) cache_bounds_kernel(const Boun
     lo[j] = INFINITY;
     hi[j] = -INFINITY;
   }
-#pragma unroll 4
-  for (int t = threadIdx.x / LPR; t < tokens; t += ROWS) {
-    uint32_t w[4];
-    if (FMT == CACHE_FP4) {
-      e2m1x8_to_f16(__ldca(reinterpret_cast<const uint32_t*>(data + (unsigned)t * RB)), w);
-    } else {
-      const uint2 y = __ldca(reinterpret_cast<const uint2*>(data + (unsigned)t * RB));
-      e4m3x4_to_f16(y.x, w[0], w[1]);
-      e4m3x4_to_f16(y.y, w[2], w[3]);
+  constexpr int BATCH = 8;                       // tokens of a thread whose loads are all ahead of the first use
+  for (int t0 = threadIdx.x / LPR; t0 < tokens; t0 += BATCH * ROWS) {
+    uint2 y[BATCH];
+    uint32_t e[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const unsigned t = min(t0 + i * ROWS, tokens - 1);          // the last token again: no bound moves
+      if (FMT == CACHE_FP4) y[i].x = __ldca(reinterpret_cast<const uint32_t*>(data + t * RB));
+      else y[i] = __ldca(reinterpret_cast<const uint2*>(data + t * RB));
+      e[i] = __ldca(sc + t * NB);
     }
-    const float s = scale_value(__ldca(sc + (unsigned)t * NB));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = f16x2_to_f32(w[j]);
-      const float v[2] = {f.x * s, f.y * s};
+    for (int i = 0; i < BATCH; ++i) {
+      uint32_t w[4];
+      if (FMT == CACHE_FP4) {
+        e2m1x8_to_f16(y[i].x, w);
+      } else {
+        e4m3x4_to_f16(y[i].x, w[0], w[1]);
+        e4m3x4_to_f16(y[i].y, w[2], w[3]);
+      }
+      const float s = scale_value(e[i]);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        odd |= !(fabsf(v[k]) < INFINITY);
-        lo[2 * j + k] = fminf(lo[2 * j + k], v[k]);
-        hi[2 * j + k] = fmaxf(hi[2 * j + k], v[k]);
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = f16x2_to_f32(w[j]);
+        const float v[2] = {f.x * s, f.y * s};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          odd |= !(fabsf(v[k]) < INFINITY);
+          lo[2 * j + k] = fminf(lo[2 * j + k], v[k]);
+          hi[2 * j + k] = fmaxf(hi[2 * j + k], v[k]);
+        }
       }
     }
   }

@@ -8,7 +8,7 @@
 namespace bsc {
 namespace {
 
-constexpr int DQ_THREADS = 256, DQ_ITEMS = 8;
+constexpr int DQ_THREADS = 128, DQ_ITEMS = 4;
 
 // Row r of the codes (in memory's order) has the scales of row scale_row(r).
 __device__ __forceinline__ uint32_t scale_row(uint32_t r, int B, int S, int H, int layout) {

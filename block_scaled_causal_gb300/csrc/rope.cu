@@ -53,22 +53,22 @@ struct Turn {
   }
 };
 
-// One tensor's heads h0, h0 + rpw, ... below h1 of a token, for this lane: `emit(head, values)` for each.  Whole warps call
-// it with the same h0 and h1 (heads of lane group `sub` are h0 + sub + k rpw).
+// One tensor's heads of a token for this lane: `rounds` of them, `step` elements apart from x on, the first `live` of which it
+// has; `emit(there, values)` for each in turn.  Whole warps call it with the same rounds.
 template <int DT, bool INTER, bool TURN, class Emit>
-__device__ __forceinline__ void heads_of(const uint16_t* x, long long step, int first, int h1, int rounds, int rpw, bool act,
-                                         int other, bool in_rot, const Turn<INTER>& turn, Emit emit) {
-  for (int k0 = 0; k0 < rounds; k0 += ROPE_BATCH) {
+__device__ __forceinline__ void heads_of(const uint16_t* x, long long step, int rounds, int live, int other, bool in_rot,
+                                         const Turn<INTER>& turn, Emit emit) {
+  for (; rounds > 0; rounds -= ROPE_BATCH, live -= ROPE_BATCH) {
     uint4 v[ROPE_BATCH];
 #pragma unroll
     for (int k = 0; k < ROPE_BATCH; ++k) {
       v[k] = make_uint4(0, 0, 0, 0);
-      if (act && first + (k0 + k) * rpw < h1) v[k] = __ldcs(reinterpret_cast<const uint4*>(x + k * step));
+      if (k < live) v[k] = __ldcs(reinterpret_cast<const uint4*>(x));
+      x += step;
     }
-    x += ROPE_BATCH * step;
 #pragma unroll
     for (int k = 0; k < ROPE_BATCH; ++k) {
-      if (k0 + k >= rounds) break;
+      if (k >= rounds) break;
       const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
       float2 f[4];
 #pragma unroll
@@ -82,8 +82,7 @@ __device__ __forceinline__ void heads_of(const uint16_t* x, long long step, int 
 #pragma unroll
           for (int j = 0; j < 4; ++j) f[j] = __ffma2_rn(f[j], turn.c[j], __fmul2_rn(o[j], turn.s[j]));
       }
-      const int h = first + (k0 + k) * rpw;
-      emit(h, act && h < h1, f);
+      emit(k < live, f);
     }
   }
 }
@@ -160,46 +159,49 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, 8) rope_kernel(const RopeArgs
     const int base = i == 0 ? 0 : i == 1 ? a.Hq : a.Hq + a.Hkv, H = i == 0 ? a.Hq : a.Hkv;
     const int h0 = max(from - base, 0), h1 = min(to - base, H);
     if (h0 >= h1 || (OUT == TO_CACHE && i != 0 && page < 0)) continue;
-    const int first = h0 + sub, rounds = (h1 - h0 + rpw - 1) / rpw;
+    const int first = h0 + sub, rounds = (h1 - h0 + rpw - 1) / rpw, live = act && first < h1 ? (h1 - first + rpw - 1) / rpw : 0;
     const uint16_t* const x = source(i, first);
     const long long step = rpw * a.xs[i].h;
     if (OUT == TO_ACT || (OUT == TO_CACHE && i == 0)) {
-      uint16_t* const y = reinterpret_cast<uint16_t*>(a.y[i]) + b * a.ys[i].b + t * a.ys[i].t + chunk * 8;
-      const long long ysh = a.ys[i].h;
-      heads_of<DT, INTER, true>(x, step, first, h1, rounds, rpw, act, other, in_rot, turn,
-                                [&](int h, bool there, const float2 (&f)[4]) {
-        if (there) __stcs(reinterpret_cast<uint4*>(y + h * ysh), real ? pack<DT>(f) : make_uint4(0, 0, 0, 0));
+      uint16_t* y = reinterpret_cast<uint16_t*>(a.y[i]) + b * a.ys[i].b + t * a.ys[i].t + first * a.ys[i].h + chunk * 8;
+      const long long y_step = rpw * a.ys[i].h;
+      heads_of<DT, INTER, true>(x, step, rounds, live, other, in_rot, turn, [&](bool there, const float2 (&f)[4]) {
+        if (there) __stcs(reinterpret_cast<uint4*>(y), real ? pack<DT>(f) : make_uint4(0, 0, 0, 0));
+        y += y_step;
       });
     } else if (OUT == TO_MX) {
-      uint8_t* const y = reinterpret_cast<uint8_t*>(a.y[i]) + b * a.ys[i].b + t * a.ys[i].t + chunk * 8;
-      uint8_t* const sc = a.sc[i] + ((long long)b * H * a.T + t) * (D / 32) + (chunk >> 2);
-      const long long ysh = a.ys[i].h, sch = (long long)a.T * (D / 32);
-      heads_of<DT, INTER, true>(x, step, first, h1, rounds, rpw, act, other, in_rot, turn,
-                                [&](int h, bool there, const float2 (&f)[4]) {
+      uint8_t* y = reinterpret_cast<uint8_t*>(a.y[i]) + b * a.ys[i].b + t * a.ys[i].t + first * a.ys[i].h + chunk * 8;
+      uint8_t* sc = a.sc[i] + (((long long)b * H + first) * a.T + t) * (D / 32) + (chunk >> 2);
+      const long long y_step = rpw * a.ys[i].h, sc_step = (long long)rpw * a.T * (D / 32);
+      heads_of<DT, INTER, true>(x, step, rounds, live, other, in_rot, turn, [&](bool there, const float2 (&f)[4]) {
         float inv;
         const uint32_t sb = chunk_scale<FMT>(f, up, inv);
         if (there) {
-          __stcs(reinterpret_cast<uint2*>(y + h * ysh), quant8_e4m3(f, inv, sb));
-          if ((chunk & 3) == 0) sc[h * sch] = (uint8_t)sb;
+          __stcs(reinterpret_cast<uint2*>(y), quant8_e4m3(f, inv, sb));
+          if ((chunk & 3) == 0) *sc = (uint8_t)sb;
         }
+        y += y_step;
+        sc += sc_step;
       });
     } else if constexpr (OUT == TO_CACHE) {
       constexpr int RB = row_bytes<FMT, DC>();
-      uint8_t* const y = (i == 2 ? a.c.v + page * a.c.v_ps : a.c.k + page * a.c.k_ps) + (unsigned long long)slot * RB + chunk * (RB / lpr);
-      uint8_t* const sc = (i == 2 ? a.c.v_sc + page * a.c.v_sc_ps : a.c.k_sc + page * a.c.k_sc_ps) +
-                          (unsigned long long)slot * (D / 32) + (chunk >> 2);
-      const long long ysh = (long long)a.c.page_size * RB, sch = (long long)a.c.page_size * (D / 32);
-      auto emit = [&](int h, bool there, const float2 (&f)[4]) {
+      const unsigned long long row = (unsigned long long)first * a.c.page_size + slot;
+      uint8_t* y = (i == 2 ? a.c.v + page * a.c.v_ps : a.c.k + page * a.c.k_ps) + row * RB + chunk * (RB / lpr);
+      uint8_t* sc = (i == 2 ? a.c.v_sc + page * a.c.v_sc_ps : a.c.k_sc + page * a.c.k_sc_ps) + row * (DC / 32) + (chunk >> 2);
+      const long long y_step = (long long)rpw * a.c.page_size * RB, sc_step = (long long)rpw * a.c.page_size * (DC / 32);
+      auto emit = [&](bool there, const float2 (&f)[4]) {
         float inv;
         const uint32_t sb = chunk_scale<FMT>(f, up, inv);
         if (there) {
-          if (FMT == CACHE_FP4) *reinterpret_cast<uint32_t*>(y + h * ysh) = quant8_e2m1(f, inv, sb);
-          else *reinterpret_cast<uint2*>(y + h * ysh) = quant8_e4m3(f, inv, sb);
-          if ((chunk & 3) == 0) sc[h * sch] = (uint8_t)sb;
+          if (FMT == CACHE_FP4) *reinterpret_cast<uint32_t*>(y) = quant8_e2m1(f, inv, sb);
+          else *reinterpret_cast<uint2*>(y) = quant8_e4m3(f, inv, sb);
+          if ((chunk & 3) == 0) *sc = (uint8_t)sb;
         }
+        y += y_step;
+        sc += sc_step;
       };
-      if (i == 1) heads_of<DT, INTER, true>(x, step, first, h1, rounds, rpw, act, other, in_rot, turn, emit);
-      else heads_of<DT, INTER, false>(x, step, first, h1, rounds, rpw, act, other, in_rot, turn, emit);
+      if (i == 1) heads_of<DT, INTER, true>(x, step, rounds, live, other, in_rot, turn, emit);
+      else heads_of<DT, INTER, false>(x, step, rounds, live, other, in_rot, turn, emit);
     }
   }
 }
