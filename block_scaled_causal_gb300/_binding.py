@@ -781,6 +781,7 @@ def mx_cache_attn(q, cache, page_table, seq_lens, new_lens=None, layout=BSHD, so
 
 
 # ------------------------------------------------------------------------------- norm and rotary positions
+# `stream` is that of the cache's calls (MxCache): like torch.cuda.stream(stream) around the call.
 _WEIGHT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _ANGLES = ctypes.sizeof(RopeAngles)
 _c_norm, _pack_norm = _packed_call("rms_norm", RmsNormParams, "8q9q5if", 0)
@@ -943,10 +944,12 @@ def rms_norm_bwd(dy, s, weight, rstd, ds=None, dx=None, dweight=None, workspace=
         _same_rows(s, dx, "dx")
     rows, inner, (dys, ss, dss, dxs) = _row_layout((dy, s, ds, dx))
     if dweight is None:
-        dweight = torch.empty_like(weight) if rows else torch.zeros_like(weight)
+        dweight = torch.empty_like(weight)
     elif dweight.shape != weight.shape or dweight.dtype != weight.dtype or dweight.device != s.device or \
             not dweight.is_contiguous():
         raise ValueError("dweight must be a contiguous tensor like weight")
+    if rows == 0:
+        dweight.zero_()                        # the call has nothing to do
     if workspace is None:
         need = rms_norm_bwd_workspace_bytes(rows, N)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=s.device)
@@ -1077,7 +1080,7 @@ rope = apply_rope      # the C call's name; `rope` is also what the calls name t
 
 
 def mxfp8_rope_quantize_qk(q, k, rope, positions=None, layout=BSHD, rule=SCALE_FLOOR, stream=None):
-    """Q and K rotated (as in `rope`) and quantised rowwise to MXFP8 in one launch, from the rotated fp32 values:
+    """Q and K (or None) rotated (as in `rope`) and quantised rowwise to MXFP8 in one launch, from the rotated fp32 values:
     (q_e4m3, q_sc, k_e4m3, k_sc), bytes dense in `layout` and scales [B, H, T, D/32]; D = 128."""
     there = _elsewhere_with(rope, q, stream)
     if there is not None:
@@ -1085,14 +1088,18 @@ def mxfp8_rope_quantize_qk(q, k, rope, positions=None, layout=BSHD, rule=SCALE_F
             return mxfp8_rope_quantize_qk(q, k, rope, positions, layout, rule)
     D = q.shape[-1]
     (B, T, Hq), qs, dt = _act_dims(q, layout, rope, "q", D)
-    (Bk, Tk, Hkv), ks, dt_k = _act_dims(k, layout, rope, "k", D)
-    if Bk != B or Tk != T or dt_k != dt:
-        raise ValueError("k must have q's batch, tokens and dtype")
     u8 = dict(dtype=torch.uint8, device=q.device)
     q8, q_sc = torch.empty(q.shape, **u8), torch.empty((B, Hq, T, D // 32), **u8)
-    k8, k_sc = torch.empty(k.shape, **u8), torch.empty((B, Hkv, T, D // 32), **u8)
-    p = rope.packed + _pack_rope_quant(q.data_ptr(), k.data_ptr(), *qs, *ks, q8.data_ptr(), q_sc.data_ptr(), k8.data_ptr(),
-                                       k_sc.data_ptr(), *_positions(positions, B, T, rope), B, T, Hq, Hkv, D, dt, layout, rule)
+    if k is None:
+        k8, k_sc, Hkv, ks, k_ptrs = None, None, 0, (0, 0, 0), (0, 0, 0)
+    else:
+        (Bk, Tk, Hkv), ks, dt_k = _act_dims(k, layout, rope, "k", D)
+        if Bk != B or Tk != T or dt_k != dt:
+            raise ValueError("k must have q's batch, tokens and dtype")
+        k8, k_sc = torch.empty(k.shape, **u8), torch.empty((B, Hkv, T, D // 32), **u8)
+        k_ptrs = k.data_ptr(), k8.data_ptr(), k_sc.data_ptr()
+    p = rope.packed + _pack_rope_quant(q.data_ptr(), k_ptrs[0], *qs, *ks, q8.data_ptr(), q_sc.data_ptr(), *k_ptrs[1:],
+                                       *_positions(positions, B, T, rope), B, T, Hq, Hkv, D, dt, layout, rule)
     _check(_c_rope_quant(p, _raw_stream(rope.index)))
     return q8, q_sc, k8, k_sc
 

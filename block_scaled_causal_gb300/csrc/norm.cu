@@ -164,8 +164,8 @@ __global__ void __launch_bounds__(WIDE ? WIDE_THREADS : NARROW_THREADS, blocks_p
           for (int i = 0; i < 4; ++i) f[i] = __fadd2_rn(f[i], g[i]);
           s[v] = pack8<DT>(f);
           unpack8<DT>(s[v], f);
-          if (a.s) __stcs(sp + v * tpr, s[v]);
         }
+        if (a.s) __stcs(sp + v * tpr, s[v]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum = __ffma2_rn(f[i], f[i], sum);
       }

@@ -53,19 +53,21 @@ struct Turn {
   }
 };
 
-// One tensor's heads of a token for this lane: `rounds` of them, `step` elements apart from x on, the first `live` of which it
-// has; `emit(there, values)` for each in turn.  Whole warps call it with the same rounds.
-template <int DT, bool INTER, bool TURN, class Emit>
-__device__ __forceinline__ void heads_of(const uint16_t* x, long long step, int rounds, int live, int other, bool in_rot,
-                                         const Turn<INTER>& turn, Emit emit) {
-  for (; rounds > 0; rounds -= ROPE_BATCH, live -= ROPE_BATCH) {
-    uint4 v[ROPE_BATCH];
+// The next heads of a tensor, `step` elements apart from x on, of which the lane has the first `live`.
+__device__ __forceinline__ void load_batch(uint4 (&v)[ROPE_BATCH], const uint16_t*& x, long long step, int live) {
 #pragma unroll
-    for (int k = 0; k < ROPE_BATCH; ++k) {
-      v[k] = make_uint4(0, 0, 0, 0);
-      if (k < live) v[k] = __ldcs(reinterpret_cast<const uint4*>(x));
-      x += step;
-    }
+  for (int k = 0; k < ROPE_BATCH; ++k) {
+    v[k] = make_uint4(0, 0, 0, 0);
+    if (k < live) v[k] = __ldcs(reinterpret_cast<const uint4*>(x));
+    x += step;
+  }
+}
+// One tensor's heads of a token for this lane: `rounds` of them, the first batch already in v and the next from x on;
+// `emit(there, values)` for each in turn.  Whole warps call it with the same rounds.
+template <int DT, bool INTER, bool TURN, class Emit>
+__device__ __forceinline__ void heads_of(uint4 (&v)[ROPE_BATCH], const uint16_t* x, long long step, int rounds, int live, int other,
+                                         bool in_rot, const Turn<INTER>& turn, Emit emit) {
+  for (;;) {
 #pragma unroll
     for (int k = 0; k < ROPE_BATCH; ++k) {
       if (k >= rounds) break;
@@ -84,6 +86,10 @@ __device__ __forceinline__ void heads_of(const uint16_t* x, long long step, int 
       }
       emit(k < live, f);
     }
+    rounds -= ROPE_BATCH;
+    live -= ROPE_BATCH;
+    if (rounds <= 0) return;
+    load_batch(v, x, step, live);
   }
 }
 
@@ -113,6 +119,32 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, 8) rope_kernel(const RopeArgs
   if (token >= (uint32_t)a.B * a.T) return;
   const int b = token / a.T, t = token - b * a.T;
 
+  const int D = DC ? DC : a.D, lpr = D / 8, rpw = 32 / lpr, sub = lane / lpr, chunk = lane - sub * lpr;
+  const bool act = sub < rpw;
+  const int half = a.rot / 16;                   // chunks of half the rotated part
+  const bool in_rot = chunk < 2 * half, low = chunk < half;
+  const int other = in_rot ? (low ? lane + half : lane - half) : lane;
+
+  // ---- the heads: this block's share of [0, Hq + Hkv (+ Hkv)); those of tensor i are h0 .. h1 - 1 of it ----
+  constexpr int TENSORS = OUT == TO_CACHE ? 3 : 2;
+  const int total = a.Hq + (TENSORS - 1) * a.Hkv, from = blockIdx.y * per, to = min(from + per, total);
+  const uint32_t up = OUT == TO_ACT ? 0u : ceil_carry<FMT>(a.rule);
+  auto base_of = [&](int i) { return i == 0 ? 0 : i == 1 ? a.Hq : a.Hq + a.Hkv; };
+  auto first_of = [&](int i) { return max(from - base_of(i), 0); };
+  auto end_of = [&](int i) { return min(to - base_of(i), i == 0 ? a.Hq : a.Hkv); };
+  auto live_of = [&](int i) {                    // heads of this lane
+    const int first = first_of(i) + sub, h1 = end_of(i);
+    return act && first < h1 ? (h1 - first + rpw - 1) / rpw : 0;
+  };
+  auto source = [&](int i) {
+    return reinterpret_cast<const uint16_t*>(a.x[i]) + b * a.xs[i].b + t * a.xs[i].t + (first_of(i) + sub) * a.xs[i].h + chunk * 8;
+  };
+  // the first heads' loads start ahead of the angles
+  const int start = from < a.Hq ? 0 : from < a.Hq + a.Hkv ? 1 : 2;
+  uint4 v[ROPE_BATCH];
+  const uint16_t* x = source(start);
+  load_batch(v, x, rpw * a.xs[start].h, live_of(start));
+
   // ---- the token's position and page, its angles ----
   long long pos = t;
   bool real = true;                              // TO_CACHE: a token of the sequence
@@ -140,32 +172,23 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, 8) rope_kernel(const RopeArgs
   }
   __syncwarp();
 
-  const int D = DC ? DC : a.D, lpr = D / 8, rpw = 32 / lpr, sub = lane / lpr, chunk = lane - sub * lpr;
-  const bool act = sub < rpw;
-  const int half = a.rot / 16;                   // chunks of half the rotated part
-  const bool in_rot = chunk < 2 * half, low = chunk < half;
-  const int other = in_rot ? (low ? lane + half : lane - half) : lane;
   Turn<INTER> turn;
   turn.load(cosines[warp], sines[warp], !in_rot ? 0 : INTER ? chunk * 4 : (low ? chunk : chunk - half) * 8, low);
 
-  // ---- the heads: this block's share of [0, Hq + Hkv (+ Hkv)) ----
-  const int total = a.Hq + (OUT == TO_CACHE ? 2 : 1) * a.Hkv, from = blockIdx.y * per, to = min(from + per, total);
-  const uint32_t up = OUT == TO_ACT ? 0u : ceil_carry<FMT>(a.rule);
-  auto source = [&](int i, int h) {
-    return reinterpret_cast<const uint16_t*>(a.x[i]) + b * a.xs[i].b + t * a.xs[i].t + h * a.xs[i].h + chunk * 8;
-  };
 #pragma unroll
-  for (int i = 0; i < (OUT == TO_CACHE ? 3 : 2); ++i) {
-    const int base = i == 0 ? 0 : i == 1 ? a.Hq : a.Hq + a.Hkv, H = i == 0 ? a.Hq : a.Hkv;
-    const int h0 = max(from - base, 0), h1 = min(to - base, H);
+  for (int i = 0; i < TENSORS; ++i) {
+    const int h0 = first_of(i), h1 = end_of(i);
     if (h0 >= h1 || (OUT == TO_CACHE && i != 0 && page < 0)) continue;
-    const int first = h0 + sub, rounds = (h1 - h0 + rpw - 1) / rpw, live = act && first < h1 ? (h1 - first + rpw - 1) / rpw : 0;
-    const uint16_t* const x = source(i, first);
+    const int H = i == 0 ? a.Hq : a.Hkv, first = h0 + sub, rounds = (h1 - h0 + rpw - 1) / rpw, live = live_of(i);
     const long long step = rpw * a.xs[i].h;
+    if (i != start) {
+      x = source(i);
+      load_batch(v, x, step, live);
+    }
     if (OUT == TO_ACT || (OUT == TO_CACHE && i == 0)) {
       uint16_t* y = reinterpret_cast<uint16_t*>(a.y[i]) + b * a.ys[i].b + t * a.ys[i].t + first * a.ys[i].h + chunk * 8;
       const long long y_step = rpw * a.ys[i].h;
-      heads_of<DT, INTER, true>(x, step, rounds, live, other, in_rot, turn, [&](bool there, const float2 (&f)[4]) {
+      heads_of<DT, INTER, true>(v, x, step, rounds, live, other, in_rot, turn, [&](bool there, const float2 (&f)[4]) {
         if (there) __stcs(reinterpret_cast<uint4*>(y), real ? pack<DT>(f) : make_uint4(0, 0, 0, 0));
         y += y_step;
       });
@@ -173,7 +196,7 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, 8) rope_kernel(const RopeArgs
       uint8_t* y = reinterpret_cast<uint8_t*>(a.y[i]) + b * a.ys[i].b + t * a.ys[i].t + first * a.ys[i].h + chunk * 8;
       uint8_t* sc = a.sc[i] + (((long long)b * H + first) * a.T + t) * (D / 32) + (chunk >> 2);
       const long long y_step = rpw * a.ys[i].h, sc_step = (long long)rpw * a.T * (D / 32);
-      heads_of<DT, INTER, true>(x, step, rounds, live, other, in_rot, turn, [&](bool there, const float2 (&f)[4]) {
+      heads_of<DT, INTER, true>(v, x, step, rounds, live, other, in_rot, turn, [&](bool there, const float2 (&f)[4]) {
         float inv;
         const uint32_t sb = chunk_scale<FMT>(f, up, inv);
         if (there) {
@@ -200,8 +223,8 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, 8) rope_kernel(const RopeArgs
         y += y_step;
         sc += sc_step;
       };
-      if (i == 1) heads_of<DT, INTER, true>(x, step, rounds, live, other, in_rot, turn, emit);
-      else heads_of<DT, INTER, false>(x, step, rounds, live, other, in_rot, turn, emit);
+      if (i == 1) heads_of<DT, INTER, true>(v, x, step, rounds, live, other, in_rot, turn, emit);
+      else heads_of<DT, INTER, false>(v, x, step, rounds, live, other, in_rot, turn, emit);
     }
   }
 }

@@ -511,7 +511,7 @@ bsc_status mxfp8_dequantize(const uint8_t* x_e4m3, const uint8_t* x_sc, int B, i
  *   BSC_ROPE_PLAIN      f_i = base^(-2i/rot)
  *   BSC_ROPE_LINEAR     f_i / factor: positions are interpolated
  *   BSC_ROPE_BASE       base * factor^(rot/(rot-2)) in the place of base: the slowest pair is interpolated by factor, the
- *                       fastest not at all (rot = 2: plain)
+ *                       fastest not at all
  *   BSC_ROPE_BY_PARTS   f_i (k + (1 - k) / factor), k = clamp((original_length f_i / 2 pi - low_turns) / (high_turns -
  *                       low_turns), 0, 1): pairs that turn often in the trained length stay, slow ones are interpolated
  *                       (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models", 3.2); magnitude
@@ -621,7 +621,9 @@ bsc_status mx_cache_write_rope(const bsc_mx_cache_write_rope_params* p, bsc_stre
  *
  * mx_cache_bounds makes the bounds of the pages that hold positions [seq_lens[b] - n_b, seq_lens[b]) of every sequence, from
  * all of a page's tokens below seq_lens[b]: after each write, with the write's lengths.  Nothing else changes.  It does not
- * read earlier bounds.  codes 16-byte aligned.
+ * read earlier bounds.  Where one call meets a page twice with different numbers of tokens (a shared prefix that ends inside
+ * it), its bounds afterwards are those of either; a page that is whole in every sequence has one answer.  codes 16-byte
+ * aligned.
  */
 typedef struct {
   bsc_mx_cache cache;     /* [in]; k and k_sc are read */

@@ -150,12 +150,25 @@ def test_rows_that_are_not_ordinary(ops):
     check_rows(y[[4, 6]], R.norm(f64(x[[4, 6]]), np.ones(64), EPS)[0], torch.bfloat16)
 
 
+def test_sum_without_a_residual(ops):
+    """The C call writes s = x where it is given a place for it and no residual."""
+    import ctypes
+    x, w, s, y = (torch.randn(n, device="cuda").bfloat16() for n in ((5, 64), (64,), (5, 64), (5, 64)))
+    p = ops.RmsNormParams(x=x.data_ptr(), weight=w.data_ptr(), y=y.data_ptr(), sum=s.data_ptr(), rows=5, x_stride=64, y_stride=64,
+                          sum_stride=64, inner=1, N=64, dtype=0, weight_dtype=0, rule=0, eps=EPS)
+    assert ops.lib.rms_norm(ctypes.byref(p), torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(s, x) and torch.equal(y, ops.rms_norm(x, w, EPS)[0])
+
+
 def test_nothing_to_do(ops):
     w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
     y, s, rstd = ops.rms_norm(w.new_empty((0, 64)), w)
     assert y.shape == (0, 64) and rstd.shape == (0,)
     dx, dw = ops.rms_norm_bwd(w.new_empty((0, 64)), w.new_empty((0, 64)), w, rstd)
     assert dx.shape == (0, 64) and torch.all(dw == 0)
+    given = torch.ones_like(w)
+    ops.rms_norm_bwd(w.new_empty((0, 64)), w.new_empty((0, 64)), w, rstd, dweight=given)
+    assert torch.all(given == 0)
     assert ops.rms_norm(w, w)[0].shape == (64,) and ops.rms_norm(w, w)[2].shape == ()
 
 

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from oracle import operands as R
+from test_cache_launch_order_cpu import code
 from test_cache_cpu import COMMON, FAKE, POOL_CASES, _pools, _strides, ops  # noqa: F401
 
 NULL, SHAPE, ALIGN, UNSUPPORTED = 1, 2, 3, 4
@@ -287,3 +288,18 @@ def test_row_layouts(ops):  # noqa: F811
     assert f((torch.zeros(1, 64).expand(4, 64),)) == (4, 1, [(0, 0)])
     assert f((torch.zeros((0, 64))[:, :32],))[0] == 0
     assert f((torch.zeros(64),)) == (1, 1, [(64, 0)])
+
+
+@pytest.mark.parametrize("name,kernels", [("norm.cu", 3), ("rope.cu", 1), ("dequant.cu", 1), ("cache_select.cu", 2)])
+def test_launch_order(name, kernels):
+    """Kernels that may start while the one ahead of them still stores: their wait is before their signal and every load,
+    and no load takes the read-only path."""
+    import re
+    s = code(name)
+    assert not re.findall(r"\b__ldg\s*\(|ld\.global(?:\.\w+)*\.nc", s) and "__restrict__" not in s
+    bodies = re.split(r"__global__", s)[1:]
+    assert len(bodies) == kernels
+    for body in bodies:
+        wait, signal = body.find("wait_for_last_kernel()"), body.find("next_kernel_may_start()")
+        loads = [m.start() for m in re.finditer(r"__ld\w\w\(|fetch\(|load_batch\(v|cache_page\(|seen_by\(", body)]
+        assert 0 <= wait < signal and (not loads or wait < min(loads))

@@ -160,6 +160,8 @@ def test_quantised(ops, B, T, Hq, Hkv, dtype, layout, rule, kind, interleaved, r
     for x, x8, sc in ((q, q8, qs), (k, k8, ks)):
         data, sb = I.to_bshd(x8, layout).cpu().numpy(), sc.permute(0, 2, 1, 3).cpu().numpy()
         enclosed(data, sb, expect(ops, x, r, at, layout), 0, "ceil" if rule else "floor")
+    alone = ops.mxfp8_rope_quantize_qk(q, None, r, pos, layout, rule)
+    assert torch.equal(alone[0], q8) and torch.equal(alone[1], qs) and alone[2:] == (None, None)
 
 
 def test_quantised_at_position_0_is_the_quantiser(ops):
