@@ -794,8 +794,8 @@ _c_bounds, _pack_bounds = _packed_call("mx_cache_bounds", CacheBoundsParams, "2i
 _c_sparse, _pack_sparse = _packed_call("mx_cache_sparse_attn", CacheSparseAttnParams, "10q4if3i2qi5q", ctypes.sizeof(CachePools) + 16)
 
 
-def _same_rows(x, t, name):
-    if t.shape != x.shape or t.dtype is not x.dtype or t.get_device() != x.get_device():
+def _same_rows(t, shape, dtype, dev, name):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
         raise ValueError("%s must have the first tensor's shape, device and dtype" % name)
 
 
@@ -840,15 +840,16 @@ def _row_layout(tensors):
     raise ValueError("the rows of every tensor must be spaced by at most two strides")
 
 
-def _weight_code(weight, x, N):
-    if weight.shape != (N,) or weight.get_device() != x.get_device() or not weight.is_contiguous() or \
-            (weight.dtype is not x.dtype and weight.dtype is not torch.float32):
+def _weight_code(weight, N, dtype, dev):
+    wd = weight.dtype
+    if weight.shape != (N,) or weight.get_device() != dev or not weight.is_contiguous() or \
+            (wd is not dtype and wd is not torch.float32):
         raise ValueError("weight must be a contiguous [N] tensor of the activations' dtype or float32")
-    return _WEIGHT[weight.dtype]
+    return _WEIGHT[wd]
 
 
-def _rstd_of(rstd, lead, x):
-    if rstd.shape != lead or rstd.dtype is not torch.float32 or rstd.get_device() != x.get_device() or not rstd.is_contiguous():
+def _rstd_of(rstd, lead, dev):
+    if rstd.shape != lead or rstd.dtype is not torch.float32 or rstd.get_device() != dev or not rstd.is_contiguous():
         raise ValueError("rstd must be a contiguous float32 tensor of the activations' leading dimensions")
 
 
@@ -860,20 +861,22 @@ def rms_norm(x, weight, eps=1e-6, residual=None, y=None, sum_out=None, rstd=None
     x itself without a residual and rstd float32 [...]; with y8_out=True, (y or None, s, rstd, y as E4M3 bytes [..., N], its
     scales [..., N/32]).  weight: [N], x's dtype or float32.  y, sum_out and rstd may be given; y and sum_out may be x or
     residual themselves."""
-    if stream is not None or not x.is_cuda or _current_device() != x.get_device():
+    dev = x.get_device()
+    if stream is not None or dev < 0 or _current_device() != dev:
         with _elsewhere_of(x, "x", stream):
             return rms_norm(x, weight, eps, residual, y, sum_out, rstd, y8_out, y_out, y8, y_sc, rule)
-    dt, shape = _ACT.get(x.dtype), x.shape
+    dtype, shape = x.dtype, x.shape
+    dt = _ACT.get(dtype)
     if dt is None or not shape:
         raise ValueError("x must be a bfloat16 or float16 tensor [..., N]")
     N, lead = shape[-1], shape[:-1]
-    wt = _weight_code(weight, x, N)
+    wt = _weight_code(weight, N, dtype, dev)
     fresh = x.is_contiguous()                  # an output that is allocated here is laid out like x
     if y_out:
         if y is None:
             y = torch.empty_like(x, memory_format=torch.contiguous_format)
         else:
-            _same_rows(x, y, "y")
+            _same_rows(y, shape, dtype, dev, "y")
             fresh = False
         y_ptr = y.data_ptr()
     elif y8_out:
@@ -885,18 +888,18 @@ def rms_norm(x, weight, eps=1e-6, residual=None, y=None, sum_out=None, rstd=None
             raise ValueError("sum_out is for a residual")
         r_ptr = s_ptr = 0
     else:
-        _same_rows(x, residual, "residual")
+        _same_rows(residual, shape, dtype, dev, "residual")
         fresh = fresh and residual.is_contiguous()
         if sum_out is None:
             sum_out = torch.empty_like(x, memory_format=torch.contiguous_format)
         else:
-            _same_rows(x, sum_out, "sum_out")
+            _same_rows(sum_out, shape, dtype, dev, "sum_out")
             fresh = False
         r_ptr, s_ptr = residual.data_ptr(), sum_out.data_ptr()
     if rstd is None:
         rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
     else:
-        _rstd_of(rstd, lead, x)
+        _rstd_of(rstd, lead, dev)
     y8_ptr = sc_ptr = 0
     if y8_out:
         shapes = (shape, lead + (N // 32,))
@@ -911,7 +914,7 @@ def rms_norm(x, weight, eps=1e-6, residual=None, y=None, sum_out=None, rstd=None
         rows, inner, (xs, rs, ys, ss) = _row_layout((x, residual, y, sum_out))
     p = _pack_norm(x.data_ptr(), r_ptr, weight.data_ptr(), y_ptr, s_ptr, rstd.data_ptr(), y8_ptr, sc_ptr, rows, *xs, *rs, *ys,
                    *ss, inner, N, dt, wt, rule, eps)
-    _check(_c_norm(p, _raw_stream(x.get_device())))
+    _check(_c_norm(p, _raw_stream(dev)))
     s = x if residual is None else sum_out
     return (y, s, rstd, y8, y_sc) if y8_out else (y, s, rstd)
 
@@ -926,22 +929,24 @@ def rms_norm_bwd(dy, s, weight, rstd, ds=None, dx=None, dweight=None, workspace=
     residual alike, with `ds`, the gradient that reaches s by the residual stream, added; dweight has weight's dtype.
     dx may be dy, s or ds themselves.  `workspace`: a device tensor of rms_norm_bwd_workspace_bytes(rows, N) bytes that no
     other running call uses, else one is allocated here."""
-    if stream is not None or not s.is_cuda or _current_device() != s.get_device():
+    dev = s.get_device()
+    if stream is not None or dev < 0 or _current_device() != dev:
         with _elsewhere_of(s, "s", stream):
             return rms_norm_bwd(dy, s, weight, rstd, ds, dx, dweight, workspace)
-    dt, shape = _ACT.get(s.dtype), s.shape
+    dtype, shape = s.dtype, s.shape
+    dt = _ACT.get(dtype)
     if dt is None or not shape:
         raise ValueError("s must be a bfloat16 or float16 tensor [..., N]")
     N = shape[-1]
-    wt = _weight_code(weight, s, N)
-    _same_rows(s, dy, "dy")
+    wt = _weight_code(weight, N, dtype, dev)
+    _same_rows(dy, shape, dtype, dev, "dy")
     if ds is not None:
-        _same_rows(s, ds, "ds")
-    _rstd_of(rstd, shape[:-1], s)
+        _same_rows(ds, shape, dtype, dev, "ds")
+    _rstd_of(rstd, shape[:-1], dev)
     if dx is None:
         dx = torch.empty_like(s, memory_format=torch.contiguous_format)
     else:
-        _same_rows(s, dx, "dx")
+        _same_rows(dx, shape, dtype, dev, "dx")
     rows, inner, (dys, ss, dss, dxs) = _row_layout((dy, s, ds, dx))
     if dweight is None:
         dweight = torch.empty_like(weight)
@@ -960,7 +965,7 @@ def rms_norm_bwd(dy, s, weight, rstd, ds=None, dx=None, dweight=None, workspace=
     p = _pack_norm_bwd(dy.data_ptr(), s.data_ptr(), weight.data_ptr(), rstd.data_ptr(), 0 if ds is None else ds.data_ptr(),
                        dx.data_ptr(), dweight.data_ptr(), rows, *dys, *ss, *dss, *dxs, inner, N, dt, wt, workspace.data_ptr(),
                        need)
-    _check(_c_norm_bwd(p, _raw_stream(s.get_device())))
+    _check(_c_norm_bwd(p, _raw_stream(dev)))
     return dx, dweight
 
 
@@ -968,33 +973,37 @@ def mxfp8_dequantize(x, sc, layout=BSHD, dtype=torch.bfloat16, out=None, stream=
     """MXFP8 rows back to values: x uint8 [B, S, H, D] (SBHD: [S, B, H, D]) with sc [B, H, S, D/32], as the rowwise
     quantisers return them, or [..., N] with sc [..., N/32], as rms_norm does (x not 4-D, or 4-D with such scales and
     layout=None)."""
-    if stream is not None or not x.is_cuda or _current_device() != x.get_device():
+    dev = x.get_device()
+    if stream is not None or dev < 0 or _current_device() != dev:
         with _elsewhere_of(x, "x", stream):
             return mxfp8_dequantize(x, sc, layout, dtype, out)
     code = _ACT.get(dtype)
     if code is None:
         raise ValueError("dtype must be bfloat16 or float16")
     for t, n in ((x, "x"), (sc, "sc")):
-        if not t.is_cuda or t.dtype != torch.uint8 or not t.is_contiguous() or t.device != x.device:
+        if t.dtype is not torch.uint8 or t.get_device() != dev or not t.is_contiguous():
             raise ValueError("%s must be a contiguous CUDA uint8 tensor on one device with the other" % n)
-    if x.dim() == 4 and layout is not None:
-        if layout not in (BSHD, SBHD):
+    shape = x.shape
+    if len(shape) == 4 and layout is not None:
+        B, S, H, D = shape
+        if layout == SBHD:
+            B, S = S, B
+        elif layout != BSHD:
             raise ValueError("layout must be BSHD or SBHD")
-        B, S, H, D = _bshd_dims(x, layout)
         want = (B, H, S, D // 32)
-    elif x.dim() >= 1:
-        B, H, D = 1, 1, x.shape[-1]
-        S, want, layout = x.numel() // D if D else 0, x.shape[:-1] + (D // 32,), BSHD
+    elif shape:
+        B, H, D = 1, 1, shape[-1]
+        S, want, layout = x.numel() // max(D, 1), shape[:-1] + (D // 32,), BSHD
     else:
         raise ValueError("x must have at least one dimension")
-    if tuple(sc.shape) != tuple(want):
+    if sc.shape != want:
         raise ValueError("sc must have the shape %s" % (tuple(want),))
     if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=x.device)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
     elif out.shape != x.shape or out.dtype != dtype or out.device != x.device or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor shaped like x, of dtype")
     _check(lib.mxfp8_dequantize(x.data_ptr(), sc.data_ptr(), B, S, H, D, layout, code, out.data_ptr(),
-                                _raw_stream(x.get_device())))
+                                _raw_stream(dev)))
     return out
 
 

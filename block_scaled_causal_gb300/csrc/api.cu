@@ -241,7 +241,7 @@ bsc_status check_norm(long long rows, int N, int inner, int dtype, int weight_dt
     *empty = true;
     return BSC_OK;
   }
-  if (N % 8 != 0 || N > BSC_NORM_MAX_N || rows >= (1LL << 40)) return BSC_ERR_UNSUPPORTED;
+  if (N % 8 != 0 || N > BSC_NORM_MAX_N || rows >= BSC_NORM_MAX_ROWS) return BSC_ERR_UNSUPPORTED;
   return BSC_OK;
 }
 

@@ -12,7 +12,6 @@
 // held in registers.  Rows of up to 1024 elements belong to part of a warp, longer ones to a block.  FLAT rows are evenly
 // spaced: addresses move by addition.
 #include <atomic>
-#include <type_traits>
 
 #include "cache.cuh"
 
@@ -83,11 +82,17 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* part) {
   return v;
 }
 
+// x^(-1/2), refined by one step so that it is within an ulp; where x is 0 or not finite, the limit as it stands.
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x);
+  return x > 0.f && x < INFINITY ? fmaf(0.5f * r, fmaf(-x * r, r, 1.f), r) : r;
+}
+
 __device__ __forceinline__ long long row_at(const NormRows& s, long long row, int inner) {
   const long long o = row / inner;
   return o * s.outer + (row - o * inner) * s.inner;
 }
-// The rows that a thread meets, one after another: at its vector t of row `row`, and gridDim rows (groups) on.
+// The rows that a thread meets, one after another: at its vector t of row `row`, and `rows_on` rows on.
 template <bool FLAT>
 struct Walk {
   uint16_t* p;
@@ -96,60 +101,76 @@ struct Walk {
     p = reinterpret_cast<uint16_t*>(const_cast<void*>(base)) + t * 8 + (FLAT ? row * s.outer : 0);
     step = FLAT ? rows_on * s.outer : 0;
   }
-  __device__ __forceinline__ uint4* at(const NormRows& s, long long row, int inner) const {
-    return reinterpret_cast<uint4*>(FLAT ? p : p + row_at(s, row, inner));
-  }
-  __device__ __forceinline__ void on() {
+  // at the next row
+  __device__ __forceinline__ uint4* next(const NormRows& s, long long row, int inner) {
+    uint4* const at = reinterpret_cast<uint4*>(FLAT ? p : p + row_at(s, row, inner));
     if (FLAT) p += step;
+    return at;
+  }
+};
+// A thread's rows: the first, the step from one to the next, how many it has, and how many the block's first thread has (the
+// rows of one warp end together: loops go by that).  Fewer than 2^31: the host checks rows, and a grid that is full has
+// 152 blocks at least.
+struct Rows {
+  long long first, step;
+  int count, rounds;
+  __device__ __forceinline__ Rows(long long rows, int per_block, int group) {
+    const long long block = (long long)blockIdx.x * per_block;
+    step = (long long)gridDim.x * per_block;
+    first = block + group;
+    rounds = (int)((rows - block + step - 1) / step);          // no block is without a row
+    count = first < rows ? (int)((rows - first + step - 1) / step) : 0;
   }
 };
 
-template <int DT, int V, bool WIDE, bool FLAT>
+// RES: a residual is added (and the sum written, where it is asked for).
+template <int DT, int V, bool WIDE, bool FLAT, bool RES>
 __global__ void __launch_bounds__(WIDE ? WIDE_THREADS : NARROW_THREADS, blocks_per_sm(V, WIDE)) norm_kernel(const NormArgs a, int tpr) {
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float part[2][32];
-  constexpr int STAGES = stages(V);
+  constexpr int STAGES = stages(V), PIECES = RES ? 2 : 1;
   wait_for_last_kernel();
   if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
-  const int threads = blockDim.x, rpb = WIDE ? 1 : NARROW_THREADS / tpr, t = WIDE ? threadIdx.x : threadIdx.x % tpr;
-  const int nv = a.N / 8, pieces = a.r ? 2 : 1;
-  const long long step = (long long)gridDim.x * rpb;
-  long long row = (long long)blockIdx.x * rpb + (WIDE ? 0 : threadIdx.x / tpr), ahead = row;
-  uint4* const own = ring + threadIdx.x;                         // piece p of stage g: own[(g * pieces * V + p) * threads]
-  Walk<FLAT> xw(a.x, a.xs, row, step, t), rw(a.r, a.rs, row, step, t), sw(a.s, a.ss, row, step, t), yw(a.y, a.ys, row, step, t);
-  auto fetch = [&](int stage) {                                  // the next row ahead
-    if (ahead < a.rows) {
-      const uint4 *const xp = xw.at(a.xs, ahead, a.inner), *const rp = a.r ? rw.at(a.rs, ahead, a.inner) : nullptr;
-      uint4* const to = own + stage * pieces * V * threads;
+  const int threads = blockDim.x, t = WIDE ? threadIdx.x : threadIdx.x % tpr, nv = a.N / 8;
+  const Rows rows(a.rows, WIDE ? 1 : NARROW_THREADS / tpr, WIDE ? 0 : threadIdx.x / tpr);
+  uint4* const own = ring + threadIdx.x;                         // piece p of stage g: own[(g * PIECES * V + p) * threads]
+  Walk<FLAT> xw(a.x, a.xs, rows.first, rows.step, t), rw(a.r, a.rs, rows.first, rows.step, t);
+  Walk<FLAT> sw(a.s, a.ss, rows.first, rows.step, t), yw(a.y, a.ys, rows.first, rows.step, t);
+  auto fetch = [&](int i, uint4* to) {                           // its i-th row
+    if (i < rows.count) {
+      const long long row = FLAT ? 0 : rows.first + i * rows.step;
+      const uint4* const xp = xw.next(a.xs, row, a.inner);
+      const uint4* const rp = RES ? rw.next(a.rs, row, a.inner) : nullptr;
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (v * tpr + t < nv) {
           copy16(to + v * threads, xp + v * tpr);
-          if (a.r) copy16(to + (V + v) * threads, rp + v * tpr);
+          if (RES) copy16(to + (V + v) * threads, rp + v * tpr);
         }
     }
-    xw.on();
-    rw.on();
-    ahead += step;
     copies_end();
   };
+  const int stage = PIECES * V * threads;
+  uint4 *from = own, *into = own;
 #pragma unroll
-  for (int g = 0; g < STAGES - 1; ++g) fetch(g);
+  for (int g = 0; g < STAGES - 1; ++g) {
+    fetch(g, into);
+    into += stage;
+  }
   float2 w[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v)
     if (v * tpr + t < nv) load_weights<DT>(a.w, a.w32, v * tpr + t, w[v]);
   const uint32_t up = ceil_carry<CACHE_FP8>(a.rule);
   const float inv_n = 1.f / (float)a.N;
-  int turn = 0, stage = 0;
-  // rows of one warp end together: the loop goes by the block's first row
-  for (long long first = (long long)blockIdx.x * rpb; first < a.rows; first += step, row += step, turn ^= 1) {
-    const bool live = row < a.rows;
+  float* rstds = a.rstd + rows.first;
+  for (int i = 0; i < rows.rounds; ++i) {
+    const bool live = i < rows.count;
+    const long long row = rows.first + i * rows.step;
     copies_wait<STAGES - 2>();
-    const uint4* const from = own + stage * pieces * V * threads;
     uint4 s[V];
     float2 sum = both(0.f);
-    uint4* const sp = a.s ? sw.at(a.ss, row, a.inner) : nullptr;
+    uint4* const sp = a.s ? sw.next(a.ss, row, a.inner) : nullptr;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       s[v] = make_uint4(0, 0, 0, 0);
@@ -157,25 +178,28 @@ __global__ void __launch_bounds__(WIDE ? WIDE_THREADS : NARROW_THREADS, blocks_p
         s[v] = from[v * threads];
         float2 f[4];
         unpack8<DT>(s[v], f);
-        if (a.r) {
+        if (RES) {
           float2 g[4];
           unpack8<DT>(from[(V + v) * threads], g);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = __fadd2_rn(f[i], g[i]);
+          for (int j = 0; j < 4; ++j) f[j] = __fadd2_rn(f[j], g[j]);
           s[v] = pack8<DT>(f);
           unpack8<DT>(s[v], f);
         }
         if (a.s) __stcs(sp + v * tpr, s[v]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum = __ffma2_rn(f[i], f[i], sum);
+        for (int j = 0; j < 4; ++j) sum = __ffma2_rn(f[j], f[j], sum);
       }
     }
-    // into the stage that was read before this one: its values are used
-    fetch(stage == 0 ? STAGES - 1 : stage - 1);
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
-    const float rstd = rsqrtf(row_sum<WIDE>(sum.x + sum.y, tpr, part[turn]) * inv_n + a.eps);
-    if (a.rstd && t == 0 && live) a.rstd[row] = rstd;
-    uint4* const yp = a.y ? yw.at(a.ys, row, a.inner) : nullptr;
+    from = from == own + (STAGES - 1) * stage ? own : from + stage;
+    fetch(i + STAGES - 1, into);                 // into the stage that was read before this one: its values are used
+    into = into == own + (STAGES - 1) * stage ? own : into + stage;
+    const float rstd = inverse_root(row_sum<WIDE>(sum.x + sum.y, tpr, part[i & 1]) * inv_n + a.eps);
+    if (a.rstd) {
+      if (t == 0 && live) *rstds = rstd;
+      rstds += rows.step;
+    }
+    uint4* const yp = a.y ? yw.next(a.ys, row, a.inner) : nullptr;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int j = v * tpr + t;
@@ -183,7 +207,7 @@ __global__ void __launch_bounds__(WIDE ? WIDE_THREADS : NARROW_THREADS, blocks_p
       float2 f[4];
       unpack8<DT>(s[v], f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(__fmul2_rn(f[i], both(rstd)), w[v][i]);
+      for (int k = 0; k < 4; ++k) f[k] = __fmul2_rn(__fmul2_rn(f[k], both(rstd)), w[v][k]);
       if (a.y && mine) __stcs(yp + v * tpr, pack8<DT>(f));
       if (a.y8) {                    // 32 elements are four neighbouring lanes
         float am = amax8(f);
@@ -197,8 +221,6 @@ __global__ void __launch_bounds__(WIDE ? WIDE_THREADS : NARROW_THREADS, blocks_p
         }
       }
     }
-    sw.on();
-    yw.on();
   }
 }
 
@@ -211,18 +233,20 @@ __global__ void __launch_bounds__(WIDE ? WIDE_THREADS : NARROW_THREADS, blocks_p
   constexpr int STAGES = stages(V);
   wait_for_last_kernel();
   if (gridDim.x <= EARLY_BLOCKS) next_kernel_may_start();
-  const int threads = blockDim.x, rpb = WIDE ? 1 : NARROW_THREADS / tpr, t = WIDE ? threadIdx.x : threadIdx.x % tpr;
-  const int nv = a.N / 8, pieces = a.ds ? 3 : 2;
-  const long long step = (long long)gridDim.x * rpb;
-  long long row = (long long)blockIdx.x * rpb + (WIDE ? 0 : threadIdx.x / tpr), ahead = row;
+  const int threads = blockDim.x, t = WIDE ? threadIdx.x : threadIdx.x % tpr, nv = a.N / 8;
+  const Rows rows(a.rows, WIDE ? 1 : NARROW_THREADS / tpr, WIDE ? 0 : threadIdx.x / tpr);
+  const int stage = (a.ds ? 3 : 2) * V * threads;
   uint4* const own = ring + threadIdx.x;
-  float* const own_rstd = reinterpret_cast<float*>(ring + STAGES * pieces * V * threads) + threadIdx.x;   // of stage g: [g * threads]
-  Walk<FLAT> dw(a.dy, a.dys, row, step, t), sw(a.s, a.ss, row, step, t), ew(a.ds, a.dss, row, step, t), ow(a.dx, a.dxs, row, step, t);
-  auto fetch = [&](int stage) {
-    if (ahead < a.rows) {
-      const uint4 *const dp = dw.at(a.dys, ahead, a.inner), *const sp = sw.at(a.ss, ahead, a.inner);
-      const uint4* const ep = a.ds ? ew.at(a.dss, ahead, a.inner) : nullptr;
-      uint4* const to = own + stage * pieces * V * threads;
+  float* const own_rstd = reinterpret_cast<float*>(ring + STAGES * stage) + threadIdx.x;    // of stage g: [g * threads]
+  Walk<FLAT> dw(a.dy, a.dys, rows.first, rows.step, t), sw(a.s, a.ss, rows.first, rows.step, t);
+  Walk<FLAT> ew(a.ds, a.dss, rows.first, rows.step, t), ow(a.dx, a.dxs, rows.first, rows.step, t);
+  const float* rstds = a.rstd + rows.first;
+  auto fetch = [&](int i, int g) {               // its i-th row, into stage g
+    if (i < rows.count) {
+      const long long row = FLAT ? 0 : rows.first + i * rows.step;
+      const uint4 *const dp = dw.next(a.dys, row, a.inner), *const sp = sw.next(a.ss, row, a.inner);
+      const uint4* const ep = a.ds ? ew.next(a.dss, row, a.inner) : nullptr;
+      uint4* const to = own + g * stage;
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (v * tpr + t < nv) {
@@ -230,30 +254,27 @@ __global__ void __launch_bounds__(WIDE ? WIDE_THREADS : NARROW_THREADS, blocks_p
           copy16(to + (V + v) * threads, sp + v * tpr);
           if (a.ds) copy16(to + (2 * V + v) * threads, ep + v * tpr);
         }
-      copy4(own_rstd + stage * threads, a.rstd + ahead);
+      copy4(own_rstd + g * threads, rstds);
+      rstds += rows.step;
     }
-    dw.on();
-    sw.on();
-    ew.on();
-    ahead += step;
     copies_end();
   };
 #pragma unroll
-  for (int g = 0; g < STAGES - 1; ++g) fetch(g);
+  for (int g = 0; g < STAGES - 1; ++g) fetch(g, g);
   float2 w[V][4], acc[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (v * tpr + t < nv) load_weights<DT>(a.w, a.w32, v * tpr + t, w[v]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[v][i] = both(0.f);
+    for (int k = 0; k < 4; ++k) acc[v][k] = both(0.f);
   }
   const float inv_n = 1.f / (float)a.N;
-  int turn = 0, stage = 0;
-  for (long long first = (long long)blockIdx.x * rpb; first < a.rows; first += step, row += step, turn ^= 1) {
-    const bool live = row < a.rows;
+  int g = 0;
+  for (int i = 0; i < rows.rounds; ++i) {
+    const bool live = i < rows.count;
     copies_wait<STAGES - 2>();
-    const uint4* const from = own + stage * pieces * V * threads;
-    const float rs = live ? own_rstd[stage * threads] : 0.f;
+    const uint4* const from = own + g * stage;
+    const float rs = live ? own_rstd[g * threads] : 0.f;
     constexpr bool KEPT = V == 1;                // dy and s stay in registers; more vectors are read again
     uint4 d0[KEPT ? V : 1], x0[KEPT ? V : 1];
     float2 sum = both(0.f);
@@ -269,15 +290,15 @@ __global__ void __launch_bounds__(WIDE ? WIDE_THREADS : NARROW_THREADS, blocks_p
         unpack8<DT>(dv, d);
         unpack8<DT>(xv, x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 p = __fmul2_rn(d[i], __fmul2_rn(x[i], both(rs)));
-          acc[v][i] = __fadd2_rn(acc[v][i], p);
-          sum = __ffma2_rn(p, w[v][i], sum);
+        for (int k = 0; k < 4; ++k) {
+          const float2 p = __fmul2_rn(d[k], __fmul2_rn(x[k], both(rs)));
+          acc[v][k] = __fadd2_rn(acc[v][k], p);
+          sum = __ffma2_rn(p, w[v][k], sum);
         }
       }
-    const float c = row_sum<WIDE>(sum.x + sum.y, tpr, part[turn]) * inv_n;
+    const float c = row_sum<WIDE>(sum.x + sum.y, tpr, part[i & 1]) * inv_n;
     if (live) {
-      uint4* const out = ow.at(a.dxs, row, a.inner);
+      uint4* const out = ow.next(a.dxs, rows.first + i * rows.step, a.inner);
       const float2 xc = both(-rs * rs * c);
 #pragma unroll
       for (int v = 0; v < V; ++v)
@@ -286,33 +307,32 @@ __global__ void __launch_bounds__(WIDE ? WIDE_THREADS : NARROW_THREADS, blocks_p
           unpack8<DT>(KEPT ? d0[KEPT ? v : 0] : from[v * threads], d);
           unpack8<DT>(KEPT ? x0[KEPT ? v : 0] : from[(V + v) * threads], x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = both(0.f);
+          for (int k = 0; k < 4; ++k) e[k] = both(0.f);
           if (a.ds) unpack8<DT>(from[(2 * V + v) * threads], e);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)     // rs d w - x rs^2 c + e
-            d[i] = __ffma2_rn(x[i], xc, __ffma2_rn(__fmul2_rn(d[i], w[v][i]), both(rs), e[i]));
+          for (int k = 0; k < 4; ++k)     // rs d w - x rs^2 c + e
+            d[k] = __ffma2_rn(x[k], xc, __ffma2_rn(__fmul2_rn(d[k], w[v][k]), both(rs), e[k]));
           __stcs(out + v * tpr, pack8<DT>(d));
         }
     }
-    // into the stage that was read before this one
-    fetch(stage == 0 ? STAGES - 1 : stage - 1);
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
-    ow.on();
+    fetch(i + STAGES - 1, g == 0 ? STAGES - 1 : g - 1);   // into the stage that was read before this one
+    g = g + 1 == STAGES ? 0 : g + 1;
   }
   float* const out = a.partial + (long long)blockIdx.x * a.N;
   float2* const group = reinterpret_cast<float2*>(ring);           // narrow: over the ring, whose copies have landed
+  const int groups = WIDE ? 1 : NARROW_THREADS / tpr;
   copies_wait<0>();
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (!WIDE) {                     // the block's rows' shares of these columns, in their order
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) group[threadIdx.x * 4 + i] = acc[v][i];
+      for (int k = 0; k < 4; ++k) group[threadIdx.x * 4 + k] = acc[v][k];
       __syncthreads();
       if (threadIdx.x < tpr)
-        for (int k = 1; k < rpb; ++k)
+        for (int q = 1; q < groups; ++q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[v][i] = __fadd2_rn(acc[v][i], group[(k * tpr + t) * 4 + i]);
+          for (int k = 0; k < 4; ++k) acc[v][k] = __fadd2_rn(acc[v][k], group[(q * tpr + t) * 4 + k]);
     }
     const int j = v * tpr + t;
     if (j < nv && (WIDE || threadIdx.x < tpr)) {
@@ -345,23 +365,37 @@ __global__ void __launch_bounds__(DW_WARPS * 32) norm_dw_kernel(const float* par
 }
 
 // How a row is cut up: vectors of 8 elements per thread, threads per row, and whether a block has one row.
+//
+// Forward: four vectors a thread, which share the row's sum and addresses, but one while there are no more rows than SMs, so
+// that a row has as many threads as it can use.  1 / 2 / 4 vectors, bf16 with fp32 weights, us: 262144 x 128 26.7 / 21.0 / 23.2
+// (with a residual 49.3 / 48.5 / 44.3, to MXFP8 34.9 / 29.2 / 21.0), 131072 x 512 - / 48.3 / 44.6 (- / 95.0 / 87.0, - / 57.6 / 41.9),
+// 16384 x 4096 44.7 / 45.4 / 46.0 (92.4 / 89.9 / 85.7, 58.4 / 50.7 / 41.7); one row of 2048 4.1 / - / 5.5.
+// Gradients keep dw's sums beside the weights: four vectors where a row is part of a warp (262144 x 256 92.3 / 121 / 87.1; 600000 x
+// 64, one per thread, 56.5 and two 76), else as few as a block of 512 threads has room for (16384 x 4096 90.1 / 94.2 / -).
 struct Cut {
   int v, tpr;
   bool wide;
   int threads() const { return wide ? tpr : NARROW_THREADS; }
   int rows() const { return wide ? 1 : NARROW_THREADS / tpr; }     // of a block at a time
 };
-Cut cut_of(int N) {
-  const int nv = N / 8;
-  if (nv <= 128) {
-    const int v = nv <= 32 ? 1 : nv <= 64 ? 2 : 4;
+Cut cut_for(int nv, int v) {
+  if (nv <= 32 * v) {
     int tpr = 4;
     while (tpr * v < nv) tpr *= 2;
     return {v, tpr, false};
   }
-  const int v = nv <= WIDE_THREADS ? 1 : nv <= 2 * WIDE_THREADS ? 2 : 4;
   return {v, ((nv + v - 1) / v + 31) / 32 * 32, true};
 }
+Cut cut_of(const NormArgs& a) {
+  const int nv = a.N / 8;
+  if (a.rows <= SMS) return cut_for(nv, nv <= WIDE_THREADS ? 1 : nv <= 2 * WIDE_THREADS ? 2 : 4);
+  return cut_for(nv, nv <= 4 ? 1 : nv <= 8 ? 2 : 4);
+}
+Cut bwd_cut(int N) {
+  const int nv = N / 8;
+  return cut_for(nv, nv <= 8 ? 1 : nv <= 128 ? 4 : nv <= WIDE_THREADS ? 1 : nv <= 2 * WIDE_THREADS ? 2 : 4);
+}
+Cut cut_of(const NormBwdArgs& a) { return bwd_cut(a.N); }
 // As many blocks as the card takes at once by registers and shared memory, or as there are rows for.
 int blocks_for(long long rows, const Cut& c, int smem) {
   const int by_regs = threads_per_sm(c.v) / c.threads(), by_smem = 225 * 1024 / (smem + 1280);
@@ -371,7 +405,7 @@ int blocks_for(long long rows, const Cut& c, int smem) {
 int smem_of(const Cut& c, int pieces, int scalars) { return c.threads() * ring_bytes(c.v, pieces, scalars); }
 // The gradients' grid decides the order of dw's sums, so it goes by rows and N alone.
 int bwd_blocks(long long rows, int N) {
-  const Cut c = cut_of(N);
+  const Cut c = bwd_cut(N);
   return blocks_for(rows, c, smem_of(c, 3, 1));
 }
 
@@ -388,12 +422,16 @@ cudaError_t go(void (*kernel)(A, int), int most_smem, const A& a, const Cut& c, 
   }
   return launch_early(kernel, (unsigned)blocks, c.threads(), smem, st, 1, a, c.tpr);
 }
+template <int DT, int V, bool WIDE, bool FLAT, bool RES>
+cudaError_t run_norm(const NormArgs& a, const Cut& c, cudaStream_t st) {
+  static std::atomic<uint64_t> opted{0};
+  const int smem = smem_of(c, RES ? 2 : 1, 0);
+  return go(norm_kernel<DT, V, WIDE, FLAT, RES>, (WIDE ? WIDE_THREADS : NARROW_THREADS) * ring_bytes(V, RES ? 2 : 1, 0), a, c,
+            blocks_for(a.rows, c, smem), smem, opted, st);
+}
 template <int DT, int V, bool WIDE, bool FLAT>
 cudaError_t run(const NormArgs& a, const Cut& c, cudaStream_t st) {
-  static std::atomic<uint64_t> opted{0};
-  const int smem = smem_of(c, a.r ? 2 : 1, 0);
-  return go(norm_kernel<DT, V, WIDE, FLAT>, (WIDE ? WIDE_THREADS : NARROW_THREADS) * ring_bytes(V, 2, 0), a, c,
-            blocks_for(a.rows, c, smem), smem, opted, st);
+  return a.r ? run_norm<DT, V, WIDE, FLAT, true>(a, c, st) : run_norm<DT, V, WIDE, FLAT, false>(a, c, st);
 }
 template <int DT, int V, bool WIDE, bool FLAT>
 cudaError_t run(const NormBwdArgs& a, const Cut& c, cudaStream_t st) {
@@ -411,7 +449,7 @@ cudaError_t pick(const A& a, const Cut& c, cudaStream_t st) {
 }
 template <class A>
 cudaError_t pick(const A& a, int dtype, cudaStream_t st) {
-  const Cut c = cut_of(a.N);
+  const Cut c = cut_of(a);
   if (dtype == 0) return a.inner == 1 ? pick<0, true>(a, c, st) : pick<0, false>(a, c, st);
   return a.inner == 1 ? pick<1, true>(a, c, st) : pick<1, false>(a, c, st);
 }

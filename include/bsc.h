@@ -437,10 +437,11 @@ size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long 
  * Row r of x starts at element (r / inner) * stride + (r % inner) * inner_stride, and so for residual, y and sum: inner = 1
  * for evenly spaced rows, inner = the heads for the heads of a slice of a fused projection.  Strides are multiples of 8
  * (ignored where they do not count: a single row or group), an output's not 0.  N is a multiple of 8 (of 32 with
- * y_e4m3) and at most BSC_NORM_MAX_N.  Pointers are 16-byte aligned, rstd 4-byte.
+ * y_e4m3) and at most BSC_NORM_MAX_N, rows below BSC_NORM_MAX_ROWS.  Pointers are 16-byte aligned, rstd 4-byte.
  * y or sum may be x or residual itself (same strides); no other outputs overlap.  rows or N of 0: BSC_OK, nothing is done.
  */
 #define BSC_NORM_MAX_N 16384
+#define BSC_NORM_MAX_ROWS (1LL << 38)
 typedef struct {
   const void* x;          /* [in] `dtype` */
   const void* residual;   /* [in] `dtype`, or NULL */

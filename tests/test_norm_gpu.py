@@ -56,7 +56,9 @@ def check_mx(codes, sc, y, rule):
 
 
 SIZES = [(1, 8), (3, 24), (2, 32), (5, 40), (130, 64), (67, 128), (9, 136), (33, 256), (17, 264), (4, 512), (300, 520),
-         (3, 1024), (2, 1032), (7, 2048), (321, 2560), (2, 4096), (3, 4104), (2, 8192), (3, 8200), (2, 16384)]
+         (3, 1024), (2, 1032), (7, 2048), (321, 2560), (2, 4096), (3, 4104), (2, 8192), (3, 8200), (2, 16384),
+         # more rows than SMs: other cuts of a row
+         (154, 32), (200, 72), (153, 128), (170, 136), (160, 1024), (155, 4104), (153, 8192), (157, 16384)]
 
 
 @pytest.mark.parametrize("rows,N", SIZES)

@@ -149,7 +149,7 @@ def _norm(ops, **kw):
     (dict(eps=-1e-6), UNSUPPORTED), (dict(eps=math.inf), UNSUPPORTED), (dict(eps=math.nan), UNSUPPORTED),
     (dict(x=FAKE + 8), ALIGN), (dict(residual=FAKE + 2), ALIGN), (dict(y=FAKE + 8), ALIGN), (dict(rstd=FAKE + 2), ALIGN),
     (dict(y_e4m3=FAKE + 8), ALIGN), (dict(x_stride=252), ALIGN), (dict(residual_inner_stride=12), ALIGN),
-    (dict(y_stride=0), SHAPE), (dict(sum_inner_stride=0), SHAPE), (dict(rows=1 << 40), UNSUPPORTED)])
+    (dict(y_stride=0), SHAPE), (dict(sum_inner_stride=0), SHAPE), (dict(rows=1 << 38), UNSUPPORTED), (dict(rows=(1 << 38) - 1, x=0), NULL)])
 def test_norm_refusals(ops, kw, want):  # noqa: F811
     assert ops.lib.rms_norm(ctypes.byref(_norm(ops, **kw)), None) == want
 
