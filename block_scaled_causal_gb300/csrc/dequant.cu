@@ -1,8 +1,9 @@
 // MXFP8 rows back to values: element * 2^(scale - 127), exact in fp32 and rounded once to 16 bits.
 //
 // Memory-bound: 1 byte in, 2 out per element.  A thread takes 8 elements at a time, so that a warp's loads and stores are
-// whole lines (16 elements, stored in two pieces of 16 bytes, took 13.6 us for 16.8 M elements in place of XX), DQ_ITEMS of them
-// with all loads ahead of the first use.
+// whole lines, DQ_ITEMS of them with all loads ahead of the first use.  For 16.8 M elements of Q, cold: 9.9 us; with 16 elements
+// per thread, stored in two pieces of 16 bytes, 13.6; with 8 items and 256 threads 12.2 (one wave and a little); of that 2 us were
+// divisions for the scales' place.  33.6 M elements in one order with their scales: 15.6 us, 6.5 TB/s.
 #include "cache.cuh"
 
 namespace bsc {

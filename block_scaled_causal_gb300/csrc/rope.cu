@@ -12,7 +12,10 @@
 // elements of a head (16 bytes), D / 8 lanes are a head, and half pairs exchange their packed elements with the lane rot / 16
 // away; four neighbouring lanes are an MX block.  From head to head an address moves by one addition.
 //
-// What bounds it: memory, with the loads of ROPE_BATCH heads ahead of the first use.
+// What bounds it: memory in 16 bits (32K tokens of 16 + 4 heads 47.9 us, 7.0 TB/s of 335 MB, cold); to MXFP8 and into the cache
+// the instructions too (8192 x 32 heads 20.6 us for 101 MB at 2.7 instructions per clock; prompts of 10K tokens 29.9 us for 173 MB).
+// The loads of ROPE_BATCH heads are ahead of their first use, those of the first heads ahead of the angles (100.6 us for both
+// directions, 102.4 behind them).  2 / 4 / 8 heads per batch: 116 / 104 / 114 us in a graph.
 #include "cache.cuh"
 
 namespace bsc {
@@ -230,7 +233,8 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, 8) rope_kernel(const RopeArgs
 }
 
 using Kernel = void (*)(RopeArgs, int);
-// Heads of a token are shared by several warps while there are fewer tokens than the card takes warps at once.
+// Heads of a token are shared by several warps while the card has room for them at once; each works the angles out again (3063
+// tokens of 25 heads, both directions: one warp 20.5 us, two 22.5, four 26.7).
 cudaError_t launch(Kernel k, const RopeArgs& a, int heads, cudaStream_t st) {
   const long long tokens = (long long)a.B * a.T;
   const int rpw = 32 / (a.D / 8);
