@@ -432,7 +432,9 @@ size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long 
  *   rstd = (mean_n s_n^2 + eps)^(-1/2),  y_n = s_n * rstd * weight_n
  * in fp32 (a sum of squares beyond 3.4e38 is infinite: rows up to 2^56 in magnitude are taken), each output rounded once.
  * y goes out in `dtype` (y), as MXFP8 rows (y_e4m3 [rows][N] and y_sc [rows][N/32], the quantisation rule at the top of
- * this file applied to the fp32 y), or both.  A row with a NaN or an infinity comes out as NaN where the formula says so.
+ * this file applied to the fp32 y), or both.  A row with a NaN or an infinity comes out as NaN where the formula says so (as
+ * does a row of zeros with eps 0).  The order of a row's sum, and so its last bits, depends on N and on whether there are
+ * more than 152 rows; on nothing else.
  *
  * Row r of x starts at element (r / inner) * stride + (r % inner) * inner_stride, and so for residual, y and sum: inner = 1
  * for evenly spaced rows, inner = the heads for the heads of a slice of a fused projection.  Strides are multiples of 8
@@ -648,7 +650,8 @@ bsc_status mx_cache_bounds(const bsc_mx_cache_bounds_params* p, bsc_stream_t str
  *   score = 2^e (sum_d u_d max_d - l_d min_d),  u = sum over the KV head's query heads of max(q_d, 0), l of max(-q_d, 0),
  * u and l rounded to 0..127 with one power of two per query and KV head (the largest in [64, 128), 127 at most).  Scores are
  * exact in fp32; equal ones are taken in the pages' order.  A page whose exps is 0xFF scores above all others; one whose
- * id is out of range comes last and is not attended (0x201).  A query with a NaN or an infinity scores every page 0.
+ * id is out of range comes last and is not attended (0x201).  A query with a NaN or an infinity, or whose sums u and l pass
+ * fp32's range or are all below 2^-126, scores every page 0.
  * O and LSE are those of mx_cache_attn over the tokens of the chosen pages.
  *   blocks [out] int32 [B][T][Hkv][top], or NULL: the chosen pages' numbers (position / page_size) in ascending order,
  *     then -1.
