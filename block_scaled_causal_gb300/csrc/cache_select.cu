@@ -155,9 +155,9 @@ __device__ __forceinline__ Seen seen_by(const SelectArgs& a, int b, int t) {
 // The scores pass through the first block's shared memory, or the workspace where a table has more pages than that holds.
 // The threshold, the score of the last page taken, is found by histograms: the scores in question are spread evenly
 // over 256 bins between their least and their largest, and those of the bin that holds the threshold are the next round's,
-// until they are all equal.  Scores that are spread by chance take two or three rounds (a bin of 512 has a few); a round takes
-// at least the largest or the least away, and a bin is 1/255 of its round's range, so that no values of fp32 take more than
-// 32.  (Two bits of the threshold at a time, sixteen counts of all scores, took 8 us for 512 pages.)  A thread then has a
+// until all of that bin are taken or all of them are equal.  Scores that are spread by chance take one to three rounds (a bin of
+// 512 has a few), about 0.6 us each; a round takes at least the largest or the least away, and a bin is 1/255 of its round's
+// range, so that no values of fp32 take more than 32.  (Two bits of the threshold at a time, sixteen counts of all scores, took 8 us for 512 pages.)  A thread then has a
 // run of neighbouring pages, so that a scan over the threads gives the list's order.
 constexpr int CHOOSE_THREADS = 256, CHOOSE_WARPS = CHOOSE_THREADS / 32, BINS = 256;
 constexpr int HELD_PAGES = 10240;                // scores in shared memory at most: 40 KB
@@ -301,24 +301,29 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) cache_choose_kernel(const Sele
     if (seen.past) report(a.dev_status, CACHE_BAD_LEN);
     a.lens[row] = k > 0 ? (k - 1) * a.page_size + seen.tokens - (n - 1) * a.page_size : 0;   // the last page is always listed
   }
-  auto put = [&](int at, int p) {
-    const int page = __ldca(table + p);
+  auto put = [&](int at, int p, int page) {
     list[at] = page >= 0 && page < a.num_pages ? page * a.pages_per_page + (int)h : -1;
     if (blocks) blocks[at] = p;
   };
   if (blocks)
     for (int i = k + threadIdx.x; i < a.top; i += CHOOSE_THREADS) blocks[i] = -1;
   if (n == k) {
-    for (int i = threadIdx.x; i < k; i += CHOOSE_THREADS) put(i, i);
+    for (int i = threadIdx.x; i < k; i += CHOOSE_THREADS) put(i, i, __ldca(table + i));
     return;
   }
+
+  // a thread's run of pages, the first two ids of it on their way
+  const int run = (n + CHOOSE_THREADS - 1) / CHOOSE_THREADS, p0 = min((int)threadIdx.x * run, n), p1 = min(p0 + run, n);
+  const int id0 = p0 < p1 ? __ldca(table + p0) : -1, id1 = p0 + 1 < p1 ? __ldca(table + p0 + 1) : -1;
 
   // ---- the threshold among pages [first, n - last): `want` of those with score `cut`, and all above it ----
   const int from = a.first, to = n - a.last;
   int want = k - a.first - a.last;
   float cut = INFINITY, base = 0.f, per = 0.f;   // the round before: bins of (score - base) * per
+  bool whole = false;                            // all of `bin` is taken, and what lies above it
   float lo = -INFINITY, hi = INFINITY;
   int bin = 0, turn = 0;
+  auto place_of = [](int bin) { return (bin & 7) * (BINS / 8) + (bin >> 3); };   // a lane's 8 bins in 8 places of one bank
   auto bin_of = [](float s, float base, float per) { return min((int)((s - base) * per), BINS - 1); };
   for (; want > 0; turn ^= 1) {
     uint32_t least = 0xFFFFFFFFu, most = 0u;
@@ -352,14 +357,14 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) cache_choose_kernel(const Sele
     per = (float)(BINS - 1) / (hi - lo);
     for (int p = from + threadIdx.x; p < to; p += CHOOSE_THREADS) {
       const float s = scores[p];
-      if (s >= lo && s <= hi) atomicAdd(&bins[turn][bin_of(s, base, per)], 1);
+      if (s >= lo && s <= hi) atomicAdd(&bins[turn][place_of(bin_of(s, base, per))], 1);
     }
     __syncthreads();
     // the bin of the want-th largest: every warp on its own, a lane with 8 bins, lane 0 the uppermost
     int c[8], mine = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      c[i] = bins[turn][BINS - 1 - (lane * 8 + i)];
+      c[i] = bins[turn][place_of(BINS - 1 - (lane * 8 + i))];
       mine += c[i];
     }
     int upto = mine;
@@ -369,37 +374,46 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) cache_choose_kernel(const Sele
       if (lane >= o) upto += y;
     }
     const int who = __ffs(__ballot_sync(0xFFFFFFFFu, upto >= want)) - 1;
-    int above = upto - mine, which = 0;
-    bool found = false;
+    int above = upto - mine, which = 0, in_it = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (!found) {
+      if (in_it == 0) {
         if (above + c[i] >= want) {
           which = BINS - 1 - (lane * 8 + i);
-          found = true;
+          in_it = c[i];
         } else {
           above += c[i];
         }
       }
     bin = __shfl_sync(0xFFFFFFFFu, which, who);
     want -= __shfl_sync(0xFFFFFFFFu, above, who);
+    if (want == __shfl_sync(0xFFFFFFFFu, in_it, who)) {
+      whole = true;
+      want = 0;
+    }
   }
 
   // ---- the list ----
-  const int run = (n + CHOOSE_THREADS - 1) / CHOOSE_THREADS, p0 = min((int)threadIdx.x * run, n), p1 = min(p0 + run, n);
-  auto taken = [&](int p) { return p < from || p >= to || scores[p] > cut; };
+  // 2: taken, 1: of those with the threshold's score
+  auto kind = [&](int p) {
+    if (p < from || p >= to) return 2;
+    const float s = scores[p];
+    if (whole) return s > hi || (s >= lo && bin_of(s, base, per) >= bin) ? 2 : 0;
+    return s > cut ? 2 : s == cut ? 1 : 0;
+  };
   int at = 0, ties = 0;
   for (int p = p0; p < p1; ++p) {
-    if (taken(p)) ++at;
-    else ties += scores[p] == cut;
+    const int is = kind(p);
+    at += is == 2;
+    ties += is == 1;
   }
   int all;
   block_scan(at, ties, sums, all);
   at += min(ties, want);
   for (int p = p0; p < p1; ++p) {
-    const bool t1 = taken(p), tie = !t1 && scores[p] == cut;
-    if (t1 || (tie && ties < want)) put(at++, p);
-    ties += tie;
+    const int is = kind(p);
+    if (is == 2 || (is == 1 && ties < want)) put(at++, p, p == p0 ? id0 : p == p0 + 1 ? id1 : __ldca(table + p));
+    ties += is == 1;
   }
 }
 
