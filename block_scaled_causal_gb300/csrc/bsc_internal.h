@@ -174,7 +174,6 @@ struct RopeArgs {
   const int32_t* pos;      // nullptr: token t is at position t
   long long pos_b, pos_t;  // its strides; pos_t 0: of the first token
   int B, T, Hq, Hkv, D;    // Hkv 0: no k
-  int tt;                  // tokens per block, set by the launcher
   int rule;
   CachePools c;            // cache form
   CacheTable pt;

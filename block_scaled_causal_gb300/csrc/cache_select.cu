@@ -157,14 +157,14 @@ __device__ __forceinline__ Seen seen_by(const SelectArgs& a, int b, int t) {
 // over 256 bins between their least and their largest, and those of the bin that holds the threshold are the next round's,
 // until all of that bin are taken or all of them are equal.  Scores that are spread by chance take one to three rounds (a bin of
 // 512 has a few), about 0.6 us each; a round takes at least the largest or the least away, and a bin is 1/255 of its round's
-// range, so that no values of fp32 take more than 32.  (Two bits of the threshold at a time, sixteen counts of all scores, took 8 us for 512 pages.)  A thread then has a
-// run of neighbouring pages, so that a scan over the threads gives the list's order.
+// range, so that no values of fp32 take more than 32.  (Two bits of the threshold at a time, sixteen counts of all scores, took
+// 8 us for 512 pages.)  A thread then has a run of neighbouring pages, so that a scan over the threads gives the list's order.
 constexpr int CHOOSE_THREADS = 256, CHOOSE_WARPS = CHOOSE_THREADS / 32, BINS = 256;
 constexpr int HELD_PAGES = 10240;                // scores in shared memory at most: 40 KB
 constexpr float FIRST_SCORE = 0x1p126f, LAST_SCORE = -0x1p126f;   // of a page with a NaN, of one that is not there
 
-// Exclusive sums over the threads of two counts, and their totals.
-__device__ __forceinline__ void block_scan(int& x, int& y, int (&sums)[2][CHOOSE_WARPS], int& all_x) {
+// Exclusive sums over the threads of two counts.
+__device__ __forceinline__ void block_scan(int& x, int& y, int (&sums)[2][CHOOSE_WARPS]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, own_x = x, own_y = y;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -181,15 +181,12 @@ __device__ __forceinline__ void block_scan(int& x, int& y, int (&sums)[2][CHOOSE
   __syncthreads();
   x -= own_x;
   y -= own_y;
-  all_x = 0;
 #pragma unroll
-  for (int k = 0; k < CHOOSE_WARPS; ++k) {
+  for (int k = 0; k + 1 < CHOOSE_WARPS; ++k)
     if (k < warp) {
       x += sums[0][k];
       y += sums[1][k];
     }
-    all_x += sums[0][k];
-  }
 }
 // Floats as unsigned integers of the same order, and back.
 __device__ __forceinline__ uint32_t key_of(float s) {
@@ -407,8 +404,7 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) cache_choose_kernel(const Sele
     at += is == 2;
     ties += is == 1;
   }
-  int all;
-  block_scan(at, ties, sums, all);
+  block_scan(at, ties, sums);
   at += min(ties, want);
   for (int p = p0; p < p1; ++p) {
     const int is = kind(p);
