@@ -252,3 +252,51 @@ def test_quantise_and_back(ops):
         y = ops.mxfp8_dequantize(*ops.mxfp8_quantize_qk_rowwise(t.cuda(), layout), layout)
         codes, sc = mx.mx_quantize(f64(t), 32, "floor")
         assert np.array_equal(f64(y), mx.mx_dequantize(codes, sc, 32))
+
+
+def test_large_offsets(ops):
+    """Rows that start past 2^32 elements: those of a call on the last rows alone, bit for bit."""
+    rows, N = 540000, 8192                             # 4.4e9 elements
+    x = torch.empty((rows, N), dtype=torch.bfloat16, device="cuda")
+    x[-300:].normal_()
+    x[:-300] = 1.0
+    w = torch.randn(N, device="cuda")
+    y, _, rstd, y8, sc = ops.rms_norm(x, w, EPS, y8_out=True)
+    want = ops.rms_norm(x[-300:], w, EPS, y8_out=True)
+    for a, b in zip((y, rstd, y8, sc), (want[0],) + want[2:]):
+        assert torch.equal(a[-300:], b)
+    assert torch.equal(y[0], y[rows - 301])
+    dx, _ = ops.rms_norm_bwd(y, x, w, rstd, dx=y)
+    assert dx is y and torch.equal(dx[-300:], ops.rms_norm_bwd(want[0], x[-300:], w, want[2])[0])
+    del x, dx, y
+    z = ops.mxfp8_dequantize(y8, sc, None)
+    assert torch.equal(z[-300:], ops.mxfp8_dequantize(want[3], want[4], None)) and torch.equal(z[0], z[rows - 301])
+
+
+def test_host_threads(ops):
+    """Calls of several host threads, each on its own stream, give the single call's bits."""
+    import threading
+    xs = [torch.randn((n, 1024), device="cuda").bfloat16() for n in (1, 300, 2000)]
+    w = torch.randn(1024, device="cuda").bfloat16()
+
+    def both(x, stream=None):
+        y, s, rstd = ops.rms_norm(x, w, EPS, residual=x, stream=stream)
+        return (y, s, rstd) + ops.rms_norm_bwd(y, s, w, rstd, ds=x, stream=stream)
+
+    want = [both(x) for x in xs]
+    torch.cuda.synchronize()
+    got = [[] for _ in xs]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got[i].append(both(xs[i], s))
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for outs, ref in zip(got, want):
+        assert len(outs) == 20 and all(torch.equal(a, b) for o in outs for a, b in zip(o, ref))

@@ -253,3 +253,31 @@ def test_streams_and_graph(ops):
         t.zero_()
     g.replay()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_large_offsets(ops):
+    """Tokens that start past 2^32 bytes, at positions of their own: those of a call on the last tokens alone."""
+    T, H = 70000, 256                                  # 2.3e9 elements
+    q = torch.empty((1, T, H, 128), dtype=torch.bfloat16, device="cuda")
+    q[:, -40:].normal_()
+    q[:, :-40] = 1.0
+    r = ops.Rope(128)
+    tail = q[:, -40:].clone()
+    start = i32([T - 40])
+    q8, qs, _, _ = ops.mxfp8_rope_quantize_qk(q, None, r)
+    want = ops.mxfp8_rope_quantize_qk(tail, None, r, start)
+    assert torch.equal(q8[:, -40:], want[0]) and torch.equal(qs[:, :, -40:], want[1])
+    y, _ = ops.rope(q, None, r, q_out=q)
+    assert y is q and torch.equal(q[:, -40:], ops.rope(tail, None, r, start)[0])
+    assert torch.equal(q[:, 1000], ops.rope(torch.ones_like(q[:, :1]), None, r, i32([1000]))[0][:, 0])
+
+
+def test_few_tokens_share_their_heads(ops):
+    """A token's heads go to one warp or to several: the same bits."""
+    rng = np.random.default_rng(12)
+    r = ops.Rope(64)
+    q, k = act(rng, 1, 3000, 33, 64, "bf16", 0), act(rng, 1, 3000, 7, 64, "bf16", 0)
+    yq, yk = ops.rope(q, k, r)
+    for t in (0, 7, 2999):
+        a, b = ops.rope(q[:, t:t + 1], k[:, t:t + 1], r, i32([t]))
+        assert torch.equal(a, yq[:, t:t + 1]) and torch.equal(b, yk[:, t:t + 1])

@@ -370,3 +370,68 @@ def test_rotation_shifts_nothing(ops):
     size = 2.0 ** -3 * 128 ** -0.5 * np.linalg.norm(nq, axis=-1).max() * np.linalg.norm(nk, axis=-1).max()
     assert (la - lc).abs().max().item() <= size + 1e-3
     assert (a.float() - c.float()).abs().max().item() <= (np.exp(2 * size) - 1 + 2.0 ** -7) * v.abs().max().item()
+
+
+def test_large_offsets(ops):
+    """Pages that start past 2^32 bytes of the pools give what pages side by side give."""
+    pages, page, Hkv, apart = 9, 16, 1, 1 << 19
+    big = []
+    for n in (64, 4, 64, 4):
+        buf = torch.zeros(((pages - 1) * apart + 1) * page * n, dtype=torch.uint8, device="cuda")
+        big.append(buf.as_strided((pages, Hkv, page, n), (apart * page * n, page * n, n, 1)))
+    big = ops.MxCache(*big, fmt=1)
+    small = ops.mx_cache_alloc(pages, page, Hkv, 128, 1)
+    g = torch.Generator().manual_seed(21)
+    x = torch.randn((1, pages * page, 1, 128), generator=g).bfloat16().cuda()
+    table, lens = torch.arange(pages, dtype=torch.int32, device="cuda").flip(0).view(1, -1).contiguous(), i32([pages * page])
+    q, r = make_q(17, 1, pages * page, 4, 128, "bf16", 0), ops.Rope(128)
+    got = []
+    for c in (big, small):
+        b = ops.mx_cache_bounds_alloc(c)
+        rq = ops.mx_cache_write_rope(c, q, x, x.flip(1), r, table, lens)
+        ops.mx_cache_bounds(c, b, table, lens, pages * page)
+        got.append((rq, b.codes, b.exps) + ops.mx_cache_sparse_attn(rq[:, -1:], c, b, table, lens, 4))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert torch.isfinite(got[0][4]).all()
+
+
+def test_sizes_of_nothing(ops):
+    f = Filled(ops, 22, [40, 0], 2, 64, 1, 16)
+    b = all_bounds(ops, f)
+    q = make_q(1, 2, 1, 4, 64, "bf16", 0)
+    o, lse, blocks = ops.mx_cache_sparse_attn(q[:, :0], f.cache, b, f.table, f.seq, 2)
+    assert o.shape == (2, 0, 4, 64) and lse.shape == (2, 4, 0) and blocks.shape == (2, 0, 2, 2)
+    o, lse, blocks = ops.mx_cache_sparse_attn(q[:0], f.cache, b, f.table[:0], f.seq[:0], 2)
+    assert o.shape == (0, 1, 4, 64) and blocks.shape == (0, 1, 2, 2)
+    before = b.codes.clone()
+    ops.mx_cache_bounds(f.cache, b, f.table, f.seq, 0)
+    ops.mx_cache_bounds(f.cache, b, f.table, f.seq, 5, i32([0, 0]))
+    assert torch.equal(b.codes, before)
+    r = ops.Rope(64)
+    assert ops.mx_cache_write_rope(f.cache, q[:, :0], q[:, :0, :2], q[:, :0, :2], r, f.table, f.seq).shape == (2, 0, 4, 64)
+
+
+def test_host_threads(ops):
+    """Calls of several host threads, each on its own stream, give the single call's bits."""
+    import threading
+    f = Filled(ops, 23, [700, 290, 33], 2, 64, 0, 16)
+    b = all_bounds(ops, f)
+    qs = [make_q(30 + i, 3, 1 + i, 8, 64, "fp16", 0) for i in range(3)]
+    want = [ops.mx_cache_sparse_attn(q, f.cache, b, f.table, f.seq, 7) for q in qs]
+    torch.cuda.synchronize()
+    got = [[] for _ in qs]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got[i].append(ops.mx_cache_sparse_attn(qs[i], f.cache, b, f.table, f.seq, 7, stream=s))
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for outs, ref in zip(got, want):
+        assert len(outs) == 20 and all(torch.equal(x, y) for o in outs for x, y in zip(o, ref))
