@@ -969,10 +969,13 @@ def rms_norm_bwd(dy, s, weight, rstd, ds=None, dx=None, dweight=None, workspace=
     return dx, dweight
 
 
-def mxfp8_dequantize(x, sc, layout=BSHD, dtype=torch.bfloat16, out=None, stream=None):
-    """MXFP8 rows back to values: x uint8 [B, S, H, D] (SBHD: [S, B, H, D]) with sc [B, H, S, D/32], as the rowwise
-    quantisers return them, or [..., N] with sc [..., N/32], as rms_norm does (x not 4-D, or 4-D with such scales and
-    layout=None)."""
+_UNSAID = object()
+
+
+def mxfp8_dequantize(x, sc, layout=_UNSAID, dtype=torch.bfloat16, out=None, stream=None):
+    """MXFP8 rows back to values.  layout BSHD or SBHD: x uint8 [B, S, H, D] or [S, B, H, D] with sc [B, H, S, D/32], as the
+    rowwise quantisers return them.  None: x [..., N] with sc [..., N/32], as rms_norm does.  A 4-D x may be either, so its
+    layout has to be said; any other is taken for the second."""
     dev = x.get_device()
     if stream is not None or dev < 0 or _current_device() != dev:
         with _elsewhere_of(x, "x", stream):
@@ -984,7 +987,11 @@ def mxfp8_dequantize(x, sc, layout=BSHD, dtype=torch.bfloat16, out=None, stream=
         if t.dtype is not torch.uint8 or t.get_device() != dev or not t.is_contiguous():
             raise ValueError("%s must be a contiguous CUDA uint8 tensor on one device with the other" % n)
     shape = x.shape
-    if len(shape) == 4 and layout is not None:
+    if len(shape) != 4 and layout is _UNSAID:
+        layout = None
+    if layout is not None:
+        if layout is _UNSAID or len(shape) != 4:
+            raise ValueError("a 4-D x needs its layout, BSHD, SBHD or None; any other has None")
         B, S, H, D = shape
         if layout == SBHD:
             B, S = S, B

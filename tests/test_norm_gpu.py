@@ -182,7 +182,9 @@ def test_refusals(ops):
               lambda: ops.rms_norm(x, w, y_out=False), lambda: ops.rms_norm(x, w, rstd=r[:2]), lambda: ops.rms_norm(x.cpu(), w),
               lambda: ops.rms_norm(x.t().contiguous().t(), w), lambda: ops.rms_norm_bwd(x, x, w, r.half()),
               lambda: ops.rms_norm_bwd(x, x, w, r, ds=x.half()), lambda: ops.mxfp8_dequantize(x, x),
-              lambda: ops.mxfp8_dequantize(x.view(torch.uint8), x.view(torch.uint8)[:, :2], layout=0)):
+              lambda: ops.mxfp8_dequantize(x.view(torch.uint8), x.view(torch.uint8)[:, :2], layout=0),
+              lambda: ops.mxfp8_dequantize(x.view(torch.uint8).view(1, 4, 4, 32), x.view(torch.uint8)[0, :16].view(1, 4, 4, 1)),
+              lambda: ops.mxfp8_dequantize(x.view(torch.uint8).view(1, 4, 4, 32), x.view(torch.uint8)[0, :16].view(1, 4, 4, 1), 2)):
         with pytest.raises(ValueError):
             f()
     for f in (lambda: ops.rms_norm(x[:, :60].contiguous(), w[:60]), lambda: ops.rms_norm(x, w, -1.0),
