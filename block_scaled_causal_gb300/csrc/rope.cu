@@ -12,8 +12,9 @@
 // elements of a head (16 bytes), D / 8 lanes are a head, and half pairs exchange their packed elements with the lane rot / 16
 // away; four neighbouring lanes are an MX block.  From head to head an address moves by one addition.
 //
-// What bounds it: memory in 16 bits (32K tokens of 16 + 4 heads 47.9 us, 7.0 TB/s of 335 MB, cold); to MXFP8 and into the cache
-// the instructions too (8192 x 32 heads 20.6 us for 101 MB at 2.7 instructions per clock; prompts of 10K tokens 29.9 us for 173 MB).
+// What bounds it: memory.  In 16 bits 32K tokens of 16 + 4 heads take 47.9 us cold (7.0 TB/s of 335 MB); to MXFP8 65536 tokens of
+// 16 + 16 heads 131 us (93% of the copy rate), 8192 of them 19.0 (80%: 1.7 waves of warps, 2.7 instructions per clock; interleaved
+// pairs, which exchange nothing, 18.8); prompts of 10K tokens into the cache 29.9 us for 173 MB.
 // The loads of ROPE_BATCH heads are ahead of their first use, those of the first heads ahead of the angles (100.6 us for both
 // directions, 102.4 behind them).  2 / 4 / 8 heads per batch: 116 / 104 / 114 us in a graph.
 #include "cache.cuh"
