@@ -283,7 +283,9 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) cache_choose_kernel(const Sele
         for (int o = LPP / 2; o; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
         if (part == 0 && p < p_last) {
           if (page[i] < 0) report(a.dev_status, CACHE_BAD_PAGE);
-          out[p] = page[i] < 0 ? LAST_SCORE : e8[i] == 0xFFu ? FIRST_SCORE : (float)d * scale_value(e8[i]);
+          // exponents that no bounds have (their buffer was never filled in) count as the nearest that they have: no score is
+          // infinite or so small that a bin's width is not
+          out[p] = page[i] < 0 ? LAST_SCORE : e8[i] == 0xFFu ? FIRST_SCORE : (float)d * scale_value(min(max(e8[i], 27u), 227u));
         }
       }
     }
@@ -408,7 +410,8 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) cache_choose_kernel(const Sele
   at += min(ties, want);
   for (int p = p0; p < p1; ++p) {
     const int is = kind(p);
-    if (is == 2 || (is == 1 && ties < want)) put(at++, p, p == p0 ? id0 : p == p0 + 1 ? id1 : __ldca(table + p));
+    // (`at` stays below k unless another call writes to the workspace meanwhile)
+    if ((is == 2 || (is == 1 && ties < want)) && at < k) put(at++, p, p == p0 ? id0 : p == p0 + 1 ? id1 : __ldca(table + p));
     ties += is == 1;
   }
 }

@@ -649,7 +649,8 @@ bsc_status mx_cache_bounds(const bsc_mx_cache_bounds_params* p, bsc_stream_t str
  * (the page of p among them), and of the others those with the largest
  *   score = 2^e (sum_d u_d max_d - l_d min_d),  u = sum over the KV head's query heads of max(q_d, 0), l of max(-q_d, 0),
  * u and l rounded to 0..127 with one power of two per query and KV head (the largest in [64, 128), 127 at most).  Scores are
- * exact in fp32; equal ones are taken in the pages' order.  A page whose exps is 0xFF scores above all others; one whose
+ * exact in fp32; equal ones are taken in the pages' order.  An exps below 27 or from 228 to 254, which mx_cache_bounds does not
+ * write, counts as 27 or 227.  A page whose exps is 0xFF scores above all others; one whose
  * id is out of range comes last and is not attended (0x201).  A query with a NaN or an infinity, or whose sums u and l pass
  * fp32's range or are all below 2^-126, scores every page 0.
  * O and LSE are those of mx_cache_attn over the tokens of the chosen pages.

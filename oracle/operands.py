@@ -93,6 +93,6 @@ def choose(q, codes, exps, pages, tokens, page_size, top, first, last):
             rank, score = 2, 0.0
         else:
             c = codes[pages[i]].astype(np.float64)
-            rank, score = 1, float(np.ldexp(u @ c[1] - l @ c[0], int(exps[pages[i]]) - 127))
+            rank, score = 1, float(np.ldexp(u @ c[1] - l @ c[0], min(max(int(exps[pages[i]]), 27), 227) - 127))
         keys.append((-rank, -score, i))
     return sorted(i for _, _, i in sorted(keys)[:top])

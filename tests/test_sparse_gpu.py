@@ -179,6 +179,22 @@ def test_queries_that_score_nothing(ops):
     assert torch.isfinite(o[0, 0]).all() and torch.isnan(o[0, 1, 0]).all() and torch.isfinite(o[0, 1, 1]).all()
 
 
+@pytest.mark.parametrize("exps", ["all", "tiny", "huge", "zero"])
+def test_bounds_that_were_never_made(ops, exps):
+    """Whatever the bounds' buffers hold, the choice ends, and is the formula's."""
+    f, b = repeated(ops, 1500, 16, 2, 64, 1, 30, 24)
+    b = random_bounds(ops, f.cache, 25)
+    if exps == "zero":
+        b.codes.zero_()
+        b.exps.zero_()
+    elif exps != "all":
+        b.exps.copy_(b.exps % 27 if exps == "tiny" else 228 + b.exps % 27)
+    q = make_q(8, 1, 1, 4, 64, "bf16", 0)
+    for top in (3, 64, 1400):
+        out = ops.mx_cache_sparse_attn(q, f.cache, b, f.table, f.seq, top)
+        check_sparse(ops, f, b, q, out, [1], 0, top, 1, 1)
+
+
 def test_nan_pages_are_taken(ops):
     f = Filled(ops, 13, [320], 1, 128, 1, 16)
     f.cache.k_sc[f.table[0, 9].item(), 0, 2, 1] = 0xFF
