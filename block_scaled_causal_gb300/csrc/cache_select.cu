@@ -321,10 +321,12 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) cache_choose_kernel(const Sele
   float cut = INFINITY, base = 0.f, per = 0.f;   // the round before: bins of (score - base) * per
   bool whole = false;                            // all of `bin` is taken, and what lies above it
   float lo = -INFINITY, hi = INFINITY;
-  int bin = 0, turn = 0;
+  int bin = 0;
+  constexpr int MOST_ROUNDS = 64;                // never reached, unless another call writes to the workspace's scores meanwhile
   auto place_of = [](int bin) { return (bin & 7) * (BINS / 8) + (bin >> 3); };   // a lane's 8 bins in 8 places of one bank
   auto bin_of = [](float s, float base, float per) { return min((int)((s - base) * per), BINS - 1); };
-  for (; want > 0; turn ^= 1) {
+  for (int round = 0; want > 0 && round < MOST_ROUNDS; ++round) {
+    const int turn = round & 1;
     uint32_t least = 0xFFFFFFFFu, most = 0u;
     for (int p = from + threadIdx.x; p < to; p += CHOOSE_THREADS) {
       const float s = scores[p];
