@@ -624,9 +624,9 @@ bsc_status mx_cache_write_rope(const bsc_mx_cache_write_rope_params* p, bsc_stre
  *
  * mx_cache_bounds makes the bounds of the pages that hold positions [seq_lens[b] - n_b, seq_lens[b]) of every sequence, from
  * all of a page's tokens below seq_lens[b]: after each write, with the write's lengths.  Nothing else changes.  It does not
- * read earlier bounds.  Where one call meets a page twice with different numbers of tokens (a shared prefix that ends inside
- * it), its bounds afterwards are those of either; a page that is whole in every sequence has one answer.  codes 16-byte
- * aligned.
+ * read earlier bounds.  Where one call meets a page several times with different numbers of tokens (a shared prefix that ends
+ * inside it), its bounds are those of the most tokens, which are bounds of the fewer ones too; a sequence that has the page,
+ * but none of its new tokens in it, does not count.  codes 16-byte aligned.
  */
 typedef struct {
   bsc_mx_cache cache;     /* [in]; k and k_sc are read */

@@ -106,6 +106,40 @@ def test_bounds_of_zeros_and_nan(ops, fmt):
     assert exps[at[2]].tolist() == [27, 255 if fmt == 0 else 27] and torch.all(b.codes[at[:4]] == 0)
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("D", [64, 128])
+def test_bounds_of_shared_pages(ops, fmt, D):
+    """Pages that sequences share with different numbers of tokens, in the same place of their tables or another, have the bounds
+    of the most tokens: every token is 4 times as large as the one before, so that no other number of them has the same."""
+    page, Hkv, T = 16, 2, 48
+    f = Filled(ops, 25, [7 * page], Hkv, D, fmt, page)
+    x = torch.tensor(np.random.default_rng(25).choice([-1.0, 1.0], (1, 7 * page, Hkv, D))).cuda()
+    x = (x * 2.0 ** (2.0 * (torch.arange(7 * page, device="cuda") % page) - 16)[:, None, None]).bfloat16()
+    ops.mx_cache_write(f.cache, x, x, f.table, f.seq)
+    K = f64(ops.mx_cache_read(f.cache, f.table, f.seq, 7 * page)[0])[0].reshape(7, page, Hkv, D)
+    p = f.table[0].tolist()
+    lens = [1, 5, 9, 16, 17, 20, 31, 33, 36, 40, 21, 3, 12, 0, 38] * 10
+    rows = [p[:3]] * 10 + [[p[3], p[2], p[4]], [p[4], p[0], p[1]], [p[2], p[5], p[3]], p[4:7], [p[1], p[3], p[5]]]
+    rows = [rows[i % 15] for i in range(150)]
+    new = [min(n, 9 if i < 75 else T) for i, n in enumerate(lens)]
+    held = {}
+    for row, n, k in zip(rows, lens, new):
+        for j in range((n - k) // page, -(-n // page) if k else 0):
+            held[row[j]] = max(held.get(row[j], 0), min(page, n - j * page))
+    assert len(set(held.values())) > 3
+    want = {q: R.page_bounds(K[p.index(q)][:n]) for q, n in held.items()}
+    b = random_bounds(ops, f.cache, 26)
+    others = [q for q in range(f.cache.num_pages) if q not in held]
+    before = b.codes[others].clone(), b.exps[others].clone()
+    for _ in range(10):
+        b.codes[list(held)] = 1
+        b.exps[list(held)] = 130
+        ops.mx_cache_bounds(f.cache, b, i32(rows).view(150, 3), i32(lens), T, i32(new))
+        for q, (codes, exps) in want.items():
+            assert np.array_equal(b.exps[q].cpu().numpy(), exps) and np.array_equal(b.codes[q].cpu().numpy(), codes), (q, held[q])
+    assert torch.equal(b.codes[others], before[0]) and torch.equal(b.exps[others], before[1])
+
+
 # ---------------------------------------------------------------------------------------- attention
 SHAPES = [([200], 1, 4, 4, 128, 16, "bf16", 0, 4, 1, 1), ([700, 33, 0, 350], 1, 16, 4, 128, 16, "bf16", 0, 8, 1, 2),
           ([300, 511], 3, 16, 2, 64, 32, "fp16", 1, 5, 0, 1), ([500, 260], 2, 5, 5, 128, 48, "fp16", 0, 6, 2, 2),
