@@ -391,6 +391,10 @@ def _operands(q, k, v, layout, token_norm, rope, positions, stream):
         if positions is not None:
             raise ValueError("positions are for rope")
         return mxfp8_quantize_qkv(q, k, v, layout, token_norm=token_norm, stream=stream)
+    if k.shape != v.shape:                     # quantised by two calls, neither of which sees the other
+        raise ValueError("k and v must have the same shape")
+    if k.device != q.device or v.device != q.device:
+        raise ValueError("q, k and v must be on one device")
     qk = mxfp8_rope_quantize_qk(q, k, rope, positions, layout, stream=stream)
     if token_norm:
         return qk + tuple(mxfp8_quantize_v_fused(v, layout, stream=stream))

@@ -273,6 +273,20 @@ def test_binding_refuses_cpu_tensors(ops):  # noqa: F811
             f()
 
 
+@pytest.mark.parametrize("shape", [(1, 32, 2, 128), (1, 64, 1, 128), (2, 64, 2, 128), (1, 64, 2, 64)])
+def test_rotated_forward_checks_k_against_v(ops, shape):  # noqa: F811
+    """K and V are quantised by two calls with Rope; that they are alike is checked ahead of both."""
+    r = ops.Rope(128, device="cpu")
+    q, k, v = (torch.zeros(s, dtype=torch.bfloat16) for s in ((1, 64, 2, 128), (1, 64, 2, 128), shape))
+    for f in (lambda: ops.forward(q, k, v, rope=r), lambda: ops.forward(q, v, k, rope=r),
+              lambda: ops.forward_backward(q, k, v, q, rope=r)):
+        with pytest.raises(ValueError, match="same shape"):
+            f()
+    meta = k.to("meta")
+    with pytest.raises(ValueError, match="one device"):
+        ops.forward(q, k, meta, rope=r)
+
+
 def test_row_layouts(ops):  # noqa: F811
     """Rows of [..., N] by at most two strides, one split for all tensors."""
     f = ops._row_layout
