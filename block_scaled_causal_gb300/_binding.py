@@ -385,16 +385,24 @@ def bsc_read_device_status(dev_status, stream=None):
     return lib.bsc_read_device_status(_ptr(dev_status), _stream(stream))
 
 
+def _rotated_elsewhere(q, k, v, rope, stream):
+    """Checks of what forward takes with a Rope (K and V are quantised by two calls, neither of which sees the other), and
+    _elsewhere for it, so that all of its calls run and allocate in one place."""
+    if rope is None:
+        return None
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    if k.device != q.device or v.device != q.device:
+        raise ValueError("q, k and v must be on one device")
+    return _elsewhere_with(rope, q, stream)
+
+
 def _operands(q, k, v, layout, token_norm, rope, positions, stream):
     """The eight operands of the attention: Q and K rotated where `rope` is given."""
     if rope is None:
         if positions is not None:
             raise ValueError("positions are for rope")
         return mxfp8_quantize_qkv(q, k, v, layout, token_norm=token_norm, stream=stream)
-    if k.shape != v.shape:                     # quantised by two calls, neither of which sees the other
-        raise ValueError("k and v must have the same shape")
-    if k.device != q.device or v.device != q.device:
-        raise ValueError("q, k and v must be on one device")
     qk = mxfp8_rope_quantize_qk(q, k, rope, positions, layout, stream=stream)
     if token_norm:
         return qk + tuple(mxfp8_quantize_v_fused(v, layout, stream=stream))
@@ -408,6 +416,10 @@ def forward(q, k, v, layout=BSHD, softmax_scale=None, p_terms=2, leaky=0, o=None
     given (laid out like q and [B, Hq, S]).  With o8_out=True the MXFP8 O is returned as well, as
     in mxfp8_causal_attn_fwd.  With `rope` (a Rope) Q and K are rotated on their way into MXFP8, at
     `positions` as in mxfp8_rope_quantize_qk; attention is causal by the tokens' order all the same."""
+    there = _rotated_elsewhere(q, k, v, rope, stream)
+    if there is not None:
+        with there:
+            return forward(q, k, v, layout, softmax_scale, p_terms, leaky, o, lse, None, o8_out, bf16_out, rope, positions)
     qq, qs, kq, ks, vt, vsc, vtn, vtn_sc = _operands(q, k, v, layout, not leaky, rope, positions, stream)
     return mxfp8_causal_attn_fwd(qq, qs, kq, ks, vt, vsc, vtn, vtn_sc, layout, softmax_scale, p_terms, leaky,
                                  o=o, lse=lse, stream=stream, o8_out=o8_out, bf16_out=bf16_out)
@@ -470,7 +482,11 @@ def bf16_attn_bwd_static_capacity():
 
 def forward_backward(q, k, v, do, layout=BSHD, softmax_scale=None, p_terms=2, stream=None, rope=None, positions=None):
     """Forward then the backward on decoded operands; returns (O, LSE, dQ, dK, dV).  With `rope` (see forward) dQ and
-    dK are those of the unrotated q and k."""
+    dK are those of the unrotated q and k: bf16 as the backward gives them, turned back and rounded once more."""
+    there = _rotated_elsewhere(q, k, v, rope, stream)
+    if there is not None:
+        with there:
+            return forward_backward(q, k, v, do, layout, softmax_scale, p_terms, None, rope, positions)
     qq, qs, kq, ks, vt, vsc, vtn, vtn_sc = _operands(q, k, v, layout, True, rope, positions, stream)
     o, lse = mxfp8_causal_attn_fwd(qq, qs, kq, ks, vt, vsc, vtn, vtn_sc, layout, softmax_scale, p_terms,
                                    stream=stream)

@@ -408,6 +408,25 @@ def test_training_step(ops, layout, interleaved):
         ops.forward(q, k, v, layout, positions=start)
 
 
+def test_training_step_on_a_stream(ops):
+    """forward_backward with rope on a given stream, behind its own inputs there, gives the current stream's bits, with all it
+    allocates on the way in that stream's memory."""
+    g = torch.Generator(device="cuda").manual_seed(24)
+    B, S, H, D = 1, 256, 4, 128
+    q, k, v, do = (torch.randn((B, S, H, D), generator=g, device="cuda").bfloat16() for _ in range(4))
+    rope, s = ops.Rope(D), torch.cuda.Stream()
+    want = ops.forward_backward(q, k, v, do, rope=rope)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(s):
+            ins = [x.clone() for x in (q, k, v, do)]
+        got = ops.forward_backward(*ins, rope=rope, stream=s)
+        for n in (1 << 16, 1 << 18, 1 << 20):        # memory that the current stream may have meanwhile
+            torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_rotation_shifts_nothing(ops):
     """Attention goes by the difference of positions: all positions moved by one amount leave O as it is up to the operands'
     E4M3 rounding: every score is off by at most 2 * 2^-4 of scale sum |q||k| <= 2^-3 * 128^-1/2 * |q||k|."""
