@@ -179,6 +179,7 @@ struct RopeArgs {
   CacheTable pt;
   const int32_t* new_lens;
   int32_t* dev_status;
+  int may_signal;          // set by the launch: the next kernel may start while this one runs
 };
 cudaError_t launch_rope(const RopeArgs& a, int dtype, int interleaved, cudaStream_t st);
 cudaError_t launch_rope_mx(const RopeArgs& a, int dtype, int interleaved, cudaStream_t st);

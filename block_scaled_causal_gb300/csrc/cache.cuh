@@ -161,8 +161,10 @@ __device__ __forceinline__ int cache_page(const CachePools& c, const CacheTable&
 // are in the way: 8 ragged prompts written and read 35.0 -> 35.9 us, 368 blocks of attention 10.9 -> 11.4.)
 //
 // A kernel gives the signal after its own wait, never before: then all but one of the kernels ahead of a resident block have
-// finished, and that one loads nothing that it stores, so no L1 can hold an old copy of what the block reads once
-// its wait is over.  Nor is anything read by ld.global.nc (__ldg), which may take it for constant while a kernel lives and
+// finished, and that one loads nothing through L1 that it stores, so no L1 can hold an old copy of what the block reads once
+// its wait is over.  (The norm, which may store in place, loads its rows past L1 by cp.async.cg; rotations in place give no
+// signal; the scores that a choice of pages keeps in its workspace are read by the cluster that wrote them, behind its
+// barrier.)  Nor is anything read by ld.global.nc (__ldg), which may take it for constant while a kernel lives and
 // promises nothing of stores made meanwhile: lengths, page ids, queries and scales come by ordinary loads (__ldca).
 constexpr unsigned EARLY_BLOCKS = 152;
 __device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

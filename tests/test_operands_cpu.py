@@ -317,3 +317,15 @@ def test_launch_order(name, kernels):
         wait, signal = body.find("wait_for_last_kernel()"), body.find("next_kernel_may_start()")
         loads = [m.start() for m in re.finditer(r"__ld\w\w\(|fetch\(|load_batch\(v|cache_page\(|seen_by\(", body)]
         assert 0 <= wait < signal and (not loads or wait < min(loads))
+
+
+def test_kernels_in_place_and_early_launches():
+    """The next kernel's blocks may share an SM, and its L1, only with kernels that load nothing through L1 that they store: the
+    norm's rows go past L1, and a rotation whose outputs are its inputs gives no signal."""
+    s = code("rope.cu")
+    assert s.count("next_kernel_may_start()") == 1 and "if (a.may_signal) next_kernel_may_start();" in s
+    assert "a.may_signal = (long long)grid.x * grid.y <= EARLY_BLOCKS && !in_place(a);" in s
+    assert "return a.y[0] == a.x[0] || (a.x[1] && a.y[1] == a.x[1]);" in s
+    s = code("norm.cu")
+    assert "cp.async.cg.shared.global [%0], [%1], 16;" in s and "__ldcs" not in s
+    assert s.count("__ldca(") == 3 and s.count("__ldca(reinterpret_cast<const float4*>(w)") == 2

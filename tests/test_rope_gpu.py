@@ -281,3 +281,42 @@ def test_few_tokens_share_their_heads(ops):
     for t in (0, 7, 2999):
         a, b = ops.rope(q[:, t:t + 1], k[:, t:t + 1], r, i32([t]))
         assert torch.equal(a, yq[:, t:t + 1]) and torch.equal(b, yk[:, t:t + 1])
+
+
+@pytest.mark.parametrize("D,pad", [(64, 8), (128, 8)])
+def test_in_place_ahead_of_attention(ops, D, pad):
+    """Q rotated in place by a few blocks, in rows that share 32-byte sectors, and read by the attention right behind: bit for
+    bit what comes of a copy, eager and captured."""
+    rng = np.random.default_rng(31)
+    B, T, Hq, Hkv, page = 4, 2, 8, 2, 16
+    cache, table = ops.mx_cache_alloc(B * 4, page, Hkv, D), torch.arange(B * 4, dtype=torch.int32).view(B, 4).cuda()
+    lens, r = i32([50, 2, 33, 64]), ops.Rope(D)
+    k, v = (act(rng, B, T, Hkv, D, "bf16", 0) for _ in "kv")
+    x = act(rng, B, T, Hq, D, "bf16", 0)
+    base = torch.zeros(B * T * Hq * (D + pad) + 8, dtype=torch.bfloat16, device="cuda")[8:].view(B, T, Hq, D + pad)[..., :D]
+    assert base.data_ptr() % 32 == 16 and base.stride(2) * 2 % 32 == 16
+    at = lens - T
+
+    def step(q, write):
+        y = ops.mx_cache_write_rope(cache, q, k, v, r, table, lens, q_out=q) if write else \
+            ops.rope(q, None, r, at, q_out=q)[0]
+        return ops.mx_cache_attn(y, cache, table, lens)
+
+    copy = x.clone()
+    want = step(copy, True)
+    torch.cuda.synchronize()
+    for write in (True, False):
+        for _ in range(30):
+            base.copy_(x)
+            got = step(base, write)
+            assert torch.equal(base, copy) and all(torch.equal(a, b) for a, b in zip(got, want))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = []
+            for _ in range(20):
+                base.copy_(x)
+                outs += step(base, write)
+        for _ in range(5):
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, want[i % 2]) for i, a in enumerate(outs))
