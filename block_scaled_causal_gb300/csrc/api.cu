@@ -11,6 +11,7 @@
 
 #include "../../include/bsc.h"
 #include "bsc_internal.h"
+#include "two_doubles.h"
 
 namespace {
 
@@ -741,21 +742,26 @@ bsc_status bsc_rope_turns(const bsc_rope_config* c, unsigned long long* turns, f
   if (parts && !(factor >= 1.0 && std::isfinite(c->original_length) && c->original_length > 0.0 && c->low_turns >= 0.0 &&
                  std::isfinite(c->high_turns) && c->low_turns < c->high_turns))
     return BSC_ERR_UNSUPPORTED;
-  const double two_pi = 6.283185307179586476925;
-  const double base = c->scaling == BSC_ROPE_BASE ? c->base * std::pow(factor, c->rot / (c->rot - 2.0)) : c->base;
-  if (!(std::isfinite(base) && base > 0.0)) return BSC_ERR_UNSUPPORTED;
-  for (int i = 0; i < c->rot / 2; ++i) {
-    double f = std::pow(base, -2.0 * i / c->rot) / two_pi;      // turns per token
-    if (c->scaling == BSC_ROPE_LINEAR) f /= factor;
+  const int n = c->rot / 2;
+  if (c->scaling == BSC_ROPE_BASE) {
+    const double scaled = c->base * std::pow(factor, n / (n - 1.0));
+    if (!(std::isfinite(scaled) && scaled > 0.0)) return BSC_ERR_UNSUPPORTED;
+  }
+  // base^(-1/n), the quotient of neighbouring frequencies.  A fraction to 2^-64 takes more bits than a double has.
+  bsc::Two quotient = bsc::inverse_root(c->base, n);
+  if (c->scaling == BSC_ROPE_BASE) quotient = quotient * bsc::inverse_root(factor, n - 1);   // factor^(n/(n-1)) to the -1/n
+  bsc::Two plain(0.15915494309189535, -9.839338337591243e-18);  // 1 / 2 pi: turns per token of the first pair
+  for (int i = 0; i < n; ++i, plain = plain * quotient) {
+    bsc::Two f = plain;
+    if (c->scaling == BSC_ROPE_LINEAR) f = f / factor;
     if (parts) {
-      double k = (c->original_length * f - c->low_turns) / (c->high_turns - c->low_turns);
-      k = k < 0.0 ? 0.0 : k > 1.0 ? 1.0 : k;
-      f *= k + (1.0 - k) / factor;
+      bsc::Two k = (f * c->original_length - c->low_turns) / (bsc::Two(c->high_turns) - c->low_turns);
+      if (k.hi <= 0.0) k = 0.0;
+      if (k.hi > 1.0 || (k.hi == 1.0 && k.lo >= 0.0)) k = 1.0;
+      f = f * (k + (bsc::Two(1.0) - k) / factor);
     }
-    if (!std::isfinite(f)) return BSC_ERR_UNSUPPORTED;
-    f -= std::floor(f);                                         // whole turns change nothing
-    const double x = std::nearbyint(std::ldexp(f, 64));
-    turns[i] = x >= 18446744073709551616.0 ? 0ull : (unsigned long long)x;
+    if (!std::isfinite(f.hi) || !std::isfinite(f.lo)) return BSC_ERR_UNSUPPORTED;
+    turns[i] = bsc::fraction_64(f);                             // whole turns change nothing
   }
   *magnitude = parts ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
   return BSC_OK;

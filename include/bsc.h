@@ -510,7 +510,7 @@ bsc_status mxfp8_dequantize(const uint8_t* x_e4m3, const uint8_t* x_sc, int B, i
  *
  * f_i is given as turns per token, times 2^64 and rounded: a 64-bit fraction, so that the angle of any 32-bit position is
  * exact to 2^-33 turns without a table of positions.  bsc_rope_turns fills them in (host only, no CUDA call; the caller copies
- * them to the device once):
+ * them to the device once), rounded to nearest for base >= 1 (where f_i is a turn or more, its own last bits are lost):
  *   BSC_ROPE_PLAIN      f_i = base^(-2i/rot)
  *   BSC_ROPE_LINEAR     f_i / factor: positions are interpolated
  *   BSC_ROPE_BASE       base * factor^(rot/(rot-2)) in the place of base: the slowest pair is interpolated by factor, the

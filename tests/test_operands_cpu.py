@@ -89,6 +89,44 @@ def test_turns(ops, rot, scaling, factor):  # noqa: F811
     assert abs(r.magnitude - m) <= 2 ** -23 and ops.Rope(rot, magnitude=0.5, device="cpu").magnitude == 0.5
 
 
+@pytest.mark.parametrize("rot", [16, 32, 96, 128, 256])
+@pytest.mark.parametrize("base", [1.0, 1.7, 10000.0, 500000.0, 1e7, 1e300])
+@pytest.mark.parametrize("scaling,factor", [("PLAIN", 1.0), ("LINEAR", 3.0), ("BASE", 1.3), ("BASE", 40.0), ("BY_PARTS", 1.0),
+                                            ("BY_PARTS", 7.3)])
+def test_turns_are_exact_to_64_bits(ops, rot, base, scaling, factor):  # noqa: F811
+    """Every frequency is the formula's to 2^-64 turns (half a unit but for what 106 bits leave), so that the angle at 2^31
+    tokens is within 2^-33."""
+    getcontext().prec = 70
+    two_pi = 2 * Decimal("3.1415926535897932384626433832795028841971693993751058209749445923078164062862")
+    r = ops.Rope(rot, base=base, scaling=getattr(ops, "ROPE_" + scaling), factor=factor, original_length=8192, low_turns=0.7,
+                 high_turns=33.3, device="cpu")
+    b, f, low, high = Decimal(base), Decimal(factor), Decimal(0.7), Decimal(33.3)
+    if scaling == "BASE":
+        b = b * f ** (Decimal(rot) / Decimal(rot - 2))
+    for i, t in enumerate(r.turns.tolist()):
+        want = b ** (-Decimal(2 * i) / Decimal(rot)) / two_pi
+        if scaling == "LINEAR":
+            want = want / f
+        if scaling == "BY_PARTS":
+            k = min(max((8192 * want - low) / (high - low), Decimal(0)), Decimal(1))
+            want = want * (k + (1 - k) / f)
+        off = Decimal(t % 2 ** 64) - want * 2 ** 64
+        assert abs(off) <= Decimal(0.5) + Decimal(2) ** -20, (i, off)
+
+
+def test_turns_of_a_small_base(ops):  # noqa: F811
+    """Frequencies of a turn and more: the fraction, to what 104 bits of the whole leave; none is left of the largest."""
+    getcontext().prec = 70
+    two_pi = 2 * Decimal("3.1415926535897932384626433832795028841971693993751058209749445923078164062862")
+    r = ops.Rope(32, base=1e-6, device="cpu")
+    for i, t in enumerate(r.turns.tolist()):
+        want = Decimal(1e-6) ** (-Decimal(2 * i) / 32) / two_pi
+        off = (Decimal(t % 2 ** 64) - want * 2 ** 64) % 2 ** 64
+        assert min(off, 2 ** 64 - off) <= Decimal(0.5) + Decimal(2) ** -20
+    for base in (1e-300, 5e-324):
+        assert len(ops.Rope(16, base=base, device="cpu").turns) == 8
+
+
 @pytest.mark.parametrize("kw", [
     dict(rot=0), dict(rot=8), dict(rot=24), dict(rot=272), dict(rot=-16), dict(scaling=4), dict(scaling=-1), dict(base=0.0),
     dict(base=-1.0), dict(base=math.inf), dict(base=math.nan), dict(scaling=1, factor=0.0), dict(scaling=2, factor=math.nan),
