@@ -1183,10 +1183,12 @@ class MxBounds:
 
 
 def mx_cache_bounds_alloc(cache):
-    """MxBounds with new buffers for `cache`; mx_cache_bounds fills in the pages that hold tokens."""
+    """MxBounds with new buffers for `cache`.  Pages count as unbounded (exps 0xFF: ahead of every scored page) until
+    mx_cache_bounds has made their bounds, which it does for the pages of the tokens that it is told of: all of a prompt's
+    behind the prompt, then each step's."""
     shape = (cache.num_pages, cache.Hkv)
     return MxBounds(cache, torch.zeros(shape + (2, cache.D), dtype=torch.int8, device=cache.device),
-                    torch.zeros(shape, dtype=torch.uint8, device=cache.device))
+                    torch.full(shape, 0xFF, dtype=torch.uint8, device=cache.device))
 
 
 def _bounds_of(bounds, cache):

@@ -441,6 +441,27 @@ def test_rotation_shifts_nothing(ops):
     assert (a.float() - c.float()).abs().max().item() <= (np.exp(2 * size) - 1 + 2.0 ** -7) * v.abs().max().item()
 
 
+def test_new_bounds_bound_nothing(ops):
+    """Pages whose bounds were never made are read ahead of those that score, and not taken for pages of zeros; the pages of a
+    prompt are all made by one call with its length."""
+    f = Filled(ops, 27, [160], 2, 64, 1, 16)
+    q = make_q(28, 1, 1, 4, 64, "bf16", 0)
+    b = ops.mx_cache_bounds_alloc(f.cache)
+    assert torch.all(b.exps == 0xFF) and torch.all(b.codes == 0)
+    made = [5, 6, 8, 9]                               # positions 80 .. 111 and 128 .. 159
+    ops.mx_cache_bounds(f.cache, b, f.table, i32([112]), 32)
+    ops.mx_cache_bounds(f.cache, b, f.table, f.seq, 32)
+    ids = f.table[0, :10].tolist()
+    assert [i for i in range(10) if torch.all(b.exps[ids[i]] < 0xFF)] == made
+    out = ops.mx_cache_sparse_attn(q, f.cache, b, f.table, f.seq, 8)
+    check_sparse(ops, f, b, q, out, [1], 0, 8, 1, 1)
+    for h in range(2):
+        assert {0, 1, 2, 3, 4, 7, 9} < set(out[2][0, 0, h].tolist())
+    ops.mx_cache_bounds(f.cache, b, f.table, f.seq, 160)
+    assert torch.all(b.exps[ids] < 0xFF)
+    check_sparse(ops, f, b, q, ops.mx_cache_sparse_attn(q, f.cache, b, f.table, f.seq, 4), [1], 0, 4, 1, 1)
+
+
 def test_large_offsets(ops):
     """Pages that start past 2^32 bytes of the pools give what pages side by side give."""
     pages, page, Hkv, apart = 9, 16, 1, 1 << 19
