@@ -1081,6 +1081,12 @@ def _elsewhere_with(rope, q, stream):
     return None if stream is None and _current_device() == rope.index else _elsewhere(rope, stream)
 
 
+def _heads(Hq, Hkv):
+    """The C calls have nothing to do where q has no heads, and k would stay behind."""
+    if Hq == 0 and Hkv > 0:
+        raise ValueError("q must have at least one head beside k")
+
+
 def apply_rope(q, k, rope, positions=None, layout=BSHD, inverse=False, q_out=None, k_out=None, stream=None):
     """Q and K (or None) rotated by a Rope in one launch; returns (q, k) of the same shapes and dtype.
 
@@ -1102,6 +1108,7 @@ def apply_rope(q, k, rope, positions=None, layout=BSHD, inverse=False, q_out=Non
     else:
         dims_k, ks, dt_k = _act_dims(k, layout, rope, "k", D)
         Bk, Tk, Hkv = dims_k
+        _heads(Hq, Hkv)
         if Bk != B or Tk != T or dt_k != dt:
             raise ValueError("k must have q's batch, tokens and dtype")
         k_out, k_os = _out_like(k, k_out, dims_k, layout, rope, "k_out", dt, D)
@@ -1130,6 +1137,7 @@ def mxfp8_rope_quantize_qk(q, k, rope, positions=None, layout=BSHD, rule=SCALE_F
         k8, k_sc, Hkv, ks, k_ptrs = None, None, 0, (0, 0, 0), (0, 0, 0)
     else:
         (Bk, Tk, Hkv), ks, dt_k = _act_dims(k, layout, rope, "k", D)
+        _heads(Hq, Hkv)
         if Bk != B or Tk != T or dt_k != dt:
             raise ValueError("k must have q's batch, tokens and dtype")
         k8, k_sc = torch.empty(k.shape, **u8), torch.empty((B, Hkv, T, D // 32), **u8)
@@ -1155,6 +1163,7 @@ def mx_cache_write_rope(cache, q, k, v, rope, page_table, seq_lens, new_lens=Non
     dims_k, ks, dt_k = _act_dims(k, layout, cache, "k")
     dims_v, vs, dt_v = _act_dims(v, layout, cache, "v")
     B, T, Hq = dims
+    _heads(Hq, cache.Hkv)
     if dims_k != (B, T, cache.Hkv) or dims_v != dims_k or dt_k != dt or dt_v != dt:
         raise ValueError("k and v must have q's batch, tokens and dtype and the cache's heads")
     q_out, q_os = _out_like(q, q_out, dims, layout, cache, "q_out", dt)

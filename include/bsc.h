@@ -545,7 +545,7 @@ typedef struct {
  * inverse 1 turns back: the gradients of q and k from those of the outputs.  fp32 inside, one rounding.
  * q, k: strides as in the cache calls (elements, multiples of 8), D a multiple of 16, at most 256.  k may be NULL (k_out
  * too), Hkv is then ignored.  q_out may be q and k_out k (same strides); no other overlap.  positions 4-byte aligned,
- * turns 8-byte.
+ * turns 8-byte.  B, T or Hq of 0: BSC_OK, nothing is done (to k neither).
  */
 typedef struct {
   bsc_rope_angles angles;
@@ -592,7 +592,7 @@ bsc_status mxfp8_rope_quantize_qk(const bsc_rope_quant_params* p, bsc_stream_t s
  * a chunk of a prompt needs ahead of mx_cache_attn.  Token t < n_b of sequence b is at position seq_lens[b] - n_b + t, where
  * its K and V are written and by which its Q and K turn.  K is quantised from the rotated fp32 values.  Rows of q_out with
  * t >= n_b or a negative position are zeros.  q_out may be q (same strides).  Checks and refusals as mx_cache_write, with
- * Hq a multiple of Hkv and B * T below 2^31.
+ * Hq a multiple of Hkv and B * T below 2^31.  Hq of 0: BSC_OK, nothing is done, to K and V neither.
  */
 typedef struct {
   bsc_mx_cache cache;     /* [out] */

@@ -320,3 +320,17 @@ def test_in_place_ahead_of_attention(ops, D, pad):
             g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, want[i % 2]) for i, a in enumerate(outs))
+
+
+def test_no_heads_of_q(ops):
+    """K beside a Q of no heads would not be rotated: refused; alone, or with no tokens, there is nothing to miss."""
+    q, k = (torch.ones((2, 3, h, 64), dtype=torch.bfloat16, device="cuda") for h in (0, 2))
+    r, cache = ops.Rope(64), ops.mx_cache_alloc(4, 16, 2, 64)
+    k128, r128 = torch.ones((2, 3, 2, 128), dtype=torch.bfloat16, device="cuda"), ops.Rope(128)
+    table, lens = i32([[0, 1], [2, 3]]), i32([3, 3])
+    for f in (lambda: ops.rope(q, k, r), lambda: ops.mxfp8_rope_quantize_qk(k128[:, :, :0], k128, r128),
+              lambda: ops.mx_cache_write_rope(cache, q, k, k, r, table, lens)):
+        with pytest.raises(ValueError, match="at least one head"):
+            f()
+    assert ops.rope(q, None, r)[0].shape == q.shape and ops.rope(q, k[:, :, :0], r)[1].shape == q.shape
+    assert ops.rope(k[:, :0], k[:, :0], r)[1].shape == (2, 0, 2, 64)
