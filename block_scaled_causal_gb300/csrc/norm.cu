@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(WIDE ? WIDE_THREADS : NARROW_THREADS, blocks_p
     const float c = row_sum<WIDE>(sum.x + sum.y, tpr, part[i & 1]) * inv_n;
     if (live) {
       uint4* const out = ow.next(a.dxs, rows.first + i * rows.step, a.inner);
-      const float2 xc = both(-rs * rs * c);
+      const float2 xc = both(-rs * c);           // times x it is no larger than g: rs^2 c may leave fp32's range where dx does not
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (v * tpr + t < nv) {
@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(WIDE ? WIDE_THREADS : NARROW_THREADS, blocks_p
           for (int k = 0; k < 4; ++k) e[k] = both(0.f);
           if (a.ds) unpack8<DT>(from[(2 * V + v) * threads], e);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)     // rs d w - x rs^2 c + e
-            d[k] = __ffma2_rn(x[k], xc, __ffma2_rn(__fmul2_rn(d[k], w[v][k]), both(rs), e[k]));
+          for (int k = 0; k < 4; ++k)     // rs (d w - x rs c) + e
+            d[k] = __ffma2_rn(__ffma2_rn(x[k], xc, __fmul2_rn(d[k], w[v][k])), both(rs), e[k]);
           __stcs(out + v * tpr, pack8<DT>(d));
         }
     }

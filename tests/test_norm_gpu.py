@@ -109,6 +109,22 @@ def test_backward(ops, rows, N, dtype, weight, residual):
     assert dx3 is into and torch.equal(into, dx) and torch.equal(dw3, dw)
 
 
+@pytest.mark.parametrize("N", [64, 512, 2560, 8192])
+@pytest.mark.parametrize("size,grad,eps", [(2.0 ** 54, 2.0 ** -50, EPS), (2.0 ** 40, 2.0 ** -62, EPS), (2.0 ** -54, 2.0 ** 26, 0.0),
+                                           (2.0 ** -50, 2.0 ** 40, 0.0), (2.0 ** 54, 2.0 ** 60, 0.0)])
+def test_gradients_of_large_and_small_rows(ops, N, size, grad, eps):
+    """Gradients that bf16 holds, of rows whose rstd^2 times the mean leaves fp32's range: test_backward's bound."""
+    rng = np.random.default_rng(N)
+    s, dy, w = rand(rng, (9, N), "bf16", size), rand(rng, (9, N), "bf16", grad), rand(rng, (N,), "fp32")
+    s = torch.where(s.abs() <= 4 * size, s, 0.0).bfloat16()
+    _, _, rstd = ops.rms_norm(s, w, eps)
+    assert np.all(np.abs(f64(rstd) * np.sqrt(np.mean(f64(s) ** 2, -1) + eps) - 1) <= Y_REL)
+    dx, _ = ops.rms_norm_bwd(dy, s, w, rstd)
+    want, _, terms, _ = R.norm_bwd(f64(dy), f64(s), f64(w), f64(rstd))
+    err = np.abs(f64(dx) - want)
+    assert np.all(err <= half_step(want, s.dtype) + 2.0 ** -18 * terms * 1.01), err.max() / np.abs(want).max()
+
+
 def test_slices_and_in_place(ops):
     """The heads of a slice of a fused projection, normed where they are; what lies between stays."""
     rng = np.random.default_rng(5)
