@@ -13,6 +13,7 @@
 // spaced: addresses move by addition.  bf16, fp32 weights: 16384 x 4096 with a residual 85.9 us (6.2 TB/s, 94% of the copy rate), its
 // gradients 90.1 (89%); 262144 x 128 23.2 and 49.8.  To MXFP8 the instructions bound it: 41.7 us for 3 bytes per element (73%).
 #include <atomic>
+#include <type_traits>
 
 #include "cache.cuh"
 
@@ -444,9 +445,11 @@ cudaError_t run(const NormBwdArgs& a, const Cut& c, cudaStream_t st) {
 }
 template <int DT, bool FLAT, class A>
 cudaError_t pick(const A& a, const Cut& c, cudaStream_t st) {
-  if (!c.wide)
-    return c.v == 1 ? run<DT, 1, false, FLAT>(a, c, st) : c.v == 2 ? run<DT, 2, false, FLAT>(a, c, st) : run<DT, 4, false, FLAT>(a, c, st);
-  return c.v == 1 ? run<DT, 1, true, FLAT>(a, c, st) : c.v == 2 ? run<DT, 2, true, FLAT>(a, c, st) : run<DT, 4, true, FLAT>(a, c, st);
+  if (c.wide)
+    return c.v == 1 ? run<DT, 1, true, FLAT>(a, c, st) : c.v == 2 ? run<DT, 2, true, FLAT>(a, c, st) : run<DT, 4, true, FLAT>(a, c, st);
+  if constexpr (std::is_same<A, NormArgs>::value)                // bwd_cut has no rows of part of a warp by two vectors
+    if (c.v == 2) return run<DT, 2, false, FLAT>(a, c, st);
+  return c.v == 1 ? run<DT, 1, false, FLAT>(a, c, st) : run<DT, 4, false, FLAT>(a, c, st);
 }
 template <class A>
 cudaError_t pick(const A& a, int dtype, cudaStream_t st) {
