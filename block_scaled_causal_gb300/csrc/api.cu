@@ -925,6 +925,8 @@ bsc_status mx_cache_bounds(const bsc_mx_cache_bounds_params* p, bsc_stream_t str
 
 size_t mx_cache_sparse_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int top) {
   if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || page_size <= 0 || max_pages < 0 || top <= 0) return 0;
+  if (Hq % Hkv != 0 || (D != 64 && D != 128) || page_size % 16 != 0 || (long long)max_pages * page_size > BSC_CACHE_MAX_TOKENS)
+    return 0;                                                  // refused by the call itself
   SparseParts w;
   return sparse_parts(B, T, Hq, Hkv, D, page_size, max_pages, top, &w) ? w.all : 0;
 }

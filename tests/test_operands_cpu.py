@@ -170,6 +170,14 @@ def test_workspaces(ops):  # noqa: F811
     assert f(1 << 20, 1, 16, 8, 128, 64, 16, 256) == 0               # 2^31 chosen pages
 
 
+@pytest.mark.parametrize("i,bad", [(2, 2), (2, 6), (4, 96), (4, 256), (5, 24), (6, 1 << 25)])
+def test_workspace_of_refused_sizes(ops, i, bad):  # noqa: F811
+    """What mx_cache_sparse_attn refuses needs no workspace: heads that are not shared evenly, head sizes, pages, long tables."""
+    good = (2, 1, 16, 4, 128, 64, 500, 32)
+    assert ops.mx_cache_sparse_attn_workspace_bytes(*good) > 0
+    assert ops.mx_cache_sparse_attn_workspace_bytes(*good[:i], bad, *good[i + 1:]) == 0
+
+
 # -------------------------------------------------------------------------------------- refusals
 def _norm(ops, **kw):
     base = dict(x=FAKE, residual=FAKE, weight=FAKE, y=FAKE, sum=FAKE, rstd=FAKE, y_e4m3=FAKE, y_sc=FAKE, rows=6, inner=2, N=64,
