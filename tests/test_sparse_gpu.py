@@ -441,6 +441,35 @@ def test_rotation_shifts_nothing(ops):
     assert (a.float() - c.float()).abs().max().item() <= (np.exp(2 * size) - 1 + 2.0 ** -7) * v.abs().max().item()
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("shift", [1, 64, 777777])
+def test_rotation_moves_scores_by_rounding_alone(ops, interleaved, shift):
+    """Scores of several units, of Q and K at positions 0 .. 31 and all moved by one amount.  They differ by the four E4M3 roundings
+    of their operands, each at most 2^-4 of an element and of random sign: by 2 * 2^-4 of the root of sum (q k)^2 in root mean
+    square.  With only one of the two moved they differ by far more, whichever it is.  The attention's LSE is that of the scores."""
+    g = torch.Generator().manual_seed(33)
+    q, k, v = (torch.randn((1, 32, h, 128), generator=g).bfloat16().cuda() for h in (4, 4, 4))
+    r = ops.Rope(128, interleaved=interleaved)
+
+    def operands(at):
+        q8, qs, k8, ks = ops.mxfp8_rope_quantize_qk(q, k, r, i32([at]))
+        return tuple(f64(ops.mxfp8_dequantize(*x, 0))[0].transpose(1, 0, 2) for x in ((q8, qs), (k8, ks)))
+
+    (q0, k0), (q1, k1) = operands(0), operands(shift)
+    scores = lambda a, b: np.einsum("htd,hsd->hts", a, b)  # noqa: E731
+    rms = lambda x: np.sqrt(np.mean(x * x))  # noqa: E731
+    bound = 2 * 2.0 ** -4 * np.sqrt(np.mean(np.einsum("htd,hsd->hts", q0 * q0, k0 * k0)))
+    s0, s1 = scores(q0, k0), scores(q1, k1)
+    assert rms(s0) > 5 * bound and rms(s0 - s1) <= bound
+    far = 3 if shift > 1 else 1                       # one token's turn of one of them moves the fast pairs alone
+    assert rms(s0 - scores(q1, k0)) > far * bound and rms(s0 - scores(q0, k1)) > far * bound
+    for at, s in ((0, s0), (shift, s1)):
+        _, lse = ops.forward(q, k, v, rope=r, positions=i32([at]))
+        s = np.where(np.tri(32, dtype=bool), s * 128 ** -0.5, -np.inf)
+        want = np.log(np.sum(np.exp(s - s.max(-1, keepdims=True)), -1)) + s.max(-1)
+        assert np.all(np.abs(lse.cpu().double().numpy()[0] - want) <= 1e-3 * np.maximum(np.abs(want), 1.0))
+
+
 def test_new_bounds_bound_nothing(ops):
     """Pages whose bounds were never made are read ahead of those that score, and not taken for pages of zeros; the pages of a
     prompt are all made by one call with its length."""
