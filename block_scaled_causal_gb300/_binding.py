@@ -1040,7 +1040,8 @@ class Rope:
 
     interleaved: pairs are neighbours (x_2i, x_2i+1), else (x_i, x_{i + rot/2}).  scaling: ROPE_PLAIN; ROPE_LINEAR (positions
     / factor); ROPE_BASE (base * factor^(rot/(rot-2))); ROPE_BY_PARTS (pairs of fewer than low_turns turns in
-    original_length tokens are interpolated by factor, those of more than high_turns are kept, what lies between is mixed).
+    original_length tokens are interpolated by factor, those of more than high_turns are kept, what lies between is mixed, linear
+    in turns).
     magnitude: the factor on what is rotated (None: 0.1 ln(factor) + 1 by parts, else 1)."""
 
     __slots__ = ("rot", "interleaved", "magnitude", "turns", "device", "index", "params", "packed")
@@ -1119,7 +1120,7 @@ def apply_rope(q, k, rope, positions=None, layout=BSHD, inverse=False, q_out=Non
     return q_out, k_out
 
 
-rope = apply_rope      # the C call's name; `rope` is also what the calls name their Rope argument
+rope = apply_rope      # the C call's name, by which the documents name it; in the calls `rope` is their Rope
 
 
 def mxfp8_rope_quantize_qk(q, k, rope, positions=None, layout=BSHD, rule=SCALE_FLOOR, stream=None):

@@ -263,7 +263,7 @@ bsc_status check_rope(int B, int T, int Hq, int Hkv, int D, int dtype, bool* emp
     return BSC_OK;
   }
   if (D == 0 || D % 16 != 0 || D > 256) return BSC_ERR_UNSUPPORTED;
-  // blocks, and rows of a block's 16 tokens
+  // tokens, and heads of a token
   if (reaches_2_31({B, T}) || (long long)Hq + 2LL * Hkv > ROPE_MOST_HEADS) return BSC_ERR_UNSUPPORTED;
   return BSC_OK;
 }

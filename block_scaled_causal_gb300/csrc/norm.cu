@@ -10,8 +10,10 @@
 // keep their columns' weights (and dw's sums) in registers as fp32, and each copies its own pieces of the rows ahead into its
 // own slots of a ring in shared memory (cp.async), so that nothing but a row's sum is shared and the bytes in flight are not
 // held in registers.  Rows of up to 1024 elements belong to part of a warp, longer ones to a block.  FLAT rows are evenly
-// spaced: addresses move by addition.  bf16, fp32 weights: 16384 x 4096 with a residual 85.9 us (6.2 TB/s, 94% of the copy rate), its
-// gradients 90.1 (89%); 262144 x 128 23.2 and 49.8.  To MXFP8 the instructions bound it: 41.7 us for 3 bytes per element (73%).
+// spaced: addresses move by addition; heads of a slice take two divisions per row and tensor (262144 x 128 25.3 us against 23.8).
+// bf16, fp32 weights: 16384 x 4096 with a residual 85.7 us (6.3 TB/s, 94% of the copy rate), its gradients with ds 89.6 (90%);
+// 262144 x 128 23.8 and 49.0.  To MXFP8 latency bounds it: 41.4 us for 3 bytes per element (74%), DRAM at 48%, issue slots at 65%,
+// 15 warps per SM that wait for their own last instructions (1.8 per issue) and for shared memory and shuffles (1.2), for memory 0.15.
 #include <atomic>
 #include <type_traits>
 

@@ -430,7 +430,8 @@ size_t mx_cache_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, long 
  * Root-mean-square norm of rows of N elements, with the residual's addition:
  *   s = x + residual, rounded to `dtype` (s = x where residual is NULL): the residual stream, which the next layer adds to
  *   rstd = (mean_n s_n^2 + eps)^(-1/2),  y_n = s_n * rstd * weight_n
- * in fp32 (a sum of squares beyond 3.4e38 is infinite: rows up to 2^56 in magnitude are taken), each output rounded once.
+ * in fp32, each output rounded once.  Rows are taken up to 2^56 in magnitude (a sum of squares beyond 3.4e38 is infinite), and
+ * where eps is below 2^-126 their largest element is at least 2^-56 or 0 (smaller squares are lost).
  * y goes out in `dtype` (y), as MXFP8 rows (y_e4m3 [rows][N] and y_sc [rows][N/32], the quantisation rule at the top of
  * this file applied to the fp32 y), or both.  A row with a NaN or an infinity comes out as NaN where the formula says so (as
  * does a row of zeros with eps 0).  The order of a row's sum, and so its last bits, depends on N and on whether there are
@@ -518,7 +519,8 @@ bsc_status mxfp8_dequantize(const uint8_t* x_e4m3, const uint8_t* x_sc, int B, i
  *   BSC_ROPE_BY_PARTS   f_i (k + (1 - k) / factor), k = clamp((original_length f_i / 2 pi - low_turns) / (high_turns -
  *                       low_turns), 0, 1): pairs that turn often in the trained length stay, slow ones are interpolated
  *                       (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models", 3.2); magnitude
- *                       0.1 ln(factor) + 1 (3.4), for every factor >= 1
+ *                       0.1 ln(factor) + 1 (3.4), for every factor >= 1.  (k is linear in a pair's turns.  Where it is
+ *                       linear in the pair's number i instead, as in some checkpoints, the caller fills in the turns.)
  * magnitude is 1 for the others.  base > 0, factor > 0 (>= 1 by parts), finite; by parts original_length > 0,
  * 0 <= low_turns < high_turns: else BSC_ERR_UNSUPPORTED.  rot is a multiple of 16 from 16 to 256.
  */
@@ -648,7 +650,8 @@ bsc_status mx_cache_bounds(const bsc_mx_cache_bounds_params* p, bsc_stream_t str
  * With top pages or fewer all are attended: the result is mx_cache_attn's.  Else the first `first` and the last `last`
  * (the page of p among them), and of the others those with the largest
  *   score = 2^e (sum_d u_d max_d - l_d min_d),  u = sum over the KV head's query heads of max(q_d, 0), l of max(-q_d, 0),
- * u and l rounded to 0..127 with one power of two per query and KV head (the largest in [64, 128), 127 at most).  Scores are
+ * u and l rounded to 0..127 with one power of two per query and KV head (the largest in [64, 128), 127 at most; less where it
+ * is below 2^-121, since the power is 2^127 at most).  Scores are
  * exact in fp32; equal ones are taken in the pages' order.  An exps below 27 or from 228 to 254, which mx_cache_bounds does not
  * write, counts as 27 or 227.  A page whose exps is 0xFF scores above all others; one whose
  * id is out of range comes last and is not attended (0x201).  A query with a NaN or an infinity, or whose sums u and l pass
