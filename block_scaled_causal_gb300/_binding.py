@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import struct
 
@@ -72,6 +73,8 @@ def _load():
     lib.mxfp8_dequantize.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
     lib.bsc_rope_turns.restype = i32
     lib.bsc_rope_turns.argtypes = [ctypes.POINTER(RopeConfig), vp, ctypes.POINTER(ctypes.c_float)]
+    lib.bsc_rope_magnitude.restype = ctypes.c_double
+    lib.bsc_rope_magnitude.argtypes = [ctypes.POINTER(RopeConfig)]
     lib.bsc_read_device_status.restype = i32
     lib.bsc_read_device_status.argtypes = [vp, vp]
     return lib
@@ -204,7 +207,7 @@ class RopeConfig(ctypes.Structure):
 class RopeAngles(ctypes.Structure):
     """Mirror of bsc_rope_angles."""
     _fields_ = [("turns", ctypes.c_void_p), ("magnitude", ctypes.c_float), ("rot", ctypes.c_int),
-                ("interleaved", ctypes.c_int)]
+                ("interleaved", ctypes.c_int), ("magnitude_low", ctypes.c_float)]
 
 
 _POSITIONS = [("positions", ctypes.c_void_p), ("position_stride_b", ctypes.c_longlong),
@@ -1054,9 +1057,11 @@ class Rope:
         signed = (ctypes.c_longlong * (rot // 2)).from_buffer(host)
         self.turns = torch.tensor(list(signed), dtype=torch.int64).to(device)
         self.rot, self.interleaved = rot, bool(interleaved)
-        self.magnitude = m.value if magnitude is None else float(magnitude)
+        self.magnitude = lib.bsc_rope_magnitude(ctypes.byref(config)) if magnitude is None else float(magnitude)
+        high = ctypes.c_float(self.magnitude).value
+        low = self.magnitude - high if 1e-30 < abs(high) < math.inf else 0.0
         self.device, self.index = self.turns.device, self.turns.get_device()
-        self.params = RopeAngles(self.turns.data_ptr(), self.magnitude, rot, int(self.interleaved))
+        self.params = RopeAngles(self.turns.data_ptr(), high, rot, int(self.interleaved), low)
         self.packed = bytes(self.params)
 
 

@@ -250,6 +250,7 @@ bsc_status check_norm(long long rows, int N, int inner, int dtype, int weight_dt
 bsc_status check_angles(const bsc_rope_angles& a, int D) {
   if (a.rot < 16 || a.rot % 16 != 0 || a.rot > D) return BSC_ERR_UNSUPPORTED;
   if ((a.interleaved != 0 && a.interleaved != 1) || !std::isfinite(a.magnitude)) return BSC_ERR_UNSUPPORTED;
+  if (!(std::fabs(a.magnitude_low) <= std::fabs(a.magnitude) * 0x1p-23f)) return BSC_ERR_UNSUPPORTED;
   if (!a.turns) return BSC_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(a.turns) & 7u) != 0) return BSC_ERR_ALIGN;
   return BSC_OK;
@@ -763,8 +764,12 @@ bsc_status bsc_rope_turns(const bsc_rope_config* c, unsigned long long* turns, f
     if (!std::isfinite(f.hi) || !std::isfinite(f.lo)) return BSC_ERR_UNSUPPORTED;
     turns[i] = bsc::fraction_64(f);                             // whole turns change nothing
   }
-  *magnitude = parts ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  *magnitude = (float)bsc_rope_magnitude(c);
   return BSC_OK;
+}
+
+double bsc_rope_magnitude(const bsc_rope_config* c) {
+  return c && c->scaling == BSC_ROPE_BY_PARTS ? 0.1 * std::log(c->factor) + 1.0 : 1.0;
 }
 
 bsc_status rope(const bsc_rope_params* p, bsc_stream_t stream) {
@@ -796,6 +801,7 @@ bsc_status rope(const bsc_rope_params* p, bsc_stream_t stream) {
   a.ys[1] = {p->k_out_stride_b, p->k_out_stride_t, p->k_out_stride_h};
   a.turns = p->angles.turns;
   a.magnitude = p->angles.magnitude;
+  a.magnitude_low = p->angles.magnitude_low;
   a.rot = p->angles.rot;
   a.inverse = p->inverse;
   a.pos = p->positions;
@@ -842,6 +848,7 @@ bsc_status mxfp8_rope_quantize_qk(const bsc_rope_quant_params* p, bsc_stream_t s
   }
   a.turns = p->angles.turns;
   a.magnitude = p->angles.magnitude;
+  a.magnitude_low = p->angles.magnitude_low;
   a.rot = p->angles.rot;
   a.pos = p->positions;
   a.pos_b = p->position_stride_b;
@@ -885,6 +892,7 @@ bsc_status mx_cache_write_rope(const bsc_mx_cache_write_rope_params* p, bsc_stre
   a.ys[0] = {p->q_out_stride_b, p->q_out_stride_t, p->q_out_stride_h};
   a.turns = p->angles.turns;
   a.magnitude = p->angles.magnitude;
+  a.magnitude_low = p->angles.magnitude_low;
   a.rot = p->angles.rot;
   a.B = p->B;
   a.T = p->T;

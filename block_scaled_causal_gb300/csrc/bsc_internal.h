@@ -169,7 +169,7 @@ struct RopeArgs {
   RowStrides ys[2];
   uint8_t* sc[2];          // MXFP8 form: scales [B][H][T][D/32]
   const unsigned long long* turns;   // [rot/2], turns per token times 2^64
-  float magnitude;
+  float magnitude, magnitude_low;
   int rot, inverse;
   const int32_t* pos;      // nullptr: token t is at position t
   long long pos_b, pos_t;  // its strides; pos_t 0: of the first token

@@ -532,6 +532,8 @@ typedef struct {
   double original_length, low_turns, high_turns;   /* BSC_ROPE_BY_PARTS only */
 } bsc_rope_config;
 bsc_status bsc_rope_turns(const bsc_rope_config* c, unsigned long long* turns, float* magnitude);
+/* The same magnitude in more bits than a float: its nearest float and what is left are a bsc_rope_angles' two. */
+double bsc_rope_magnitude(const bsc_rope_config* c);
 
 /* What a call rotates by. */
 typedef struct {
@@ -539,6 +541,7 @@ typedef struct {
   float magnitude;        /* finite */
   int rot;                /* a multiple of 16, at most D */
   int interleaved;        /* 0 or 1 */
+  float magnitude_low;    /* added to magnitude, 2^-23 of it at most: what a float does not hold of the factor, or 0 */
 } bsc_rope_angles;
 
 /*

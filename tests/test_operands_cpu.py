@@ -139,6 +139,21 @@ def test_rope_refusals(ops, kw):  # noqa: F811
     assert e.value.status == UNSUPPORTED
 
 
+def test_magnitude_in_two_floats(ops):  # noqa: F811
+    """A Rope's factor is a double, passed as its nearest float and the rest; the C call refuses a rest that is none."""
+    r = ops.Rope(64, scaling=ops.ROPE_BY_PARTS, factor=8.0, original_length=8192, device="cpu")
+    assert r.magnitude == 0.1 * math.log(8.0) + 1.0
+    for m in (r.magnitude, 1.0, 0.7, -1.3, 0.0, 1e-40, 3e38):
+        p = ops.Rope(64, magnitude=m, device="cpu").params
+        assert p.magnitude == np.float32(m) and abs(p.magnitude_low) <= abs(p.magnitude) * 2.0 ** -24
+        assert m == 1e-40 or abs(p.magnitude + p.magnitude_low - m) <= abs(m) * 2.0 ** -47
+    x = dict(q=FAKE, q_out=FAKE, B=2, T=4, Hq=4, D=128, dtype=0, inverse=0, **_strides(("q", "q_out")))
+    for low, want in ((1e-6, UNSUPPORTED), (-1e-6, UNSUPPORTED), (math.nan, UNSUPPORTED), (1e-8, ALIGN)):
+        a = _angles(ops, magnitude_low=low)
+        assert ops.lib.rope(ctypes.byref(ops.RopeParams(angles=a, **dict(x, q=FAKE + 8))), None) == want
+    assert ops.lib.bsc_rope_magnitude(None) == 1.0
+
+
 # ------------------------------------------------------------------------------- structures, sizes
 def test_struct_layouts(ops):  # noqa: F811
     sizes = dict(RmsNormParams=160, RmsNormBwdParams=160, RopeConfig=48, RopeAngles=24, RopeParams=208, RopeQuantParams=176,

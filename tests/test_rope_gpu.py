@@ -334,3 +334,36 @@ def test_no_heads_of_q(ops):
             f()
     assert ops.rope(q, None, r)[0].shape == q.shape and ops.rope(q, k[:, :, :0], r)[1].shape == q.shape
     assert ops.rope(k[:, :0], k[:, :0], r)[1].shape == (2, 0, 2, 64)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("magnitude", [1.0, 0.1 * np.log(8.0) + 1, 0.7])
+def test_cosines_are_rounded_about_once(ops, interleaved, magnitude):
+    """Pairs (a, 2048) for which a cos - 2048 sin all but cancels: the product by a power of two is exact, the sum is rounded
+    where it is small, so what is left are the cosine's and sine's own errors.  One rounding of each is 0.289 units of its last
+    place in root mean square (0.29 and 5% are allowed), and at most 0.72 in [1/2, 1), 0.8 here, for what a sum of two parts
+    that is rounded at the end has beyond its half."""
+    rng = np.random.default_rng(37)
+    B, T, rot = 4, 2048, 128
+    r = ops.Rope(rot, base=500000.0, interleaved=interleaved, magnitude=magnitude)
+    pos = rng.integers(-2 ** 31, 2 ** 31, (B, T))
+    angle = R.angles(r.turns.cpu().numpy().view(np.uint64), pos)
+    c, s = np.cos(angle), np.sin(angle)
+    b = np.full_like(c, 2048.0)
+    a = np.rint(b * s / c)
+    exact = magnitude * (a * c - b * s)
+    few = (np.abs(a) <= 2048) & (np.abs(exact) < 2.0 ** -6)
+    assert few.sum() > 3000
+    i = np.arange(rot // 2)
+    ia, ib = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
+    x = np.zeros((B, T, 1, rot))
+    x[:, :, 0, ia], x[:, :, 0, ib] = np.where(few, a, 0), np.where(few, b, 0)
+    q = torch.tensor(x).half().cuda()
+    y = f64(ops.rope(q, None, r, torch.tensor(pos, dtype=torch.int32).cuda())[0])[:, :, 0, ia]
+    err, a, b, exact = np.abs(y - exact)[few], a[few], b[few], exact[few]
+    last = lambda v: np.spacing(np.abs(magnitude * v[few]).astype(np.float32)).astype(np.float64)  # noqa: E731
+    out = np.abs(exact) * 2.0 ** -11 + 2.0 ** -25                 # the output's rounding, half a step
+    unit = 2.0 ** -24 * (2 if magnitude > 1 else 1)
+    assert np.all(err <= 0.8 * unit * (np.abs(a) + b) + out)
+    size = np.mean((0.29 * last(c) * a) ** 2 + (0.29 * last(s) * b) ** 2 + out ** 2)
+    assert np.sqrt(np.mean(err ** 2) / size) <= 1.05, np.sqrt(np.mean(err ** 2) / size)
