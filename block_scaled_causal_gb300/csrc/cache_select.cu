@@ -13,9 +13,9 @@
 // Choice.  The first and the last pages, then the best scores, ties to the lower page; the list in ascending order, as
 // slices (page, head) of the pools, so that the attention reads it as it reads a page table.
 //
-// What bounds it: latency.  512 pages of 4 KV heads: bounds of the newest page 4.4 us (of 32 prompts of 2048 tokens, 64 to a page, 15.6), choice 9.1 us cold (chains of length,
-// page id, data; then rounds of barriers); 128 rows of up to 512 pages 12.1 us for 6.8 MB of bounds (2 D + 1 bytes per page and
-// head, against 8.7 KB of a page of 64 tokens in 4 bits).
+// What bounds it: latency.  512 pages of 4 KV heads: bounds of the newest page 4.4 us (of 32 prompts of 2048 tokens, 64 to a
+// page, 15.6), choice 9.1 us cold (chains of length, page id, data; then rounds of barriers); 128 rows of up to 512 pages 12.1 us
+// for 6.8 MB of bounds (2 D + 1 bytes per page and head, against 8.7 KB of a page of 64 tokens in 4 bits).
 #include <cooperative_groups.h>
 
 #include "cache.cuh"
@@ -40,7 +40,8 @@ __device__ __forceinline__ int new_page(const BoundsArgs& a, int b, int i, long 
 // Several sequences may have the page, with different numbers of tokens: the one with the most writes, and no other, so that
 // codes and exponent are always of one block, and bound what every sequence has in the page.  Those with as many make the same
 // bytes.  Nothing has more than a whole page, so only a sequence's last page looks for such a sequence; last pages are
-// among the first blocks, so that their search is not what the call ends with (32 prompts of 2048 tokens 18.0 -> 15.7 us, 15.2 without it).
+// among the first blocks, so that their search is not what the call ends with (32 prompts of 2048 tokens 18.0 -> 15.7 us, 15.2
+// without it).
 template <int FMT, int D>
 __global__ void __launch_bounds__(BOUNDS_THREADS) cache_bounds_kernel(const BoundsArgs a, int per_seq) {
   constexpr int LPR = D / 8, ROWS = BOUNDS_THREADS / LPR, RB = row_bytes<FMT, D>(), NB = D / 32;
